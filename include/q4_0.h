@@ -62,7 +62,8 @@ typedef enum {
     Q4_ERR_SHAPE = 2,     /* M, N or K out of range, or K % 32 != 0           */
     Q4_ERR_ALIGN = 3,     /* a device pointer is not 16-byte aligned          */
     Q4_ERR_SEGMENTS = 4,  /* nseg outside 1..8, or a bad segment entry        */
-    Q4_ERR_HIP = 5        /* the HIP runtime reported an error at launch      */
+    Q4_ERR_HIP = 5,       /* the HIP runtime reported an error at launch      */
+    Q4_ERR_RANGE = 6      /* a size or flag of a q4_decoder.h call is out of range */
 } q4_status;
 
 /* Static English text for a status code (never NULL). */

@@ -1,7 +1,8 @@
-"""MI355X-native GGUF Q4_0 weight-only linear layer.
+"""MI355X-native GGUF Q4_0 weight-only linear layer, and the decoder operators
+between the linears.
 
 The computation lives in libq4amd.so (HIP kernels for gfx950 behind the C ABI
-of include/q4_0.h); this package is its thin Python binding.  The library is
+of include/q4_0.h and include/q4_decoder.h); this package is its thin Python binding.  The library is
 loaded on first use and a missing build raises instead of falling back.
 """
 
@@ -35,4 +36,16 @@ from ._binding import (  # noqa: F401
     status_str,
     time_next_launch,
     unpack,
+)
+from ._decoder import (  # noqa: F401
+    DECODER_EXPORTS,
+    KV_BLOCK,
+    KVCache,
+    add_rmsnorm,
+    kv_append,
+    kv_attention,
+    kv_attention_workspace,
+    kv_cache_bytes,
+    logits_adjust,
+    rope_table,
 )

@@ -19,7 +19,7 @@ _lock = threading.Lock()
 
 Q4_OK = 0
 STATUS_NAMES = {0: "Q4_OK", 1: "Q4_ERR_NULL", 2: "Q4_ERR_SHAPE", 3: "Q4_ERR_ALIGN",
-                4: "Q4_ERR_SEGMENTS", 5: "Q4_ERR_HIP"}
+                4: "Q4_ERR_SEGMENTS", 5: "Q4_ERR_HIP", 6: "Q4_ERR_RANGE"}
 EXPORTS = ("q4_status_str", "q4_0_packed_bytes", "q4_0_quantize", "q4_0_quantize_bf16", "q4_0_pack", "q4_0_unpack",
            "q4_0_dequant", "q4_0_linear", "q4_0_linear_multi", "q4_0_time_next_launch",
            "q4_0_linear_kernel", "q4_0_linear_swiglu", "q4_0_linear_swiglu_kernel", "q4_0_embed",
