@@ -21,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libq4amd.so")
+BINDING = os.path.join(PKG, "_q4decoder.so")     # the decoder operators' Python binding
 
 SOURCES = ("q4_0_format.hip", "q4_1_format.hip", "q4_0_linear.hip", "q4_0_measure.hip", "q4_0_abi.hip",
            "q4_kv_append.hip", "q4_kv_attention.hip", "q4_rmsnorm.hip", "q4_logits.hip", "q4_decoder_abi.hip")
@@ -85,8 +86,30 @@ def _write_build_info() -> None:
         json.dump(info, f)
 
 
+def _binding_command(out: str):
+    """The C++ compiler's line for the decoder operators' binding (host code
+    against torch's and Python's headers)."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(_hipcc())))
+    flags = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wno-unknown-pragmas", "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__=1",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    dirs = [f"-I{INCLUDE}", *(f"-isystem{d}" for d in (
+        os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+        os.path.join(rocm, "include"), sysconfig.get_paths()["include"]))]
+    libs = [f"-L{PKG}", "-l:libq4amd.so", "-Wl,-rpath,$ORIGIN", f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch_cpu",
+            "-ltorch_hip", "-lc10", "-lc10_hip"]
+    src = os.path.join(CSRC, "decoder_binding.cpp")
+    return ([shutil.which("g++") or "c++", *flags, *dirs, "-c", src, "-o", os.path.join(BUILD_DIR, "decoder_binding.o")],
+            [shutil.which("g++") or "c++", "-shared", "-o", out, os.path.join(BUILD_DIR, "decoder_binding.o"), *libs])
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every HIP source for gfx950 and link libq4amd.so; return its path."""
+    """Compile every HIP source for gfx950 and link libq4amd.so, and the Python
+    binding of the decoder operators on top of it; return the library's path."""
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = []
@@ -95,6 +118,9 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         objs.append(obj)
         cmds.append([hipcc, *COMMON_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
+    binding_tmp = BINDING + f".tmp{os.getpid()}"
+    compile_binding, link_binding = _binding_command(binding_tmp)
+    cmds.append(compile_binding)
     with ThreadPoolExecutor(max_workers=len(cmds)) as ex:
         outs = list(ex.map(_run, cmds))
     for o in outs:
@@ -106,6 +132,8 @@ def build(verbose: bool = False) -> str:
     tmp = LIB + f".tmp{os.getpid()}"
     _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    _run(link_binding)
+    os.replace(binding_tmp, BINDING)
     return LIB
 
 
