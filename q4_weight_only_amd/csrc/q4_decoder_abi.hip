@@ -131,6 +131,8 @@ q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, co
     a.q_heads = static_cast<int32_t>(q_heads);
     a.group = static_cast<int32_t>(q_heads / cache->kv_heads);
     a.scale_log2 = scale * 1.44269504088896340736f;
+    // the kernels give a token that is not seen a score of -inf * |scale|
+    if (fabsf(a.scale_log2) < 1e-20f) a.scale_log2 = 1e-20f;
     a.window = static_cast<int32_t>(window);
     a.out_bf16 = out_dtype == Q4_BF16;
     a.max_rows = static_cast<int32_t>(batch->max_rows);

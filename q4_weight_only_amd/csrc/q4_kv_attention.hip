@@ -37,6 +37,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 
+constexpr float kNan = __builtin_nanf("");
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kSlack = 8.0f;   // how far a score may pass m before m is raised
 
@@ -99,17 +100,126 @@ __device__ __forceinline__ float row_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
-// The blocks that a tile of rows reads, and their division over the splits of
-// the launch: split i has blocks [first + i * chunk, first + (i + 1) * chunk).
+// One 16-row tile's running state in a wave: lane (r, g4) holds, for row r, the
+// reference m, its share of the sum l, and dimensions 16 i + 4 g4 + j of O.
+template <int D>
+struct Tile {
+    float m, l;
+    floatx4 o[D / 16];
+
+    __device__ __forceinline__ void clear() {
+        m = kLowest;
+        l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i] = (floatx4){0, 0, 0, 0};
+    }
+
+    // m is raised to the rows' largest score where some score passes it by
+    // kSlack, and the sums follow.  (A score that is not a number raises
+    // nothing; its weight is not a number either.)
+    __device__ __forceinline__ void raise(float top) {
+        if (__any(top > m + kSlack)) {
+            const float raised = fmaxf(m, row_max(top));
+            const float f = __builtin_amdgcn_exp2f(m - raised);
+            m = raised;
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) o[i] = o[i] * f;
+        }
+    }
+
+    // Weights of a block.  st: q . k, -inf where the row does not see the
+    // token; c > 0.
+    __device__ __forceinline__ halfx8 weights(const floatx4 (&st)[2], float c, float ev, float inv_ev) {
+        float top = st[0][0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, st[i / 4][i % 4]);
+        raise(fmaf(top, c, ev));
+        const float shift = ev - m;
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __builtin_amdgcn_exp2f(fmaf(st[i / 4][i % 4], c, shift));
+        l = fmaf(((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7])), inv_ev, l);
+        return weights_f16(w);
+    }
+
+    // A value that is not a number reaches the rows that see its token and no
+    // others (0 * NaN is NaN): such tokens are counted for each output, and
+    // the product gets 0 for them.  n0, n1: nan_bytes of operand d's words.
+    __device__ __forceinline__ void mark_nans(int d, uint32_t n0, uint32_t n1, halfx8 seen) {
+        floatx4 hits = {0, 0, 0, 0};
+        // 0x38 is 1.0
+        hits = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16((n0 >> 7) * 0x38u, (n1 >> 7) * 0x38u), seen, hits, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (hits[j] > 0.0f) o[d][j] = __builtin_nanf("");
+    }
+};
+
+// The lane's tokens of a block are first + i and first + 16 + i; a row sees
+// tokens lo .. pos.
+__device__ __forceinline__ void hide_unseen(floatx4 (&st)[2], int first, int lo, int pos) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int j = first + i / 4 * 16 + i % 4;
+        st[i / 4][i % 4] = j >= lo && j <= pos ? st[i / 4][i % 4] : -__builtin_inff();
+    }
+}
+
+__device__ __forceinline__ halfx8 seen_tokens(int first, int lo, int pos) {   // 1 for each that the row sees
+    float one[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int j = first + i / 4 * 16 + i % 4;
+        one[i] = j >= lo && j <= pos ? 1.0f : 0.0f;
+    }
+    return weights_f16(one);
+}
+
+// Which row of q a lane has, and what it sees.
+struct LaneRow {
+    bool live;
+    int t, pos, lo;    // row of the sequence, its position, the first token that it sees
+    int64_t at;        // its first element in q and out
+};
+
+// Rows times heads of a group are at most 2^20 * 64: 32 bits hold them.
+__device__ __forceinline__ LaneRow lane_row(const AttentionArgs &a, const KvSequence &s, int head, int rr, int all_rows, int D) {
+    LaneRow x;
+    x.live = rr < all_rows;
+    const int last = x.live ? rr : all_rows - 1;
+    x.t = last / a.group;
+    x.pos = s.pos0 + x.t;
+    x.lo = a.window ? x.pos - a.window + 1 : 0;
+    x.at = (static_cast<int64_t>(s.row0 + x.t) * a.q_heads + head * a.group + last % a.group) * D;
+    return x;
+}
+
+// The lane's operand slices of its row of q, the sign of a negative scale taken in.
+template <int D>
+__device__ __forceinline__ void load_q(const AttentionArgs &a, int64_t at, int g4, bf16x8 (&q)[D / 32]) {
+    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        u32x4 w = reinterpret_cast<const u32x4 *>(a.q + at + 64 * (i / 2) + 16 * g4 + 8 * (i % 2))[0];
+        w.x ^= flip;
+        w.y ^= flip;
+        w.z ^= flip;
+        w.w ^= flip;
+        q[i] = __builtin_bit_cast(bf16x8, w);
+    }
+}
+
+// The blocks that a group of rows reads, and their division over the splits
+// of the launch: split i has blocks [first + i * chunk, first + (i + 1) * chunk).
 struct Span {
     int first, last, chunk, splits;   // blocks [first, last), splits that have some
 };
 
-// p_first, p_last: positions of the tile's first and last row (p_last < 0:
+// p_first, p_last: positions of the group's first and last row (p_last < 0:
 // nothing is seen).  Tokens past the block table are not read: the rows that
 // would see them give what is not a number (`past` below).
-__device__ __forceinline__ Span span_of(const KvView &kv, int p_first, int p_last, int window, int chunk,
-                                        int grid_splits) {
+__device__ __forceinline__ Span span_of(const KvView &kv, int p_first, int p_last, int window, int chunk, int grid_splits) {
     Span s;
     int lo = window ? p_first - window + 1 : 0;
     if (lo < 0) lo = 0;
@@ -131,6 +241,38 @@ __device__ __forceinline__ Span span_of(const KvView &kv, int p_first, int p_las
 
 __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 0 && pos / kKvBlock >= kv.table_width; }
 
+// How a launch is shaped: groups of `group_rows` rows of a sequence and kv
+// head, and the split of their blocks.
+struct Plan {
+    int group_rows;      // 16, or kTileWaves * 16 * NR of the tile kernel
+    int groups;          // of the sequence with most rows
+    int chunk, splits;
+};
+
+// Where a split's partial results of a row are in the workspace: first
+// {m, l} [row][split], then O [row][split][D], rows counted over batch, kv
+// head, group and row of the group.
+struct Partials {
+    floatx2 *ml;
+    float *o;
+};
+
+__device__ __forceinline__ int64_t partial_row(const KvView &kv, const Plan &p, int b, int head, int64_t group) {
+    return ((static_cast<int64_t>(b) * kv.kv_heads + head) * p.groups + group) * p.group_rows;
+}
+
+__device__ __forceinline__ Partials partials(const AttentionArgs &a, const Plan &p) {
+    Partials w;
+    w.ml = reinterpret_cast<floatx2 *>(a.workspace);
+    const int64_t rows = static_cast<int64_t>(a.kv.batch) * a.kv.kv_heads * p.groups * p.group_rows;
+    w.o = a.workspace + rows * p.splits * 2;
+    return w;
+}
+
+__device__ __forceinline__ float inverse(const KvView &kv, int pos, float total) {
+    return past(kv, pos) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
+}
+
 // ------------------------------------------------------- few rows: decode
 // A workgroup has 16 rows (of rows x heads of the group) of one sequence and
 // kv head, and one chunk of its blocks; its four waves take every fourth block.
@@ -139,12 +281,7 @@ __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 
 constexpr int kWaves = 4;
 
 template <int D>
-struct Partial {
-    static constexpr int kFloats = 16 * (D + 2);   // one tile's m[16], l[16], O[16][D]
-};
-
-template <int D>
-__global__ __launch_bounds__(64 * kWaves) void attention_rows_kernel(AttentionArgs a, int chunk, int tiles) {
+__global__ __launch_bounds__(64 * kWaves, 3) void attention_rows_kernel(AttentionArgs a, Plan plan) {
     constexpr int KQ = D / 32;   // k slices of the first product
     constexpr int DT = D / 16;   // 16-dimension tiles of the output
     __shared__ float part_m[kWaves][16], part_l[kWaves][16];
@@ -153,285 +290,548 @@ __global__ __launch_bounds__(64 * kWaves) void attention_rows_kernel(AttentionAr
     const int r = lane & 15, g4 = lane >> 4;
     const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads;
     const KvSequence s = kv_sequence(a.kv, b);
-    const int grid_tiles = gridDim.y / a.kv.kv_heads;
-    const int64_t all_rows = static_cast<int64_t>(s.rows) * a.group;
-    for (int64_t tile = blockIdx.y / a.kv.kv_heads; tile * 16 < all_rows; tile += grid_tiles) {
-        const int64_t rr = tile * 16 + r;
-        const bool live = rr < all_rows;
-        const int t = static_cast<int>((live ? rr : all_rows - 1) / a.group);
-        const int g = static_cast<int>((live ? rr : all_rows - 1) % a.group);
-        const int pos = s.pos0 + t;
-        const int t_first = static_cast<int>(tile * 16 / a.group);
-        const int64_t r_last = tile * 16 + 15 < all_rows ? tile * 16 + 15 : all_rows - 1;
-        const int p_first = s.pos0 + t_first, p_last = s.pos0 + static_cast<int>(r_last / a.group);
-        // tiles past those that the launch was shaped for are not split: they
+    const int grid_groups = gridDim.y / a.kv.kv_heads;
+    const int all_rows = s.rows * a.group;
+    for (int group = blockIdx.y / a.kv.kv_heads; group * 16 < all_rows; group += grid_groups) {
+        const LaneRow row = lane_row(a, s, head, group * 16 + r, all_rows, D);
+        const int r_last = group * 16 + 15 < all_rows ? group * 16 + 15 : all_rows - 1;
+        const int p_first = s.pos0 + group * 16 / a.group;
+        const int p_last = s.pos0 + r_last / a.group;
+        // groups past those that the launch was shaped for are not split: they
         // have no place in the workspace
-        const Span sp = span_of(a.kv, p_first, p_last, a.window, chunk, tile < tiles ? gridDim.x : 1);
+        const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, group < plan.groups ? gridDim.x : 1);
         const int split = blockIdx.x;
         if (split >= (sp.splits ? sp.splits : 1)) continue;   // uniform
         const int blk0 = sp.first + split * sp.chunk;
         const int blk1 = blk0 + sp.chunk < sp.last ? blk0 + sp.chunk : sp.last;
-        // the tokens that all rows and that any row of the tile see
-        const int lo = a.window ? pos - a.window + 1 : 0;
+        // the first tokens that all rows and that any row of the group see
         const int all_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
-        const int64_t out_row = s.row0 + t;
-        const int64_t out_at = (out_row * a.q_heads + head * a.group + g) * D;
 
         bf16x8 q[KQ];
+        load_q<D>(a, row.at, g4, q);
+        Tile<D> tile;
+        tile.clear();
+        // a block's ids and exponents are read 64 blocks at a time, one a lane,
+        // its codes one block ahead
+        for (int first = blk0 + wave; first < blk1; first += 64 * kWaves) {
+            const int count = (blk1 - first + kWaves - 1) / kWaves, blocks = count < 64 ? count : 64;
+            const int my_id = lane < blocks ? kv_block_id(a.kv, b, first + lane * kWaves) : -1;
+            const int my_exps =
+                reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(my_id < 0 ? 0 : my_id) * a.kv.kv_heads + head];
+            u32x4 codes[2][2 * KQ];
+            // (past the end the last block is read again)
+            auto fetch = [&](int i, u32x4(&to)[2 * KQ]) {
+                const int id = __builtin_amdgcn_readlane(my_id, i < blocks ? i : blocks - 1);
+                const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
+                const u32x4 *src = reinterpret_cast<const u32x4 *>(a.kv.data + plane * (kKvBlock * D)) + lane;
 #pragma unroll
-        for (int i = 0; i < KQ; ++i)
-            q[i] = reinterpret_cast<const bf16x8 *>(a.q + out_at + 64 * (i / 2) + 16 * g4 + 8 * (i % 2))[0];
-
-        float m = kLowest, l = 0.0f;
-        floatx4 o[DT];
+                for (int j = 0; j < 2 * KQ; ++j) to[j] = src[64 * j];
+            };
+            fetch(0, codes[0]);
+            for (int i0 = 0; i0 < blocks; i0 += 2) {
 #pragma unroll
-        for (int i = 0; i < DT; ++i) o[i] = (floatx4){0, 0, 0, 0};
-
-        for (int blk = blk0 + wave; blk < blk1; blk += kWaves) {
-            const int id = __builtin_amdgcn_readfirstlane(kv_block_id(a.kv, b, blk));
-            const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
-            const u32x4 *src = reinterpret_cast<const u32x4 *>(a.kv.data + plane * (kKvBlock * D)) + lane;
-            u32x4 kc[KQ], vc[KQ];
+                for (int u = 0; u < 2; ++u) {
+                    const int i = i0 + u;
+                    fetch(i + 1, codes[u ^ 1]);
+                    if (i >= blocks) continue;
+                    u32x4(&kc)[2 * KQ] = codes[u];
+                    const int e2 = __builtin_amdgcn_readlane(my_exps, i);
+                    const float ek = static_cast<float>(static_cast<int8_t>(e2 & 0xFF));
+                    const float ev = static_cast<float>(static_cast<int8_t>(e2 >> 8));
+                    const bool known = __builtin_amdgcn_readlane(my_id, i) >= 0;
+                    const float c = fabsf(a.scale_log2) * __builtin_amdgcn_exp2f(ek);
+                    const float inv_ev = __builtin_amdgcn_exp2f(-ev);
+                    floatx4 st[2];
 #pragma unroll
-            for (int i = 0; i < KQ; ++i) kc[i] = src[64 * i];
+                    for (int tt = 0; tt < 2; ++tt) {
+                        st[tt] = (floatx4){0, 0, 0, 0};
 #pragma unroll
-            for (int i = 0; i < KQ; ++i) vc[i] = src[64 * (KQ + i)];
-            const float ek = static_cast<float>(a.kv.exps[plane]), ev = static_cast<float>(a.kv.exps[plane + 1]);
-            const float c = id < 0 ? __builtin_nanf("") : a.scale_log2 * __builtin_amdgcn_exp2f(ek);
-            floatx4 st[2];
+                        for (int k = 0; k < KQ; ++k) {
+                            const u32x4 w = kc[tt * (KQ / 2) + k / 2];
+                            const bf16x8 kf = k % 2 ? codes_bf16(w.z, w.w) : codes_bf16(w.x, w.y);
+                            st[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[k], st[tt], 0, 0, 0);
+                        }
+                        if (!known) st[tt] = (floatx4){kNan, kNan, kNan, kNan};
+                    }
+                    const int start = (first + i * kWaves) * kKvBlock;
+                    if (start < all_lo || start + kKvBlock - 1 > p_first) {   // some row does not see some token
+                        const int tok = start + 4 * g4;
+                        hide_unseen(st, tok, row.lo, row.pos);
+                        // bytes that no row of the group sees may hold anything
+                        const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
+                        uint32_t bad = 0;
 #pragma unroll
-            for (int tt = 0; tt < 2; ++tt) {
-                st[tt] = (floatx4){0, 0, 0, 0};
+                        for (int j = KQ; j < 2 * KQ; ++j) {
+                            kc[j].x &= in0;
+                            kc[j].y &= in1;
+                            kc[j].z &= in0;
+                            kc[j].w &= in1;
+                            bad |= nan_bytes(kc[j].x) | nan_bytes(kc[j].y) | nan_bytes(kc[j].z) | nan_bytes(kc[j].w);
+                        }
+                        if (__any(bad != 0)) {
+                            const halfx8 seen = seen_tokens(tok, row.lo, row.pos);
 #pragma unroll
-                for (int i = 0; i < KQ; ++i) {
-                    const u32x4 w = kc[tt * (KQ / 2) + i / 2];
-                    const bf16x8 kf = i % 2 ? codes_bf16(w.z, w.w) : codes_bf16(w.x, w.y);
-                    st[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[i], st[tt], 0, 0, 0);
-                }
-            }
-            float w[8];   // scores, then weights, of tokens 4 g4 + i and 16 + 4 g4 + i
+                            for (int d = 0; d < DT; ++d) {
+                                const int at = d % 2 * 2;
+                                const uint32_t n0 = nan_bytes(kc[KQ + d / 2][at]), n1 = nan_bytes(kc[KQ + d / 2][at + 1]);
+                                tile.mark_nans(d, n0, n1, seen);
+                                kc[KQ + d / 2][at] = without(kc[KQ + d / 2][at], n0);
+                                kc[KQ + d / 2][at + 1] = without(kc[KQ + d / 2][at + 1], n1);
+                            }
+                        }
+                    }
+                    const halfx8 wf = tile.weights(st, c, ev, inv_ev);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = fmaf(st[i / 4][i % 4], c, ev);
-            const int start = blk * kKvBlock;
-            const bool whole = start >= all_lo && start + kKvBlock - 1 <= p_first;   // all rows see all tokens
-            uint32_t seen = 0xFF;
-            if (!whole) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int j = start + i / 4 * 16 + 4 * g4 + i % 4;
-                    if (j < lo || j > pos) {
-                        w[i] = -__builtin_inff();
-                        seen &= ~(1u << i);
+                    for (int d = 0; d < DT; ++d) {
+                        const u32x4 v = kc[KQ + d / 2];
+                        const halfx8 vf = d % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
+                        tile.o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf, tile.o[d], 0, 0, 0);
                     }
                 }
-            }
-            float top = w[0];
-#pragma unroll
-            for (int i = 1; i < 8; ++i) top = fmaxf(top, w[i]);
-            if (__any(top > m + kSlack)) {
-                const float raised = fmaxf(m, row_max(top));
-                const float f = __builtin_amdgcn_exp2f(m - raised);
-                m = raised;
-                l *= f;
-#pragma unroll
-                for (int i = 0; i < DT; ++i) o[i] = o[i] * f;
-            }
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[i] = __builtin_amdgcn_exp2f(w[i] - m);
-                sum += w[i];
-            }
-            l = fmaf(sum, __builtin_amdgcn_exp2f(-ev), l);
-            const halfx8 wf = weights_f16(w);
-            if (!whole) {
-                // bytes that no row of the tile sees may hold anything
-                const uint32_t in0 = bytes_in(start + 4 * g4, any_lo, p_last + 1);
-                const uint32_t in1 = bytes_in(start + 16 + 4 * g4, any_lo, p_last + 1);
-                uint32_t bad = 0;
-#pragma unroll
-                for (int i = 0; i < KQ; ++i) {
-                    vc[i].x &= in0;
-                    vc[i].y &= in1;
-                    vc[i].z &= in0;
-                    vc[i].w &= in1;
-                    bad |= nan_bytes(vc[i].x) | nan_bytes(vc[i].y) | nan_bytes(vc[i].z) | nan_bytes(vc[i].w);
-                }
-                if (__any(bad != 0)) {
-                    // a value that is not a number reaches the rows that see
-                    // its token, and no others (0 * NaN is NaN): count such
-                    // tokens for each output and leave them out of the product
-                    float one[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) one[i] = (seen >> i) & 1u ? 1.0f : 0.0f;
-                    const halfx8 sf = weights_f16(one);
-#pragma unroll
-                    for (int i = 0; i < DT; ++i) {
-                        const int at = i % 2 * 2;
-                        const uint32_t n0 = nan_bytes(vc[i / 2][at]), n1 = nan_bytes(vc[i / 2][at + 1]);
-                        floatx4 hits = {0, 0, 0, 0};
-                        // 0x38 is 1.0
-                        hits = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16((n0 >> 7) * 0x38u, (n1 >> 7) * 0x38u),
-                                                                      sf, hits, 0, 0, 0);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (hits[j] > 0.0f) o[i][j] = __builtin_nanf("");
-                        vc[i / 2][at] = without(vc[i / 2][at], n0);
-                        vc[i / 2][at + 1] = without(vc[i / 2][at + 1], n1);
-                    }
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < DT; ++i) {
-                const u32x4 v = vc[i / 2];
-                const halfx8 vf = i % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
-                o[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf, o[i], 0, 0, 0);
             }
         }
-        l = row_sum(l);
+        // hides the lane from the loop over the groups, out of which the
+        // compiler would take the addresses below and hold them all
+        int re = r, ge = g4;
+        asm volatile("" : "+v"(re), "+v"(ge));
+        tile.l = row_sum(tile.l);
         // join the four waves
-        __syncthreads();   // the previous tile's sums have been read
-        if (g4 == 0) {
-            part_m[wave][r] = m;
-            part_l[wave][r] = l;
+        __syncthreads();   // the previous group's sums have been read
+        if (ge == 0) {
+            part_m[wave][re] = tile.m;
+            part_l[wave][re] = tile.l;
         }
 #pragma unroll
         for (int i = 0; i < DT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) part_o[wave][(16 * i + 4 * g4 + j) * 16 + r] = o[i][j];
+            for (int j = 0; j < 4; ++j) part_o[wave][(16 * i + 4 * ge + j) * 16 + re] = tile.o[i][j];
         __syncthreads();
-        float top = part_m[0][r];
+        float top = part_m[0][re];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][r]);
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
         float f[kWaves], total = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(part_m[w][r] - top);
-            total += f[w] * part_l[w][r];
+            f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
+            total += f[w] * part_l[w][re];
         }
+        if (!row.live) continue;
         // thread: row r, dimensions tid / 16 + 16 i
-        const int d0 = threadIdx.x >> 4;
-        const bool final_out = sp.splits <= 1;
-        float *ws = a.workspace +
-                    (((static_cast<int64_t>(b) * a.kv.kv_heads + head) * tiles + tile) * gridDim.x + split) * Partial<D>::kFloats;
-        const float inv = past(a.kv, pos) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
+        const int d0 = 4 * wave + ge;
+        const bool whole = sp.splits <= 1;
+        const Partials ws = partials(a, plan);
+        const int64_t at = (partial_row(a.kv, plan, b, head, group) + re) * plan.splits + split;
+        const float inv = inverse(a.kv, row.pos, total);
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
             const int d = d0 + 16 * i;
             float acc = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) acc += f[w] * part_o[w][d * 16 + r];
-            if (!final_out)
-                ws[32 + r * D + d] = acc;
-            else if (live) {
-                acc *= inv;
-                if (a.out_bf16) static_cast<__bf16 *>(a.out)[out_at + d] = static_cast<__bf16>(acc);
-                else static_cast<float *>(a.out)[out_at + d] = acc;
-            }
+            for (int w = 0; w < kWaves; ++w) acc += f[w] * part_o[w][d * 16 + re];
+            if (!whole) ws.o[at * D + d] = acc;
+            else if (a.out_bf16) static_cast<__bf16 *>(a.out)[row.at + d] = static_cast<__bf16>(acc * inv);
+            else static_cast<float *>(a.out)[row.at + d] = acc * inv;
         }
-        if (!final_out && threadIdx.x < 16) {
-            ws[r] = top;
-            ws[16 + r] = total;
-        }
+        if (!whole && d0 == 0) ws.ml[at] = (floatx2){top, total};
     }
 }
 
-// Joins the splits of a tile: one workgroup a row.
-template <int D>
-__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, int chunk, int tiles, int splits) {
-    constexpr int LANES = D / 4;            // threads with four dimensions each
-    constexpr int PARTS = 256 / LANES;      // splits summed side by side
-    __shared__ floatx4 part[PARTS][LANES];
-    __shared__ float part_l[PARTS];
+// ------------------------------------------------- many rows: prompts
+// A workgroup has kTileWaves * NR tiles of 16 rows and two sets of kTileWaves
+// waves, which have the same rows, NR tiles to a wave, and take the blocks in
+// turn: a long row's blocks follow each other half as often, and each SIMD has
+// a wave of either set to run while the other waits.  All waves walk the
+// blocks together, two at a time: each loads its part of a pair two pairs early
+// into registers, and the pair passes to all waves through LDS in the cache's
+// own order (a lane's 16 bytes are its operand slices, so the reads have no
+// bank conflicts).  Every slice that a wave converts feeds NR products.
+// Groups with the most tokens start first.
+constexpr int kTileWaves = 4;
+constexpr int kTileThreads = 2 * 64 * kTileWaves;
+constexpr int kSegment = kTileThreads;   // blocks whose ids and exponents are held in LDS
+
+template <int D, int NR>
+__global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(AttentionArgs a, Plan plan) {
+    constexpr int KQ = D / 32, DT = D / 16;
+    constexpr int kRows = kTileWaves * 16 * NR;
+    constexpr int kBlock16 = 2 * KQ * 64;                  // 16-byte pieces of a block
+    constexpr int kLoads = 2 * kBlock16 / kTileThreads;    // a thread's of a pair
+    __shared__ u32x4 stage[2][2][kBlock16];
+    __shared__ u32x4 nans[2][2][kBlock16 / 2];   // nan_bytes of the V codes, where there are some (nan_block)
+    __shared__ int32_t nan_block[2][2];
+    __shared__ u32x2 meta[kSegment];             // id and exponents
+    __shared__ floatx2 other[kTileWaves][64];    // the second set's m and l
+    const int lane = threadIdx.x & 63;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kTileWaves, set = wave8 / kTileWaves;
+    const int r = lane & 15, g4 = lane >> 4;
     const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads;
     const KvSequence s = kv_sequence(a.kv, b);
-    const int64_t all_rows = static_cast<int64_t>(s.rows) * a.group;
-    const int64_t tile = blockIdx.y / a.kv.kv_heads;
-    const int r = blockIdx.x;
-    const int64_t rr = tile * 16 + r;
-    if (rr >= all_rows) return;
-    const int64_t r_last = tile * 16 + 15 < all_rows ? tile * 16 + 15 : all_rows - 1;
-    const Span sp = span_of(a.kv, s.pos0 + static_cast<int>(tile * 16 / a.group), s.pos0 + static_cast<int>(r_last / a.group),
-                            a.window, chunk, splits);
-    if (sp.splits <= 1) return;
-    const float *ws = a.workspace +
-                      ((static_cast<int64_t>(b) * a.kv.kv_heads + head) * tiles + tile) * splits * Partial<D>::kFloats;
-    float top = kLowest;
-    for (int i = 0; i < sp.splits; ++i) top = fmaxf(top, ws[static_cast<int64_t>(i) * Partial<D>::kFloats + r]);
-    const int x = threadIdx.x % LANES, y = threadIdx.x / LANES;
-    floatx4 acc = {0, 0, 0, 0};
-    float total = 0.0f;
-    for (int i = y; i < sp.splits; i += PARTS) {
-        const float *p = ws + static_cast<int64_t>(i) * Partial<D>::kFloats;
-        const float f = __builtin_amdgcn_exp2f(p[r] - top);
-        total += f * p[16 + r];
-        acc = acc + reinterpret_cast<const floatx4 *>(p + 32 + r * D)[x] * f;
-    }
-    part[y][x] = acc;
-    if (x == 0) part_l[y] = total;
-    __syncthreads();
-    if (y != 0) return;
+    const int grid_groups = gridDim.y / a.kv.kv_heads;
+    const int all_rows = s.rows * a.group;
+    const int groups = (all_rows + kRows - 1) / kRows;
+    for (int back = blockIdx.y / a.kv.kv_heads; back < groups; back += grid_groups) {
+        const int group = groups - 1 - back;
+        const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
+        const int p_first = s.pos0 + rr0 / a.group, p_last = s.pos0 + (rr1 - 1) / a.group;
+        const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, group < plan.groups ? gridDim.x : 1);
+        const int split = blockIdx.x;
+        if (split >= (sp.splits ? sp.splits : 1)) continue;   // uniform
+        const int blk0 = sp.first + split * sp.chunk;
+        const int blk1 = blk0 + sp.chunk < sp.last ? blk0 + sp.chunk : sp.last;
+        // the wave's own rows
+        const int wr0 = rr0 + wave * (16 * NR), wr1 = wr0 + 16 * NR < rr1 ? wr0 + 16 * NR : rr1;
+        const int w_first = s.pos0 + wr0 / a.group;
+        const int w_last = wr0 < rr1 ? s.pos0 + (wr1 - 1) / a.group : -1;
+        const int wave_lo = a.window ? w_first - a.window + 1 : 0;
+        // the first tokens that all rows and that any row of the group see
+        const int group_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
+
+        LaneRow row[NR];
+        bf16x8 q[NR][KQ];
+        Tile<D> tile[NR];
 #pragma unroll
-    for (int i = 1; i < PARTS; ++i) {
-        acc = acc + part[i][x];
-        total += part_l[i];
+        for (int n = 0; n < NR; ++n) {
+            row[n] = lane_row(a, s, head, wr0 + 16 * n + r, all_rows, D);
+            load_q<D>(a, row[n].at, g4, q[n]);
+            tile[n].clear();
+        }
+        for (int seg = blk0; seg < blk1; seg += kSegment) {
+            const int blocks = blk1 - seg < kSegment ? blk1 - seg : kSegment;
+            __syncthreads();   // the last segment's ids and stages have been read
+            if (threadIdx.x < 4) (&nan_block[0][0])[threadIdx.x] = -1;
+            {
+                // (past the segment's end the last block stands in)
+                const int i = static_cast<int>(threadIdx.x) < blocks ? threadIdx.x : blocks - 1;
+                const int id = kv_block_id(a.kv, b, seg + i);
+                const uint32_t e2 =
+                    reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head];
+                meta[threadIdx.x] = (u32x2){static_cast<uint32_t>(id), e2};
+            }
+            __syncthreads();
+            u32x4 ahead[2][kLoads];
+            auto meta_of = [&](int i) { return meta[i < kSegment ? i : kSegment - 1]; };
+            // the thread's part of a pair is of its first or second block
+            auto in_pair = [&](int j) { return (static_cast<int>(threadIdx.x) + kTileThreads * j) / kBlock16; };
+            auto fetch = [&](int pair, u32x4(&to)[kLoads]) {
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    const int id = __builtin_amdgcn_readfirstlane(meta_of(2 * pair + in_pair(j)).x);
+                    const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
+                    to[j] = reinterpret_cast<const u32x4 *>(a.kv.data + plane * (kKvBlock * D))[(threadIdx.x + kTileThreads * j) % kBlock16];
+                }
+            };
+            // some row of the group does not see some token of the pair
+            auto partly_seen = [&](int pair) {
+                const int first = (seg + 2 * pair) * kKvBlock;
+                return first < group_lo || first + 2 * kKvBlock - 1 > p_first;
+            };
+            // Puts a pair, which `from` holds, into its stage for all waves.
+            auto put = [&](int pair, int buf, u32x4(&from)[kLoads]) {
+                if (partly_seen(pair)) {
+                    // what no row sees may hold anything, and what is not a
+                    // number must not meet a weight of 0
+#pragma unroll
+                    for (int j = 0; j < kLoads; ++j) {
+                        const int which = in_pair(j), at = (threadIdx.x + kTileThreads * j) % kBlock16 - KQ * 64;
+                        if (at < 0) continue;
+                        const int tok = (seg + 2 * pair + which) * kKvBlock + 4 * g4;
+                        const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
+                        u32x4 v = from[j], n;
+                        v.x &= in0;
+                        v.y &= in1;
+                        v.z &= in0;
+                        v.w &= in1;
+                        uint32_t bad = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            n[k] = nan_bytes(v[k]);
+                            bad |= n[k];
+                            v[k] = without(v[k], n[k]);
+                        }
+                        nans[buf][which][at] = n;
+                        if (bad) nan_block[buf][which] = pair;
+                        from[j] = v;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) (&stage[buf][0][0])[threadIdx.x + kTileThreads * j] = from[j];
+            };
+            // One barrier a pair, between the softmax and the second product:
+            // before it the waves put the next pair into the other stage and
+            // take the last of this one's codes, after it they take the next
+            // one's first, which the product hides.
+            fetch(0, ahead[0]);
+            asm volatile("" ::: "memory");   // in this order, which the waits in the loop go by
+            fetch(1, ahead[1]);
+            u32x4 kw[KQ], vw[KQ];
+            put(0, 0, ahead[0]);
+            fetch(2, ahead[0]);
+            u32x2 here = meta_of(set);
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < KQ; ++k) kw[k] = stage[0][set][64 * k + lane];
+            const int pairs = (blocks + 1) / 2;
+            for (int p0 = 0; p0 < pairs; p0 += 2) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int pair = p0 + u, i = 2 * pair + set;
+                    put(pair + 1, u ^ 1, ahead[u ^ 1]);
+                    fetch(pair + 3, ahead[u ^ 1]);
+                    const int id = __builtin_amdgcn_readfirstlane(here.x), e2 = __builtin_amdgcn_readfirstlane(here.y);
+                    here = meta_of(i + 2);
+                    const int start = (seg + i) * kKvBlock;
+                    // not past the end, and something that the wave's rows see
+                    const bool work = i < blocks && start <= w_last && start + kKvBlock > wave_lo;
+                    halfx8 wf[NR];
+                    if (work) {
+                        const float ek = static_cast<float>(static_cast<int8_t>(e2 & 0xFF));
+                        const float ev = static_cast<float>(static_cast<int8_t>(e2 >> 8));
+                        const float c = fabsf(a.scale_log2) * __builtin_amdgcn_exp2f(ek);
+                        const float inv_ev = __builtin_amdgcn_exp2f(-ev);
+#pragma unroll
+                        for (int k = 0; k < KQ; ++k) vw[k] = stage[u][set][64 * (KQ + k) + lane];
+                        floatx4 st[NR][2];
+#pragma unroll
+                        for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){0, 0, 0, 0};
+#pragma unroll
+                            for (int k = 0; k < KQ; ++k) {
+                                const u32x4 w = kw[tt * (KQ / 2) + k / 2];
+                                const bf16x8 kf = k % 2 ? codes_bf16(w.z, w.w) : codes_bf16(w.x, w.y);
+#pragma unroll
+                                for (int n = 0; n < NR; ++n)
+                                    st[n][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][k], st[n][tt], 0, 0, 0);
+                            }
+                            if (id < 0)
+#pragma unroll
+                                for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){kNan, kNan, kNan, kNan};
+                        }
+                        if (partly_seen(pair)) {   // as put() decided
+                            const int tok = start + 4 * g4;
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) hide_unseen(st[n], tok, row[n].lo, row[n].pos);
+                            if (__builtin_amdgcn_readfirstlane(nan_block[u][set]) == pair) {
+#pragma unroll
+                                for (int n = 0; n < NR; ++n) {
+                                    const halfx8 seen = seen_tokens(tok, row[n].lo, row[n].pos);
+#pragma unroll
+                                    for (int d = 0; d < DT; ++d) {
+                                        const u32x4 x = nans[u][set][64 * (d / 2) + lane];
+                                        tile[n].mark_nans(d, d % 2 ? x.z : x.x, d % 2 ? x.w : x.y, seen);
+                                    }
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) wf[n] = tile[n].weights(st[n], c, ev, inv_ev);
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int k = 0; k < KQ; ++k) kw[k] = stage[u ^ 1][set][64 * k + lane];
+                    if (work) {
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            const u32x4 v = vw[d / 2];
+                            const halfx8 vf = d % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
+#pragma unroll
+                            for (int n = 0; n < NR; ++n)
+                                tile[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[n], tile[n].o[d], 0, 0, 0);
+                        }
+                    }
+                }
+            }
+        }
+        int re = r, ge = g4;   // as in attention_rows_kernel
+        asm volatile("" : "+v"(re), "+v"(ge));
+        const bool whole = sp.splits <= 1;
+        const Partials ws = partials(a, plan);
+        floatx4 *pass = reinterpret_cast<floatx4 *>(&stage[0][0][0]) + wave * (DT * 64) + ge * 16 + re;
+        static_assert(sizeof(stage) >= kTileWaves * DT * 64 * sizeof(floatx4), "a tile of every wave passes through the stages");
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float sum = row_sum(tile[n].l);
+            __syncthreads();   // the stages, and the tile before, have been read
+            if (set == 1) {
+#pragma unroll
+                for (int d = 0; d < DT; ++d) pass[64 * d] = tile[n].o[d];
+                other[wave][lane] = (floatx2){tile[n].m, sum};
+            }
+            __syncthreads();
+            if (set == 1 || wr0 + 16 * n + re >= all_rows) continue;
+            const floatx2 ml = other[wave][lane];
+            const float top = fmaxf(tile[n].m, ml.x);
+            const float f0 = __builtin_amdgcn_exp2f(tile[n].m - top), f1 = __builtin_amdgcn_exp2f(ml.x - top);
+            const float total = f0 * sum + f1 * ml.y;
+            const float inv = inverse(a.kv, row[n].pos, total);
+            const int64_t at = (partial_row(a.kv, plan, b, head, group) + wave * (16 * NR) + 16 * n + re) * plan.splits + split;
+#pragma unroll
+            for (int i = 0; i < DT; ++i) {
+                const int d = 16 * i + 4 * ge;
+                const floatx4 acc = tile[n].o[i] * f0 + pass[64 * i] * f1;
+                if (!whole) *reinterpret_cast<floatx4 *>(ws.o + at * D + d) = acc;
+                else if (a.out_bf16)
+                    *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row[n].at + d) =
+                        __builtin_convertvector(acc * inv, bf16x4);
+                else *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + row[n].at + d) = acc * inv;
+            }
+            if (!whole && ge == 0) ws.ml[at] = (floatx2){top, total};
+        }
     }
-    const int t = static_cast<int>(rr / a.group), g = static_cast<int>(rr % a.group);
-    acc = acc * (past(a.kv, s.pos0 + t) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total);
-    const int64_t at = ((static_cast<int64_t>(s.row0 + t)) * a.q_heads + head * a.group + g) * D / 4 + x;
-    if (a.out_bf16)
-        reinterpret_cast<bf16x4 *>(a.out)[at] = __builtin_convertvector(acc, bf16x4);
-    else
-        reinterpret_cast<floatx4 *>(a.out)[at] = acc;
 }
 
-// The launch of the row kernel: 16-row tiles of a sequence, and how its
-// blocks are split.
-struct RowsPlan {
-    int tiles;          // tiles of the longest sequence
-    int chunk, splits;
+// Joins the splits of a row.  D / 4 threads have four dimensions each; PARTS
+// of them sum splits side by side, and a workgroup has 256 / (D / 4 * PARTS)
+// rows.
+template <int D, int PARTS>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Plan plan) {
+    constexpr int LANES = D / 4, ROWS = 256 / (LANES * PARTS);
+    constexpr int kRun = 256;   // splits whose factors are held at once
+    static_assert(ROWS == 1 || PARTS == 1, "");
+    __shared__ floatx4 part[PARTS][LANES];
+    __shared__ float factor[kRun];
+    __shared__ float wave_part[4];
+    const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads;
+    const KvSequence s = kv_sequence(a.kv, b);
+    const int all_rows = s.rows * a.group;
+    const int group = blockIdx.y / a.kv.kv_heads;
+    const int tid = threadIdx.x, x = tid % LANES, y = tid / LANES;
+    const int in_group = blockIdx.x * ROWS + (PARTS == 1 ? y : 0);
+    const int rr0 = group * plan.group_rows, rr = rr0 + in_group;
+    if (rr0 + static_cast<int>(blockIdx.x) * ROWS >= all_rows) return;
+    const int rr1 = rr0 + plan.group_rows < all_rows ? rr0 + plan.group_rows : all_rows;
+    const Span sp =
+        span_of(a.kv, s.pos0 + rr0 / a.group, s.pos0 + (rr1 - 1) / a.group, a.window, plan.chunk, plan.splits);
+    if (sp.splits <= 1) return;
+    const Partials ws = partials(a, plan);
+    const int64_t at0 = (partial_row(a.kv, plan, b, head, group) + in_group) * plan.splits;
+    floatx4 acc = {0, 0, 0, 0};
+    float top = kLowest, total = 0.0f;
+    if constexpr (PARTS == 1) {
+        if (rr >= rr1) return;
+        for (int i = 0; i < sp.splits; ++i) top = fmaxf(top, ws.ml[at0 + i].x);
+        const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + at0 * D) + x;
+        for (int i = 0; i < sp.splits; ++i) {
+            const floatx2 ml = ws.ml[at0 + i];
+            const float f = __builtin_amdgcn_exp2f(ml.x - top);
+            total += f * ml.y;
+            acc = acc + src[i * LANES] * f;
+        }
+    } else {
+        // every wave finds the largest m by itself
+        for (int i = tid & 63; i < sp.splits; i += 64) top = fmaxf(top, ws.ml[at0 + i].x);
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+        for (int i0 = 0; i0 < sp.splits; i0 += kRun) {
+            const int n = sp.splits - i0 < kRun ? sp.splits - i0 : kRun;
+            if (tid < n) {
+                const floatx2 ml = ws.ml[at0 + i0 + tid];
+                const float f = __builtin_amdgcn_exp2f(ml.x - top);
+                factor[tid] = f;
+                total += f * ml.y;
+            }
+            __syncthreads();
+            const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + (at0 + i0) * D) + x;
+#pragma unroll 4
+            for (int i = y; i < n; i += PARTS) acc = acc + src[i * LANES] * factor[i];
+            __syncthreads();
+        }
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) total += __shfl_xor(total, m);
+        if ((tid & 63) == 0) wave_part[tid >> 6] = total;
+        part[y][x] = acc;
+        __syncthreads();
+        if (y != 0) return;
+        total = wave_part[0] + wave_part[1] + wave_part[2] + wave_part[3];
+#pragma unroll
+        for (int i = 1; i < PARTS; ++i) acc = acc + part[i][x];
+    }
+    const LaneRow row = lane_row(a, s, head, rr, all_rows, D);
+    acc = acc * inverse(a.kv, row.pos, total);
+    if (a.out_bf16)
+        reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row.at)[x] = __builtin_convertvector(acc, bf16x4);
+    else
+        reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + row.at)[x] = acc;
+}
+
+// ------------------------------------------------------------------ launch
+template <int D>
+constexpr int tile_nr() { return 2; }
+
+struct Shape {
+    int group_rows, min_chunk;
+    int64_t groups, splits;   // splits: as many as fill the chip
 };
 
-RowsPlan rows_plan(const AttentionArgs &a) {
-    RowsPlan p;
-    p.tiles = static_cast<int>((static_cast<int64_t>(a.max_rows) * a.group + 15) / 16);
-    const int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
-    const int64_t work = static_cast<int64_t>(p.tiles) * a.kv.kv_heads * a.kv.batch;
-    // about four workgroups a compute unit, each with a block for every wave
-    int64_t splits = (1024 + work - 1) / work;
-    int64_t chunk = (blocks + splits - 1) / splits;
-    if (chunk < kWaves) chunk = kWaves;
+Shape shape_of(const AttentionArgs &a, int D) {
+    const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group;
+    const bool many = rows > 32;
+    Shape s;
+    s.group_rows = !many ? 16 : kTileWaves * 16 * (D == 128 ? tile_nr<128>() : tile_nr<64>());
+    s.min_chunk = many ? 32 : kWaves;
+    s.groups = (rows + s.group_rows - 1) / s.group_rows;
+    // about four workgroups a compute unit (one of the larger ones)
+    const int64_t work = s.groups * a.kv.kv_heads * a.kv.batch;
+    s.splits = ((many ? 128 : 1024) + work - 1) / work;
+    return s;
+}
+
+int64_t blocks_of(const AttentionArgs &a) { return (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock; }
+
+Plan plan_of(const AttentionArgs &a, int D) {
+    const Shape s = shape_of(a, D);
+    int64_t blocks = blocks_of(a);
+    if (a.window) {   // no group reads more than its rows and their window
+        const int64_t reach = (static_cast<int64_t>(a.window) + s.group_rows / a.group + kKvBlock) / kKvBlock + 1;
+        if (reach < blocks) blocks = reach;
+    }
+    int64_t chunk = (blocks + s.splits - 1) / s.splits;
+    if (chunk < s.min_chunk) chunk = s.min_chunk;
+    Plan p;
+    p.group_rows = s.group_rows;
+    p.groups = static_cast<int>(s.groups);
     p.chunk = static_cast<int>(chunk);
     p.splits = static_cast<int>((blocks + chunk - 1) / chunk);
     return p;
 }
 
 template <int D>
-hipError_t launch_rows(const AttentionArgs &a, hipStream_t s) {
-    const RowsPlan p = rows_plan(a);
-    int grid_tiles = p.tiles;
-    if (static_cast<int64_t>(grid_tiles) * a.kv.kv_heads > 65535) grid_tiles = 65535 / a.kv.kv_heads;
-    // the tiles of a launch with splits fit its workspace: such a launch has
-    // fewer than 1024 tiles
-    const dim3 grid(p.splits, grid_tiles * a.kv.kv_heads, a.kv.batch);
-    hipLaunchKernelGGL((attention_rows_kernel<D>), grid, dim3(64 * kWaves), 0, s, a, p.chunk, p.tiles);
-    hipError_t e = hipGetLastError();
+hipError_t launch(const AttentionArgs &a, hipStream_t s) {
+    const Plan p = plan_of(a, D);
+    int grid_groups = p.groups;   // the kernels loop where a launch cannot hold them all
+    if (static_cast<int64_t>(grid_groups) * a.kv.kv_heads > 65535) grid_groups = 65535 / a.kv.kv_heads;
+    const dim3 grid(p.splits, grid_groups * a.kv.kv_heads, a.kv.batch);
+    if (p.group_rows == 16)
+        hipLaunchKernelGGL((attention_rows_kernel<D>), grid, dim3(64 * kWaves), 0, s, a, p);
+    else
+        hipLaunchKernelGGL((attention_tiles_kernel<D, tile_nr<D>()>), grid, dim3(kTileThreads), 0, s, a, p);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    hipLaunchKernelGGL((attention_join_kernel<D>), dim3(16, p.tiles * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a,
-                       p.chunk, p.tiles, p.splits);
+    // launches that are split have fewer than 1024 groups
+    // a row to a workgroup where it has many splits or there are few rows
+    constexpr int kSide = 1024 / D;   // rows of a workgroup, or splits summed side by side
+    if (p.splits > 8 || p.group_rows == 16)
+        hipLaunchKernelGGL((attention_join_kernel<D, kSide>), dim3(p.group_rows, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);
+    else
+        hipLaunchKernelGGL((attention_join_kernel<D, 1>), dim3(p.group_rows / kSide, p.groups * a.kv.kv_heads, a.kv.batch),
+                           dim3(256), 0, s, a, p);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Enough for any window: a plan has no more splits than its shape's, and none
+// shorter than min_chunk.
 size_t attention_workspace(const AttentionArgs &a, int head_dim) {
-    const RowsPlan p = rows_plan(a);
-    if (p.splits == 1) return 0;
-    return static_cast<size_t>(p.tiles) * a.kv.kv_heads * a.kv.batch * p.splits * 16 * (head_dim + 2) * sizeof(float);
+    const Shape s = shape_of(a, head_dim);
+    const int64_t most = (blocks_of(a) + s.min_chunk - 1) / s.min_chunk;
+    const int64_t splits = s.splits < most ? s.splits : most;
+    if (splits == 1) return 0;
+    return static_cast<size_t>(s.groups) * s.group_rows * a.kv.kv_heads * a.kv.batch * splits * (head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s) {
-    return head_dim == 128 ? launch_rows<128>(a, s) : launch_rows<64>(a, s);
+    return head_dim == 128 ? launch<128>(a, s) : launch<64>(a, s);
 }
 
 }  // namespace q4

@@ -187,6 +187,16 @@ def test_blocks_outside_the_cache_are_nan():
 
     for rows in (1, 50):
         _check([64 + rows, 20 + rows], [rows, rows], seed=15, change=change)
+    # rows before the tokens of such a block are not touched by it
+    def far(c, table, q):
+        table = table.copy()
+        table[0, 1] = -3
+        return table, q
+
+    got = _check([70, 20], [70, 1], seed=15, change=far)
+    assert np.isfinite(got[:32]).all() and np.isnan(got[32:70]).all()
+    _check([70, 20], [70, 1], seed=15, change=far, window=12)
+    _check([40, 20], [12, 1], seed=15, change=far, group=1)
     # past the table's width
     for rows in (1, 50):
         c, table, q = _setup([100], [rows], 2, 2, 64, 15)
@@ -207,6 +217,7 @@ def test_small_hints_change_nothing_that_matters(rows):
     _check([700, 90], [rows, 3], seed=17, max_rows=1, max_length=1)
     _check([700, 90], [rows, 3], seed=17, max_rows=1, max_length=128)
     _check([700, 90], [rows, 3], seed=17, max_rows=rows, max_length=300)
+    _check([700, 90], [rows, 3], seed=17, max_rows=1, max_length=700)
     _check([700, 90], [rows, 3], seed=17, max_rows=4096, max_length=1 << 25)
 
 
