@@ -86,9 +86,8 @@ __device__ __forceinline__ uint32_t bytes_in(int first, int lo, int hi) {
     return m;
 }
 
-// 0x80 in each byte that is not a number, and the word with those bytes zero.
+// 0x80 in each byte that is not a number.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ uint32_t without(uint32_t w, uint32_t nan) { return w & ~((nan >> 7) * 0xFFu); }
 
 // Largest over the four lanes that hold one row (lane % 16).
 __device__ __forceinline__ float row_max(float v) {
@@ -145,11 +144,11 @@ struct Tile {
 
     // A value that is not a number reaches the rows that see its token and no
     // others (0 * NaN is NaN): such tokens are counted for each output, and
-    // the product gets 0 for them.  n0, n1: nan_bytes of operand d's words.
+    // the product gets 0 for them.  n0, n1: 1 in such bytes of operand d.
     __device__ __forceinline__ void mark_nans(int d, uint32_t n0, uint32_t n1, halfx8 seen) {
         floatx4 hits = {0, 0, 0, 0};
         // 0x38 is 1.0
-        hits = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16((n0 >> 7) * 0x38u, (n1 >> 7) * 0x38u), seen, hits, 0, 0, 0);
+        hits = __builtin_amdgcn_mfma_f32_16x16x32_f16(codes_f16(n0 * 0x38u, n1 * 0x38u), seen, hits, 0, 0, 0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             if (hits[j] > 0.0f) o[d][j] = __builtin_nanf("");
@@ -244,78 +243,107 @@ __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 
 // How a launch is shaped: groups of `group_rows` rows of a sequence and kv
 // head, and the split of their blocks.
 struct Plan {
-    int group_rows;      // 16, or kTileWaves * 16 * NR of the tile kernel
+    int group_rows;      // 16, or kTileWaves * 16 * NR of the kernel for many rows
     int groups;          // of the sequence with most rows
+    int rows_held;       // rows of a group that the workspace has room for
     int chunk, splits;
 };
 
+// Whether a group's blocks are split: groups and rows past those that the
+// launch was shaped for have no place in the workspace.
+__device__ __forceinline__ bool is_split(const Plan &p, int group, int rows) {
+    return p.splits > 1 && group < p.groups && rows <= p.rows_held;
+}
+
 // Where a split's partial results of a row are in the workspace: first
 // {m, l} [row][split], then O [row][split][D], rows counted over batch, kv
-// head, group and row of the group.
+// head, group and row of the group.  A split without blocks has {kLowest, 0}
+// and no O.
 struct Partials {
     floatx2 *ml;
     float *o;
 };
 
-__device__ __forceinline__ int64_t partial_row(const KvView &kv, const Plan &p, int b, int head, int64_t group) {
-    return ((static_cast<int64_t>(b) * kv.kv_heads + head) * p.groups + group) * p.group_rows;
+__device__ __forceinline__ int64_t partial_row(const KvView &kv, const Plan &p, int b, int head, int group) {
+    return ((static_cast<int64_t>(b) * kv.kv_heads + head) * p.groups + group) * p.rows_held;
 }
 
 __device__ __forceinline__ Partials partials(const AttentionArgs &a, const Plan &p) {
     Partials w;
     w.ml = reinterpret_cast<floatx2 *>(a.workspace);
-    const int64_t rows = static_cast<int64_t>(a.kv.batch) * a.kv.kv_heads * p.groups * p.group_rows;
+    const int64_t rows = static_cast<int64_t>(a.kv.batch) * a.kv.kv_heads * p.groups * p.rows_held;
     w.o = a.workspace + rows * p.splits * 2;
     return w;
+}
+
+// A split without blocks says so.
+__device__ __forceinline__ void write_empty(const AttentionArgs &a, const Plan &p, int b, int head, int group, int rows, int split) {
+    const Partials ws = partials(a, p);
+    const int64_t row = partial_row(a.kv, p, b, head, group);
+    for (int i = threadIdx.x; i < rows; i += blockDim.x) ws.ml[(row + i) * p.splits + split] = (floatx2){kLowest, 0.0f};
 }
 
 __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total) {
     return past(kv, pos) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
 }
 
-// ------------------------------------------------------- few rows: decode
-// A workgroup has 16 rows (of rows x heads of the group) of one sequence and
-// kv head, and one chunk of its blocks; its four waves take every fourth block.
-// Each lane's loads are its operand slices, so the cache goes from memory to
-// registers and nowhere else.
+// A workgroup has NR tiles of 16 rows (of rows x heads of the group) of one
+// sequence and kv head, and one chunk of its blocks; its four waves take every
+// fourth block with all the rows, so a block's codes go from memory to the
+// registers of one wave, as its operand slices, and nowhere else, a slice that
+// is converted feeds NR products, and no wave waits for another before the
+// end.  Groups with the most tokens start first.
 constexpr int kWaves = 4;
 
-template <int D>
-__global__ __launch_bounds__(64 * kWaves, 3) void attention_rows_kernel(AttentionArgs a, Plan plan) {
+template <int D, int NR>
+__global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs a, Plan plan) {
     constexpr int KQ = D / 32;   // k slices of the first product
     constexpr int DT = D / 16;   // 16-dimension tiles of the output
+    constexpr int kRows = 16 * NR;
     __shared__ float part_m[kWaves][16], part_l[kWaves][16];
     __shared__ float part_o[kWaves][D * 16];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g4 = lane >> 4;
     const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads;
+    // the ids of the blocks that the wave has where there is no window, read
+    // before the length is known
+    const int guessed = blockIdx.x * plan.chunk + wave;
+    const int guess = kv_block_id(a.kv, b, guessed + lane * kWaves);
     const KvSequence s = kv_sequence(a.kv, b);
     const int grid_groups = gridDim.y / a.kv.kv_heads;
     const int all_rows = s.rows * a.group;
-    for (int group = blockIdx.y / a.kv.kv_heads; group * 16 < all_rows; group += grid_groups) {
-        const LaneRow row = lane_row(a, s, head, group * 16 + r, all_rows, D);
-        const int r_last = group * 16 + 15 < all_rows ? group * 16 + 15 : all_rows - 1;
-        const int p_first = s.pos0 + group * 16 / a.group;
-        const int p_last = s.pos0 + r_last / a.group;
-        // groups past those that the launch was shaped for are not split: they
-        // have no place in the workspace
-        const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, group < plan.groups ? gridDim.x : 1);
+    const int groups = (all_rows + kRows - 1) / kRows;
+    for (int back = blockIdx.y / a.kv.kv_heads; back < groups; back += grid_groups) {
+        const int group = groups - 1 - back;
+        const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
+        const int p_first = s.pos0 + rr0 / a.group, p_last = s.pos0 + (rr1 - 1) / a.group;
         const int split = blockIdx.x;
-        if (split >= (sp.splits ? sp.splits : 1)) continue;   // uniform
+        const bool whole = !is_split(plan, group, rr1 - rr0);
+        const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, whole ? 1 : plan.splits);
+        if (whole ? split > 0 : split >= sp.splits) {   // uniform
+            if (!whole) write_empty(a, plan, b, head, group, rr1 - rr0, split);
+            continue;
+        }
         const int blk0 = sp.first + split * sp.chunk;
         const int blk1 = blk0 + sp.chunk < sp.last ? blk0 + sp.chunk : sp.last;
         // the first tokens that all rows and that any row of the group see
         const int all_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
 
-        bf16x8 q[KQ];
-        load_q<D>(a, row.at, g4, q);
-        Tile<D> tile;
-        tile.clear();
+        LaneRow row[NR];
+        bf16x8 q[NR][KQ];
+        Tile<D> tile[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            row[n] = lane_row(a, s, head, rr0 + 16 * n + r, all_rows, D);
+            load_q<D>(a, row[n].at, g4, q[n]);
+            tile[n].clear();
+        }
         // a block's ids and exponents are read 64 blocks at a time, one a lane,
         // its codes one block ahead
         for (int first = blk0 + wave; first < blk1; first += 64 * kWaves) {
             const int count = (blk1 - first + kWaves - 1) / kWaves, blocks = count < 64 ? count : 64;
-            const int my_id = lane < blocks ? kv_block_id(a.kv, b, first + lane * kWaves) : -1;
+            int my_id = guess;
+            if (first != guessed) my_id = kv_block_id(a.kv, b, first + lane * kWaves);
             const int my_exps =
                 reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(my_id < 0 ? 0 : my_id) * a.kv.kv_heads + head];
             u32x4 codes[2][2 * KQ];
@@ -323,17 +351,23 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attention_rows_kernel(Attentio
             auto fetch = [&](int i, u32x4(&to)[2 * KQ]) {
                 const int id = __builtin_amdgcn_readlane(my_id, i < blocks ? i : blocks - 1);
                 const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
-                const u32x4 *src = reinterpret_cast<const u32x4 *>(a.kv.data + plane * (kKvBlock * D)) + lane;
+                // a base that is the same for all lanes and a lane's offset,
+                // which is hidden so that the compiler keeps them apart: the
+                // loads then need no address registers of their own
+                const uint8_t *src = a.kv.data + plane * (kKvBlock * D);
+                uint32_t at = lane * 16;
+                asm volatile("" : "+v"(at));
 #pragma unroll
-                for (int j = 0; j < 2 * KQ; ++j) to[j] = src[64 * j];
+                for (int j = 0; j < 2 * KQ; ++j) to[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(src + 1024 * j + at));
             };
             fetch(0, codes[0]);
+            asm volatile("" ::"v"(my_exps));   // has arrived before the loop, whose waits are for codes alone
             for (int i0 = 0; i0 < blocks; i0 += 2) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int i = i0 + u;
+                    if (i >= blocks) break;
                     fetch(i + 1, codes[u ^ 1]);
-                    if (i >= blocks) continue;
                     u32x4(&kc)[2 * KQ] = codes[u];
                     const int e2 = __builtin_amdgcn_readlane(my_exps, i);
                     const float ek = static_cast<float>(static_cast<int8_t>(e2 & 0xFF));
@@ -341,98 +375,110 @@ __global__ __launch_bounds__(64 * kWaves, 3) void attention_rows_kernel(Attentio
                     const bool known = __builtin_amdgcn_readlane(my_id, i) >= 0;
                     const float c = fabsf(a.scale_log2) * __builtin_amdgcn_exp2f(ek);
                     const float inv_ev = __builtin_amdgcn_exp2f(-ev);
-                    floatx4 st[2];
+                    floatx4 st[NR][2];
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) {
-                        st[tt] = (floatx4){0, 0, 0, 0};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){0, 0, 0, 0};
 #pragma unroll
                         for (int k = 0; k < KQ; ++k) {
                             const u32x4 w = kc[tt * (KQ / 2) + k / 2];
                             const bf16x8 kf = k % 2 ? codes_bf16(w.z, w.w) : codes_bf16(w.x, w.y);
-                            st[tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[k], st[tt], 0, 0, 0);
+#pragma unroll
+                            for (int n = 0; n < NR; ++n)
+                                st[n][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][k], st[n][tt], 0, 0, 0);
                         }
-                        if (!known) st[tt] = (floatx4){kNan, kNan, kNan, kNan};
+                        if (!known)
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){kNan, kNan, kNan, kNan};
                     }
                     const int start = (first + i * kWaves) * kKvBlock;
                     if (start < all_lo || start + kKvBlock - 1 > p_first) {   // some row does not see some token
                         const int tok = start + 4 * g4;
-                        hide_unseen(st, tok, row.lo, row.pos);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) hide_unseen(st[n], tok, row[n].lo, row[n].pos);
                         // bytes that no row of the group sees may hold anything
                         const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
-                        uint32_t bad = 0;
+                        // and what is not a number must not meet a weight of 0:
+                        // such bytes are noted, a bit each, and cleared
+                        uint32_t bad[2] = {0, 0};
 #pragma unroll
-                        for (int j = KQ; j < 2 * KQ; ++j) {
-                            kc[j].x &= in0;
-                            kc[j].y &= in1;
-                            kc[j].z &= in0;
-                            kc[j].w &= in1;
-                            bad |= nan_bytes(kc[j].x) | nan_bytes(kc[j].y) | nan_bytes(kc[j].z) | nan_bytes(kc[j].w);
+                        for (int j = 0; j < 4 * KQ; ++j) {
+                            const uint32_t v = kc[KQ + j / 4][j % 4] & (j % 2 ? in1 : in0), n = nan_bytes(v) >> 7;
+                            bad[j / 8] |= n << (j % 8);
+                            kc[KQ + j / 4][j % 4] = v & ~(n * 0xFFu);
                         }
-                        if (__any(bad != 0)) {
-                            const halfx8 seen = seen_tokens(tok, row.lo, row.pos);
+                        if (__any((bad[0] | bad[1]) != 0)) {
 #pragma unroll
-                            for (int d = 0; d < DT; ++d) {
-                                const int at = d % 2 * 2;
-                                const uint32_t n0 = nan_bytes(kc[KQ + d / 2][at]), n1 = nan_bytes(kc[KQ + d / 2][at + 1]);
-                                tile.mark_nans(d, n0, n1, seen);
-                                kc[KQ + d / 2][at] = without(kc[KQ + d / 2][at], n0);
-                                kc[KQ + d / 2][at + 1] = without(kc[KQ + d / 2][at + 1], n1);
+                            for (int n = 0; n < NR; ++n) {
+                                const halfx8 seen = seen_tokens(tok, row[n].lo, row[n].pos);
+#pragma unroll
+                                for (int d = 0; d < DT; ++d) {
+                                    const uint32_t n0 = bad[d / 4] >> (d % 4 * 2), n1 = n0 >> 1;
+                                    tile[n].mark_nans(d, n0 & 0x01010101u, n1 & 0x01010101u, seen);
+                                }
                             }
                         }
                     }
-                    const halfx8 wf = tile.weights(st, c, ev, inv_ev);
+                    halfx8 wf[NR];
+#pragma unroll
+                    for (int n = 0; n < NR; ++n) wf[n] = tile[n].weights(st[n], c, ev, inv_ev);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
                         const u32x4 v = kc[KQ + d / 2];
                         const halfx8 vf = d % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
-                        tile.o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf, tile.o[d], 0, 0, 0);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            tile[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[n], tile[n].o[d], 0, 0, 0);
                     }
                 }
             }
         }
-        // hides the lane from the loop over the groups, out of which the
-        // compiler would take the addresses below and hold them all
+        // join the four waves, a tile at a time.  (The lane is hidden from the
+        // loop over the groups, out of which the compiler would take the
+        // addresses below and hold them all.)
         int re = r, ge = g4;
         asm volatile("" : "+v"(re), "+v"(ge));
-        tile.l = row_sum(tile.l);
-        // join the four waves
-        __syncthreads();   // the previous group's sums have been read
-        if (ge == 0) {
-            part_m[wave][re] = tile.m;
-            part_l[wave][re] = tile.l;
-        }
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part_o[wave][(16 * i + 4 * ge + j) * 16 + re] = tile.o[i][j];
-        __syncthreads();
-        float top = part_m[0][re];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
-        float f[kWaves], total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
-            total += f[w] * part_l[w][re];
-        }
-        if (!row.live) continue;
-        // thread: row r, dimensions tid / 16 + 16 i
-        const int d0 = 4 * wave + ge;
-        const bool whole = sp.splits <= 1;
         const Partials ws = partials(a, plan);
-        const int64_t at = (partial_row(a.kv, plan, b, head, group) + re) * plan.splits + split;
-        const float inv = inverse(a.kv, row.pos, total);
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
-            const int d = d0 + 16 * i;
-            float acc = 0.0f;
+        for (int n = 0; n < NR; ++n) {
+            const float sum = row_sum(tile[n].l);
+            __syncthreads();   // the tile before has been read
+            if (ge == 0) {
+                part_m[wave][re] = tile[n].m;
+                part_l[wave][re] = sum;
+            }
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) acc += f[w] * part_o[w][d * 16 + re];
-            if (!whole) ws.o[at * D + d] = acc;
-            else if (a.out_bf16) static_cast<__bf16 *>(a.out)[row.at + d] = static_cast<__bf16>(acc * inv);
-            else static_cast<float *>(a.out)[row.at + d] = acc * inv;
+            for (int i = 0; i < DT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part_o[wave][(16 * i + 4 * ge + j) * 16 + re] = tile[n].o[i][j];
+            __syncthreads();
+            float top = part_m[0][re];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
+            float f[kWaves], total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
+                total += f[w] * part_l[w][re];
+            }
+            if (!row[n].live) continue;
+            // thread: row re, dimensions 4 wave + ge + 16 i
+            const int d0 = 4 * wave + ge;
+            const int64_t at = (partial_row(a.kv, plan, b, head, group) + 16 * n + re) * plan.splits + split;
+            const float inv = inverse(a.kv, row[n].pos, total);
+#pragma unroll
+            for (int i = 0; i < DT; ++i) {
+                const int d = d0 + 16 * i;
+                float acc = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) acc += f[w] * part_o[w][d * 16 + re];
+                if (!whole) ws.o[at * D + d] = acc;
+                else if (a.out_bf16) static_cast<__bf16 *>(a.out)[row[n].at + d] = static_cast<__bf16>(acc * inv);
+                else static_cast<float *>(a.out)[row[n].at + d] = acc * inv;
+            }
+            if (!whole && d0 == 0) ws.ml[at] = (floatx2){top, total};
         }
-        if (!whole && d0 == 0) ws.ml[at] = (floatx2){top, total};
     }
 }
 
@@ -473,9 +519,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
         const int group = groups - 1 - back;
         const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
         const int p_first = s.pos0 + rr0 / a.group, p_last = s.pos0 + (rr1 - 1) / a.group;
-        const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, group < plan.groups ? gridDim.x : 1);
         const int split = blockIdx.x;
-        if (split >= (sp.splits ? sp.splits : 1)) continue;   // uniform
+        const bool whole = !is_split(plan, group, rr1 - rr0);
+        const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, whole ? 1 : plan.splits);
+        if (whole ? split > 0 : split >= sp.splits) {   // uniform
+            if (!whole) write_empty(a, plan, b, head, group, rr1 - rr0, split);
+            continue;
+        }
         const int blk0 = sp.first + split * sp.chunk;
         const int blk1 = blk0 + sp.chunk < sp.last ? blk0 + sp.chunk : sp.last;
         // the wave's own rows
@@ -508,16 +558,16 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
                 meta[threadIdx.x] = (u32x2){static_cast<uint32_t>(id), e2};
             }
             __syncthreads();
-            u32x4 ahead[2][kLoads];
+            u32x4 ahead[kLoads];
             auto meta_of = [&](int i) { return meta[i < kSegment ? i : kSegment - 1]; };
             // the thread's part of a pair is of its first or second block
             auto in_pair = [&](int j) { return (static_cast<int>(threadIdx.x) + kTileThreads * j) / kBlock16; };
-            auto fetch = [&](int pair, u32x4(&to)[kLoads]) {
+            auto fetch = [&](int pair) {
 #pragma unroll
                 for (int j = 0; j < kLoads; ++j) {
                     const int id = __builtin_amdgcn_readfirstlane(meta_of(2 * pair + in_pair(j)).x);
                     const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
-                    to[j] = reinterpret_cast<const u32x4 *>(a.kv.data + plane * (kKvBlock * D))[(threadIdx.x + kTileThreads * j) % kBlock16];
+                    ahead[j] = reinterpret_cast<const u32x4 *>(a.kv.data + plane * (kKvBlock * D))[(threadIdx.x + kTileThreads * j) % kBlock16];
                 }
             };
             // some row of the group does not see some token of the pair
@@ -525,8 +575,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
                 const int first = (seg + 2 * pair) * kKvBlock;
                 return first < group_lo || first + 2 * kKvBlock - 1 > p_first;
             };
-            // Puts a pair, which `from` holds, into its stage for all waves.
-            auto put = [&](int pair, int buf, u32x4(&from)[kLoads]) {
+            // Puts the pair that was fetched into its stage for all waves.
+            auto put = [&](int pair, int buf) {
                 if (partly_seen(pair)) {
                     // what no row sees may hold anything, and what is not a
                     // number must not meet a weight of 0
@@ -536,7 +586,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
                         if (at < 0) continue;
                         const int tok = (seg + 2 * pair + which) * kKvBlock + 4 * g4;
                         const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
-                        u32x4 v = from[j], n;
+                        u32x4 v = ahead[j], n;
                         v.x &= in0;
                         v.y &= in1;
                         v.z &= in0;
@@ -546,26 +596,24 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
                         for (int k = 0; k < 4; ++k) {
                             n[k] = nan_bytes(v[k]);
                             bad |= n[k];
-                            v[k] = without(v[k], n[k]);
+                            v[k] &= ~((n[k] >> 7) * 0xFFu);
                         }
                         nans[buf][which][at] = n;
                         if (bad) nan_block[buf][which] = pair;
-                        from[j] = v;
+                        ahead[j] = v;
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < kLoads; ++j) (&stage[buf][0][0])[threadIdx.x + kTileThreads * j] = from[j];
+                for (int j = 0; j < kLoads; ++j) (&stage[buf][0][0])[threadIdx.x + kTileThreads * j] = ahead[j];
             };
             // One barrier a pair, between the softmax and the second product:
             // before it the waves put the next pair into the other stage and
             // take the last of this one's codes, after it they take the next
             // one's first, which the product hides.
-            fetch(0, ahead[0]);
-            asm volatile("" ::: "memory");   // in this order, which the waits in the loop go by
-            fetch(1, ahead[1]);
             u32x4 kw[KQ], vw[KQ];
-            put(0, 0, ahead[0]);
-            fetch(2, ahead[0]);
+            fetch(0);
+            put(0, 0);
+            fetch(1);
             u32x2 here = meta_of(set);
             __syncthreads();
 #pragma unroll
@@ -575,8 +623,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     const int pair = p0 + u, i = 2 * pair + set;
-                    put(pair + 1, u ^ 1, ahead[u ^ 1]);
-                    fetch(pair + 3, ahead[u ^ 1]);
+                    put(pair + 1, u ^ 1);
+                    fetch(pair + 2);
                     const int id = __builtin_amdgcn_readfirstlane(here.x), e2 = __builtin_amdgcn_readfirstlane(here.y);
                     here = meta_of(i + 2);
                     const int start = (seg + i) * kKvBlock;
@@ -618,7 +666,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
 #pragma unroll
                                     for (int d = 0; d < DT; ++d) {
                                         const u32x4 x = nans[u][set][64 * (d / 2) + lane];
-                                        tile[n].mark_nans(d, d % 2 ? x.z : x.x, d % 2 ? x.w : x.y, seen);
+                                        tile[n].mark_nans(d, (d % 2 ? x.z : x.x) >> 7, (d % 2 ? x.w : x.y) >> 7, seen);
                                     }
                                 }
                             }
@@ -644,7 +692,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
         }
         int re = r, ge = g4;   // as in attention_rows_kernel
         asm volatile("" : "+v"(re), "+v"(ge));
-        const bool whole = sp.splits <= 1;
         const Partials ws = partials(a, plan);
         floatx4 *pass = reinterpret_cast<floatx4 *>(&stage[0][0][0]) + wave * (DT * 64) + ge * 16 + re;
         static_assert(sizeof(stage) >= kTileWaves * DT * 64 * sizeof(floatx4), "a tile of every wave passes through the stages");
@@ -691,49 +738,47 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
     __shared__ floatx4 part[PARTS][LANES];
     __shared__ float factor[kRun];
     __shared__ float wave_part[4];
-    const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads;
-    const KvSequence s = kv_sequence(a.kv, b);
-    const int all_rows = s.rows * a.group;
-    const int group = blockIdx.y / a.kv.kv_heads;
+    const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads, group = blockIdx.y / a.kv.kv_heads;
     const int tid = threadIdx.x, x = tid % LANES, y = tid / LANES;
     const int in_group = blockIdx.x * ROWS + (PARTS == 1 ? y : 0);
-    const int rr0 = group * plan.group_rows, rr = rr0 + in_group;
-    if (rr0 + static_cast<int>(blockIdx.x) * ROWS >= all_rows) return;
-    const int rr1 = rr0 + plan.group_rows < all_rows ? rr0 + plan.group_rows : all_rows;
-    const Span sp =
-        span_of(a.kv, s.pos0 + rr0 / a.group, s.pos0 + (rr1 - 1) / a.group, a.window, plan.chunk, plan.splits);
-    if (sp.splits <= 1) return;
     const Partials ws = partials(a, plan);
     const int64_t at0 = (partial_row(a.kv, plan, b, head, group) + in_group) * plan.splits;
+    const KvSequence s = kv_sequence(a.kv, b);
+    const int all_rows = s.rows * a.group, rr0 = group * plan.group_rows;
+    const int rows = rr0 + plan.group_rows < all_rows ? plan.group_rows : all_rows - rr0;
+    if (static_cast<int>(blockIdx.x) * ROWS >= rows || !is_split(plan, group, rows)) return;
     floatx4 acc = {0, 0, 0, 0};
     float top = kLowest, total = 0.0f;
+    // a split without blocks has no O to read
+    auto weight = [&](floatx2 ml) { return ml.x == kLowest && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top); };
     if constexpr (PARTS == 1) {
-        if (rr >= rr1) return;
-        for (int i = 0; i < sp.splits; ++i) top = fmaxf(top, ws.ml[at0 + i].x);
+        if (in_group >= rows) return;
+        for (int i = 0; i < plan.splits; ++i) top = fmaxf(top, ws.ml[at0 + i].x);
         const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + at0 * D) + x;
-        for (int i = 0; i < sp.splits; ++i) {
+        for (int i = 0; i < plan.splits; ++i) {
             const floatx2 ml = ws.ml[at0 + i];
-            const float f = __builtin_amdgcn_exp2f(ml.x - top);
+            const float f = weight(ml);
             total += f * ml.y;
-            acc = acc + src[i * LANES] * f;
+            if (f != 0.0f) acc = acc + src[i * LANES] * f;
         }
     } else {
         // every wave finds the largest m by itself
-        for (int i = tid & 63; i < sp.splits; i += 64) top = fmaxf(top, ws.ml[at0 + i].x);
+        for (int i = tid & 63; i < plan.splits; i += 64) top = fmaxf(top, ws.ml[at0 + i].x);
 #pragma unroll
         for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-        for (int i0 = 0; i0 < sp.splits; i0 += kRun) {
-            const int n = sp.splits - i0 < kRun ? sp.splits - i0 : kRun;
+        for (int i0 = 0; i0 < plan.splits; i0 += kRun) {
+            const int n = plan.splits - i0 < kRun ? plan.splits - i0 : kRun;
             if (tid < n) {
                 const floatx2 ml = ws.ml[at0 + i0 + tid];
-                const float f = __builtin_amdgcn_exp2f(ml.x - top);
+                const float f = weight(ml);
                 factor[tid] = f;
                 total += f * ml.y;
             }
             __syncthreads();
             const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + (at0 + i0) * D) + x;
 #pragma unroll 4
-            for (int i = y; i < n; i += PARTS) acc = acc + src[i * LANES] * factor[i];
+            for (int i = y; i < n; i += PARTS)
+                if (factor[i] != 0.0f) acc = acc + src[i * LANES] * factor[i];
             __syncthreads();
         }
 #pragma unroll
@@ -746,7 +791,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 #pragma unroll
         for (int i = 1; i < PARTS; ++i) acc = acc + part[i][x];
     }
-    const LaneRow row = lane_row(a, s, head, rr, all_rows, D);
+    const LaneRow row = lane_row(a, s, head, rr0 + in_group, all_rows, D);
     acc = acc * inverse(a.kv, row.pos, total);
     if (a.out_bf16)
         reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row.at)[x] = __builtin_convertvector(acc, bf16x4);
@@ -758,8 +803,12 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 template <int D>
 constexpr int tile_nr() { return 2; }
 
+constexpr int64_t kMaxChunk = 256;
+
+int64_t blocks_of(const AttentionArgs &a) { return (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock; }
+
 struct Shape {
-    int group_rows, min_chunk;
+    int group_rows, rows_held, min_chunk;
     int64_t groups, splits;   // splits: as many as fill the chip
 };
 
@@ -769,14 +818,16 @@ Shape shape_of(const AttentionArgs &a, int D) {
     Shape s;
     s.group_rows = !many ? 16 : kTileWaves * 16 * (D == 128 ? tile_nr<128>() : tile_nr<64>());
     s.min_chunk = many ? 32 : kWaves;
+    s.rows_held = rows < s.group_rows ? static_cast<int>(rows) : s.group_rows;
     s.groups = (rows + s.group_rows - 1) / s.group_rows;
-    // about four workgroups a compute unit (one of the larger ones)
+    // a workgroup for every compute unit, and none with more than kMaxChunk
+    // blocks of a sequence much longer than the others
     const int64_t work = s.groups * a.kv.kv_heads * a.kv.batch;
-    s.splits = ((many ? 128 : 1024) + work - 1) / work;
+    s.splits = ((many ? 128 : 256) + work - 1) / work;
+    const int64_t least = (blocks_of(a) + kMaxChunk - 1) / kMaxChunk;
+    if (!many && s.splits < least) s.splits = least;
     return s;
 }
-
-int64_t blocks_of(const AttentionArgs &a) { return (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock; }
 
 Plan plan_of(const AttentionArgs &a, int D) {
     const Shape s = shape_of(a, D);
@@ -789,6 +840,7 @@ Plan plan_of(const AttentionArgs &a, int D) {
     if (chunk < s.min_chunk) chunk = s.min_chunk;
     Plan p;
     p.group_rows = s.group_rows;
+    p.rows_held = s.rows_held;
     p.groups = static_cast<int>(s.groups);
     p.chunk = static_cast<int>(chunk);
     p.splits = static_cast<int>((blocks + chunk - 1) / chunk);
@@ -802,18 +854,17 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
     if (static_cast<int64_t>(grid_groups) * a.kv.kv_heads > 65535) grid_groups = 65535 / a.kv.kv_heads;
     const dim3 grid(p.splits, grid_groups * a.kv.kv_heads, a.kv.batch);
     if (p.group_rows == 16)
-        hipLaunchKernelGGL((attention_rows_kernel<D>), grid, dim3(64 * kWaves), 0, s, a, p);
+        hipLaunchKernelGGL((attention_kernel<D, 1>), grid, dim3(64 * kWaves), 0, s, a, p);
     else
         hipLaunchKernelGGL((attention_tiles_kernel<D, tile_nr<D>()>), grid, dim3(kTileThreads), 0, s, a, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    // launches that are split have fewer than 1024 groups
     // a row to a workgroup where it has many splits or there are few rows
     constexpr int kSide = 1024 / D;   // rows of a workgroup, or splits summed side by side
     if (p.splits > 8 || p.group_rows == 16)
-        hipLaunchKernelGGL((attention_join_kernel<D, kSide>), dim3(p.group_rows, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);
+        hipLaunchKernelGGL((attention_join_kernel<D, kSide>), dim3(p.rows_held, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);
     else
-        hipLaunchKernelGGL((attention_join_kernel<D, 1>), dim3(p.group_rows / kSide, p.groups * a.kv.kv_heads, a.kv.batch),
+        hipLaunchKernelGGL((attention_join_kernel<D, 1>), dim3((p.rows_held + kSide - 1) / kSide, p.groups * a.kv.kv_heads, a.kv.batch),
                            dim3(256), 0, s, a, p);
     return hipGetLastError();
 }
@@ -827,7 +878,7 @@ size_t attention_workspace(const AttentionArgs &a, int head_dim) {
     const int64_t most = (blocks_of(a) + s.min_chunk - 1) / s.min_chunk;
     const int64_t splits = s.splits < most ? s.splits : most;
     if (splits == 1) return 0;
-    return static_cast<size_t>(s.groups) * s.group_rows * a.kv.kv_heads * a.kv.batch * splits * (head_dim + 2) * sizeof(float);
+    return static_cast<size_t>(s.groups) * s.rows_held * a.kv.kv_heads * a.kv.batch * splits * (head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s) {
