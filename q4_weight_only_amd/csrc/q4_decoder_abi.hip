@@ -130,6 +130,7 @@ q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, co
     a.out = out;
     a.q_heads = static_cast<int32_t>(q_heads);
     a.group = static_cast<int32_t>(q_heads / cache->kv_heads);
+    a.group_inverse = a.group > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + a.group - 1) / a.group) : 0;
     a.scale_log2 = scale * 1.44269504088896340736f;
     // the kernels give a token that is not seen a score of -inf * |scale|
     if (fabsf(a.scale_log2) < 1e-20f) a.scale_log2 = 1e-20f;

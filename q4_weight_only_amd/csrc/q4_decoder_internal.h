@@ -78,6 +78,7 @@ struct AttentionArgs {
     const uint16_t *q;
     void *out;
     int32_t q_heads, group;
+    uint32_t group_inverse;  // 2^32 / group, rounded up: i / group = i * it >> 32 up to 2^26
     float scale_log2;        // softmax scale times log2(e)
     int32_t window;          // 0: none
     int32_t out_bf16;

@@ -99,6 +99,21 @@ __device__ __forceinline__ float row_sum(float v) {
     return v + __shfl_xor(v, 32);
 }
 
+// What a block's exponents (eK in bits 0-7, eV in 8-15, the same for all
+// lanes) make of the softmax scale, worked out on the bits of the powers of two.
+struct BlockScales {
+    float c, ev, inv_ev;   // |scale_log2| 2^eK, eV, 2^-eV
+};
+
+__device__ __forceinline__ BlockScales block_scales(const AttentionArgs &a, int e2) {
+    BlockScales s;
+    const int ek = static_cast<int8_t>(e2 & 0xFF), ev = static_cast<int8_t>(e2 >> 8);
+    s.c = fabsf(a.scale_log2) * __uint_as_float(static_cast<uint32_t>(ek + 127) << 23);
+    s.ev = static_cast<float>(ev);
+    s.inv_ev = __uint_as_float(static_cast<uint32_t>(127 - ev) << 23);
+    return s;
+}
+
 // One 16-row tile's running state in a wave: lane (r, g4) holds, for row r, the
 // reference m, its share of the sum l, and dimensions 16 i + 4 g4 + j of O.
 template <int D>
@@ -113,27 +128,27 @@ struct Tile {
         for (int i = 0; i < D / 16; ++i) o[i] = (floatx4){0, 0, 0, 0};
     }
 
-    // m is raised to the rows' largest score where some score passes it by
-    // kSlack, and the sums follow.  (A score that is not a number raises
-    // nothing; its weight is not a number either.)
-    __device__ __forceinline__ void raise(float top) {
-        if (__any(top > m + kSlack)) {
-            const float raised = fmaxf(m, row_max(top));
-            const float f = __builtin_amdgcn_exp2f(m - raised);
-            m = raised;
-            l *= f;
+    // The lane's largest score of a block.  st: q . k, -inf where the row does
+    // not see the token; c > 0.
+    __device__ __forceinline__ float top(const floatx4 (&st)[2], float c, float ev) const {
+        float x = st[0][0];
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) o[i] = o[i] * f;
-        }
+        for (int i = 1; i < 8; ++i) x = fmaxf(x, st[i / 4][i % 4]);
+        return fmaf(x, c, ev);
     }
 
-    // Weights of a block.  st: q . k, -inf where the row does not see the
-    // token; c > 0.
-    __device__ __forceinline__ halfx8 weights(const floatx4 (&st)[2], float c, float ev, float inv_ev) {
-        float top = st[0][0];
+    // m is raised to the rows' largest score, and the sums follow.  (A score
+    // that is not a number raises nothing; its weight is not a number either.)
+    __device__ __forceinline__ void raise(float top) {
+        const float raised = fmaxf(m, row_max(top));
+        const float f = __builtin_amdgcn_exp2f(m - raised);
+        m = raised;
+        l *= f;
 #pragma unroll
-        for (int i = 1; i < 8; ++i) top = fmaxf(top, st[i / 4][i % 4]);
-        raise(fmaf(top, c, ev));
+        for (int i = 0; i < D / 16; ++i) o[i] = o[i] * f;
+    }
+
+    __device__ __forceinline__ halfx8 weights(const floatx4 (&st)[2], float c, float ev, float inv_ev) {
         const float shift = ev - m;
         float w[8];
 #pragma unroll
@@ -175,6 +190,25 @@ __device__ __forceinline__ halfx8 seen_tokens(int first, int lo, int pos) {   //
     return weights_f16(one);
 }
 
+// A block's weights for all of a wave's tiles; m is raised where some score
+// passes it by kSlack.
+template <int D, int NR>
+__device__ __forceinline__ void block_weights(Tile<D> (&tile)[NR], const floatx4 (&st)[NR][2], const BlockScales &e,
+                                              halfx8 (&wf)[NR]) {
+    float top[NR];
+    bool over = false;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+        top[n] = tile[n].top(st[n], e.c, e.ev);
+        over |= top[n] > tile[n].m + kSlack;
+    }
+    if (__any(over))
+#pragma unroll
+        for (int n = 0; n < NR; ++n) tile[n].raise(top[n]);
+#pragma unroll
+    for (int n = 0; n < NR; ++n) wf[n] = tile[n].weights(st[n], e.c, e.ev, e.inv_ev);
+}
+
 // Which row of q a lane has, and what it sees.
 struct LaneRow {
     bool live;
@@ -183,29 +217,37 @@ struct LaneRow {
 };
 
 // Rows times heads of a group are at most 2^20 * 64: 32 bits hold them.
+__device__ __forceinline__ int row_of(const AttentionArgs &a, int i) {   // i / group
+    return a.group == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), a.group_inverse));
+}
+
 __device__ __forceinline__ LaneRow lane_row(const AttentionArgs &a, const KvSequence &s, int head, int rr, int all_rows, int D) {
     LaneRow x;
     x.live = rr < all_rows;
     const int last = x.live ? rr : all_rows - 1;
-    x.t = last / a.group;
+    x.t = row_of(a, last);
     x.pos = s.pos0 + x.t;
     x.lo = a.window ? x.pos - a.window + 1 : 0;
-    x.at = (static_cast<int64_t>(s.row0 + x.t) * a.q_heads + head * a.group + last % a.group) * D;
+    x.at = (static_cast<int64_t>(s.row0 + x.t) * a.q_heads + head * a.group + last - x.t * a.group) * D;
     return x;
 }
 
-// The lane's operand slices of its row of q, the sign of a negative scale taken in.
+// The lane's operand slices of its row of q.
 template <int D>
 __device__ __forceinline__ void load_q(const AttentionArgs &a, int64_t at, int g4, bf16x8 (&q)[D / 32]) {
-    const uint32_t flip = a.scale_log2 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        u32x4 w = reinterpret_cast<const u32x4 *>(a.q + at + 64 * (i / 2) + 16 * g4 + 8 * (i % 2))[0];
-        w.x ^= flip;
-        w.y ^= flip;
-        w.z ^= flip;
-        w.w ^= flip;
-        q[i] = __builtin_bit_cast(bf16x8, w);
+    for (int i = 0; i < D / 32; ++i)
+        q[i] = reinterpret_cast<const bf16x8 *>(a.q + at + 64 * (i / 2) + 16 * g4 + 8 * (i % 2))[0];
+    if (a.scale_log2 < 0.0f) {   // its sign is taken in here (and only then is q waited for)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            u32x4 w = __builtin_bit_cast(u32x4, q[i]);
+            w.x ^= 0x80008000u;
+            w.y ^= 0x80008000u;
+            w.z ^= 0x80008000u;
+            w.w ^= 0x80008000u;
+            q[i] = __builtin_bit_cast(bf16x8, w);
+        }
     }
 }
 
@@ -232,8 +274,13 @@ __device__ __forceinline__ Span span_of(const KvView &kv, int p_first, int p_las
         return s;
     }
     const int n = s.last - s.first;
+    if (grid_splits == 1) {
+        s.chunk = n;
+        s.splits = 1;
+        return s;
+    }
     s.chunk = chunk;
-    if (grid_splits == 1 || static_cast<int64_t>(chunk) * grid_splits < n) s.chunk = (n + grid_splits - 1) / grid_splits;
+    if (static_cast<int64_t>(chunk) * grid_splits < n) s.chunk = (n + grid_splits - 1) / grid_splits;
     s.splits = (n + s.chunk - 1) / s.chunk;
     return s;
 }
@@ -243,7 +290,7 @@ __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 
 // How a launch is shaped: groups of `group_rows` rows of a sequence and kv
 // head, and the split of their blocks.
 struct Plan {
-    int group_rows;      // 16, or kTileWaves * 16 * NR of the kernel for many rows
+    int group_rows;      // 16, or 64 or 128 in the kernel for many rows
     int groups;          // of the sequence with most rows
     int rows_held;       // rows of a group that the workspace has room for
     int chunk, splits;
@@ -304,20 +351,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
     __shared__ float part_o[kWaves][D * 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g4 = lane >> 4;
-    const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads;
+    const int b = blockIdx.z, head = blockIdx.x;
+    const int split = plan.splits == 1 ? 0 : blockIdx.y % plan.splits;
     // the ids of the blocks that the wave has where there is no window, read
     // before the length is known
-    const int guessed = blockIdx.x * plan.chunk + wave;
+    const int guessed = split * plan.chunk + wave;
     const int guess = kv_block_id(a.kv, b, guessed + lane * kWaves);
     const KvSequence s = kv_sequence(a.kv, b);
-    const int grid_groups = gridDim.y / a.kv.kv_heads;
+    const int grid_groups = plan.splits == 1 ? gridDim.y : gridDim.y / plan.splits;
     const int all_rows = s.rows * a.group;
     const int groups = (all_rows + kRows - 1) / kRows;
-    for (int back = blockIdx.y / a.kv.kv_heads; back < groups; back += grid_groups) {
+    for (int back = plan.splits == 1 ? blockIdx.y : blockIdx.y / plan.splits; back < groups; back += grid_groups) {
         const int group = groups - 1 - back;
         const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
-        const int p_first = s.pos0 + rr0 / a.group, p_last = s.pos0 + (rr1 - 1) / a.group;
-        const int split = blockIdx.x;
+        const int p_first = s.pos0 + row_of(a, rr0), p_last = s.pos0 + row_of(a, rr1 - 1);
         const bool whole = !is_split(plan, group, rr1 - rr0);
         const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, whole ? 1 : plan.splits);
         if (whole ? split > 0 : split >= sp.splits) {   // uniform
@@ -370,11 +417,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                     fetch(i + 1, codes[u ^ 1]);
                     u32x4(&kc)[2 * KQ] = codes[u];
                     const int e2 = __builtin_amdgcn_readlane(my_exps, i);
-                    const float ek = static_cast<float>(static_cast<int8_t>(e2 & 0xFF));
-                    const float ev = static_cast<float>(static_cast<int8_t>(e2 >> 8));
+                    const BlockScales scales = block_scales(a, e2);
                     const bool known = __builtin_amdgcn_readlane(my_id, i) >= 0;
-                    const float c = fabsf(a.scale_log2) * __builtin_amdgcn_exp2f(ek);
-                    const float inv_ev = __builtin_amdgcn_exp2f(-ev);
                     floatx4 st[NR][2];
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) {
@@ -421,8 +465,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                         }
                     }
                     halfx8 wf[NR];
-#pragma unroll
-                    for (int n = 0; n < NR; ++n) wf[n] = tile[n].weights(st[n], c, ev, inv_ev);
+                    block_weights<D, NR>(tile, st, scales, wf);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
                         const u32x4 v = kc[KQ + d / 2];
@@ -483,43 +526,48 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
 }
 
 // ------------------------------------------------- many rows: prompts
-// A workgroup has kTileWaves * NR tiles of 16 rows and two sets of kTileWaves
-// waves, which have the same rows, NR tiles to a wave, and take the blocks in
-// turn: a long row's blocks follow each other half as often, and each SIMD has
-// a wave of either set to run while the other waits.  All waves walk the
-// blocks together, two at a time: each loads its part of a pair two pairs early
-// into registers, and the pair passes to all waves through LDS in the cache's
-// own order (a lane's 16 bytes are its operand slices, so the reads have no
-// bank conflicts).  Every slice that a wave converts feeds NR products.
-// Groups with the most tokens start first.
-constexpr int kTileWaves = 4;
-constexpr int kTileThreads = 2 * 64 * kTileWaves;
-constexpr int kSegment = kTileThreads;   // blocks whose ids and exponents are held in LDS
+// A workgroup has W * NR tiles of 16 rows and two sets of W waves, which have
+// the same rows, NR tiles to a wave, and take the blocks in turn: a long row's
+// blocks follow each other half as often, and each SIMD has a wave of either
+// set to run while the other waits.  All waves walk the blocks together, two
+// at a time: each loads its part of a pair one pair early into registers, and
+// the pair passes to all waves through LDS in the cache's own order (a lane's
+// 16 bytes are its operand slices, so the reads have no bank conflicts).
+// Every slice that a wave converts feeds NR products.  Groups with the most
+// tokens start first.
+constexpr int kTileNr = 2;
 
-template <int D, int NR>
-__global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(AttentionArgs a, Plan plan) {
+template <int D, int NR, int W>
+__global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(AttentionArgs a, Plan plan) {
+    constexpr int kTileThreads = 2 * 64 * W;
+    constexpr int kSegment = kTileThreads;   // blocks whose ids and exponents are held in LDS
     constexpr int KQ = D / 32, DT = D / 16;
-    constexpr int kRows = kTileWaves * 16 * NR;
+    constexpr int kRows = W * 16 * NR;
     constexpr int kBlock16 = 2 * KQ * 64;                  // 16-byte pieces of a block
     constexpr int kLoads = 2 * kBlock16 / kTileThreads;    // a thread's of a pair
     __shared__ u32x4 stage[2][2][kBlock16];
     __shared__ u32x4 nans[2][2][kBlock16 / 2];   // nan_bytes of the V codes, where there are some (nan_block)
     __shared__ int32_t nan_block[2][2];
-    __shared__ u32x2 meta[kSegment];             // id and exponents
-    __shared__ floatx2 other[kTileWaves][64];    // the second set's m and l
+    __shared__ int32_t ids[kSegment];
+    __shared__ uint16_t exps[kSegment];
+    __shared__ floatx2 other[W][64];    // the second set's m and l
     const int lane = threadIdx.x & 63;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % kTileWaves, set = wave8 / kTileWaves;
+    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % W, set = wave8 / W;
     const int r = lane & 15, g4 = lane >> 4;
-    const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads;
+    const int b = blockIdx.z, head = blockIdx.x;
+    const int split = plan.splits == 1 ? 0 : blockIdx.y % plan.splits;
+    // the ids of the first segment where there is no window, read before the
+    // length is known
+    const int guessed = split * plan.chunk;
+    const int guess = kv_block_id(a.kv, b, guessed + threadIdx.x);
     const KvSequence s = kv_sequence(a.kv, b);
-    const int grid_groups = gridDim.y / a.kv.kv_heads;
+    const int grid_groups = plan.splits == 1 ? gridDim.y : gridDim.y / plan.splits;
     const int all_rows = s.rows * a.group;
     const int groups = (all_rows + kRows - 1) / kRows;
-    for (int back = blockIdx.y / a.kv.kv_heads; back < groups; back += grid_groups) {
+    for (int back = plan.splits == 1 ? blockIdx.y : blockIdx.y / plan.splits; back < groups; back += grid_groups) {
         const int group = groups - 1 - back;
         const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
-        const int p_first = s.pos0 + rr0 / a.group, p_last = s.pos0 + (rr1 - 1) / a.group;
-        const int split = blockIdx.x;
+        const int p_first = s.pos0 + row_of(a, rr0), p_last = s.pos0 + row_of(a, rr1 - 1);
         const bool whole = !is_split(plan, group, rr1 - rr0);
         const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, whole ? 1 : plan.splits);
         if (whole ? split > 0 : split >= sp.splits) {   // uniform
@@ -530,12 +578,13 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
         const int blk1 = blk0 + sp.chunk < sp.last ? blk0 + sp.chunk : sp.last;
         // the wave's own rows
         const int wr0 = rr0 + wave * (16 * NR), wr1 = wr0 + 16 * NR < rr1 ? wr0 + 16 * NR : rr1;
-        const int w_first = s.pos0 + wr0 / a.group;
-        const int w_last = wr0 < rr1 ? s.pos0 + (wr1 - 1) / a.group : -1;
+        const int w_first = s.pos0 + row_of(a, wr0);
+        const int w_last = wr0 < rr1 ? s.pos0 + row_of(a, wr1 - 1) : -1;
         const int wave_lo = a.window ? w_first - a.window + 1 : 0;
         // the first tokens that all rows and that any row of the group see
         const int group_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
 
+        const int first_id = blk0 == guessed ? guess : kv_block_id(a.kv, b, blk0 + threadIdx.x);
         LaneRow row[NR];
         bf16x8 q[NR][KQ];
         Tile<D> tile[NR];
@@ -549,26 +598,31 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
             const int blocks = blk1 - seg < kSegment ? blk1 - seg : kSegment;
             __syncthreads();   // the last segment's ids and stages have been read
             if (threadIdx.x < 4) (&nan_block[0][0])[threadIdx.x] = -1;
-            {
-                // (past the segment's end the last block stands in)
-                const int i = static_cast<int>(threadIdx.x) < blocks ? threadIdx.x : blocks - 1;
-                const int id = kv_block_id(a.kv, b, seg + i);
-                const uint32_t e2 =
-                    reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head];
-                meta[threadIdx.x] = (u32x2){static_cast<uint32_t>(id), e2};
-            }
+            // (past the segment's end the blocks of what follows, or none, are read)
+            const int id = seg == blk0 ? first_id : kv_block_id(a.kv, b, seg + threadIdx.x);
+            ids[threadIdx.x] = id;
             __syncthreads();
             u32x4 ahead[kLoads];
-            auto meta_of = [&](int i) { return meta[i < kSegment ? i : kSegment - 1]; };
+            auto held = [&](int i) { return i < kSegment ? i : kSegment - 1; };
             // the thread's part of a pair is of its first or second block
             auto in_pair = [&](int j) { return (static_cast<int>(threadIdx.x) + kTileThreads * j) / kBlock16; };
+            // a fetch uses ids that were taken from LDS one pair before
+            int next_id[kLoads];
+            auto take_ids = [&](int pair) {
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) next_id[j] = ids[held(2 * pair + in_pair(j))];
+            };
             auto fetch = [&](int pair) {
 #pragma unroll
                 for (int j = 0; j < kLoads; ++j) {
-                    const int id = __builtin_amdgcn_readfirstlane(meta_of(2 * pair + in_pair(j)).x);
+                    const int id = __builtin_amdgcn_readfirstlane(next_id[j]);
                     const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
-                    ahead[j] = reinterpret_cast<const u32x4 *>(a.kv.data + plane * (kKvBlock * D))[(threadIdx.x + kTileThreads * j) % kBlock16];
+                    const uint8_t *src = a.kv.data + plane * (kKvBlock * D);
+                    uint32_t at = (threadIdx.x + kTileThreads * j) % kBlock16 * 16;
+                    asm volatile("" : "+v"(at));   // as in attention_kernel
+                    ahead[j] = *reinterpret_cast<const u32x4 *>(src + at);
                 }
+                take_ids(pair + 1);
             };
             // some row of the group does not see some token of the pair
             auto partly_seen = [&](int pair) {
@@ -611,11 +665,14 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
             // take the last of this one's codes, after it they take the next
             // one's first, which the product hides.
             u32x4 kw[KQ], vw[KQ];
+            take_ids(0);
             fetch(0);
+            exps[threadIdx.x] =
+                reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head];
             put(0, 0);
             fetch(1);
-            u32x2 here = meta_of(set);
             __syncthreads();
+            int id_here = ids[set], e2_here = exps[set];
 #pragma unroll
             for (int k = 0; k < KQ; ++k) kw[k] = stage[0][set][64 * k + lane];
             const int pairs = (blocks + 1) / 2;
@@ -625,17 +682,15 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
                     const int pair = p0 + u, i = 2 * pair + set;
                     put(pair + 1, u ^ 1);
                     fetch(pair + 2);
-                    const int id = __builtin_amdgcn_readfirstlane(here.x), e2 = __builtin_amdgcn_readfirstlane(here.y);
-                    here = meta_of(i + 2);
+                    const int id = __builtin_amdgcn_readfirstlane(id_here), e2 = __builtin_amdgcn_readfirstlane(e2_here);
+                    id_here = ids[held(i + 2)];
+                    e2_here = exps[held(i + 2)];
                     const int start = (seg + i) * kKvBlock;
                     // not past the end, and something that the wave's rows see
                     const bool work = i < blocks && start <= w_last && start + kKvBlock > wave_lo;
                     halfx8 wf[NR];
                     if (work) {
-                        const float ek = static_cast<float>(static_cast<int8_t>(e2 & 0xFF));
-                        const float ev = static_cast<float>(static_cast<int8_t>(e2 >> 8));
-                        const float c = fabsf(a.scale_log2) * __builtin_amdgcn_exp2f(ek);
-                        const float inv_ev = __builtin_amdgcn_exp2f(-ev);
+                        const BlockScales scales = block_scales(a, e2);
 #pragma unroll
                         for (int k = 0; k < KQ; ++k) vw[k] = stage[u][set][64 * (KQ + k) + lane];
                         floatx4 st[NR][2];
@@ -671,8 +726,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
                                 }
                             }
                         }
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) wf[n] = tile[n].weights(st[n], c, ev, inv_ev);
+                        block_weights<D, NR>(tile, st, scales, wf);
                     }
                     __syncthreads();
 #pragma unroll
@@ -694,7 +748,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
         asm volatile("" : "+v"(re), "+v"(ge));
         const Partials ws = partials(a, plan);
         floatx4 *pass = reinterpret_cast<floatx4 *>(&stage[0][0][0]) + wave * (DT * 64) + ge * 16 + re;
-        static_assert(sizeof(stage) >= kTileWaves * DT * 64 * sizeof(floatx4), "a tile of every wave passes through the stages");
+        static_assert(sizeof(stage) >= W * DT * 64 * sizeof(floatx4), "a tile of every wave passes through the stages");
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const float sum = row_sum(tile[n].l);
@@ -710,19 +764,26 @@ __global__ __launch_bounds__(kTileThreads, 2) void attention_tiles_kernel(Attent
             const float top = fmaxf(tile[n].m, ml.x);
             const float f0 = __builtin_amdgcn_exp2f(tile[n].m - top), f1 = __builtin_amdgcn_exp2f(ml.x - top);
             const float total = f0 * sum + f1 * ml.y;
-            const float inv = inverse(a.kv, row[n].pos, total);
-            const int64_t at = (partial_row(a.kv, plan, b, head, group) + wave * (16 * NR) + 16 * n + re) * plan.splits + split;
+            const float inv = whole ? inverse(a.kv, row[n].pos, total) : 1.0f;
+            floatx4 acc[DT];
 #pragma unroll
-            for (int i = 0; i < DT; ++i) {
-                const int d = 16 * i + 4 * ge;
-                const floatx4 acc = tile[n].o[i] * f0 + pass[64 * i] * f1;
-                if (!whole) *reinterpret_cast<floatx4 *>(ws.o + at * D + d) = acc;
-                else if (a.out_bf16)
-                    *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row[n].at + d) =
-                        __builtin_convertvector(acc * inv, bf16x4);
-                else *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + row[n].at + d) = acc * inv;
+            for (int i = 0; i < DT; ++i) acc[i] = pass[64 * i];
+#pragma unroll
+            for (int i = 0; i < DT; ++i) acc[i] = (tile[n].o[i] * f0 + acc[i] * f1) * inv;
+            if (whole && a.out_bf16) {
+                bf16x4 *to = reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row[n].at + 4 * ge);
+#pragma unroll
+                for (int i = 0; i < DT; ++i) to[4 * i] = __builtin_convertvector(acc[i], bf16x4);
+                continue;
             }
-            if (!whole && ge == 0) ws.ml[at] = (floatx2){top, total};
+            float *to = static_cast<float *>(a.out) + row[n].at;
+            if (!whole) {
+                const int64_t at = (partial_row(a.kv, plan, b, head, group) + wave * (16 * NR) + 16 * n + re) * plan.splits + split;
+                if (ge == 0) ws.ml[at] = (floatx2){top, total};
+                to = ws.o + at * D;
+            }
+#pragma unroll
+            for (int i = 0; i < DT; ++i) *reinterpret_cast<floatx4 *>(to + 16 * i + 4 * ge) = acc[i];
         }
     }
 }
@@ -800,37 +861,46 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 }
 
 // ------------------------------------------------------------------ launch
-template <int D>
-constexpr int tile_nr() { return 2; }
-
-constexpr int64_t kMaxChunk = 256;
+constexpr int kRowsMany = 32;        // more rows than this go to the kernel for many rows
+constexpr int64_t kMaxChunk = 256;   // blocks
 
 int64_t blocks_of(const AttentionArgs &a) { return (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock; }
 
 struct Shape {
     int group_rows, rows_held, min_chunk;
-    int64_t groups, splits;   // splits: as many as fill the chip
+    int64_t groups, splits;   // splits: the most that a plan has
 };
 
-Shape shape_of(const AttentionArgs &a, int D) {
+Shape shape_of(const AttentionArgs &a) {
     const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group;
-    const bool many = rows > 32;
+    const bool many = rows > kRowsMany;
     Shape s;
-    s.group_rows = !many ? 16 : kTileWaves * 16 * (D == 128 ? tile_nr<128>() : tile_nr<64>());
-    s.min_chunk = many ? 32 : kWaves;
-    s.rows_held = rows < s.group_rows ? static_cast<int>(rows) : s.group_rows;
-    s.groups = (rows + s.group_rows - 1) / s.group_rows;
-    // a workgroup for every compute unit, and none with more than kMaxChunk
-    // blocks of a sequence much longer than the others
-    const int64_t work = s.groups * a.kv.kv_heads * a.kv.batch;
-    s.splits = ((many ? 128 : 256) + work - 1) / work;
-    const int64_t least = (blocks_of(a) + kMaxChunk - 1) / kMaxChunk;
-    if (!many && s.splits < least) s.splits = least;
+    auto grouped = [&](int group_rows) {
+        s.group_rows = group_rows;
+        s.rows_held = rows < group_rows ? static_cast<int>(rows) : group_rows;
+        s.groups = (rows + group_rows - 1) / group_rows;
+        return s.groups * a.kv.kv_heads * a.kv.batch;
+    };
+    if (!many) {
+        // a workgroup for every compute unit, and none with more than kMaxChunk
+        // blocks of a sequence much longer than the others
+        s.min_chunk = 4;
+        s.splits = (256 + grouped(16) - 1) / grouped(16);
+        const int64_t least = (blocks_of(a) + kMaxChunk - 1) / kMaxChunk;
+        if (s.splits < least) s.splits = least;
+    } else {
+        s.min_chunk = 32;
+        const int64_t work = grouped(128);
+        s.splits = (128 + work - 1) / work;
+        // where compute units would be left over, and the blocks are too few
+        // to be split, groups of half the rows
+        if (work <= 256 && (s.splits == 1 || blocks_of(a) <= s.min_chunk)) s.splits = 1, grouped(64);
+    }
     return s;
 }
 
-Plan plan_of(const AttentionArgs &a, int D) {
-    const Shape s = shape_of(a, D);
+Plan plan_of(const AttentionArgs &a) {
+    const Shape s = shape_of(a);
     int64_t blocks = blocks_of(a);
     if (a.window) {   // no group reads more than its rows and their window
         const int64_t reach = (static_cast<int64_t>(a.window) + s.group_rows / a.group + kKvBlock) / kKvBlock + 1;
@@ -849,14 +919,16 @@ Plan plan_of(const AttentionArgs &a, int D) {
 
 template <int D>
 hipError_t launch(const AttentionArgs &a, hipStream_t s) {
-    const Plan p = plan_of(a, D);
+    const Plan p = plan_of(a);
     int grid_groups = p.groups;   // the kernels loop where a launch cannot hold them all
-    if (static_cast<int64_t>(grid_groups) * a.kv.kv_heads > 65535) grid_groups = 65535 / a.kv.kv_heads;
-    const dim3 grid(p.splits, grid_groups * a.kv.kv_heads, a.kv.batch);
+    if (static_cast<int64_t>(grid_groups) * p.splits > 65535) grid_groups = 65535 / p.splits;
+    const dim3 grid(a.kv.kv_heads, grid_groups * p.splits, a.kv.batch);
     if (p.group_rows == 16)
         hipLaunchKernelGGL((attention_kernel<D, 1>), grid, dim3(64 * kWaves), 0, s, a, p);
+    else if (p.group_rows == 64)
+        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 2>), grid, dim3(256), 0, s, a, p);
     else
-        hipLaunchKernelGGL((attention_tiles_kernel<D, tile_nr<D>()>), grid, dim3(kTileThreads), 0, s, a, p);
+        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 4>), grid, dim3(512), 0, s, a, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     // a row to a workgroup where it has many splits or there are few rows
@@ -874,7 +946,7 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
 // Enough for any window: a plan has no more splits than its shape's, and none
 // shorter than min_chunk.
 size_t attention_workspace(const AttentionArgs &a, int head_dim) {
-    const Shape s = shape_of(a, head_dim);
+    const Shape s = shape_of(a);
     const int64_t most = (blocks_of(a) + s.min_chunk - 1) / s.min_chunk;
     const int64_t splits = s.splits < most ? s.splits : most;
     if (splits == 1) return 0;
