@@ -245,11 +245,13 @@ __global__ __launch_bounds__(2 * D) void kv_append_kernel(AppendArgs a, int bloc
 
 template <int D, typename T>
 hipError_t launch(const AppendArgs &a, hipStream_t s) {
-    // a sequence of n rows touches at most (n + 30) / 32 + 1 blocks
-    const int64_t blocks = (static_cast<int64_t>(a.max_rows) + kKvBlock - 2) / kKvBlock + 1;
+    // a sequence of n rows touches at most (n + 30) / 32 + 1 blocks; the kernel
+    // loops where a launch has fewer units than that
+    int64_t blocks = (static_cast<int64_t>(a.max_rows) + kKvBlock - 2) / kKvBlock + 1;
+    if (blocks > 4096) blocks = 4096;
     const int64_t block_units = blocks * a.kv.kv_heads * 2;
-    const int64_t q_units = (static_cast<int64_t>(a.max_rows) * a.q_heads * (D / 16) + 2 * D - 1) / (2 * D);
-    if (block_units + q_units > (int64_t(1) << 30)) return hipErrorInvalidValue;
+    int64_t q_units = (static_cast<int64_t>(a.max_rows) * a.q_heads * (D / 16) + 2 * D - 1) / (2 * D);
+    if (q_units > (1 << 20)) q_units = 1 << 20;
     hipLaunchKernelGGL((kv_append_kernel<D, T>),
                        dim3(static_cast<uint32_t>(block_units + q_units), static_cast<uint32_t>(a.kv.batch)),
                        dim3(2 * D), 0, s, a, static_cast<int>(block_units), static_cast<int>(q_units));

@@ -290,7 +290,7 @@ __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 
 // How a launch is shaped: groups of `group_rows` rows of a sequence and kv
 // head, and the split of their blocks.
 struct Plan {
-    int group_rows;      // 16, or 64 or 128 in the kernel for many rows
+    int group_rows;      // 16, or 64 or 128 in attention_tiles_kernel
     int groups;          // of the sequence with most rows
     int rows_held;       // rows of a group that the workspace has room for
     int chunk, splits;
@@ -334,19 +334,26 @@ __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total)
     return past(kv, pos) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
 }
 
-// A workgroup has NR tiles of 16 rows (of rows x heads of the group) of one
-// sequence and kv head, and one chunk of its blocks; its four waves take every
-// fourth block with all the rows, so a block's codes go from memory to the
-// registers of one wave, as its operand slices, and nowhere else, a slice that
-// is converted feeds NR products, and no wave waits for another before the
-// end.  Groups with the most tokens start first.
+// ------------------------------------------------------- few rows: decode
+// A workgroup has 16 rows (of rows x heads of the group) of one sequence and
+// kv head, and one chunk of its blocks; its four waves take every fourth block
+// with all the rows, so a block's codes go from memory to the registers of one
+// wave, as its operand slices, and nowhere else, and no wave waits for another
+// before the end.  Groups with the most tokens start first.
+//
+// What bounds it is reading the cache: two sequences of 131072 tokens of 8
+// heads of 128 (537 MB) take 86 us, 6.2 TB/s; 32 sequences of 2048 to 8191
+// (332 MB) 59 us, 5.6 TB/s.  The loads are nontemporal, as nothing is read
+// twice (99 -> 91 us for the former, 80 -> 74 for the latter when measured).
+// One token over 1505 takes 5.5 us, of which the loads that follow from each
+// other (length and block ids together, then codes) are the most, and the join
+// 3.5.
 constexpr int kWaves = 4;
 
-template <int D, int NR>
+template <int D>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs a, Plan plan) {
     constexpr int KQ = D / 32;   // k slices of the first product
     constexpr int DT = D / 16;   // 16-dimension tiles of the output
-    constexpr int kRows = 16 * NR;
     __shared__ float part_m[kWaves][16], part_l[kWaves][16];
     __shared__ float part_o[kWaves][D * 16];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -360,10 +367,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
     const KvSequence s = kv_sequence(a.kv, b);
     const int grid_groups = plan.splits == 1 ? gridDim.y : gridDim.y / plan.splits;
     const int all_rows = s.rows * a.group;
-    const int groups = (all_rows + kRows - 1) / kRows;
+    const int groups = (all_rows + 15) / 16;
     for (int back = plan.splits == 1 ? blockIdx.y : blockIdx.y / plan.splits; back < groups; back += grid_groups) {
         const int group = groups - 1 - back;
-        const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
+        const int rr0 = group * 16, rr1 = rr0 + 16 < all_rows ? rr0 + 16 : all_rows;
         const int p_first = s.pos0 + row_of(a, rr0), p_last = s.pos0 + row_of(a, rr1 - 1);
         const bool whole = !is_split(plan, group, rr1 - rr0);
         const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, whole ? 1 : plan.splits);
@@ -376,15 +383,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
         // the first tokens that all rows and that any row of the group see
         const int all_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
 
-        LaneRow row[NR];
-        bf16x8 q[NR][KQ];
-        Tile<D> tile[NR];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            row[n] = lane_row(a, s, head, rr0 + 16 * n + r, all_rows, D);
-            load_q<D>(a, row[n].at, g4, q[n]);
-            tile[n].clear();
-        }
+        const LaneRow row = lane_row(a, s, head, rr0 + r, all_rows, D);
+        bf16x8 q[KQ];
+        load_q<D>(a, row.at, g4, q);
+        Tile<D> tile[1];
+        tile[0].clear();
         // a block's ids and exponents are read 64 blocks at a time, one a lane,
         // its codes one block ahead
         for (int first = blk0 + wave; first < blk1; first += 64 * kWaves) {
@@ -405,7 +408,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                 uint32_t at = lane * 16;
                 asm volatile("" : "+v"(at));
 #pragma unroll
-                for (int j = 0; j < 2 * KQ; ++j) to[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(src + 1024 * j + at));
+                for (int j = 0; j < 2 * KQ; ++j)
+                    to[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(src + 1024 * j + at));
             };
             fetch(0, codes[0]);
             asm volatile("" ::"v"(my_exps));   // has arrived before the loop, whose waits are for codes alone
@@ -416,31 +420,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                     if (i >= blocks) break;
                     fetch(i + 1, codes[u ^ 1]);
                     u32x4(&kc)[2 * KQ] = codes[u];
-                    const int e2 = __builtin_amdgcn_readlane(my_exps, i);
-                    const BlockScales scales = block_scales(a, e2);
+                    const BlockScales scales = block_scales(a, __builtin_amdgcn_readlane(my_exps, i));
                     const bool known = __builtin_amdgcn_readlane(my_id, i) >= 0;
-                    floatx4 st[NR][2];
+                    floatx4 st[1][2];
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) {
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){0, 0, 0, 0};
+                        st[0][tt] = (floatx4){0, 0, 0, 0};
 #pragma unroll
                         for (int k = 0; k < KQ; ++k) {
                             const u32x4 w = kc[tt * (KQ / 2) + k / 2];
                             const bf16x8 kf = k % 2 ? codes_bf16(w.z, w.w) : codes_bf16(w.x, w.y);
-#pragma unroll
-                            for (int n = 0; n < NR; ++n)
-                                st[n][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][k], st[n][tt], 0, 0, 0);
+                            st[0][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[k], st[0][tt], 0, 0, 0);
                         }
-                        if (!known)
-#pragma unroll
-                            for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){kNan, kNan, kNan, kNan};
+                        if (!known) st[0][tt] = (floatx4){kNan, kNan, kNan, kNan};
                     }
                     const int start = (first + i * kWaves) * kKvBlock;
                     if (start < all_lo || start + kKvBlock - 1 > p_first) {   // some row does not see some token
                         const int tok = start + 4 * g4;
-#pragma unroll
-                        for (int n = 0; n < NR; ++n) hide_unseen(st[n], tok, row[n].lo, row[n].pos);
+                        hide_unseen(st[0], tok, row.lo, row.pos);
                         // bytes that no row of the group sees may hold anything
                         const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
                         // and what is not a number must not meet a weight of 0:
@@ -453,75 +450,67 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                             kc[KQ + j / 4][j % 4] = v & ~(n * 0xFFu);
                         }
                         if (__any((bad[0] | bad[1]) != 0)) {
+                            const halfx8 seen = seen_tokens(tok, row.lo, row.pos);
 #pragma unroll
-                            for (int n = 0; n < NR; ++n) {
-                                const halfx8 seen = seen_tokens(tok, row[n].lo, row[n].pos);
-#pragma unroll
-                                for (int d = 0; d < DT; ++d) {
-                                    const uint32_t n0 = bad[d / 4] >> (d % 4 * 2), n1 = n0 >> 1;
-                                    tile[n].mark_nans(d, n0 & 0x01010101u, n1 & 0x01010101u, seen);
-                                }
+                            for (int d = 0; d < DT; ++d) {
+                                const uint32_t n0 = bad[d / 4] >> (d % 4 * 2), n1 = n0 >> 1;
+                                tile[0].mark_nans(d, n0 & 0x01010101u, n1 & 0x01010101u, seen);
                             }
                         }
                     }
-                    halfx8 wf[NR];
-                    block_weights<D, NR>(tile, st, scales, wf);
+                    halfx8 wf[1];
+                    block_weights<D, 1>(tile, st, scales, wf);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
                         const u32x4 v = kc[KQ + d / 2];
                         const halfx8 vf = d % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
-#pragma unroll
-                        for (int n = 0; n < NR; ++n)
-                            tile[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[n], tile[n].o[d], 0, 0, 0);
+                        tile[0].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[0], tile[0].o[d], 0, 0, 0);
                     }
                 }
             }
         }
-        // join the four waves, a tile at a time.  (The lane is hidden from the
-        // loop over the groups, out of which the compiler would take the
-        // addresses below and hold them all.)
+        // join the four waves.  (The lane is hidden from the loop over the
+        // groups, out of which the compiler would take the addresses below and
+        // hold them all.)
         int re = r, ge = g4;
         asm volatile("" : "+v"(re), "+v"(ge));
-        const Partials ws = partials(a, plan);
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const float sum = row_sum(tile[n].l);
-            __syncthreads();   // the tile before has been read
-            if (ge == 0) {
-                part_m[wave][re] = tile[n].m;
-                part_l[wave][re] = sum;
-            }
-#pragma unroll
-            for (int i = 0; i < DT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) part_o[wave][(16 * i + 4 * ge + j) * 16 + re] = tile[n].o[i][j];
-            __syncthreads();
-            float top = part_m[0][re];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
-            float f[kWaves], total = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
-                total += f[w] * part_l[w][re];
-            }
-            if (!row[n].live) continue;
-            // thread: row re, dimensions 4 wave + ge + 16 i
-            const int d0 = 4 * wave + ge;
-            const int64_t at = (partial_row(a.kv, plan, b, head, group) + 16 * n + re) * plan.splits + split;
-            const float inv = inverse(a.kv, row[n].pos, total);
-#pragma unroll
-            for (int i = 0; i < DT; ++i) {
-                const int d = d0 + 16 * i;
-                float acc = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) acc += f[w] * part_o[w][d * 16 + re];
-                if (!whole) ws.o[at * D + d] = acc;
-                else if (a.out_bf16) static_cast<__bf16 *>(a.out)[row[n].at + d] = static_cast<__bf16>(acc * inv);
-                else static_cast<float *>(a.out)[row[n].at + d] = acc * inv;
-            }
-            if (!whole && d0 == 0) ws.ml[at] = (floatx2){top, total};
+        const float sum = row_sum(tile[0].l);
+        __syncthreads();   // the group before has been read
+        if (ge == 0) {
+            part_m[wave][re] = tile[0].m;
+            part_l[wave][re] = sum;
         }
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) part_o[wave][(16 * i + 4 * ge + j) * 16 + re] = tile[0].o[i][j];
+        __syncthreads();
+        float top = part_m[0][re];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
+        float f[kWaves], total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
+            total += f[w] * part_l[w][re];
+        }
+        if (!row.live) continue;
+        // thread: row re, dimensions 4 wave + ge + 16 i
+        const int d0 = 4 * wave + ge;
+        const Partials ws = partials(a, plan);
+        const int64_t at = (partial_row(a.kv, plan, b, head, group) + re) * plan.splits + split;
+        const float inv = inverse(a.kv, row.pos, total);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+            const int d = d0 + 16 * i;
+            float acc = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) acc += f[w] * part_o[w][d * 16 + re];
+            if (!whole) ws.o[at * D + d] = acc;
+            else if (a.out_bf16) static_cast<__bf16 *>(a.out)[row.at + d] = static_cast<__bf16>(acc * inv);
+            else static_cast<float *>(a.out)[row.at + d] = acc * inv;
+        }
+        if (!whole && d0 == 0) ws.ml[at] = (floatx2){top, total};
     }
 }
 
@@ -538,7 +527,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
 constexpr int kTileNr = 2;
 
 template <int D, int NR, int W>
-__global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(AttentionArgs a, Plan plan) {
+__global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(AttentionArgs a) {
     constexpr int kTileThreads = 2 * 64 * W;
     constexpr int kSegment = kTileThreads;   // blocks whose ids and exponents are held in LDS
     constexpr int KQ = D / 32, DT = D / 16;
@@ -555,27 +544,18 @@ __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(Attentio
     const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % W, set = wave8 / W;
     const int r = lane & 15, g4 = lane >> 4;
     const int b = blockIdx.z, head = blockIdx.x;
-    const int split = plan.splits == 1 ? 0 : blockIdx.y % plan.splits;
     // the ids of the first segment where there is no window, read before the
     // length is known
-    const int guessed = split * plan.chunk;
-    const int guess = kv_block_id(a.kv, b, guessed + threadIdx.x);
+    const int guess = kv_block_id(a.kv, b, threadIdx.x);
     const KvSequence s = kv_sequence(a.kv, b);
-    const int grid_groups = plan.splits == 1 ? gridDim.y : gridDim.y / plan.splits;
     const int all_rows = s.rows * a.group;
     const int groups = (all_rows + kRows - 1) / kRows;
-    for (int back = plan.splits == 1 ? blockIdx.y : blockIdx.y / plan.splits; back < groups; back += grid_groups) {
+    for (int back = blockIdx.y; back < groups; back += gridDim.y) {
         const int group = groups - 1 - back;
         const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
         const int p_first = s.pos0 + row_of(a, rr0), p_last = s.pos0 + row_of(a, rr1 - 1);
-        const bool whole = !is_split(plan, group, rr1 - rr0);
-        const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, whole ? 1 : plan.splits);
-        if (whole ? split > 0 : split >= sp.splits) {   // uniform
-            if (!whole) write_empty(a, plan, b, head, group, rr1 - rr0, split);
-            continue;
-        }
-        const int blk0 = sp.first + split * sp.chunk;
-        const int blk1 = blk0 + sp.chunk < sp.last ? blk0 + sp.chunk : sp.last;
+        const Span sp = span_of(a.kv, p_first, p_last, a.window, 0, 1);
+        const int blk0 = sp.first, blk1 = sp.last;
         // the wave's own rows
         const int wr0 = rr0 + wave * (16 * NR), wr1 = wr0 + 16 * NR < rr1 ? wr0 + 16 * NR : rr1;
         const int w_first = s.pos0 + row_of(a, wr0);
@@ -584,7 +564,7 @@ __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(Attentio
         // the first tokens that all rows and that any row of the group see
         const int group_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
 
-        const int first_id = blk0 == guessed ? guess : kv_block_id(a.kv, b, blk0 + threadIdx.x);
+        const int first_id = blk0 == 0 ? guess : kv_block_id(a.kv, b, blk0 + threadIdx.x);
         LaneRow row[NR];
         bf16x8 q[NR][KQ];
         Tile<D> tile[NR];
@@ -746,7 +726,6 @@ __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(Attentio
         }
         int re = r, ge = g4;   // as in attention_rows_kernel
         asm volatile("" : "+v"(re), "+v"(ge));
-        const Partials ws = partials(a, plan);
         floatx4 *pass = reinterpret_cast<floatx4 *>(&stage[0][0][0]) + wave * (DT * 64) + ge * 16 + re;
         static_assert(sizeof(stage) >= W * DT * 64 * sizeof(floatx4), "a tile of every wave passes through the stages");
 #pragma unroll
@@ -764,94 +743,74 @@ __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(Attentio
             const float top = fmaxf(tile[n].m, ml.x);
             const float f0 = __builtin_amdgcn_exp2f(tile[n].m - top), f1 = __builtin_amdgcn_exp2f(ml.x - top);
             const float total = f0 * sum + f1 * ml.y;
-            const float inv = whole ? inverse(a.kv, row[n].pos, total) : 1.0f;
+            const float inv = inverse(a.kv, row[n].pos, total);
             floatx4 acc[DT];
 #pragma unroll
             for (int i = 0; i < DT; ++i) acc[i] = pass[64 * i];
 #pragma unroll
             for (int i = 0; i < DT; ++i) acc[i] = (tile[n].o[i] * f0 + acc[i] * f1) * inv;
-            if (whole && a.out_bf16) {
+            if (a.out_bf16) {
                 bf16x4 *to = reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row[n].at + 4 * ge);
 #pragma unroll
                 for (int i = 0; i < DT; ++i) to[4 * i] = __builtin_convertvector(acc[i], bf16x4);
                 continue;
             }
             float *to = static_cast<float *>(a.out) + row[n].at;
-            if (!whole) {
-                const int64_t at = (partial_row(a.kv, plan, b, head, group) + wave * (16 * NR) + 16 * n + re) * plan.splits + split;
-                if (ge == 0) ws.ml[at] = (floatx2){top, total};
-                to = ws.o + at * D;
-            }
 #pragma unroll
             for (int i = 0; i < DT; ++i) *reinterpret_cast<floatx4 *>(to + 16 * i + 4 * ge) = acc[i];
         }
     }
 }
 
-// Joins the splits of a row.  D / 4 threads have four dimensions each; PARTS
-// of them sum splits side by side, and a workgroup has 256 / (D / 4 * PARTS)
-// rows.
-template <int D, int PARTS>
+// Joins the splits of a row, a workgroup a row: D / 4 threads have four
+// dimensions each, and 1024 / D of such sets sum splits side by side.
+template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Plan plan) {
-    constexpr int LANES = D / 4, ROWS = 256 / (LANES * PARTS);
+    constexpr int LANES = D / 4, PARTS = 256 / LANES;
     constexpr int kRun = 256;   // splits whose factors are held at once
-    static_assert(ROWS == 1 || PARTS == 1, "");
     __shared__ floatx4 part[PARTS][LANES];
     __shared__ float factor[kRun];
     __shared__ float wave_part[4];
     const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads, group = blockIdx.y / a.kv.kv_heads;
     const int tid = threadIdx.x, x = tid % LANES, y = tid / LANES;
-    const int in_group = blockIdx.x * ROWS + (PARTS == 1 ? y : 0);
+    const int in_group = blockIdx.x;
     const Partials ws = partials(a, plan);
     const int64_t at0 = (partial_row(a.kv, plan, b, head, group) + in_group) * plan.splits;
     const KvSequence s = kv_sequence(a.kv, b);
-    const int all_rows = s.rows * a.group, rr0 = group * plan.group_rows;
-    const int rows = rr0 + plan.group_rows < all_rows ? plan.group_rows : all_rows - rr0;
-    if (static_cast<int>(blockIdx.x) * ROWS >= rows || !is_split(plan, group, rows)) return;
+    const int all_rows = s.rows * a.group, rr0 = group * 16;
+    const int rows = rr0 + 16 < all_rows ? 16 : all_rows - rr0;
+    if (in_group >= rows || !is_split(plan, group, rows)) return;
     floatx4 acc = {0, 0, 0, 0};
     float top = kLowest, total = 0.0f;
-    // a split without blocks has no O to read
-    auto weight = [&](floatx2 ml) { return ml.x == kLowest && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top); };
-    if constexpr (PARTS == 1) {
-        if (in_group >= rows) return;
-        for (int i = 0; i < plan.splits; ++i) top = fmaxf(top, ws.ml[at0 + i].x);
-        const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + at0 * D) + x;
-        for (int i = 0; i < plan.splits; ++i) {
-            const floatx2 ml = ws.ml[at0 + i];
-            const float f = weight(ml);
+    // every wave finds the largest m by itself
+    for (int i = tid & 63; i < plan.splits; i += 64) top = fmaxf(top, ws.ml[at0 + i].x);
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
+    for (int i0 = 0; i0 < plan.splits; i0 += kRun) {
+        const int n = plan.splits - i0 < kRun ? plan.splits - i0 : kRun;
+        if (tid < n) {
+            const floatx2 ml = ws.ml[at0 + i0 + tid];
+            // (a split without blocks has no O to read)
+            const float f = ml.x == kLowest && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+            factor[tid] = f;
             total += f * ml.y;
-            if (f != 0.0f) acc = acc + src[i * LANES] * f;
         }
-    } else {
-        // every wave finds the largest m by itself
-        for (int i = tid & 63; i < plan.splits; i += 64) top = fmaxf(top, ws.ml[at0 + i].x);
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-        for (int i0 = 0; i0 < plan.splits; i0 += kRun) {
-            const int n = plan.splits - i0 < kRun ? plan.splits - i0 : kRun;
-            if (tid < n) {
-                const floatx2 ml = ws.ml[at0 + i0 + tid];
-                const float f = weight(ml);
-                factor[tid] = f;
-                total += f * ml.y;
-            }
-            __syncthreads();
-            const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + (at0 + i0) * D) + x;
-#pragma unroll 4
-            for (int i = y; i < n; i += PARTS)
-                if (factor[i] != 0.0f) acc = acc + src[i * LANES] * factor[i];
-            __syncthreads();
-        }
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) total += __shfl_xor(total, m);
-        if ((tid & 63) == 0) wave_part[tid >> 6] = total;
-        part[y][x] = acc;
         __syncthreads();
-        if (y != 0) return;
-        total = wave_part[0] + wave_part[1] + wave_part[2] + wave_part[3];
-#pragma unroll
-        for (int i = 1; i < PARTS; ++i) acc = acc + part[i][x];
+        const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + (at0 + i0) * D) + x;
+#pragma unroll 4
+        for (int i = y; i < n; i += PARTS)
+            if (factor[i] != 0.0f) acc = acc + src[i * LANES] * factor[i];
+        __syncthreads();
     }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) total += __shfl_xor(total, m);
+    if ((tid & 63) == 0) wave_part[tid >> 6] = total;
+    part[y][x] = acc;
+    __syncthreads();
+    if (y != 0) return;
+    total = wave_part[0] + wave_part[1] + wave_part[2] + wave_part[3];
+#pragma unroll
+    for (int i = 1; i < PARTS; ++i) acc = acc + part[i][x];
     const LaneRow row = lane_row(a, s, head, rr0 + in_group, all_rows, D);
     acc = acc * inverse(a.kv, row.pos, total);
     if (a.out_bf16)
@@ -861,57 +820,51 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 }
 
 // ------------------------------------------------------------------ launch
-constexpr int kRowsMany = 32;        // more rows than this go to the kernel for many rows
-constexpr int64_t kMaxChunk = 256;   // blocks
+// attention_tiles_kernel needs enough groups of rows to fill the chip, as it
+// does not split their blocks: from 1.5 groups of 64 rows a compute unit on it
+// takes less time (at 400: 800 rows of 800 tokens 23.0 against 26.0 us; 8 times
+// 100 rows 12.8 against 20.4; the prompt of 2048 62 against 86), below that
+// attention_kernel does, which splits (at 256: 512 rows over 8192 tokens 113
+// against 141 us; 400 rows of 20 heads over 3000 17.9 against 34.2).
+constexpr int64_t kManyWork = 384;
+// Blocks of a workgroup of attention_kernel at most, for a sequence much longer
+// than the others of its batch: 8192 tokens, at which a workgroup takes about
+// 50 us and the join of two splits another 5.
+constexpr int64_t kMaxChunk = 256;
 
-int64_t blocks_of(const AttentionArgs &a) { return (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock; }
-
-struct Shape {
-    int group_rows, rows_held, min_chunk;
-    int64_t groups, splits;   // splits: the most that a plan has
-};
-
-Shape shape_of(const AttentionArgs &a) {
-    const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group;
-    const bool many = rows > kRowsMany;
-    Shape s;
-    auto grouped = [&](int group_rows) {
-        s.group_rows = group_rows;
-        s.rows_held = rows < group_rows ? static_cast<int>(rows) : group_rows;
-        s.groups = (rows + group_rows - 1) / group_rows;
-        return s.groups * a.kv.kv_heads * a.kv.batch;
-    };
-    if (!many) {
-        // a workgroup for every compute unit, and none with more than kMaxChunk
-        // blocks of a sequence much longer than the others
-        s.min_chunk = 4;
-        s.splits = (256 + grouped(16) - 1) / grouped(16);
-        const int64_t least = (blocks_of(a) + kMaxChunk - 1) / kMaxChunk;
-        if (s.splits < least) s.splits = least;
-    } else {
-        s.min_chunk = 32;
-        const int64_t work = grouped(128);
-        s.splits = (128 + work - 1) / work;
-        // where compute units would be left over, and the blocks are too few
-        // to be split, groups of half the rows
-        if (work <= 256 && (s.splits == 1 || blocks_of(a) <= s.min_chunk)) s.splits = 1, grouped(64);
-    }
-    return s;
+// Into how many parts attention_kernel's `work` groups have their blocks split:
+// a workgroup for every compute unit (more of them take longer to join: 32
+// sequences up to 8191 tokens 60.6 us in 256, 68.7 in 512), and no chunk over
+// kMaxChunk until sixteen groups a compute unit even out their lengths (and
+// would need much workspace).
+int64_t splits_wanted(int64_t work, int64_t blocks) {
+    const int64_t fill = (256 + work - 1) / work, least = (blocks + kMaxChunk - 1) / kMaxChunk;
+    return work >= 4096 || least < fill ? fill : least;
 }
 
 Plan plan_of(const AttentionArgs &a) {
-    const Shape s = shape_of(a);
-    int64_t blocks = blocks_of(a);
+    const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group, sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
+    Plan p;
+    p.chunk = p.splits = 1;
+    if (rows > 32 && (rows + 63) / 64 * sets >= kManyWork) {
+        // half the rows where no more than one workgroup a compute unit would
+        // be there (1024 tokens: 25.8 against 31.0 us)
+        p.group_rows = (rows + 127) / 128 * sets <= 256 ? 64 : 128;
+        p.rows_held = 0;
+        p.groups = static_cast<int>((rows + p.group_rows - 1) / p.group_rows);
+        return p;
+    }
+    p.group_rows = 16;
+    p.rows_held = rows < 16 ? static_cast<int>(rows) : 16;
+    p.groups = static_cast<int>((rows + 15) / 16);
+    int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
     if (a.window) {   // no group reads more than its rows and their window
-        const int64_t reach = (static_cast<int64_t>(a.window) + s.group_rows / a.group + kKvBlock) / kKvBlock + 1;
+        const int64_t reach = (static_cast<int64_t>(a.window) + 16 / a.group + kKvBlock) / kKvBlock + 1;
         if (reach < blocks) blocks = reach;
     }
-    int64_t chunk = (blocks + s.splits - 1) / s.splits;
-    if (chunk < s.min_chunk) chunk = s.min_chunk;
-    Plan p;
-    p.group_rows = s.group_rows;
-    p.rows_held = s.rows_held;
-    p.groups = static_cast<int>(s.groups);
+    const int64_t splits = splits_wanted(p.groups * sets, blocks);
+    int64_t chunk = (blocks + splits - 1) / splits;
+    if (chunk < kWaves) chunk = kWaves;   // a block for every wave
     p.chunk = static_cast<int>(chunk);
     p.splits = static_cast<int>((blocks + chunk - 1) / chunk);
     return p;
@@ -924,33 +877,31 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
     if (static_cast<int64_t>(grid_groups) * p.splits > 65535) grid_groups = 65535 / p.splits;
     const dim3 grid(a.kv.kv_heads, grid_groups * p.splits, a.kv.batch);
     if (p.group_rows == 16)
-        hipLaunchKernelGGL((attention_kernel<D, 1>), grid, dim3(64 * kWaves), 0, s, a, p);
+        hipLaunchKernelGGL((attention_kernel<D>), grid, dim3(64 * kWaves), 0, s, a, p);
     else if (p.group_rows == 64)
-        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 2>), grid, dim3(256), 0, s, a, p);
+        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 2>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 4>), grid, dim3(512), 0, s, a, p);
+        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 4>), grid, dim3(512), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
-    // a row to a workgroup where it has many splits or there are few rows
-    constexpr int kSide = 1024 / D;   // rows of a workgroup, or splits summed side by side
-    if (p.splits > 8 || p.group_rows == 16)
-        hipLaunchKernelGGL((attention_join_kernel<D, kSide>), dim3(p.rows_held, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);
-    else
-        hipLaunchKernelGGL((attention_join_kernel<D, 1>), dim3((p.rows_held + kSide - 1) / kSide, p.groups * a.kv.kv_heads, a.kv.batch),
-                           dim3(256), 0, s, a, p);
+    hipLaunchKernelGGL((attention_join_kernel<D>), dim3(p.rows_held, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Enough for any window: a plan has no more splits than its shape's, and none
-// shorter than min_chunk.
+// Enough for any window: fewer blocks may be split into more parts, but never
+// into more than there are for all of them with the smallest chunk, nor than
+// fill the chip or keep the chunks at kMaxChunk.
 size_t attention_workspace(const AttentionArgs &a, int head_dim) {
-    const Shape s = shape_of(a);
-    const int64_t most = (blocks_of(a) + s.min_chunk - 1) / s.min_chunk;
-    const int64_t splits = s.splits < most ? s.splits : most;
+    const Plan p = plan_of(a);
+    if (p.group_rows != 16) return 0;
+    const int64_t sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
+    const int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
+    int64_t splits = splits_wanted(p.groups * sets, blocks);
+    if (splits > (blocks + kWaves - 1) / kWaves) splits = (blocks + kWaves - 1) / kWaves;
     if (splits == 1) return 0;
-    return static_cast<size_t>(s.groups) * s.rows_held * a.kv.kv_heads * a.kv.batch * splits * (head_dim + 2) * sizeof(float);
+    return static_cast<size_t>(p.groups) * p.rows_held * sets * splits * (head_dim + 2) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s) {

@@ -2,6 +2,8 @@
 oracle derives for the kernels' arithmetic plus the output's rounding (fp32
 results: 4 roundings; bf16: 2^-8 of the value at the bound's edge)."""
 
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -13,6 +15,26 @@ from decoder_helpers import DEV, assert_close, bf16, dev, device_cache, random_t
 from gpu_helpers import say
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, params=["chosen", "groups of 64", "groups of 128"])
+def kernel(request, monkeypatch):
+    """Every test runs with the kernel that its sizes choose, and with those for
+    many rows: max_rows, which shapes a launch, changes no result."""
+    monkeypatch.setattr(sys.modules[__name__], "KERNEL", request.param)
+
+
+KERNEL = "chosen"
+
+
+def _hint(sets, group):
+    """max_rows that brings a launch of `sets` sequences x kv heads to the kernel."""
+    if KERNEL == "groups of 128":
+        return 1 << 19
+    if KERNEL == "groups of 64":      # at least 384 groups of 64 rows, at most 256 of 128
+        k = max(1, 256 // sets)
+        return max(1, 64 * (2 * k - 1) // group)
+    return None
 
 
 def _setup(lengths, rows, heads, group, D, seed, garbage=True, blocks=None):
@@ -36,6 +58,8 @@ def _setup(lengths, rows, heads, group, D, seed, garbage=True, blocks=None):
 
 def _call(c, table, q, lengths, rows, *, cu=True, dtype=torch.float32, **kw):
     bounds = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32) if cu is True else cu
+    if "max_rows" not in kw and KERNEL != "chosen":
+        kw["max_rows"] = _hint(c.heads * len(lengths), q.shape[1] // c.heads)
     out = q4.kv_attention(dev(q.reshape(q.shape[0], -1), torch.bfloat16), device_cache(c), dev(table),
                           dev(np.array(lengths, dtype=np.int32)), dev(bounds), dtype=dtype, **kw)
     return out.double().cpu().numpy().reshape(q.shape)
@@ -89,6 +113,12 @@ def test_windows(window, rows):
 def test_windows_of_a_prompt_with_many_heads():
     _check([300], [300], window=70, heads=3, group=1, D=64, seed=6)
     _check([300], [200], window=70, heads=1, group=5, D=128, seed=6)
+
+
+def test_sizes_that_choose_the_kernels_for_many_rows():
+    """384 and 400 groups of 64 rows, by their own number."""
+    _check([65] * 8, [65] * 8, heads=24, group=1, seed=21)
+    _check([40, 33], [33, 33], heads=8, group=48, seed=21)
 
 
 def test_scale():
