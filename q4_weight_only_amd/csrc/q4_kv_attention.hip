@@ -832,12 +832,19 @@ constexpr int64_t kManyWork = 384;
 // 50 us and the join of two splits another 5.
 constexpr int64_t kMaxChunk = 256;
 
+// Up to so many blocks one workgroup takes no longer than a split and its join
+// (1024 tokens 8.8 against 11.6 us, 1505 11.4 each), and where blocks are split,
+// a wave has four of them at least (512 tokens 8.8 us, 11.5 with one).
+constexpr int64_t kUnsplit = 40;
+constexpr int64_t kMinChunk = 4 * kWaves;
+
 // Into how many parts attention_kernel's `work` groups have their blocks split:
 // a workgroup for every compute unit (more of them take longer to join: 32
 // sequences up to 8191 tokens 60.6 us in 256, 68.7 in 512), and no chunk over
 // kMaxChunk until sixteen groups a compute unit even out their lengths (and
 // would need much workspace).
 int64_t splits_wanted(int64_t work, int64_t blocks) {
+    if (blocks <= kUnsplit) return 1;
     const int64_t fill = (256 + work - 1) / work, least = (blocks + kMaxChunk - 1) / kMaxChunk;
     return work >= 4096 || least < fill ? fill : least;
 }
@@ -864,7 +871,7 @@ Plan plan_of(const AttentionArgs &a) {
     }
     const int64_t splits = splits_wanted(p.groups * sets, blocks);
     int64_t chunk = (blocks + splits - 1) / splits;
-    if (chunk < kWaves) chunk = kWaves;   // a block for every wave
+    if (chunk < kMinChunk) chunk = kMinChunk;
     p.chunk = static_cast<int>(chunk);
     p.splits = static_cast<int>((blocks + chunk - 1) / chunk);
     return p;
@@ -899,7 +906,7 @@ size_t attention_workspace(const AttentionArgs &a, int head_dim) {
     const int64_t sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
     const int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
     int64_t splits = splits_wanted(p.groups * sets, blocks);
-    if (splits > (blocks + kWaves - 1) / kWaves) splits = (blocks + kWaves - 1) / kWaves;
+    if (splits > (blocks + kMinChunk - 1) / kMinChunk) splits = (blocks + kMinChunk - 1) / kMinChunk;
     if (splits == 1) return 0;
     return static_cast<size_t>(p.groups) * p.rows_held * sets * splits * (head_dim + 2) * sizeof(float);
 }

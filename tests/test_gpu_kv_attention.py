@@ -256,6 +256,36 @@ def test_long_cache():
     _check([20001], [3], heads=1, group=4, D=128, window=5000, seed=18)
 
 
+@pytest.mark.parametrize("rows", [1, 6, 40])
+def test_split_caches_with_small_hints(rows):
+    """Caches that are split, with more rows, tokens or both than the launch was
+    shaped for, and a sequence that fewer splits have blocks of."""
+    _check([3000, 90], [rows, 3], seed=22, max_rows=1, max_length=2000)
+    _check([3000, 90], [rows, 3], seed=22, max_rows=rows, max_length=2000)
+    _check([3000, 90, 0], [rows, 3, 1], seed=22, max_rows=rows, max_length=4096)
+    _check([3000, 90], [rows, 3], seed=22, max_rows=1, max_length=3000, window=1700)
+
+
+def test_split_caches_with_nans_and_missing_blocks():
+    def nan_value(c, table, q):
+        for t, which in ((100, 1), (2998, 1), (1500, 0)):
+            i = table[0, t // 32]
+            codes = c.block_codes(i, 1, which).copy()
+            codes[t % 32, 7] = 0x7F
+            c.put(i, 1, which, codes, c.exps[i, 1, which])
+
+    got = _check([3000], [5], seed=23, change=nan_value)
+    assert np.isfinite(got[:, :2]).all() and np.isnan(got[:, 2:]).all()
+
+    def missing(c, table, q):
+        table = table.copy()
+        table[0, 93] = -1
+        return table, q
+
+    got = _check([3000], [40], seed=23, change=missing)
+    assert np.isfinite(got[:16]).all() and np.isnan(got[16:]).all()
+
+
 def test_offsets_past_32_bits():
     """Blocks whose bytes lie past 2^32 in the cache."""
     heads, D = 8, 128
