@@ -2,10 +2,16 @@
 // block's output, gate, residual scale, residual add, norm for the next block
 // and its modulation, in one pass over the rows.
 //
-// A workgroup of 256 threads has one row; a thread holds NV groups of four
-// consecutive elements of it in registers from the first sum to the last
-// store, so that y and the residual are read once.  Rows longer than
-// 256 * 4 * kMaxGroups are read again for each sum instead.
+// T threads have one row, and a thread holds NV groups of four consecutive
+// elements of it in registers from the first sum to the last store, so that y
+// and the residual are read once.  Rows longer than 16384 are read again for
+// each sum instead.
+//
+// What bounds it is memory: 2048 rows of 3072 (fp32 in, bf16 x out) take
+// 15.6 us, 5.6 TB/s, with post norm, gate and modulation 17; 6020 rows of 1280
+// 17.7, 6.1 TB/s.  The stores carry the nontemporal hint, without which the
+// same take 17.7, 18.2 and 22.6.  Two rows of 3072 take 2.5 us: a launch, a
+// load and a sum.
 
 #include "q4_decoder_internal.h"
 
@@ -14,8 +20,6 @@ namespace {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kThreads = 256;
 
 template <int BF16>
 __device__ __forceinline__ floatx4 load4(const void *p, int64_t i) {   // i: group of four elements
@@ -28,19 +32,24 @@ __device__ __forceinline__ floatx4 load4(const void *p, int64_t i) {   // i: gro
 template <int BF16>
 __device__ __forceinline__ void store4(void *p, int64_t i, floatx4 v) {
     if constexpr (BF16)
-        reinterpret_cast<bf16x4 *>(p)[i] = __builtin_convertvector(v, bf16x4);
+        __builtin_nontemporal_store(__builtin_convertvector(v, bf16x4), reinterpret_cast<bf16x4 *>(p) + i);
     else
-        reinterpret_cast<floatx4 *>(p)[i] = v;
+        __builtin_nontemporal_store(v, reinterpret_cast<floatx4 *>(p) + i);
 }
 
 __device__ __forceinline__ float sum_sq(floatx4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
 
-__device__ __forceinline__ float block_sum(float v, float *part) {
+template <int T>
+__device__ __forceinline__ float row_sum(float v, float *part) {
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+    if constexpr (T == 64) return v;
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
     __syncthreads();
-    return part[0] + part[1] + part[2] + part[3];
+    float sum = part[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) sum += part[i];
+    return sum;
 }
 
 // y's group i, normed (where post_weight is given) and gated
@@ -51,10 +60,16 @@ __device__ __forceinline__ floatx4 update(const NormArgs &a, floatx4 y, float in
     return y * a.scale;
 }
 
-template <int RB, int YB, int XB, int NV>
-__global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
-    __shared__ float part[2][4];
-    const int64_t m = blockIdx.x;
+template <int T>
+constexpr int kBlock = T < 256 ? 256 : T;   // threads of a workgroup
+
+template <int RB, int YB, int XB, int T, int NV>
+__global__ __launch_bounds__(kBlock<T>) void add_rmsnorm_kernel(NormArgs a) {
+    __shared__ float part[2][kBlock<T> / 64];
+    constexpr int kRows = kBlock<T> / T;
+    const int64_t m = kRows == 1 ? blockIdx.x : static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
+    if (m >= a.M) return;   // rows that share a workgroup have a wave each, and no barrier
+    const int tid = threadIdx.x % T;
     const int groups = a.C / 4;
     const int64_t base = m * groups;
     const float *gate = a.gate ? a.gate + m / a.gate_run * a.C : nullptr;
@@ -64,7 +79,7 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
         floatx4 r[NV], y[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int i = threadIdx.x + kThreads * v;
+            const int i = tid + T * v;
             r[v] = y[v] = (floatx4){0, 0, 0, 0};
             if (i < groups) {
                 r[v] = load4<RB>(a.residual, base + i);
@@ -76,22 +91,22 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
             float ss = 0.0f;
 #pragma unroll
             for (int v = 0; v < NV; ++v) ss += sum_sq(y[v]);
-            inv = 1.0f / sqrtf(block_sum(ss, part[0]) * inv_c + a.eps);
+            inv = 1.0f / sqrtf(row_sum<T>(ss, part[0]) * inv_c + a.eps);
         }
         float ss = 0.0f;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int i = threadIdx.x + kThreads * v;
+            const int i = tid + T * v;
             if (a.y && i < groups) {
                 r[v] = r[v] + update<YB>(a, y[v], inv, gate, i);
                 store4<RB>(a.residual_out, base + i, r[v]);
             }
             ss += sum_sq(r[v]);
         }
-        inv = 1.0f / sqrtf(block_sum(ss, part[1]) * inv_c + a.eps);
+        inv = 1.0f / sqrtf(row_sum<T>(ss, part[1]) * inv_c + a.eps);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            const int i = threadIdx.x + kThreads * v;
+            const int i = tid + T * v;
             if (i < groups) {
                 floatx4 x = r[v] * inv * load4<0>(a.weight, i);
                 if (mod) x = x * (1.0f + load4<0>(mod, i));
@@ -101,8 +116,8 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
     } else {
         float inv = 1.0f, ss = 0.0f;
         if (a.post_weight) {
-            for (int i = threadIdx.x; i < groups; i += kThreads) ss += sum_sq(load4<YB>(a.y, base + i));
-            inv = 1.0f / sqrtf(block_sum(ss, part[0]) * inv_c + a.eps);
+            for (int i = tid; i < groups; i += T) ss += sum_sq(load4<YB>(a.y, base + i));
+            inv = 1.0f / sqrtf(row_sum<T>(ss, part[0]) * inv_c + a.eps);
         }
         auto value = [&](int i) {
             floatx4 r = load4<RB>(a.residual, base + i);
@@ -110,9 +125,9 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
             return r;
         };
         ss = 0.0f;
-        for (int i = threadIdx.x; i < groups; i += kThreads) ss += sum_sq(value(i));
-        const float inv_r = 1.0f / sqrtf(block_sum(ss, part[1]) * inv_c + a.eps);
-        for (int i = threadIdx.x; i < groups; i += kThreads) {
+        for (int i = tid; i < groups; i += T) ss += sum_sq(value(i));
+        const float inv_r = 1.0f / sqrtf(row_sum<T>(ss, part[1]) * inv_c + a.eps);
+        for (int i = tid; i < groups; i += T) {
             const floatx4 r = value(i);   // before residual_out, which may be the residual itself, gets it
             if (a.y) store4<RB>(a.residual_out, base + i, r);
             floatx4 x = r * inv_r * load4<0>(a.weight, i);
@@ -124,15 +139,29 @@ __global__ __launch_bounds__(kThreads) void add_rmsnorm_kernel(NormArgs a) {
 
 template <int RB, int YB, int XB>
 hipError_t launch(const NormArgs &a, hipStream_t s) {
-    const dim3 grid(static_cast<uint32_t>(a.M));
-    const int nv = (a.C / 4 + kThreads - 1) / kThreads;
-#define Q4_NORM(NV) hipLaunchKernelGGL((add_rmsnorm_kernel<RB, YB, XB, NV>), grid, dim3(kThreads), 0, s, a)
-    if (nv <= 1) Q4_NORM(1);
-    else if (nv <= 2) Q4_NORM(2);
-    else if (nv <= 3) Q4_NORM(3);
-    else if (nv <= 4) Q4_NORM(4);
-    else if (nv <= 8) Q4_NORM(8);
-    else Q4_NORM(0);
+#define Q4_NORM(T, NV)                                                                                       \
+    hipLaunchKernelGGL((add_rmsnorm_kernel<RB, YB, XB, T, NV>),                                              \
+                       dim3(static_cast<uint32_t>((a.M * T + kBlock<T> - 1) / kBlock<T>)), dim3(kBlock<T>), 0, s, a)
+    // While all rows can be on the chip together (2048 threads a compute unit),
+    // as many threads a row as have four elements each: two rows of 3072 take
+    // 2.5 against 3.6 us with 256 threads, 512 rows 5.1 against 5.6, but 1024
+    // rows 9.1 against 7.9; 2048 rows of 512 3.4 against 3.8 with a wave.
+    // Past that, a wave a row as long as that holds it in few registers (6020
+    // rows of 256 5.7 against 7.1, of 512 9.1 against 10.0, but of 1024 17.8
+    // against 16.1), then 256 threads, and above 4096 elements 1024 of them
+    // (2048 rows of 5120 32 us, 75 with 256 threads).
+    auto fit = [&](int64_t threads) { return a.M * threads <= 2048 * 256; };
+    if (a.C <= 256) Q4_NORM(64, 1);
+    else if (a.C <= 512 && !fit(256)) Q4_NORM(64, 2);
+    else if (a.C <= 1024) Q4_NORM(256, 1);
+    else if (a.C <= 4096 && fit(1024)) Q4_NORM(1024, 1);
+    else if (a.C <= 2048) Q4_NORM(256, 2);
+    else if (a.C <= 3072) Q4_NORM(256, 3);
+    else if (a.C <= 4096) Q4_NORM(256, 4);
+    else if (a.C <= 8192) Q4_NORM(1024, 2);
+    else if (a.C <= 12288) Q4_NORM(1024, 3);
+    else if (a.C <= 16384) Q4_NORM(1024, 4);
+    else Q4_NORM(1024, 0);
 #undef Q4_NORM
     return hipGetLastError();
 }

@@ -69,6 +69,13 @@ def test_many_rows(M, C):
     _check(M, C, rd=torch.bfloat16, xd=torch.bfloat16)
 
 
+@pytest.mark.parametrize("M,C", [(4, 256), (4, 288), (2047, 512), (2050, 288), (2051, 512), (4097, 32), (511, 3072), (513, 3104),
+                                 (3, 8224), (3, 12320), (3, 16384), (3, 16416)])
+def test_sizes_at_which_the_launch_changes(M, C):
+    _check(M, C, post=True, gate=1, mod=M, scale=0.5)
+    _check(M, C, rd=torch.bfloat16, xd=torch.bfloat16, inplace=True)
+
+
 @pytest.mark.parametrize("rd", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("yd", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("xd", [torch.float32, torch.bfloat16])
