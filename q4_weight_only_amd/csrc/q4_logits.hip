@@ -2,12 +2,19 @@
 // (include/q4_decoder.h).
 //
 // A workgroup has CH consecutive tokens of one row, eight to a thread, and
-// loads them, the row's bounds and the first ids of its lists together.  It
-// counts in LDS how often each of its tokens occurs in the history, applies
-// the penalties in registers, adds up the biases in the same LDS and writes
-// its tokens: one pass over the logits, no counts in memory.  The counts are
-// whole numbers, so the order of the LDS atomics does not matter; biases of
-// one token are added one by one in the order of the list.
+// loads them, the row's bounds and the first entries of its lists together.
+// It counts in LDS how often each of its tokens occurs in the history, notes
+// there the token's bias, and applies both in registers, where some lane's
+// four tokens have any: one pass over the logits, no counts in memory.  The
+// counts are whole numbers, so the order of the LDS atomics does not matter;
+// biases of one token are added one by one in the order of the list.
+//
+// 32 rows of 131072 tokens with the mask alone take 6.6 us (34 MB: 5.1 TB/s),
+// with 4099 ids and 300 biases each 8.9, of which the chain from the bounds to
+// the ids to the counts is the most; one row with 200 ids 3.6.  What cost time
+// here: instructions for every token (a second array of counts took 0.9 us),
+// the length of the code, which short calls fetch as they go (0.5 us for ids
+// read one by one), stores without the nontemporal hint (1.6 us).
 
 #include "q4_decoder_internal.h"
 
@@ -15,22 +22,23 @@ namespace q4 {
 namespace {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
+// rows start on 4 bytes only, which such loads and stores allow
+typedef float floatx4_row __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kAtOnce = 16;  // ids of a thread in flight
+constexpr int kQuads = 4;     // of ids of a thread in flight
+constexpr int kBiases = 4;    // entries of the bias list that a thread has at first
 
 struct RowParams {
     float rho, inv_rho, frequency, presence;
 };
 
-// Without branches: among 64 tokens some are nearly always seen.  z / rho is
-// z * (1 / rho), within 2 roundings of it, as a division of every token takes
-// longer than the rest of the kernel.
-__device__ __forceinline__ float penalized(float z, uint32_t in_prompt, uint32_t n, const RowParams &p) {
+// Without branches; z / rho is z * (1 / rho), within 2 roundings of it.  n: how
+// often the token is in the answer.
+__device__ __forceinline__ float penalized(float z, bool seen, uint32_t n, const RowParams &p) {
     const float scale = z > 0.0f ? p.inv_rho : p.rho;
-    z *= in_prompt | n ? scale : 1.0f;
-    z -= n ? p.frequency * static_cast<float>(n) : 0.0f;
-    return z - (n ? p.presence : 0.0f);
+    const float off = fmaf(p.frequency, static_cast<float>(n), p.presence);
+    return z * (seen ? scale : 1.0f) - (n ? off : 0.0f);
 }
 
 // p[i], or, where p is null, `none`: a load either way (of other memory that
@@ -41,11 +49,13 @@ __device__ __forceinline__ T value_or(const T *p, int64_t i, const void *there, 
     return p ? v : none;
 }
 
-template <int CH, int VEC>
+template <int CH>
 __global__ __launch_bounds__(CH / 8) void logits_adjust_kernel(LogitsArgs a) {
     constexpr int kThreads = CH / 8;
-    __shared__ __align__(16) uint32_t slot[CH];    // a token's count in the answer, later its bias
-    __shared__ __align__(16) uint32_t other[CH];   // its count in the prompt, later of pending biases
+    __shared__ __align__(16) uint32_t count[CH];   // how often a token is in the answer
+    __shared__ __align__(4) uint8_t seen[CH];      // 1 where it is in the history at all
+    __shared__ __align__(16) float noted[CH];      // its bias, where `biased` has its bit
+    __shared__ uint32_t biased[CH / 32];           // a bit for each token of the bias list
     const int m = blockIdx.y, base = blockIdx.x * CH;
     const int tid = threadIdx.x;
     const int n = a.V - base < CH ? a.V - base : CH;
@@ -54,7 +64,8 @@ __global__ __launch_bounds__(CH / 8) void logits_adjust_kernel(LogitsArgs a) {
     const uint32_t *mask = a.mask ? a.mask + static_cast<int64_t>(m) * ((a.V + 31) / 32) + base / 32 : nullptr;
     int32_t h0 = value_or(a.cu_history, m, src, 0), h1 = value_or(a.cu_history, m + 1, src, 0);
     int32_t b0 = value_or(a.cu_bias, m, src, 0), b1 = value_or(a.cu_bias, m + 1, src, 0);
-    const int32_t prompt = value_or(a.prompt_lengths, m, src, 0);
+    const int32_t prompt_length = value_or(a.prompt_lengths, m, src, 0);
+    const int32_t prompt = prompt_length > 0 ? prompt_length : 0;
     RowParams p;
     p.rho = value_or(a.repetition, m, src, 1.0f);
     p.frequency = value_or(a.frequency, m, src, 0.0f);
@@ -72,114 +83,155 @@ __global__ __launch_bounds__(CH / 8) void logits_adjust_kernel(LogitsArgs a) {
     const float *biases = a.bias + b0;
 
     // token of the thread's j-th value of half u
-    auto token = [&](int u, int j) { return VEC ? 4 * (tid + kThreads * u) + j : tid + kThreads * (4 * u + j); };
+    auto token = [&](int u, int j) { return 4 * (tid + kThreads * u) + j; };
     floatx4 z[2];
     uint32_t bits[2] = {15u, 15u};   // which values the mask allows
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        if constexpr (VEC) {
-            const int i = tid + kThreads * u;
-            if (4 * i < n) {
-                z[u] = reinterpret_cast<const floatx4 *>(src)[i];
-                if (mask) bits[u] = mask[i / 8] >> (i % 8 * 4);
-            }
+        const int t = token(u, 0);
+        if (t < n && mask) bits[u] = mask[t / 32] >> t % 32;
+        if (t + 4 <= n) {
+            z[u] = *reinterpret_cast<const floatx4_row *>(src + t);
         } else {
-            if (mask) bits[u] = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int i = token(u, j);
-                if (i < n) z[u][j] = src[i];
-                if (mask && i < n) bits[u] |= ((mask[i / 32] >> (i % 32)) & 1u) << j;
-            }
+            for (int j = 0; j < 3; ++j)
+                if (t + j < n) z[u][j] = src[t + j];
         }
     }
-    auto load_ids = [&](uint32_t i0, int32_t(&to)[kAtOnce]) {
+    int32_t id[4 * kQuads], bias_id[kBiases];
+    float bias[kBiases];
+    // the thread's entries i0 + 4 * (tid + kThreads * k) + j of the history
+    // (what lies past its end reads as 0 and is not counted)
+    auto load_ids = [&](int32_t i0) {
+        const int32_t left = nh - i0 < 4 * kQuads * kThreads ? nh - i0 : 4 * kQuads * kThreads;
+        const __amdgpu_buffer_rsrc_t list =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<int32_t *>(history + i0), 0, 4 * left, 0x00020000);
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-            const uint32_t i = i0 + tid + kThreads * k;
-            to[k] = -1;
-            if (i0 + kThreads * k < static_cast<uint32_t>(nh) && i < static_cast<uint32_t>(nh)) to[k] = history[i];
+        for (int k = 0; k < kQuads; ++k) {
+            if (4 * kThreads * k >= left) break;
+            const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(list, 16 * (tid + kThreads * k), 0, 0));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) id[4 * k + j] = static_cast<int32_t>(v[j]);
         }
     };
-    int32_t bias_id;
-    float bias;
-    auto load_bias = [&](uint32_t i) {
-        bias_id = i < static_cast<uint32_t>(nb) ? bias_ids[i] : -1;
-        bias = i < static_cast<uint32_t>(nb) ? biases[i] : 0.0f;
-    };
-    int32_t id[kAtOnce];
-    load_ids(0, id);
-    load_bias(tid);
-    auto clear = [&] {
+    if (nh > 0) load_ids(0);
+#pragma unroll
+    for (int k = 0; k < kBiases; ++k) {
+        const uint32_t i = tid + kThreads * k;
+        bias_id[k] = -1;
+        if (kThreads * k < nb && i < static_cast<uint32_t>(nb)) {
+            bias_id[k] = bias_ids[i];
+            bias[k] = biases[i];
+        }
+    }
+    if (nh > 0 || nb > 0) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) slot[token(u, j)] = other[token(u, j)] = 0;
-    };
-    if (nh > 0) {
-        clear();
+            for (int j = 0; j < 4; ++j) count[token(u, j)] = seen[token(u, j)] = 0;
+        if (tid < CH / 32) biased[tid] = 0;
         __syncthreads();
-        for (uint32_t i0 = 0; i0 < static_cast<uint32_t>(nh); i0 += kThreads * kAtOnce) {
+        for (int32_t i0 = 0;;) {
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                if (i0 + kThreads * k >= static_cast<uint32_t>(nh)) break;
-                const uint32_t t = static_cast<uint32_t>(id[k] - base);
-                const bool answer = static_cast<int64_t>(i0 + tid + kThreads * k) >= prompt;
-                if (id[k] >= base && t < CH) atomicAdd(&(answer ? slot : other)[t], 1u);
-            }
-            load_ids(i0 + kThreads * kAtOnce, id);
-        }
-        __syncthreads();
+            for (int k = 0; k < kQuads; ++k) {
+                const int32_t first = 4 * kThreads * k;
+                if (first >= nh - i0) break;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) z[u][j] = penalized(z[u][j], other[token(u, j)], slot[token(u, j)], p);
-    }
-    if (nb > 0) {
-        clear();   // each thread its own slots, which it has read
-        __syncthreads();
-        for (uint32_t i0 = 0; i0 < static_cast<uint32_t>(nb); i0 += kThreads) {
-            const uint32_t t = static_cast<uint32_t>(bias_id - base);
-            bool pending = bias_id >= base && t < CH;
-            const float value = bias;
-            const bool repeated = pending && atomicAdd(&other[t], 1u) > 0;
-            if (__syncthreads_or(repeated)) {
-                // the first pending entry of a token adds its bias, then the next
-                while (__syncthreads_or(pending)) {
-                    if (pending) other[t] = 0xFFFFFFFFu;
-                    __syncthreads();
-                    if (pending) atomicMin(&other[t], static_cast<uint32_t>(tid));
-                    __syncthreads();
-                    if (pending && other[t] == static_cast<uint32_t>(tid)) {
-                        slot[t] = __float_as_uint(__uint_as_float(slot[t]) + value);
-                        pending = false;
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t i = first + 4 * tid + j;
+                    const uint32_t t = static_cast<uint32_t>(id[4 * k + j] - base);
+                    if (t < CH && i < nh - i0) {   // not for ids below base or 0 either
+                        atomicAdd(&count[t], i >= prompt - i0 ? 1u : 0u);
+                        seen[t] = 1;
                     }
                 }
-                if (bias_id >= base && t < CH) other[t] = 0;
-            } else if (pending) {
-                slot[t] = __float_as_uint(__uint_as_float(slot[t]) + value);
-                other[t] = 0;
             }
-            __syncthreads();
-            load_bias(i0 + kThreads + tid);
+            if (nh - i0 <= 4 * kQuads * kThreads) break;
+            i0 += 4 * kQuads * kThreads;
+            load_ids(i0);
         }
+        // whether some token has more than one bias, or some thread more than kBiases
+        bool again = nb > kThreads * kBiases;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int k = 0; k < kBiases; ++k) {
+            const uint32_t t = static_cast<uint32_t>(bias_id[k] - base);
+            if (t < CH) {
+                noted[t] = bias[k];
+                again |= (atomicOr(&biased[t / 32], 1u << t % 32) >> t % 32) & 1;
+            }
+        }
+        again = __syncthreads_or(again);
+        if (nh > 0)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) z[u][j] += __uint_as_float(slot[token(u, j)]);
+            for (int u = 0; u < 2; ++u) {
+                bool any = false, is_seen[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) any |= is_seen[j] = seen[token(u, j)] != 0;
+                if (any)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) z[u][j] = penalized(z[u][j], is_seen[j], count[token(u, j)], p);
+            }
+        if (nb > 0 && !again)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int t = token(u, 0);
+                const uint32_t has = biased[t / 32] >> t % 32 & 15u;
+                if (has)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (has >> j & 1u) z[u][j] += noted[token(u, j)];
+            }
+        if (again) {   // noted: the sum of a token's biases; count: its pending entries
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    count[token(u, j)] = 0;
+                    noted[token(u, j)] = 0.0f;
+                }
+            __syncthreads();
+            for (uint32_t i0 = 0; i0 < static_cast<uint32_t>(nb); i0 += kThreads) {
+                const uint32_t i = i0 + tid;
+                const uint32_t t = static_cast<uint32_t>((i < static_cast<uint32_t>(nb) ? bias_ids[i] : -1) - base);
+                const float add = i < static_cast<uint32_t>(nb) ? biases[i] : 0.0f;
+                bool pending = t < CH;
+                const bool repeated = pending && atomicAdd(&count[t], 1u) > 0;
+                if (__syncthreads_or(repeated)) {
+                    // the first pending entry of a token adds its bias, then the next
+                    while (__syncthreads_or(pending)) {
+                        if (pending) count[t] = 0xFFFFFFFFu;
+                        __syncthreads();
+                        if (pending) atomicMin(&count[t], static_cast<uint32_t>(tid));
+                        __syncthreads();
+                        if (pending && count[t] == static_cast<uint32_t>(tid)) {
+                            noted[t] += add;
+                            pending = false;
+                        }
+                    }
+                } else if (pending) {
+                    noted[t] += add;
+                }
+                if (t < CH) count[t] = 0;
+                __syncthreads();
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) z[u][j] += noted[token(u, j)];
+        }
     }
     const float ninf = -__builtin_inff();
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[u][j] = (bits[u] >> j) & 1u ? z[u][j] : ninf;
-        if constexpr (VEC) {
-            const int i = tid + kThreads * u;
-            if (4 * i < n) reinterpret_cast<floatx4 *>(dst)[i] = z[u];
+        const int t = token(u, 0);
+        if (t + 4 <= n) {
+            __builtin_nontemporal_store(static_cast<floatx4_row>(z[u]), reinterpret_cast<floatx4_row *>(dst + t));
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (token(u, j) < n) dst[token(u, j)] = z[u][j];
+            for (int j = 0; j < 3; ++j)
+                if (t + j < n) dst[t + j] = z[u][j];
         }
     }
 }
@@ -187,20 +239,19 @@ __global__ __launch_bounds__(CH / 8) void logits_adjust_kernel(LogitsArgs a) {
 template <int CH>
 hipError_t launch(const LogitsArgs &a, hipStream_t s) {
     const dim3 grid(static_cast<uint32_t>((a.V + CH - 1) / CH), static_cast<uint32_t>(a.M));
-    // rows start on 16 bytes only where V is a multiple of four
-    if (a.V % 4 == 0)
-        hipLaunchKernelGGL((logits_adjust_kernel<CH, 1>), grid, dim3(CH / 8), 0, s, a);
-    else
-        hipLaunchKernelGGL((logits_adjust_kernel<CH, 0>), grid, dim3(CH / 8), 0, s, a);
+    hipLaunchKernelGGL((logits_adjust_kernel<CH>), grid, dim3(CH / 8), 0, s, a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_logits_adjust(const LogitsArgs &a, hipStream_t s) {
-    // Every workgroup reads its row's history, so long runs of tokens read it
-    // less often; short ones spread few rows over the chip.
-    return static_cast<int64_t>(a.M) * a.V >= int64_t(4096) * 256 ? launch<4096>(a, s) : launch<1024>(a, s);
+    // Every workgroup reads its row's history, so where that is long, long runs
+    // of tokens take less time (4099 ids and 300 biases a row of 131072: 4.7
+    // against 5.4 us for one row, 8.9 against 11.3 for 32), and where it is
+    // short, short ones do, which spread few rows over the chip (200 and 16: 3.6
+    // against 4.0 us for one row, 7.3 against 7.4 for 32).
+    return a.history_size > int64_t(1000) * a.M ? launch<4096>(a, s) : launch<1024>(a, s);
 }
 
 }  // namespace q4

@@ -66,6 +66,32 @@ def test_long_history():
     _check(_case(2, 20000, np.random.default_rng(4), history=30000, bias=3000), "long")
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 127, 511, 512, 513, 999, 1000, 1001, 2047, 2048, 2049, 4099, 8191, 8192, 8193, 8195,
+                               16387])
+def test_history_of(n):
+    rng = np.random.default_rng([41, n])
+    for M, V, prompt in ((1, 5003, n // 2), (2, 131, n), (3, 4098, 0)):
+        c = _case(M, V, rng, bias=7)
+        c["cu"] = (np.arange(M + 1) * n).astype(np.int32)
+        c["history"] = rng.integers(0, V, M * n).astype(np.int32)
+        c["prompt"] = np.full(M, prompt, dtype=np.int32)
+        _check(c, f"history of {n}")
+
+
+@pytest.mark.parametrize("n", [1, 127, 128, 129, 511, 512, 513, 2047, 2048, 2049, 4100])
+@pytest.mark.parametrize("history", [10, 3000])
+def test_biases_of(n, history):   # of different tokens, and with one that is there twice
+    rng = np.random.default_rng([42, n, history])
+    for repeated in (False, True):
+        c = _case(2, 9001, rng, history=history, bias=0)
+        c["cu_bias"] = np.array([0, n, 2 * n], dtype=np.int32)
+        c["bias_ids"] = np.concatenate([rng.permutation(9001)[:n], rng.permutation(9001)[:n]]).astype(np.int32)
+        if repeated:
+            c["bias_ids"][n - 1] = c["bias_ids"][n // 2]
+        c["bias"] = rng.standard_normal(2 * n).astype(np.float32) * 5
+        _check(c, f"biases of {n}")
+
+
 def test_everything_masked():
     c = _case(2, 5000, np.random.default_rng(5), mask="none")
     _check(c, "masked")
