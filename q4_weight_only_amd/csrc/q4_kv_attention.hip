@@ -319,7 +319,7 @@ __device__ __forceinline__ Partials partials(const AttentionArgs &a, const Plan 
     Partials w;
     w.ml = reinterpret_cast<floatx2 *>(a.workspace);
     const int64_t rows = static_cast<int64_t>(a.kv.batch) * a.kv.kv_heads * p.groups * p.rows_held;
-    w.o = a.workspace + rows * p.splits * 2;
+    w.o = a.workspace + (rows * p.splits * 2 + 3) / 4 * 4;   // 16-byte aligned
     return w;
 }
 
@@ -342,12 +342,13 @@ __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total)
 // before the end.  Groups with the most tokens start first.
 //
 // What bounds it is reading the cache: two sequences of 131072 tokens of 8
-// heads of 128 (537 MB) take 86 us, 6.2 TB/s; 32 sequences of 2048 to 8191
+// heads of 128 (537 MB) take 85 us, 6.3 TB/s; 32 sequences of 2048 to 8191
 // (332 MB) 59 us, 5.6 TB/s.  The loads are nontemporal, as nothing is read
 // twice (99 -> 91 us for the former, 80 -> 74 for the latter when measured).
-// One token over 1505 takes 5.5 us, of which the loads that follow from each
-// other (length and block ids together, then codes) are the most, and the join
-// 3.5.
+// Short caches are bound by what follows from each other: length and block ids
+// together, codes, a block's products, the join of the waves: one token over 64
+// takes 4.2 us, over 512 5.8 and over 1505, in 12 splits, 7.7, of which the
+// join of the splits is 2.5.
 constexpr int kWaves = 4;
 
 template <int D>
@@ -355,7 +356,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
     constexpr int KQ = D / 32;   // k slices of the first product
     constexpr int DT = D / 16;   // 16-dimension tiles of the output
     __shared__ float part_m[kWaves][16], part_l[kWaves][16];
-    __shared__ float part_o[kWaves][D * 16];
+    __shared__ floatx4 part_o[kWaves][DT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g4 = lane >> 4;
     const int b = blockIdx.z, head = blockIdx.x;
@@ -481,9 +482,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
             part_l[wave][re] = sum;
         }
 #pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) part_o[wave][(16 * i + 4 * ge + j) * 16 + re] = tile[0].o[i][j];
+        for (int i = 0; i < DT; ++i) part_o[wave][i][16 * ge + re] = tile[0].o[i];
         __syncthreads();
         float top = part_m[0][re];
 #pragma unroll
@@ -495,22 +494,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
             total += f[w] * part_l[w][re];
         }
         if (!row.live) continue;
-        // thread: row re, dimensions 4 wave + ge + 16 i
-        const int d0 = 4 * wave + ge;
+        // every wave sums some of the 16-dimension tiles
         const Partials ws = partials(a, plan);
         const int64_t at = (partial_row(a.kv, plan, b, head, group) + re) * plan.splits + split;
         const float inv = inverse(a.kv, row.pos, total);
 #pragma unroll
-        for (int i = 0; i < DT; ++i) {
-            const int d = d0 + 16 * i;
-            float acc = 0.0f;
+        for (int i = 0; i < DT / kWaves; ++i) {
+            const int tile_i = wave * (DT / kWaves) + i, d = 16 * tile_i + 4 * ge;
+            floatx4 acc = part_o[0][tile_i][16 * ge + re] * f[0];
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) acc += f[w] * part_o[w][d * 16 + re];
-            if (!whole) ws.o[at * D + d] = acc;
-            else if (a.out_bf16) static_cast<__bf16 *>(a.out)[row.at + d] = static_cast<__bf16>(acc * inv);
-            else static_cast<float *>(a.out)[row.at + d] = acc * inv;
+            for (int w = 1; w < kWaves; ++w) acc = acc + part_o[w][tile_i][16 * ge + re] * f[w];
+            if (!whole) *reinterpret_cast<floatx4 *>(ws.o + at * D + d) = acc;
+            else if (a.out_bf16)
+                *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row.at + d) = __builtin_convertvector(acc * inv, bf16x4);
+            else *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + row.at + d) = acc * inv;
         }
-        if (!whole && d0 == 0) ws.ml[at] = (floatx2){top, total};
+        if (!whole && wave == 0 && ge == 0) ws.ml[at] = (floatx2){top, total};
     }
 }
 
@@ -724,7 +723,7 @@ __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(Attentio
                 }
             }
         }
-        int re = r, ge = g4;   // as in attention_rows_kernel
+        int re = r, ge = g4;   // as in attention_kernel
         asm volatile("" : "+v"(re), "+v"(ge));
         floatx4 *pass = reinterpret_cast<floatx4 *>(&stage[0][0][0]) + wave * (DT * 64) + ge * 16 + re;
         static_assert(sizeof(stage) >= W * DT * 64 * sizeof(floatx4), "a tile of every wave passes through the stages");
@@ -763,52 +762,54 @@ __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(Attentio
 }
 
 // Joins the splits of a row, a workgroup a row: D / 4 threads have four
-// dimensions each, and 1024 / D of such sets sum splits side by side.
+// dimensions each, and 1024 / D of such sets sum splits side by side.  Every
+// wave has all splits' m and l, 64 at a time, one a lane.  What is read does
+// not depend on the sequence's length, so that all loads, for up to kAhead
+// splits a thread, are on their way together.
 template <int D>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Plan plan) {
-    constexpr int LANES = D / 4, PARTS = 256 / LANES;
-    constexpr int kRun = 256;   // splits whose factors are held at once
+    constexpr int LANES = D / 4, PARTS = 256 / LANES, kAhead = 4;
     __shared__ floatx4 part[PARTS][LANES];
-    __shared__ float factor[kRun];
-    __shared__ float wave_part[4];
     const int b = blockIdx.z, head = blockIdx.y % a.kv.kv_heads, group = blockIdx.y / a.kv.kv_heads;
-    const int tid = threadIdx.x, x = tid % LANES, y = tid / LANES;
+    const int tid = threadIdx.x, lane = tid & 63, x = tid % LANES, y = tid / LANES;
     const int in_group = blockIdx.x;
     const Partials ws = partials(a, plan);
     const int64_t at0 = (partial_row(a.kv, plan, b, head, group) + in_group) * plan.splits;
+    const floatx2 none = {kLowest, 0.0f};
+    floatx2 ml = lane < plan.splits ? ws.ml[at0 + lane] : none;
+    const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + at0 * D) + x;
+    floatx4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (y + PARTS * k < plan.splits) ahead[k] = src[(y + PARTS * k) * LANES];
     const KvSequence s = kv_sequence(a.kv, b);
     const int all_rows = s.rows * a.group, rr0 = group * 16;
     const int rows = rr0 + 16 < all_rows ? 16 : all_rows - rr0;
     if (in_group >= rows || !is_split(plan, group, rows)) return;
     floatx4 acc = {0, 0, 0, 0};
-    float top = kLowest, total = 0.0f;
-    // every wave finds the largest m by itself
-    for (int i = tid & 63; i < plan.splits; i += 64) top = fmaxf(top, ws.ml[at0 + i].x);
+    float top = ml.x, total = 0.0f;
+    for (int i = 64 + lane; i < plan.splits; i += 64) top = fmaxf(top, ws.ml[at0 + i].x);
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor(top, m));
-    for (int i0 = 0; i0 < plan.splits; i0 += kRun) {
-        const int n = plan.splits - i0 < kRun ? plan.splits - i0 : kRun;
-        if (tid < n) {
-            const floatx2 ml = ws.ml[at0 + i0 + tid];
-            // (a split without blocks has no O to read)
-            const float f = ml.x == kLowest && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-            factor[tid] = f;
-            total += f * ml.y;
+    for (int i0 = 0; i0 < plan.splits; i0 += 64) {
+        const int n = plan.splits - i0 < 64 ? plan.splits - i0 : 64;
+        if (i0 > 0) ml = lane < n ? ws.ml[at0 + i0 + lane] : none;
+        // (a split without blocks has no O: what was read for it is not used)
+        const float f = ml.x == kLowest && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
+        total += f * ml.y;
+#pragma unroll
+        for (int k = 0; k < 64 / PARTS; ++k) {
+            const int i = y + PARTS * k;
+            if (PARTS * k >= n) break;   // the same for the workgroup
+            const float fi = __shfl(f, i);
+            if (i < n && fi != 0.0f) acc = acc + (k < kAhead && i0 == 0 ? ahead[k % kAhead] : src[static_cast<int64_t>(i0 + i) * LANES]) * fi;
         }
-        __syncthreads();
-        const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + (at0 + i0) * D) + x;
-#pragma unroll 4
-        for (int i = y; i < n; i += PARTS)
-            if (factor[i] != 0.0f) acc = acc + src[i * LANES] * factor[i];
-        __syncthreads();
     }
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) total += __shfl_xor(total, m);
-    if ((tid & 63) == 0) wave_part[tid >> 6] = total;
     part[y][x] = acc;
     __syncthreads();
     if (y != 0) return;
-    total = wave_part[0] + wave_part[1] + wave_part[2] + wave_part[3];
 #pragma unroll
     for (int i = 1; i < PARTS; ++i) acc = acc + part[i][x];
     const LaneRow row = lane_row(a, s, head, rr0 + in_group, all_rows, D);
@@ -832,11 +833,15 @@ constexpr int64_t kManyWork = 384;
 // 50 us and the join of two splits another 5.
 constexpr int64_t kMaxChunk = 256;
 
-// Up to so many blocks one workgroup takes no longer than a split and its join
-// (1024 tokens 8.8 against 11.6 us, 1505 11.4 each), and where blocks are split,
-// a wave has four of them at least (512 tokens 8.8 us, 11.5 with one).
-constexpr int64_t kUnsplit = 40;
-constexpr int64_t kMinChunk = 4 * kWaves;
+// A wave takes 0.43 us a block where it does not wait for memory (the products,
+// conversions and exponentials of a block follow from each other), and a split's
+// join 2.5 us and 1 more a thousand rows: blocks are split where that leaves a
+// workgroup kSaved fewer of them, and one more for every 128 rows.  (One row:
+// 700 tokens 7.1 us either way, 1200 7.4 against 8.8, 1505 7.7 against 10; 128
+// rows of 20 heads over 1000 tokens 12.0 against 6.7.)  The smallest chunk has a
+// block for each wave (3000 tokens 7.7 us, 9.0 with four).
+constexpr int64_t kSaved = 22;
+constexpr int64_t kMinChunk = kWaves;
 
 // Into how many parts attention_kernel's `work` groups have their blocks split:
 // a workgroup for every compute unit (more of them take longer to join: 32
@@ -844,7 +849,7 @@ constexpr int64_t kMinChunk = 4 * kWaves;
 // kMaxChunk until sixteen groups a compute unit even out their lengths (and
 // would need much workspace).
 int64_t splits_wanted(int64_t work, int64_t blocks) {
-    if (blocks <= kUnsplit) return 1;
+    if (blocks <= kSaved) return 1;
     const int64_t fill = (256 + work - 1) / work, least = (blocks + kMaxChunk - 1) / kMaxChunk;
     return work >= 4096 || least < fill ? fill : least;
 }
@@ -872,6 +877,7 @@ Plan plan_of(const AttentionArgs &a) {
     const int64_t splits = splits_wanted(p.groups * sets, blocks);
     int64_t chunk = (blocks + splits - 1) / splits;
     if (chunk < kMinChunk) chunk = kMinChunk;
+    if (blocks - chunk < kSaved + p.rows_held * p.groups * sets / 128) chunk = blocks < 1 ? 1 : blocks;
     p.chunk = static_cast<int>(chunk);
     p.splits = static_cast<int>((blocks + chunk - 1) / chunk);
     return p;
@@ -908,7 +914,7 @@ size_t attention_workspace(const AttentionArgs &a, int head_dim) {
     int64_t splits = splits_wanted(p.groups * sets, blocks);
     if (splits > (blocks + kMinChunk - 1) / kMinChunk) splits = (blocks + kMinChunk - 1) / kMinChunk;
     if (splits == 1) return 0;
-    return static_cast<size_t>(p.groups) * p.rows_held * sets * splits * (head_dim + 2) * sizeof(float);
+    return (static_cast<size_t>(p.groups) * p.rows_held * sets * splits * (head_dim + 2) + 2) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s) {
