@@ -2,12 +2,20 @@
 // the paged cache (include/q4_decoder.h).
 //
 // A workgroup of 2 * D threads has one of two tasks.  The first: one block of
-// one sequence, one kv head, K or V.  Each thread holds 16 dimensions of one
-// of the block's 32 tokens; the largest finite value of the new tokens gives
-// the block's exponent, the codes of tokens that were there before are
-// rescaled where the exponent rises, and the codes go out as 16-byte pieces
-// of the block's layout (V, whose bytes run along the tokens, turns through
-// LDS).  The second: 16 dimensions a thread of the rotated q.
+// one sequence, one kv head, K or V.  Each thread holds 16 values of the
+// block's 32 tokens; the largest finite value of the new tokens gives the
+// block's exponent, the codes of tokens that were there before are rescaled
+// where the exponent rises, and the codes pass through LDS, where they take the
+// block's order, as words of four.  The second: pieces of the rotated q, of two
+// heads a thread.
+//
+// What bounds it is memory: 4515 rows of 32 + 2 * 8 heads of 128 in fp32
+// (157 MB) take 31 us, 5.1 TB/s; 8192 rows of 20 + 2 * 20 heads of 64 37 us,
+// 4.5 TB/s.  Lanes run along a row's dimensions four at a time, so that a
+// wave's loads are whole lines (16 dimensions a lane: 52 and 66 us), and both
+// halves of the turned pairs are in one thread, which reads each of them once.
+// One token for each of 32 sequences takes 4.8 us: bounds and block ids, rows
+// and old codes, the largest value, the codes, one after the other.
 //
 // The rotation's products are rounded before they are added, so that a value
 // on the edge between two exponents does not depend on how the compiler pairs
@@ -23,62 +31,70 @@ namespace {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float floatx4 __attribute__((ext_vector_type(4)));
 typedef float floatx2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-__device__ __forceinline__ void load16(const float *p, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const floatx4 v = reinterpret_cast<const floatx4 *>(p)[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[4 * i + j] = v[j];
-    }
+__device__ __forceinline__ floatx4 load4(const float *p) { return *reinterpret_cast<const floatx4 *>(p); }
+__device__ __forceinline__ floatx4 load4(const uint16_t *p) {
+    const u32x2 v = *reinterpret_cast<const u32x2 *>(p);
+    return (floatx4){__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                     __uint_as_float(v.y & 0xFFFF0000u)};
 }
 
-__device__ __forceinline__ void load16(const uint16_t *p, float (&x)[16]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const u32x4 v = reinterpret_cast<const u32x4 *>(p)[i];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(v[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
-        }
-    }
+// Piece c of a head's dimensions, c in [0, D / 8): four pairs that are turned
+// together, as four dimensions from lo and four from hi (the halves of the
+// pairs, or pairs side by side), or eight that are not turned.
+struct Piece {
+    bool turned, split;
+    int lo, hi;
+};
+
+__device__ __forceinline__ Piece piece_of(const AppendArgs &a, int c) {
+    Piece p;
+    p.turned = 8 * c < a.rot;
+    p.split = p.turned && !a.interleaved;
+    p.lo = p.split ? 4 * c : 8 * c;
+    p.hi = p.split ? p.lo + a.rot / 2 : p.lo + 4;
+    return p;
 }
 
-// The 16 values at dimension d0 of a head's row, rotated by position pos.
-template <typename T>
-__device__ __forceinline__ void rotated16(const T *head, int d0, int pos, const AppendArgs &a, float (&x)[16]) {
-#pragma clang fp contract(off)
-    load16(head + d0, x);
-    if (d0 >= a.rot) return;
-    if (pos >= a.positions) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __builtin_nanf("");
-        return;
-    }
-    const int half = a.rot / 2;
-    const floatx2 *row = reinterpret_cast<const floatx2 *>(a.rope) + static_cast<int64_t>(pos) * half;
-    if (a.interleaved) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const floatx2 cs = row[d0 / 2 + j];
-            const float xa = x[2 * j], xb = x[2 * j + 1];
-            x[2 * j] = xa * cs.x - xb * cs.y;
-            x[2 * j + 1] = xb * cs.x + xa * cs.y;
-        }
+// Cosines and sines of the piece's pairs: not numbers past the table.
+struct Angles {
+    floatx4 cs[2];
+};
+
+__device__ __forceinline__ Angles angles(const AppendArgs &a, const Piece &p, int c, int pos) {
+    Angles x;
+    if (p.turned && pos >= 0 && pos < a.positions) {
+        const floatx4 *row = reinterpret_cast<const floatx4 *>(a.rope + (static_cast<int64_t>(pos) * (a.rot / 2) + 4 * c) * 2);
+        x.cs[0] = row[0];
+        x.cs[1] = row[1];
     } else {
-        const bool first = d0 < half;
-        float m[16];   // the other value of each pair
-        load16(head + (first ? d0 + half : d0 - half), m);
-        const floatx2 *cs16 = row + (first ? d0 : d0 - half);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const floatx2 cs = cs16[j];
-            const float turn = m[j] * cs.y;
-            x[j] = first ? x[j] * cs.x - turn : x[j] * cs.x + turn;
-        }
+        const float nan = __builtin_nanf("");
+        x.cs[0] = x.cs[1] = (floatx4){nan, nan, nan, nan};
     }
+    return x;
+}
+
+__device__ __forceinline__ void turn_pair(float &xa, float &xb, float c, float s) {
+#pragma clang fp contract(off)
+    const float ya = xa * c - xb * s, yb = xb * c + xa * s;
+    xa = ya;
+    xb = yb;
+}
+
+__device__ __forceinline__ void turn(const Piece &p, const Angles &w, floatx4 &lo, floatx4 &hi) {
+    if (!p.turned) return;
+    float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (p.split) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) turn_pair(x[j], x[4 + j], w.cs[j / 2][j % 2 * 2], w.cs[j / 2][j % 2 * 2 + 1]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) turn_pair(x[2 * j], x[2 * j + 1], w.cs[j / 2][j % 2 * 2], w.cs[j / 2][j % 2 * 2 + 1]);
+    }
+    lo = (floatx4){x[0], x[1], x[2], x[3]};
+    hi = (floatx4){x[4], x[5], x[6], x[7]};
 }
 
 __device__ __forceinline__ float finite_abs(float x) {
@@ -115,10 +131,12 @@ __device__ __forceinline__ uint32_t rescaled4(uint32_t w, float factor) {
     return codes4(lo.x * factor, lo.y * factor, hi.x * factor, hi.y * factor);
 }
 
-// One block of one sequence, kv head `head`, K (which = 0) or V (1).
+// One block of one sequence, kv head `head`, K (which = 0) or V (1).  A thread
+// has 16 values: of K a piece of two tokens, of V four dimensions of four
+// tokens, so that four of its codes are a word of the block's layout.
 template <int D, typename T>
 __device__ __forceinline__ void append_block(const AppendArgs &a, const KvSequence &s, int b, int blk, int head,
-                                             int which, uint8_t *turn, float *wave_max) {
+                                             int which, u32x4 *block, float *wave_max) {
     const int tid = threadIdx.x;
     // the tokens of this block that the call writes: slots [s0, s1)
     const int p0 = s.pos0 > 0 ? s.pos0 : 0, start = blk * kKvBlock;
@@ -126,86 +144,129 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, const KvSequen
     const int s1 = s.length - start < kKvBlock ? s.length - start : kKvBlock;
     const int id = kv_block_id(a.kv, b, blk);
     if (id < 0) return;   // uniform over the workgroup
-    // K: the thread's 16 bytes of the block are 16 dimensions of one token;
-    // V: threads run along a token's dimensions
-    int slot, d0;
-    if (which == 0) {
-        slot = tid / (64 * (D / 64)) * 16 + tid % 16;
-        d0 = tid / 64 % (D / 64) * 64 + tid / 16 % 4 * 16;
-    } else {
-        slot = tid / (D / 16);
-        d0 = tid % (D / 16) * 16;
-    }
-    const bool mine = slot >= s0 && slot < s1;
-    float x[16];
+    const int64_t plane = (static_cast<int64_t>(id) * a.kv.kv_heads + head) * 2 + which;
+    u32x4 *dst = reinterpret_cast<u32x4 *>(a.kv.data + plane * (kKvBlock * D)) + tid;
+    const bool whole = s1 - s0 == kKvBlock;
+    u32x4 old = {0, 0, 0, 0};
+    int before = kExpMin;
+    if (!whole) old = *dst;
+    if (s0 > 0) before = a.kv.exps[plane];
+    auto row_of = [&](int slot) { return s.row0 + (start + slot - s.pos0); };
+    auto mine = [&](int slot) { return slot >= s0 && slot < s1; };
+    // K: x[2 t], x[2 t + 1] of token slot0 + t; V: x[t]
+    const int slot0 = which == 0 ? tid / (D / 8) * 2 : tid / (D / 4) * 4;
+    const int c = which == 0 ? tid % (D / 8) : tid % (D / 4);
+    const Piece piece = piece_of(a, c);
+    floatx4 x[4];
     float amax = 0.0f;
-    if (mine) {
-        const int pos = start + slot;
-        const int64_t row = s.row0 + (pos - s.pos0);
-        if (which == 0)
-            rotated16(static_cast<const T *>(a.k) + row * a.k_stride + head * D, d0, pos, a, x);
-        else
-            load16(static_cast<const T *>(a.v) + row * a.v_stride + head * D + d0, x);
+    if (which == 0) {
+        Angles w[2];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) amax = fmaxf(amax, finite_abs(x[j]));
+        for (int t = 0; t < 2; ++t) {
+            x[2 * t] = x[2 * t + 1] = (floatx4){0, 0, 0, 0};
+            if (!mine(slot0 + t)) continue;
+            const T *src = static_cast<const T *>(a.k) + row_of(slot0 + t) * a.k_stride + head * D;
+            x[2 * t] = load4(src + piece.lo);
+            x[2 * t + 1] = load4(src + piece.hi);
+            w[t] = angles(a, piece, c, start + slot0 + t);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            if (mine(slot0 + t)) turn(piece, w[t], x[2 * t], x[2 * t + 1]);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            x[t] = (floatx4){0, 0, 0, 0};
+            if (mine(slot0 + t)) x[t] = load4(static_cast<const T *>(a.v) + row_of(slot0 + t) * a.v_stride + head * D + 4 * c);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(x[i / 4][i % 4]));
 #pragma unroll
     for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m));
     if ((tid & 63) == 0) wave_max[tid >> 6] = amax;
+    if (!whole) block[tid] = old;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) amax = fmaxf(amax, wave_max[w]);
-    const int64_t plane = (static_cast<int64_t>(id) * a.kv.kv_heads + head) * 2 + which;
     int e = exponent_of(amax);
-    float factor = 1.0f;   // of the codes that are there
-    if (s0 > 0) {
-        const int before = a.kv.exps[plane];
-        if (before > e) e = before;
-        factor = pow2(before - e < -126 ? -126 : before - e);
+    if (before > e) e = before;
+    if (s0 > 0 && before < e) {   // the codes that are there follow (uniform)
+        const float factor = pow2(before - e < -126 ? -126 : before - e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) old[i] = rescaled4(old[i], factor);
+        block[tid] = old;
+        __syncthreads();
     }
     const float inv = pow2(-e);
-    u32x4 *dst = reinterpret_cast<u32x4 *>(a.kv.data + plane * (kKvBlock * D)) + tid;
-    u32x4 w = {0, 0, 0, 0};
-    if (mine)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            w[i] = codes4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
+    for (int i = 0; i < 4; ++i) x[i] = x[i] * inv;
+    uint32_t *words = reinterpret_cast<uint32_t *>(block);
     if (which == 0) {
-        if (mine) {
-            *dst = w;
-        } else if (factor != 1.0f) {
-            u32x4 old = *dst;
+        // K: token / 16, d / 64, d / 16 % 4, token % 16, d % 16
+        auto put = [&](int slot, int d, floatx4 v) {
+            words[((slot / 16 * (D / 64) + d / 64) * 4 + d / 16 % 4) * 64 + slot % 16 * 4 + d % 16 / 4] = codes4(v.x, v.y, v.z, v.w);
+        };
 #pragma unroll
-            for (int i = 0; i < 4; ++i) old[i] = rescaled4(old[i], factor);
-            *dst = old;
-        }
+        for (int t = 0; t < 2; ++t)
+            if (mine(slot0 + t)) {
+                put(slot0 + t, piece.lo, x[2 * t]);
+                put(slot0 + t, piece.hi, x[2 * t + 1]);
+            }
     } else {
-        if (s1 - s0 < kKvBlock) {
-            u32x4 old = *dst;
-            if (factor != 1.0f)
+        // V: d / 32, token / 4 % 4, d % 16, d / 16 % 2, token / 16, token % 4
+        uint32_t keep = 0;   // bytes of tokens that were there
 #pragma unroll
-                for (int i = 0; i < 4; ++i) old[i] = rescaled4(old[i], factor);
-            reinterpret_cast<u32x4 *>(turn)[tid] = old;
-            __syncthreads();
-        }
-        if (mine) {
-            const int piece = d0 / 16;
-            uint8_t *to = turn + (piece / 2 * 4 + slot / 4 % 4) * 256 + piece % 2 * 8 + slot / 16 * 4 + slot % 4;
+        for (int t = 0; t < 4; ++t)
+            if (!mine(slot0 + t)) keep |= 0xFFu << (8 * t);
+        if (keep != 0xFFFFFFFFu) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) to[16 * j] = static_cast<uint8_t>(w[j / 4] >> (8 * (j % 4)));
+            for (int j = 0; j < 4; ++j) {
+                const int d = 4 * c + j;
+                uint32_t &word = words[(d / 32 * 4 + slot0 / 4 % 4) * 64 + d % 16 * 4 + d / 16 % 2 * 2 + slot0 / 16];
+                const uint32_t now = codes4(x[0][j], x[1][j], x[2][j], x[3][j]);
+                word = keep ? (word & keep) | (now & ~keep) : now;
+            }
         }
-        __syncthreads();
-        *dst = reinterpret_cast<const u32x4 *>(turn)[tid];
     }
-    // read above by every thread, before its data-dependent stores; the
-    // exponent changes only after all have it
     __syncthreads();
-    if (tid == 0) a.kv.exps[plane] = static_cast<int8_t>(e);
+    *dst = block[tid];
+    if (tid == 0) a.kv.exps[plane] = static_cast<int8_t>(e);   // all have read it
+    __syncthreads();   // the block has been read
+}
+
+// A piece of kHeads heads' rotated q, for which the angles are read once.
+constexpr int kHeads = 2;
+
+template <int D, typename T>
+__device__ __forceinline__ void rotate_q(const AppendArgs &a, int64_t row, int pos, int head0, int c) {
+    const int heads = a.q_heads - head0 < kHeads ? a.q_heads - head0 : kHeads;
+    const Piece piece = piece_of(a, c);
+    const T *src = static_cast<const T *>(a.q) + row * a.q_stride + head0 * D;
+    const Angles w = angles(a, piece, c, pos);
+    floatx4 x[kHeads][2];
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+        if (h < heads) {
+            x[h][0] = load4(src + h * D + piece.lo);
+            x[h][1] = load4(src + h * D + piece.hi);
+        }
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+        if (h >= heads) break;
+        turn(piece, w, x[h][0], x[h][1]);
+        uint16_t *dst = a.q_out + (row * a.q_heads + head0 + h) * D;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const bf16x4 y = pos >= 0 ? __builtin_convertvector(x[h][i], bf16x4) : (bf16x4){};
+            __builtin_nontemporal_store(y, reinterpret_cast<bf16x4 *>(dst + (i ? piece.hi : piece.lo)));
+        }
+    }
 }
 
 template <int D, typename T>
 __global__ __launch_bounds__(2 * D) void kv_append_kernel(AppendArgs a, int block_units, int q_units) {
-    __shared__ __align__(16) uint8_t turn[kKvBlock * D];
+    __shared__ u32x4 block[2 * D];
     __shared__ float wave_max[D / 32];
     const int b = blockIdx.y;
     const KvSequence s = kv_sequence(a.kv, b);
@@ -217,29 +278,16 @@ __global__ __launch_bounds__(2 * D) void kv_append_kernel(AppendArgs a, int bloc
         const int j0 = (s.pos0 > 0 ? s.pos0 : 0) / kKvBlock, j1 = (s.length - 1) / kKvBlock;
         const int step = block_units / heads2;
         for (int blk = j0 + unit / heads2; blk <= j1; blk += step)
-            append_block<D, T>(a, s, b, blk, unit % heads2 / 2, unit % 2, turn, wave_max);
+            append_block<D, T>(a, s, b, blk, unit % heads2 / 2, unit % 2, block, wave_max);
         return;
     }
     unit -= block_units;
-    const int per_row = a.q_heads * (D / 16);
+    const int per_row = (a.q_heads + kHeads - 1) / kHeads * (D / 8);
     const int64_t total = static_cast<int64_t>(s.rows) * per_row;
     for (int64_t u = static_cast<int64_t>(unit) * (2 * D) + threadIdx.x; u < total;
          u += static_cast<int64_t>(q_units) * (2 * D)) {
-        const int t = static_cast<int>(u / per_row), piece = static_cast<int>(u % per_row);
-        const int64_t row = s.row0 + t;
-        const int pos = s.pos0 + t, head = piece / (D / 16), d0 = piece % (D / 16) * 16;
-        u32x4 o[2] = {};
-        if (pos >= 0) {
-            float x[16];
-            rotated16(static_cast<const T *>(a.q) + row * a.q_stride + head * D, d0, pos, a, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                o[i / 4][i % 4] =
-                    __builtin_bit_cast(uint32_t, __builtin_convertvector((floatx2){x[2 * i], x[2 * i + 1]}, bf16x2));
-        }
-        u32x4 *dst = reinterpret_cast<u32x4 *>(a.q_out + (row * a.q_heads + head) * D + d0);
-        dst[0] = o[0];
-        dst[1] = o[1];
+        const int t = static_cast<int>(u / per_row), in_row = static_cast<int>(u % per_row);
+        rotate_q<D, T>(a, s.row0 + t, s.pos0 + t, in_row / (D / 8) * kHeads, in_row % (D / 8));
     }
 }
 
@@ -250,7 +298,8 @@ hipError_t launch(const AppendArgs &a, hipStream_t s) {
     int64_t blocks = (static_cast<int64_t>(a.max_rows) + kKvBlock - 2) / kKvBlock + 1;
     if (blocks > 4096) blocks = 4096;
     const int64_t block_units = blocks * a.kv.kv_heads * 2;
-    int64_t q_units = (static_cast<int64_t>(a.max_rows) * a.q_heads * (D / 16) + 2 * D - 1) / (2 * D);
+    const int64_t per_row = (a.q_heads + kHeads - 1) / kHeads * (D / 8);
+    int64_t q_units = (a.max_rows * per_row + 2 * D - 1) / (2 * D);
     if (q_units > (1 << 20)) q_units = 1 << 20;
     hipLaunchKernelGGL((kv_append_kernel<D, T>),
                        dim3(static_cast<uint32_t>(block_units + q_units), static_cast<uint32_t>(a.kv.batch)),
