@@ -79,11 +79,9 @@ __device__ __forceinline__ halfx8 weights_f16(const float (&w)[8]) {
 // Bytes of a word of 4 consecutive tokens, the first `first`, that lie in
 // [lo, hi): 0xFF each.
 __device__ __forceinline__ uint32_t bytes_in(int first, int lo, int hi) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (first + j >= lo && first + j < hi) m |= 0xFFu << (8 * j);
-    return m;
+    const int skip = lo - first < 0 ? 0 : lo - first > 4 ? 4 : lo - first;
+    const int count = hi - first < 0 ? 0 : hi - first > 4 ? 4 : hi - first;
+    return static_cast<uint32_t>(((1ull << (8 * count)) - 1) & ~((1ull << (8 * skip)) - 1));
 }
 
 // 0x80 in each byte that is not a number.
@@ -171,22 +169,17 @@ struct Tile {
 };
 
 // The lane's tokens of a block are first + i and first + 16 + i; a row sees
-// tokens lo .. pos.
-__device__ __forceinline__ void hide_unseen(floatx4 (&st)[2], int first, int lo, int pos) {
+// `seen` tokens from lo on.
+__device__ __forceinline__ void hide_unseen(floatx4 (&st)[2], int first, int lo, uint32_t seen) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int j = first + i / 4 * 16 + i % 4;
-        st[i / 4][i % 4] = j >= lo && j <= pos ? st[i / 4][i % 4] : -__builtin_inff();
-    }
+    for (int i = 0; i < 8; ++i)
+        st[i / 4][i % 4] = static_cast<uint32_t>(first - lo + (i / 4 * 16 + i % 4)) < seen ? st[i / 4][i % 4] : -__builtin_inff();
 }
 
-__device__ __forceinline__ halfx8 seen_tokens(int first, int lo, int pos) {   // 1 for each that the row sees
+__device__ __forceinline__ halfx8 seen_tokens(int first, int lo, uint32_t seen) {   // 1 for each that the row sees
     float one[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int j = first + i / 4 * 16 + i % 4;
-        one[i] = j >= lo && j <= pos ? 1.0f : 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) one[i] = static_cast<uint32_t>(first - lo + (i / 4 * 16 + i % 4)) < seen ? 1.0f : 0.0f;
     return weights_f16(one);
 }
 
@@ -212,7 +205,8 @@ __device__ __forceinline__ void block_weights(Tile<D> (&tile)[NR], const floatx4
 // Which row of q a lane has, and what it sees.
 struct LaneRow {
     bool live;
-    int t, pos, lo;    // row of the sequence, its position, the first token that it sees
+    int t, pos, lo;    // row of the sequence, its position, the first token that it sees (or a place before them)
+    uint32_t seen;     // how many from lo on
     int64_t at;        // its first element in q and out
 };
 
@@ -228,6 +222,7 @@ __device__ __forceinline__ LaneRow lane_row(const AttentionArgs &a, const KvSequ
     x.t = row_of(a, last);
     x.pos = s.pos0 + x.t;
     x.lo = a.window ? x.pos - a.window + 1 : 0;
+    x.seen = a.window ? a.window : x.pos < 0 ? 0 : x.pos + 1;
     x.at = (static_cast<int64_t>(s.row0 + x.t) * a.q_heads + head * a.group + last - x.t * a.group) * D;
     return x;
 }
@@ -438,7 +433,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                     const int start = (first + i * kWaves) * kKvBlock;
                     if (start < all_lo || start + kKvBlock - 1 > p_first) {   // some row does not see some token
                         const int tok = start + 4 * g4;
-                        hide_unseen(st[0], tok, row.lo, row.pos);
+                        hide_unseen(st[0], tok, row.lo, row.seen);
                         // bytes that no row of the group sees may hold anything
                         const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
                         // and what is not a number must not meet a weight of 0:
@@ -451,7 +446,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                             kc[KQ + j / 4][j % 4] = v & ~(n * 0xFFu);
                         }
                         if (__any((bad[0] | bad[1]) != 0)) {
-                            const halfx8 seen = seen_tokens(tok, row.lo, row.pos);
+                            const halfx8 seen = seen_tokens(tok, row.lo, row.seen);
 #pragma unroll
                             for (int d = 0; d < DT; ++d) {
                                 const uint32_t n0 = bad[d / 4] >> (d % 4 * 2), n1 = n0 >> 1;
@@ -692,11 +687,11 @@ __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(Attentio
                         if (partly_seen(pair)) {   // as put() decided
                             const int tok = start + 4 * g4;
 #pragma unroll
-                            for (int n = 0; n < NR; ++n) hide_unseen(st[n], tok, row[n].lo, row[n].pos);
+                            for (int n = 0; n < NR; ++n) hide_unseen(st[n], tok, row[n].lo, row[n].seen);
                             if (__builtin_amdgcn_readfirstlane(nan_block[u][set]) == pair) {
 #pragma unroll
                                 for (int n = 0; n < NR; ++n) {
-                                    const halfx8 seen = seen_tokens(tok, row[n].lo, row[n].pos);
+                                    const halfx8 seen = seen_tokens(tok, row[n].lo, row[n].seen);
 #pragma unroll
                                     for (int d = 0; d < DT; ++d) {
                                         const u32x4 x = nans[u][set][64 * (d / 2) + lane];
