@@ -518,8 +518,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
 // 16 bytes are its operand slices, so the reads have no bank conflicts).
 // Every slice that a wave converts feeds NR products.  Groups with the most
 // tokens start first.
-constexpr int kTileNr = 2;
-
+//
+// What bounds it is the issue of instructions: a wave's 32 rows and a block of
+// heads of 128 are 32 MFMAs of 16 cycles and about 210 other instructions of 4
+// (64 conversions of codes, 80 to 90 for 32 rows' weights), and little of the
+// two runs at once.  A prompt of 2048 with 32 heads of 128 takes 57 us, 600
+// TFLOP/s, one of 8192 691 us, 796.  NR = 2 fills the registers for D = 128
+// (with 3, 48 values spill: the same prompts take 79 and 798 us); for D = 64
+// four tiles fit, which take 98 -> 76 us for 4096 rows of 20 heads.  Codes that
+// are converted once on their way to LDS, where they take twice the room, take
+// 65 instead of 61 us for the prompt (when measured), waves that read the cache
+// themselves without LDS 64 to 69.
 template <int D, int NR, int W>
 __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(AttentionArgs a) {
     constexpr int kTileThreads = 2 * 64 * W;
@@ -887,9 +896,14 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
     if (p.group_rows == 16)
         hipLaunchKernelGGL((attention_kernel<D>), grid, dim3(64 * kWaves), 0, s, a, p);
     else if (p.group_rows == 64)
-        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 2>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((attention_tiles_kernel<D, 2, 2>), grid, dim3(256), 0, s, a);
+    else if (D == 64 && static_cast<int64_t>(p.groups) * a.kv.kv_heads * a.kv.batch > 512)
+        // more workgroups than fit at once, two a compute unit, so that their
+        // lengths even out: 3 times 1000 rows of 24 heads (576) 28 against 37
+        // us, but twice 2048 rows of 16 heads (512) 54 against 43
+        hipLaunchKernelGGL((attention_tiles_kernel<D, D == 64 ? 4 : 2, D == 64 ? 2 : 4>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((attention_tiles_kernel<D, kTileNr, 4>), grid, dim3(512), 0, s, a);
+        hipLaunchKernelGGL((attention_tiles_kernel<D, 2, 4>), grid, dim3(512), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     hipLaunchKernelGGL((attention_join_kernel<D>), dim3(p.rows_held, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);

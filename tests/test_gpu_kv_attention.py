@@ -17,7 +17,7 @@ from gpu_helpers import say
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(autouse=True, params=["chosen", "groups of 64", "groups of 128"])
+@pytest.fixture(autouse=True, params=["chosen", "groups of 64", "groups of 128", "few groups of 128"])
 def kernel(request, monkeypatch):
     """Every test runs with the kernel that its sizes choose, and with those for
     many rows: max_rows, which shapes a launch, changes no result."""
@@ -31,6 +31,8 @@ def _hint(sets, group):
     """max_rows that brings a launch of `sets` sequences x kv heads to the kernel."""
     if KERNEL == "groups of 128":
         return 1 << 19
+    if KERNEL == "few groups of 128":      # from 257 to 512 of them
+        return max(1, 128 * max(1, 512 // sets) // group)
     if KERNEL == "groups of 64":      # at least 384 groups of 64 rows, at most 256 of 128
         k = max(1, 256 // sets)
         return max(1, 64 * (2 * k - 1) // group)
@@ -116,7 +118,8 @@ def test_windows_of_a_prompt_with_many_heads():
 
 
 def test_sizes_that_choose_the_kernels_for_many_rows():
-    """384 and 400 groups of 64 rows, by their own number."""
+    """384 and 400 groups of 64 rows, and 684 of 128, by their own number."""
+    _check([150] * 9, [150] * 9, heads=19, group=3, seed=21)
     _check([65] * 8, [65] * 8, heads=24, group=1, seed=21)
     _check([40, 33], [33, 33], heads=8, group=48, seed=21)
 
