@@ -923,7 +923,8 @@ size_t attention_workspace(const AttentionArgs &a, int head_dim) {
     int64_t splits = splits_wanted(p.groups * sets, blocks);
     if (splits > (blocks + kMinChunk - 1) / kMinChunk) splits = (blocks + kMinChunk - 1) / kMinChunk;
     if (splits == 1) return 0;
-    return (static_cast<size_t>(p.groups) * p.rows_held * sets * splits * (head_dim + 2) + 2) * sizeof(float);
+    const size_t parts = static_cast<size_t>(p.groups) * p.rows_held * sets * splits;   // as in partials()
+    return ((parts * 2 + 3) / 4 * 4 + parts * head_dim) * sizeof(float);
 }
 
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s) {
