@@ -285,7 +285,7 @@ __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 
 // How a launch is shaped: groups of `group_rows` rows of a sequence and kv
 // head, and the split of their blocks.
 struct Plan {
-    int group_rows;      // 16, or 64 or 128 in attention_tiles_kernel
+    int group_rows;      // 16 or 32, or 64 or 128 in attention_tiles_kernel
     int groups;          // of the sequence with most rows
     int rows_held;       // rows of a group that the workspace has room for
     int chunk, splits;
@@ -329,25 +329,31 @@ __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total)
     return past(kv, pos) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
 }
 
-// ------------------------------------------------------- few rows: decode
-// A workgroup has 16 rows (of rows x heads of the group) of one sequence and
-// kv head, and one chunk of its blocks; its four waves take every fourth block
-// with all the rows, so a block's codes go from memory to the registers of one
-// wave, as its operand slices, and nowhere else, and no wave waits for another
-// before the end.  Groups with the most tokens start first.
+// ------------------------------------ rows with a workgroup's waves apart
+// A workgroup has NR tiles of 16 rows (of rows x heads of the group) of one
+// sequence and kv head, and one chunk of its blocks; its four waves take every
+// fourth block with all the rows, so a block's codes go from memory to the
+// registers of one wave, as its operand slices, and nowhere else, and no wave
+// waits for another before the end.  Groups with the most tokens start first.
 //
-// What bounds it is reading the cache: two sequences of 131072 tokens of 8
-// heads of 128 (537 MB) take 85 us, 6.3 TB/s; 32 sequences of 2048 to 8191
-// (332 MB) 59 us, 5.6 TB/s.  The loads are nontemporal, as nothing is read
-// twice (99 -> 91 us for the former, 80 -> 74 for the latter when measured).
-// Short caches are bound by what follows from each other: length and block ids
-// together, codes, a block's products, the join of the waves: one token over 64
-// takes 4.2 us, over 512 5.8 and over 1505, in 12 splits, 7.7, of which the
-// join of the splits is 2.5.
+// What bounds it for single tokens is reading the cache: two sequences of
+// 131072 tokens of 8 heads of 128 (537 MB) take 85 us, 6.3 TB/s; 32 sequences
+// of 2048 to 8191 (332 MB) 59 us, 5.6 TB/s.  The loads are nontemporal, as
+// nothing is read twice (99 -> 91 us for the former, 80 -> 74 for the latter
+// when measured).  Short caches are bound by what follows from each other:
+// length and block ids together, codes, a block's products, the join of the
+// waves: one token over 64 takes 4.2 us, over 512 5.8 and over 1505, in 12
+// splits, 7.7, of which the join of the splits is 2.5.
+//
+// For many rows it is the issue of instructions, as in attention_tiles_kernel:
+// 2048 rows over 16384 tokens with 32 heads of 128 take 550 us, 937 TFLOP/s.
+// Two tiles share what a wave converts (one tile: 1086 us), and fill the
+// registers.
 constexpr int kWaves = 4;
 
-template <int D>
+template <int D, int NR>
 __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs a, Plan plan) {
+    constexpr int kRows = 16 * NR;
     constexpr int KQ = D / 32;   // k slices of the first product
     constexpr int DT = D / 16;   // 16-dimension tiles of the output
     __shared__ float part_m[kWaves][16], part_l[kWaves][16];
@@ -363,10 +369,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
     const KvSequence s = kv_sequence(a.kv, b);
     const int grid_groups = plan.splits == 1 ? gridDim.y : gridDim.y / plan.splits;
     const int all_rows = s.rows * a.group;
-    const int groups = (all_rows + 15) / 16;
+    const int groups = (all_rows + kRows - 1) / kRows;
     for (int back = plan.splits == 1 ? blockIdx.y : blockIdx.y / plan.splits; back < groups; back += grid_groups) {
         const int group = groups - 1 - back;
-        const int rr0 = group * 16, rr1 = rr0 + 16 < all_rows ? rr0 + 16 : all_rows;
+        const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
         const int p_first = s.pos0 + row_of(a, rr0), p_last = s.pos0 + row_of(a, rr1 - 1);
         const bool whole = !is_split(plan, group, rr1 - rr0);
         const Span sp = span_of(a.kv, p_first, p_last, a.window, plan.chunk, whole ? 1 : plan.splits);
@@ -379,11 +385,15 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
         // the first tokens that all rows and that any row of the group see
         const int all_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
 
-        const LaneRow row = lane_row(a, s, head, rr0 + r, all_rows, D);
-        bf16x8 q[KQ];
-        load_q<D>(a, row.at, g4, q);
-        Tile<D> tile[1];
-        tile[0].clear();
+        LaneRow row[NR];
+        bf16x8 q[NR][KQ];
+        Tile<D> tile[NR];
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            row[n] = lane_row(a, s, head, rr0 + 16 * n + r, all_rows, D);
+            load_q<D>(a, row[n].at, g4, q[n]);
+            tile[n].clear();
+        }
         // a block's ids and exponents are read 64 blocks at a time, one a lane,
         // its codes one block ahead
         for (int first = blk0 + wave; first < blk1; first += 64 * kWaves) {
@@ -418,22 +428,28 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                     u32x4(&kc)[2 * KQ] = codes[u];
                     const BlockScales scales = block_scales(a, __builtin_amdgcn_readlane(my_exps, i));
                     const bool known = __builtin_amdgcn_readlane(my_id, i) >= 0;
-                    floatx4 st[1][2];
+                    floatx4 st[NR][2];
 #pragma unroll
                     for (int tt = 0; tt < 2; ++tt) {
-                        st[0][tt] = (floatx4){0, 0, 0, 0};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){0, 0, 0, 0};
 #pragma unroll
                         for (int k = 0; k < KQ; ++k) {
                             const u32x4 w = kc[tt * (KQ / 2) + k / 2];
                             const bf16x8 kf = k % 2 ? codes_bf16(w.z, w.w) : codes_bf16(w.x, w.y);
-                            st[0][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[k], st[0][tt], 0, 0, 0);
+#pragma unroll
+                            for (int n = 0; n < NR; ++n)
+                                st[n][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][k], st[n][tt], 0, 0, 0);
                         }
-                        if (!known) st[0][tt] = (floatx4){kNan, kNan, kNan, kNan};
+                        if (!known)
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){kNan, kNan, kNan, kNan};
                     }
                     const int start = (first + i * kWaves) * kKvBlock;
                     if (start < all_lo || start + kKvBlock - 1 > p_first) {   // some row does not see some token
                         const int tok = start + 4 * g4;
-                        hide_unseen(st[0], tok, row.lo, row.seen);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) hide_unseen(st[n], tok, row[n].lo, row[n].seen);
                         // bytes that no row of the group sees may hold anything
                         const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
                         // and what is not a number must not meet a weight of 0:
@@ -446,21 +462,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                             kc[KQ + j / 4][j % 4] = v & ~(n * 0xFFu);
                         }
                         if (__any((bad[0] | bad[1]) != 0)) {
-                            const halfx8 seen = seen_tokens(tok, row.lo, row.seen);
 #pragma unroll
-                            for (int d = 0; d < DT; ++d) {
-                                const uint32_t n0 = bad[d / 4] >> (d % 4 * 2), n1 = n0 >> 1;
-                                tile[0].mark_nans(d, n0 & 0x01010101u, n1 & 0x01010101u, seen);
+                            for (int n = 0; n < NR; ++n) {
+                                const halfx8 seen = seen_tokens(tok, row[n].lo, row[n].seen);
+#pragma unroll
+                                for (int d = 0; d < DT; ++d) {
+                                    const uint32_t n0 = bad[d / 4] >> (d % 4 * 2), n1 = n0 >> 1;
+                                    tile[n].mark_nans(d, n0 & 0x01010101u, n1 & 0x01010101u, seen);
+                                }
                             }
                         }
                     }
-                    halfx8 wf[1];
-                    block_weights<D, 1>(tile, st, scales, wf);
+                    halfx8 wf[NR];
+                    block_weights<D, NR>(tile, st, scales, wf);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
                         const u32x4 v = kc[KQ + d / 2];
                         const halfx8 vf = d % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
-                        tile[0].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[0], tile[0].o[d], 0, 0, 0);
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            tile[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[n], tile[n].o[d], 0, 0, 0);
                     }
                 }
             }
@@ -470,45 +491,48 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
         // hold them all.)
         int re = r, ge = g4;
         asm volatile("" : "+v"(re), "+v"(ge));
-        const float sum = row_sum(tile[0].l);
-        __syncthreads();   // the group before has been read
-        if (ge == 0) {
-            part_m[wave][re] = tile[0].m;
-            part_l[wave][re] = sum;
+#pragma unroll
+        for (int n = 0; n < NR; ++n) {
+            const float sum = row_sum(tile[n].l);
+            __syncthreads();   // the tile before has been read
+            if (ge == 0) {
+                part_m[wave][re] = tile[n].m;
+                part_l[wave][re] = sum;
+            }
+#pragma unroll
+            for (int i = 0; i < DT; ++i) part_o[wave][i][16 * ge + re] = tile[n].o[i];
+            __syncthreads();
+            float top = part_m[0][re];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
+            float f[kWaves], total = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
+                total += f[w] * part_l[w][re];
+            }
+            if (!row[n].live) continue;
+            // every wave sums some of the 16-dimension tiles
+            const Partials ws = partials(a, plan);
+            const int64_t at = (partial_row(a.kv, plan, b, head, group) + 16 * n + re) * plan.splits + split;
+            const float inv = inverse(a.kv, row[n].pos, total);
+#pragma unroll
+            for (int i = 0; i < DT / kWaves; ++i) {
+                const int tile_i = wave * (DT / kWaves) + i, d = 16 * tile_i + 4 * ge;
+                floatx4 acc = part_o[0][tile_i][16 * ge + re] * f[0];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) acc = acc + part_o[w][tile_i][16 * ge + re] * f[w];
+                if (!whole) *reinterpret_cast<floatx4 *>(ws.o + at * D + d) = acc;
+                else if (a.out_bf16)
+                    *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row[n].at + d) = __builtin_convertvector(acc * inv, bf16x4);
+                else *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + row[n].at + d) = acc * inv;
+            }
+            if (!whole && wave == 0 && ge == 0) ws.ml[at] = (floatx2){top, total};
         }
-#pragma unroll
-        for (int i = 0; i < DT; ++i) part_o[wave][i][16 * ge + re] = tile[0].o[i];
-        __syncthreads();
-        float top = part_m[0][re];
-#pragma unroll
-        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
-        float f[kWaves], total = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
-            total += f[w] * part_l[w][re];
-        }
-        if (!row.live) continue;
-        // every wave sums some of the 16-dimension tiles
-        const Partials ws = partials(a, plan);
-        const int64_t at = (partial_row(a.kv, plan, b, head, group) + re) * plan.splits + split;
-        const float inv = inverse(a.kv, row.pos, total);
-#pragma unroll
-        for (int i = 0; i < DT / kWaves; ++i) {
-            const int tile_i = wave * (DT / kWaves) + i, d = 16 * tile_i + 4 * ge;
-            floatx4 acc = part_o[0][tile_i][16 * ge + re] * f[0];
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) acc = acc + part_o[w][tile_i][16 * ge + re] * f[w];
-            if (!whole) *reinterpret_cast<floatx4 *>(ws.o + at * D + d) = acc;
-            else if (a.out_bf16)
-                *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row.at + d) = __builtin_convertvector(acc * inv, bf16x4);
-            else *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + row.at + d) = acc * inv;
-        }
-        if (!whole && wave == 0 && ge == 0) ws.ml[at] = (floatx2){top, total};
     }
 }
 
-// ------------------------------------------------- many rows: prompts
+// ------------------------------------------ rows with their blocks shared
 // A workgroup has W * NR tiles of 16 rows and two sets of W waves, which have
 // the same rows, NR tiles to a wave, and take the blocks in turn: a long row's
 // blocks follow each other half as often, and each SIMD has a wave of either
@@ -523,12 +547,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
 // heads of 128 are 32 MFMAs of 16 cycles and about 210 other instructions of 4
 // (64 conversions of codes, 80 to 90 for 32 rows' weights), and little of the
 // two runs at once.  A prompt of 2048 with 32 heads of 128 takes 57 us, 600
-// TFLOP/s, one of 8192 691 us, 796.  NR = 2 fills the registers for D = 128
-// (with 3, 48 values spill: the same prompts take 79 and 798 us); for D = 64
-// four tiles fit, which take 98 -> 76 us for 4096 rows of 20 heads.  Codes that
-// are converted once on their way to LDS, where they take twice the room, take
-// 65 instead of 61 us for the prompt (when measured), waves that read the cache
-// themselves without LDS 64 to 69.
+// TFLOP/s.  NR = 2 fills the registers for D = 128 (with 3, 48 values spill:
+// 79 us); for D = 64 four tiles fit, but take 76 against 72 us for 4096 rows of
+// 20 heads, as there are fewer waves.  Codes that are converted once on their
+// way to LDS, where they take twice the room, take 65 instead of 61 us for the
+// prompt (when measured).
 template <int D, int NR, int W>
 __global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(AttentionArgs a) {
     constexpr int kTileThreads = 2 * 64 * W;
@@ -787,8 +810,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
     for (int k = 0; k < kAhead; ++k)
         if (y + PARTS * k < plan.splits) ahead[k] = src[(y + PARTS * k) * LANES];
     const KvSequence s = kv_sequence(a.kv, b);
-    const int all_rows = s.rows * a.group, rr0 = group * 16;
-    const int rows = rr0 + 16 < all_rows ? 16 : all_rows - rr0;
+    const int all_rows = s.rows * a.group, rr0 = group * plan.group_rows;
+    const int rows = rr0 + plan.group_rows < all_rows ? plan.group_rows : all_rows - rr0;
     if (in_group >= rows || !is_split(plan, group, rows)) return;
     floatx4 acc = {0, 0, 0, 0};
     float top = ml.x, total = 0.0f;
@@ -825,13 +848,30 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 }
 
 // ------------------------------------------------------------------ launch
-// attention_tiles_kernel needs enough groups of rows to fill the chip, as it
-// does not split their blocks: from 1.5 groups of 64 rows a compute unit on it
-// takes less time (at 400: 800 rows of 800 tokens 23.0 against 26.0 us; 8 times
-// 100 rows 12.8 against 20.4; the prompt of 2048 62 against 86), below that
-// attention_kernel does, which splits (at 256: 512 rows over 8192 tokens 113
-// against 141 us; 400 rows of 20 heads over 3000 17.9 against 34.2).
-constexpr int64_t kManyWork = 384;
+// Which kernel: attention_tiles_kernel where there are enough groups of 64 rows
+// to fill the chip, as it does not split their blocks, and these are not so
+// many that its waits for other waves weigh more than its shorter start:
+//   D = 128: 512 groups, 4 blocks a row (4 times 256 rows) 15 against 22 us,
+//     16 blocks (1024 rows) 24 against 26, 32 (2048 rows) 57 against 61, 48
+//     (1024 rows over 2048 tokens) 45 against 42, 240 (over 8192) 165 against
+//     145; 256 groups, 8 blocks 15 against 13;
+//   D = 64: 640 groups, 32 blocks (2048 rows) 28.6 against 28.1, 1280 groups,
+//     64 blocks 72 against 77, 320 groups, 240 blocks 118 against 79; 440
+//     groups, 11 blocks 16 against 14.
+constexpr int64_t many_groups(int D) { return D == 64 ? 450 : 384; }
+constexpr int64_t kManyBytes = 40 * 128;   // of blocks times D
+
+// Two tiles a wave of attention_kernel where the tiles' blocks are many:
+//   D = 128: 16 thousand (64 rows over 4096 tokens) 19.9 against 18.3 us with
+//     one, 63 thousand (256 rows) 30.7 against 31.6, 126 thousand (over 8192)
+//     55 against 62, 249 thousand (512 rows) 84 against 114;
+//   D = 64: 80 thousand 37.6 against 41.8 us, 131 thousand 41.3 each, 190
+//     thousand 56 against 55, 307 thousand 79 against 106.
+// (With few tiles in many splits each, one a wave takes no longer: 5 rows over
+// 131072 tokens 52 against 57 us.)
+constexpr int64_t many_blocks(int D) { return D == 64 ? 200000 : 40000; }
+constexpr int64_t kManyTiles = 64;
+
 // Blocks of a workgroup of attention_kernel at most, for a sequence much longer
 // than the others of its batch: 8192 tokens, at which a workgroup takes about
 // 50 us and the join of two splits another 5.
@@ -848,34 +888,39 @@ constexpr int64_t kSaved = 22;
 constexpr int64_t kMinChunk = kWaves;
 
 // Into how many parts attention_kernel's `work` groups have their blocks split:
-// a workgroup for every compute unit (more of them take longer to join: 32
-// sequences up to 8191 tokens 60.6 us in 256, 68.7 in 512), and no chunk over
-// kMaxChunk until sixteen groups a compute unit even out their lengths (and
-// would need much workspace).
+// no more than a workgroup for every compute unit (32 sequences up to 8191
+// tokens 60 us in 256, 62 in 512; 20 sequences of 4000 28 us in 160, 36 in 320),
+// and no chunk over kMaxChunk until sixteen groups a compute unit even out
+// their lengths (and would need much workspace).
 int64_t splits_wanted(int64_t work, int64_t blocks) {
     if (blocks <= kSaved) return 1;
-    const int64_t fill = (256 + work - 1) / work, least = (blocks + kMaxChunk - 1) / kMaxChunk;
+    const int64_t fill = work < 256 ? 256 / work : 1, least = (blocks + kMaxChunk - 1) / kMaxChunk;
     return work >= 4096 || least < fill ? fill : least;
 }
 
-Plan plan_of(const AttentionArgs &a) {
+Plan plan_of(const AttentionArgs &a, int D) {
     const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group, sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
+    // blocks that a row reads
+    int64_t seen = a.max_length - (a.max_rows < a.max_length ? a.max_rows : a.max_length) / 2;
+    if (a.window && a.window < seen) seen = a.window;
+    const int64_t each = seen / kKvBlock + 1;
     Plan p;
     p.chunk = p.splits = 1;
-    if (rows > 32 && (rows + 63) / 64 * sets >= kManyWork) {
-        // half the rows where no more than one workgroup a compute unit would
-        // be there (1024 tokens: 25.8 against 31.0 us)
-        p.group_rows = (rows + 127) / 128 * sets <= 256 ? 64 : 128;
+    if (rows > 32 && (rows + 63) / 64 * sets >= many_groups(D) && each * D < kManyBytes) {
+        // 128 rows where that leaves two workgroups a compute unit, with some
+        // blocks (2048 rows 57 against 60 us, 4 times 512 33 against 30)
+        p.group_rows = D == 128 && (rows + 127) / 128 * sets >= 512 && each >= 16 ? 128 : 64;
         p.rows_held = 0;
         p.groups = static_cast<int>((rows + p.group_rows - 1) / p.group_rows);
         return p;
     }
-    p.group_rows = 16;
-    p.rows_held = rows < 16 ? static_cast<int>(rows) : 16;
-    p.groups = static_cast<int>((rows + 15) / 16);
+    const int64_t tiles = (rows + 15) / 16 * sets;
+    p.group_rows = rows > 16 && tiles >= kManyTiles && tiles * each >= many_blocks(D) ? 32 : 16;
+    p.rows_held = rows < p.group_rows ? static_cast<int>(rows) : p.group_rows;
+    p.groups = static_cast<int>((rows + p.group_rows - 1) / p.group_rows);
     int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
     if (a.window) {   // no group reads more than its rows and their window
-        const int64_t reach = (static_cast<int64_t>(a.window) + 16 / a.group + kKvBlock) / kKvBlock + 1;
+        const int64_t reach = (static_cast<int64_t>(a.window) + p.group_rows / a.group + kKvBlock) / kKvBlock + 1;
         if (reach < blocks) blocks = reach;
     }
     const int64_t splits = splits_wanted(p.groups * sets, blocks);
@@ -889,20 +934,17 @@ Plan plan_of(const AttentionArgs &a) {
 
 template <int D>
 hipError_t launch(const AttentionArgs &a, hipStream_t s) {
-    const Plan p = plan_of(a);
+    const Plan p = plan_of(a, D);
     int grid_groups = p.groups;   // the kernels loop where a launch cannot hold them all
     if (static_cast<int64_t>(grid_groups) * p.splits > 65535) grid_groups = 65535 / p.splits;
     const dim3 grid(a.kv.kv_heads, grid_groups * p.splits, a.kv.batch);
     if (p.group_rows == 16)
-        hipLaunchKernelGGL((attention_kernel<D>), grid, dim3(64 * kWaves), 0, s, a, p);
+        hipLaunchKernelGGL((attention_kernel<D, 1>), grid, dim3(64 * kWaves), 0, s, a, p);
+    else if (p.group_rows == 32)
+        hipLaunchKernelGGL((attention_kernel<D, 2>), grid, dim3(64 * kWaves), 0, s, a, p);
     else if (p.group_rows == 64)
         hipLaunchKernelGGL((attention_tiles_kernel<D, 2, 2>), grid, dim3(256), 0, s, a);
-    else if (D == 64 && static_cast<int64_t>(p.groups) * a.kv.kv_heads * a.kv.batch > 512)
-        // more workgroups than fit at once, two a compute unit, so that their
-        // lengths even out: 3 times 1000 rows of 24 heads (576) 28 against 37
-        // us, but twice 2048 rows of 16 heads (512) 54 against 43
-        hipLaunchKernelGGL((attention_tiles_kernel<D, D == 64 ? 4 : 2, D == 64 ? 2 : 4>), grid, dim3(256), 0, s, a);
-    else
+    else if constexpr (D == 128)
         hipLaunchKernelGGL((attention_tiles_kernel<D, 2, 4>), grid, dim3(512), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
@@ -912,19 +954,26 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Enough for any window: fewer blocks may be split into more parts, but never
-// into more than there are for all of them with the smallest chunk, nor than
-// fill the chip or keep the chunks at kMaxChunk.
+// Which kernel runs and in how many parts depends on the window, which may be
+// any: the most that some window takes.  With less to see a launch may have one
+// tile a group instead of two, or none of attention_tiles_kernel's instead of
+// it; fewer blocks may be split into more parts, but never into more than there
+// are for all of them with the smallest chunk, nor than fill the chip or keep
+// the chunks at kMaxChunk.
 size_t attention_workspace(const AttentionArgs &a, int head_dim) {
-    const Plan p = plan_of(a);
-    if (p.group_rows != 16) return 0;
-    const int64_t sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
+    const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group, sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
     const int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
-    int64_t splits = splits_wanted(p.groups * sets, blocks);
-    if (splits > (blocks + kMinChunk - 1) / kMinChunk) splits = (blocks + kMinChunk - 1) / kMinChunk;
-    if (splits == 1) return 0;
-    const size_t parts = static_cast<size_t>(p.groups) * p.rows_held * sets * splits;   // as in partials()
-    return ((parts * 2 + 3) / 4 * 4 + parts * head_dim) * sizeof(float);
+    size_t most = 0;
+    for (int64_t tile = 16; tile <= 32; tile += 16) {
+        const int64_t held = rows < tile ? rows : tile, groups = (rows + tile - 1) / tile;
+        int64_t splits = splits_wanted(groups * sets, blocks);
+        if (splits > (blocks + kMinChunk - 1) / kMinChunk) splits = (blocks + kMinChunk - 1) / kMinChunk;
+        if (splits <= 1) continue;
+        const size_t parts = static_cast<size_t>(groups) * held * sets * splits;   // as in partials()
+        const size_t bytes = ((parts * 2 + 3) / 4 * 4 + parts * head_dim) * sizeof(float);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s) {

@@ -17,10 +17,10 @@ from gpu_helpers import say
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(autouse=True, params=["chosen", "groups of 64", "groups of 128", "few groups of 128"])
+@pytest.fixture(autouse=True, params=["chosen", "32 rows", "32 rows, split", "64 rows", "128 rows"])
 def kernel(request, monkeypatch):
     """Every test runs with the kernel that its sizes choose, and with those for
-    many rows: max_rows, which shapes a launch, changes no result."""
+    more rows: max_rows and max_length, which shape a launch, change no result."""
     monkeypatch.setattr(sys.modules[__name__], "KERNEL", request.param)
 
 
@@ -28,15 +28,10 @@ KERNEL = "chosen"
 
 
 def _hint(sets, group):
-    """max_rows that brings a launch of `sets` sequences x kv heads to the kernel."""
-    if KERNEL == "groups of 128":
-        return 1 << 19
-    if KERNEL == "few groups of 128":      # from 257 to 512 of them
-        return max(1, 128 * max(1, 512 // sets) // group)
-    if KERNEL == "groups of 64":      # at least 384 groups of 64 rows, at most 256 of 128
-        k = max(1, 256 // sets)
-        return max(1, 64 * (2 * k - 1) // group)
-    return None
+    """max_rows and max_length that bring a launch of `sets` sequences x kv heads
+    to the kernel (128 rows: with heads of 128 and a window that leaves them)."""
+    return {"32 rows": (1 << 19, 1 << 20), "32 rows, split": (1100 // (sets * group) + 17, 1 << 20),
+            "64 rows": (1 << 19, 64), "128 rows": (1 << 19, 1024)}[KERNEL]
 
 
 def _setup(lengths, rows, heads, group, D, seed, garbage=True, blocks=None):
@@ -60,8 +55,8 @@ def _setup(lengths, rows, heads, group, D, seed, garbage=True, blocks=None):
 
 def _call(c, table, q, lengths, rows, *, cu=True, dtype=torch.float32, **kw):
     bounds = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32) if cu is True else cu
-    if "max_rows" not in kw and KERNEL != "chosen":
-        kw["max_rows"] = _hint(c.heads * len(lengths), q.shape[1] // c.heads)
+    if not {"max_rows", "max_length"} & kw.keys() and KERNEL != "chosen":
+        kw["max_rows"], kw["max_length"] = _hint(c.heads * len(lengths), q.shape[1] // c.heads)
     out = q4.kv_attention(dev(q.reshape(q.shape[0], -1), torch.bfloat16), device_cache(c), dev(table),
                           dev(np.array(lengths, dtype=np.int32)), dev(bounds), dtype=dtype, **kw)
     return out.double().cpu().numpy().reshape(q.shape)
@@ -112,16 +107,26 @@ def test_windows(window, rows):
     _check([260], [rows], window=window, seed=5)
 
 
+def test_windows_that_leave_each_kernel():
+    """A window that cuts, and yet chooses the launch as the hints do."""
+    _check([900, 700], [200, 90], window=600, heads=1, group=3, D=128, seed=26)
+    _check([3400], [70], window=3000, heads=2, group=2, D=64, seed=26)
+
+
 def test_windows_of_a_prompt_with_many_heads():
     _check([300], [300], window=70, heads=3, group=1, D=64, seed=6)
     _check([300], [200], window=70, heads=1, group=5, D=128, seed=6)
 
 
 def test_sizes_that_choose_the_kernels_for_many_rows():
-    """384 and 400 groups of 64 rows, and 684 of 128, by their own number."""
+    """By their own number: 1368, 384 and 400 groups of 64 rows, and 32 of 32
+    rows whose blocks are many."""
+    if KERNEL != "chosen":
+        return
     _check([150] * 9, [150] * 9, heads=19, group=3, seed=21)
-    _check([65] * 8, [65] * 8, heads=24, group=1, seed=21)
-    _check([40, 33], [33, 33], heads=8, group=48, seed=21)
+    _check([65] * 8, [65] * 8, heads=24, group=1, D=128, seed=21)
+    _check([40, 33], [33, 33], heads=8, group=48, D=128, seed=21)
+    _check([21000], [64], heads=1, group=16, D=128, max_length=21000, seed=21)
 
 
 def test_scale():
