@@ -285,7 +285,7 @@ __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 
 // How a launch is shaped: groups of `group_rows` rows of a sequence and kv
 // head, and the split of their blocks.
 struct Plan {
-    int group_rows;      // 16 or 32, or 64 or 128 in attention_tiles_kernel
+    int group_rows;      // 16 or 32, or 64 in attention_tiles_kernel
     int groups;          // of the sequence with most rows
     int rows_held;       // rows of a group that the workspace has room for
     int chunk, splits;
@@ -345,10 +345,12 @@ __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total)
 // waves: one token over 64 takes 4.2 us, over 512 5.8 and over 1505, in 12
 // splits, 7.7, of which the join of the splits is 2.5.
 //
-// For many rows it is the issue of instructions, as in attention_tiles_kernel:
-// 2048 rows over 16384 tokens with 32 heads of 128 take 550 us, 937 TFLOP/s.
-// Two tiles share what a wave converts (one tile: 1086 us), and fill the
-// registers.
+// For many rows it is the issue of instructions: a wave's 32 rows and a block of
+// heads of 128 are 32 MFMAs of 16 cycles and about 210 other instructions of 4
+// (64 conversions of codes, 80 to 90 for 32 rows' weights), and little of the
+// two runs at once.  A prompt of 2048 with 32 heads of 128 takes 55 us, 627
+// TFLOP/s, 2048 rows over 16384 tokens 525 us, 982.  Two tiles share what a wave
+// converts (one tile: 75 and 1086 us), and fill the registers.
 constexpr int kWaves = 4;
 
 template <int D, int NR>
@@ -356,6 +358,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
     constexpr int kRows = 16 * NR;
     constexpr int KQ = D / 32;   // k slices of the first product
     constexpr int DT = D / 16;   // 16-dimension tiles of the output
+    // Codes of the next block: in registers of their own while this one is
+    // worked on, or, with two tiles, in this one's as soon as a product has read
+    // them (with 20 spilled values otherwise; one tile, which reads more than it
+    // computes, takes 61.6 instead of 59.5 us so for 32 sequences up to 8191)
+    constexpr int BUFS = NR == 1 ? 2 : 1;
     __shared__ float part_m[kWaves][16], part_l[kWaves][16];
     __shared__ floatx4 part_o[kWaves][DT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -394,17 +401,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
             load_q<D>(a, row[n].at, g4, q[n]);
             tile[n].clear();
         }
-        // a block's ids and exponents are read 64 blocks at a time, one a lane,
-        // its codes one block ahead
+        // a block's ids and exponents are read 64 blocks at a time, one a lane
         for (int first = blk0 + wave; first < blk1; first += 64 * kWaves) {
             const int count = (blk1 - first + kWaves - 1) / kWaves, blocks = count < 64 ? count : 64;
             int my_id = guess;
             if (first != guessed) my_id = kv_block_id(a.kv, b, first + lane * kWaves);
             const int my_exps =
                 reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(my_id < 0 ? 0 : my_id) * a.kv.kv_heads + head];
-            u32x4 codes[2][2 * KQ];
+            u32x4 codes[BUFS][2 * KQ];
             // (past the end the last block is read again)
-            auto fetch = [&](int i, u32x4(&to)[2 * KQ]) {
+            auto fetch = [&](int i, int from, int end, u32x4(&to)[2 * KQ]) {   // K's slices are [0, KQ), V's follow
                 const int id = __builtin_amdgcn_readlane(my_id, i < blocks ? i : blocks - 1);
                 const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
                 // a base that is the same for all lanes and a lane's offset,
@@ -414,17 +420,20 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                 uint32_t at = lane * 16;
                 asm volatile("" : "+v"(at));
 #pragma unroll
-                for (int j = 0; j < 2 * KQ; ++j)
-                    to[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(src + 1024 * j + at));
+                for (int j = from; j < end; ++j) {
+                    const u32x4 *p = reinterpret_cast<const u32x4 *>(src + 1024 * j + at);
+                    // many rows read a block again (2048 over 8192 tokens: 257 against 268 us)
+                    to[j] = NR == 1 ? __builtin_nontemporal_load(p) : *p;
+                }
             };
-            fetch(0, codes[0]);
+            fetch(0, 0, 2 * KQ, codes[0]);
             asm volatile("" ::"v"(my_exps));   // has arrived before the loop, whose waits are for codes alone
-            for (int i0 = 0; i0 < blocks; i0 += 2) {
+            for (int i0 = 0; i0 < blocks; i0 += BUFS) {
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int u = 0; u < BUFS; ++u) {
                     const int i = i0 + u;
                     if (i >= blocks) break;
-                    fetch(i + 1, codes[u ^ 1]);
+                    if constexpr (BUFS == 2) fetch(i + 1, 0, 2 * KQ, codes[u ^ 1]);
                     u32x4(&kc)[2 * KQ] = codes[u];
                     const BlockScales scales = block_scales(a, __builtin_amdgcn_readlane(my_exps, i));
                     const bool known = __builtin_amdgcn_readlane(my_id, i) >= 0;
@@ -445,6 +454,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
 #pragma unroll
                             for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){kNan, kNan, kNan, kNan};
                     }
+                    if constexpr (BUFS == 1) fetch(i + 1, 0, KQ, kc);
                     const int start = (first + i * kWaves) * kKvBlock;
                     if (start < all_lo || start + kKvBlock - 1 > p_first) {   // some row does not see some token
                         const int tok = start + 4 * g4;
@@ -483,6 +493,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                         for (int n = 0; n < NR; ++n)
                             tile[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[n], tile[n].o[d], 0, 0, 0);
                     }
+                    if constexpr (BUFS == 1) fetch(i + 1, KQ, 2 * KQ, kc);
                 }
             }
         }
@@ -533,27 +544,26 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
 }
 
 // ------------------------------------------ rows with their blocks shared
-// A workgroup has W * NR tiles of 16 rows and two sets of W waves, which have
-// the same rows, NR tiles to a wave, and take the blocks in turn: a long row's
-// blocks follow each other half as often, and each SIMD has a wave of either
-// set to run while the other waits.  All waves walk the blocks together, two
-// at a time: each loads its part of a pair one pair early into registers, and
-// the pair passes to all waves through LDS in the cache's own order (a lane's
-// 16 bytes are its operand slices, so the reads have no bank conflicts).
-// Every slice that a wave converts feeds NR products.  Groups with the most
-// tokens start first.
+// A workgroup has kShared waves' rows, two tiles to a wave, and two sets of
+// such waves, which have the same rows and take the blocks in turn.  All waves
+// walk the blocks together, two at a time: each loads its part of a pair one
+// pair early into registers, and the pair passes to all waves through LDS in
+// the cache's own order (a lane's 16 bytes are its operand slices, so the reads
+// have no bank conflicts).  Groups with the most tokens start first.
 //
-// What bounds it is the issue of instructions: a wave's 32 rows and a block of
-// heads of 128 are 32 MFMAs of 16 cycles and about 210 other instructions of 4
-// (64 conversions of codes, 80 to 90 for 32 rows' weights), and little of the
-// two runs at once.  A prompt of 2048 with 32 heads of 128 takes 57 us, 600
-// TFLOP/s.  NR = 2 fills the registers for D = 128 (with 3, 48 values spill:
-// 79 us); for D = 64 four tiles fit, but take 76 against 72 us for 4096 rows of
-// 20 heads, as there are fewer waves.  Codes that are converted once on their
-// way to LDS, where they take twice the room, take 65 instead of 61 us for the
-// prompt (when measured).
-template <int D, int NR, int W>
-__global__ __launch_bounds__(2 * 64 * W, 2) void attention_tiles_kernel(AttentionArgs a) {
+// Against attention_kernel with two tiles a workgroup has twice the rows for one
+// start and one join of waves, but its waves wait for each other at every pair:
+// it is for many rows that see little.  What bounds it is the issue of
+// instructions and that start: 8 times 512 rows of 32 heads of 128 take 55 us,
+// 315 TFLOP/s, 8 times 1024 146, 471.  Measured when it ran prompts of 2048 (57
+// us): three tiles a wave 79 (48 values spill); codes that are converted once on
+// their way to LDS, where they take twice the room, 65 against 61; four waves a
+// set 57 against 60.
+constexpr int kShared = 2;
+
+template <int D>
+__global__ __launch_bounds__(2 * 64 * kShared, 2) void attention_tiles_kernel(AttentionArgs a) {
+    constexpr int NR = 2, W = kShared;
     constexpr int kTileThreads = 2 * 64 * W;
     constexpr int kSegment = kTileThreads;   // blocks whose ids and exponents are held in LDS
     constexpr int KQ = D / 32, DT = D / 16;
@@ -848,27 +858,31 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 }
 
 // ------------------------------------------------------------------ launch
-// Which kernel: attention_tiles_kernel where there are enough groups of 64 rows
-// to fill the chip, as it does not split their blocks, and these are not so
-// many that its waits for other waves weigh more than its shorter start:
-//   D = 128: 512 groups, 4 blocks a row (4 times 256 rows) 15 against 22 us,
-//     16 blocks (1024 rows) 24 against 26, 32 (2048 rows) 57 against 61, 48
-//     (1024 rows over 2048 tokens) 45 against 42, 240 (over 8192) 165 against
-//     145; 256 groups, 8 blocks 15 against 13;
-//   D = 64: 640 groups, 32 blocks (2048 rows) 28.6 against 28.1, 1280 groups,
-//     64 blocks 72 against 77, 320 groups, 240 blocks 118 against 79; 440
-//     groups, 11 blocks 16 against 14.
-constexpr int64_t many_groups(int D) { return D == 64 ? 450 : 384; }
-constexpr int64_t kManyBytes = 40 * 128;   // of blocks times D
+// Which kernel.  Rows see `each` blocks.  attention_tiles_kernel where there
+// are enough groups of 64 rows to fill the chip, as it does not split their
+// blocks, and where these are few, the fewer the fewer groups there are
+// (heads of 128, us against attention_kernel with two tiles):
+//   groups  256: 3 blocks 8.7 / 8.9, 5 blocks 10.5 / 9.7
+//   groups  512: 5 blocks 15.2 / 17.6, 17 blocks 24.3 / 22.7
+//   groups 1024: 9 blocks 32.5 / 34.9, 33 blocks 57 / 55
+//   groups 2048: 9 blocks 55 / 66, 17 blocks 75 / 77;  4096: 17 blocks 146 / 157
+// and heads of 64:
+//   groups 440: 12 blocks 16 / 13;  880: 12 blocks 20.4 / 20.9
+//   groups 1280: 9 blocks 24.5 / 25.7, 64 blocks 72 / 66
+bool share_blocks(int64_t groups64, int64_t each) { return groups64 >= 384 && each < 24 && each < 8 + groups64 / 128; }
 
-// Two tiles a wave of attention_kernel where the tiles' blocks are many:
-//   D = 128: 16 thousand (64 rows over 4096 tokens) 19.9 against 18.3 us with
-//     one, 63 thousand (256 rows) 30.7 against 31.6, 126 thousand (over 8192)
-//     55 against 62, 249 thousand (512 rows) 84 against 114;
-//   D = 64: 80 thousand 37.6 against 41.8 us, 131 thousand 41.3 each, 190
-//     thousand 56 against 55, 307 thousand 79 against 106.
-// (With few tiles in many splits each, one a wave takes no longer: 5 rows over
-// 131072 tokens 52 against 57 us.)
+// attention_kernel has two tiles a wave where there are more tiles than fit on
+// the chip at once with one (two workgroups a compute unit for heads of 128,
+// four for heads of 64; us with one / two):
+//   D = 128: 512 tiles, 5 blocks 6.6 / 7.3, 28 blocks 11.3 each; 1024 tiles, 3
+//     blocks 10.6 / 8.9, 9 blocks 12.6 / 10.4; 2048 tiles, 17 blocks 29 / 23
+//   D = 64: 640 tiles, 9 blocks 6.0 / 7.3; 1280 tiles, 5 blocks 8.7 / 8.9, 17
+//     blocks 11.4 / 11.8; 1536 tiles, 5 blocks 9.2 / 8.4
+// or, of at least kManyTiles, where these have many blocks:
+//   D = 128: 256 tiles, 126 blocks 19 / 25, 254 blocks 35.5 / 35.4, 510 blocks
+//     74 / 56; 512 tiles, 60 blocks 16.6 / 16.4, 250 blocks 56 / 47
+//   D = 64: 320 tiles, 252 blocks 41 / 38; 768 tiles, 248 blocks 48 / 52
+constexpr int64_t tiles_at_once(int D) { return D == 64 ? 1024 : 512; }
 constexpr int64_t many_blocks(int D) { return D == 64 ? 200000 : 40000; }
 constexpr int64_t kManyTiles = 64;
 
@@ -906,16 +920,15 @@ Plan plan_of(const AttentionArgs &a, int D) {
     const int64_t each = seen / kKvBlock + 1;
     Plan p;
     p.chunk = p.splits = 1;
-    if (rows > 32 && (rows + 63) / 64 * sets >= many_groups(D) && each * D < kManyBytes) {
-        // 128 rows where that leaves two workgroups a compute unit, with some
-        // blocks (2048 rows 57 against 60 us, 4 times 512 33 against 30)
-        p.group_rows = D == 128 && (rows + 127) / 128 * sets >= 512 && each >= 16 ? 128 : 64;
+    if (rows > 32 && share_blocks((rows + 63) / 64 * sets, each)) {
+        p.group_rows = 64;
         p.rows_held = 0;
-        p.groups = static_cast<int>((rows + p.group_rows - 1) / p.group_rows);
+        p.groups = static_cast<int>((rows + 63) / 64);
         return p;
     }
     const int64_t tiles = (rows + 15) / 16 * sets;
-    p.group_rows = rows > 16 && tiles >= kManyTiles && tiles * each >= many_blocks(D) ? 32 : 16;
+    const bool two = tiles > tiles_at_once(D) || (tiles >= kManyTiles && tiles * each >= many_blocks(D));
+    p.group_rows = rows > 16 && two ? 32 : 16;
     p.rows_held = rows < p.group_rows ? static_cast<int>(rows) : p.group_rows;
     p.groups = static_cast<int>((rows + p.group_rows - 1) / p.group_rows);
     int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
@@ -942,10 +955,8 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
         hipLaunchKernelGGL((attention_kernel<D, 1>), grid, dim3(64 * kWaves), 0, s, a, p);
     else if (p.group_rows == 32)
         hipLaunchKernelGGL((attention_kernel<D, 2>), grid, dim3(64 * kWaves), 0, s, a, p);
-    else if (p.group_rows == 64)
-        hipLaunchKernelGGL((attention_tiles_kernel<D, 2, 2>), grid, dim3(256), 0, s, a);
-    else if constexpr (D == 128)
-        hipLaunchKernelGGL((attention_tiles_kernel<D, 2, 4>), grid, dim3(512), 0, s, a);
+    else
+        hipLaunchKernelGGL((attention_tiles_kernel<D>), grid, dim3(2 * 64 * kShared), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     hipLaunchKernelGGL((attention_join_kernel<D>), dim3(p.rows_held, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);

@@ -17,7 +17,7 @@ from gpu_helpers import say
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(autouse=True, params=["chosen", "32 rows", "32 rows, split", "64 rows", "128 rows"])
+@pytest.fixture(autouse=True, params=["chosen", "32 rows", "32 rows, split", "64 rows"])
 def kernel(request, monkeypatch):
     """Every test runs with the kernel that its sizes choose, and with those for
     more rows: max_rows and max_length, which shape a launch, change no result."""
@@ -29,9 +29,9 @@ KERNEL = "chosen"
 
 def _hint(sets, group):
     """max_rows and max_length that bring a launch of `sets` sequences x kv heads
-    to the kernel (128 rows: with heads of 128 and a window that leaves them)."""
+    to the kernel (without a window)."""
     return {"32 rows": (1 << 19, 1 << 20), "32 rows, split": (1100 // (sets * group) + 17, 1 << 20),
-            "64 rows": (1 << 19, 64), "128 rows": (1 << 19, 1024)}[KERNEL]
+            "64 rows": (1 << 19, 64)}[KERNEL]
 
 
 def _setup(lengths, rows, heads, group, D, seed, garbage=True, blocks=None):
@@ -119,13 +119,14 @@ def test_windows_of_a_prompt_with_many_heads():
 
 
 def test_sizes_that_choose_the_kernels_for_many_rows():
-    """By their own number: 1368, 384 and 400 groups of 64 rows, and 32 of 32
-    rows whose blocks are many."""
+    """By their own number: 1368, 384 and 400 groups of 64 rows, 272 of 32, and 32
+    of 32 whose blocks are many."""
     if KERNEL != "chosen":
         return
     _check([150] * 9, [150] * 9, heads=19, group=3, seed=21)
     _check([65] * 8, [65] * 8, heads=24, group=1, D=128, seed=21)
     _check([40, 33], [33, 33], heads=8, group=48, D=128, seed=21)
+    _check([90], [90], heads=17, group=6, D=128, seed=21)
     _check([21000], [64], heads=1, group=16, D=128, max_length=21000, seed=21)
 
 
