@@ -192,17 +192,19 @@ PyObject *kv_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int out_code = type_code(type, "dtype");
     at::Tensor out = output(a[12], "out", q.sizes(), type, dev);
     const int64_t need = static_cast<int64_t>(q4_kv_attention_workspace(&c, &b, heads));
-    at::Tensor ws;
-    if (const at::Tensor *given = optional(a[14], "workspace")) {
-        address(given, "workspace", at::kByte, dev);
-        TORCH_CHECK_VALUE(given->numel() >= need, "workspace must hold ", need, " bytes");
-        ws = *given;
-    } else if (need) {
-        ws = at::empty({need}, at::TensorOptions().dtype(at::kByte).device(dev));
-    }
     const c10::hip::HIPGuard guard(dev.index());
-    check(q4_kv_attention(&c, &b, src, heads, scale, window, out.data_ptr(), out_code, ws.defined() ? ws.data_ptr() : nullptr,
-                          ws.defined() ? static_cast<size_t>(ws.numel()) : 0,
+    c10::DataPtr own;   // goes back to the allocator, for work on this stream after the call's
+    void *ws = nullptr;
+    int64_t ws_bytes = need;
+    if (const at::Tensor *given = optional(a[14], "workspace")) {
+        ws = address(given, "workspace", at::kByte, dev);
+        ws_bytes = given->numel();
+        TORCH_CHECK_VALUE(ws_bytes >= need, "workspace must hold ", need, " bytes");
+    } else if (need) {
+        own = c10::GetAllocator(dev.type())->allocate(need);
+        ws = own.get();
+    }
+    check(q4_kv_attention(&c, &b, src, heads, scale, window, out.data_ptr(), out_code, ws, static_cast<size_t>(ws_bytes),
                           c10::hip::getCurrentHIPStream(dev.index()).stream()),
           "q4_kv_attention");
     return THPVariable_Wrap(std::move(out));
