@@ -3,12 +3,13 @@
 // stream, and the call.
 //
 // It is native because these operators are short: a decode step's norm runs
-// for 3 us, and the same checks written in Python with a ctypes call take 13 us
-// (this: 5 us).  Nothing is computed here.
+// for 2.5 us, and the same checks written in Python with a ctypes call take 13 us
+// (this: 4.5 us, launch included).  Nothing is computed here.
 
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -67,7 +68,7 @@ at::Tensor output(PyObject *given, const char *name, at::IntArrayRef shape, at::
         has_shape(t, name, shape);
         return *t;
     }
-    return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+    return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));   // at::empty without its dispatch
 }
 
 int64_t integer(PyObject *o) {
