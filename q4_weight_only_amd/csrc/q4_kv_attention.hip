@@ -285,7 +285,8 @@ __device__ __forceinline__ bool past(const KvView &kv, int pos) { return pos >= 
 // How a launch is shaped: groups of `group_rows` rows of a sequence and kv
 // head, and the split of their blocks.
 struct Plan {
-    int group_rows;      // 16 or 32, or 64 in attention_tiles_kernel
+    int group_rows;      // 16 or 32
+    int waves;           // of a workgroup
     int groups;          // of the sequence with most rows
     int rows_held;       // rows of a group that the workspace has room for
     int chunk, splits;
@@ -329,10 +330,9 @@ __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total)
     return past(kv, pos) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
 }
 
-// ------------------------------------ rows with a workgroup's waves apart
 // A workgroup has NR tiles of 16 rows (of rows x heads of the group) of one
-// sequence and kv head, and one chunk of its blocks; its four waves take every
-// fourth block with all the rows, so a block's codes go from memory to the
+// sequence and kv head, and one chunk of its blocks; its W waves take the
+// blocks in turn with all the rows, so a block's codes go from memory to the
 // registers of one wave, as its operand slices, and nowhere else, and no wave
 // waits for another before the end.  Groups with the most tokens start first.
 //
@@ -342,19 +342,22 @@ __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total)
 // nothing is read twice (99 -> 91 us for the former, 80 -> 74 for the latter
 // when measured).  Short caches are bound by what follows from each other:
 // length and block ids together, codes, a block's products, the join of the
-// waves: one token over 64 takes 4.2 us, over 512 5.8 and over 1505, in 12
+// waves: one token over 64 takes 4.1 us, over 512 5.7 and over 1505, in 12
 // splits, 7.7, of which the join of the splits is 2.5.
 //
 // For many rows it is the issue of instructions: a wave's 32 rows and a block of
-// heads of 128 are 32 MFMAs of 16 cycles and about 210 other instructions of 4
-// (64 conversions of codes, 80 to 90 for 32 rows' weights), and little of the
-// two runs at once.  A prompt of 2048 with 32 heads of 128 takes 55 us, 627
-// TFLOP/s, 2048 rows over 16384 tokens 525 us, 982.  Two tiles share what a wave
-// converts (one tile: 75 and 1086 us), and fill the registers.
-constexpr int kWaves = 4;
+// heads of 128 are 32 MFMAs of 16 cycles and about 170 other instructions of 2
+// to 8 (64 conversions of codes, 16 exponentials), and little of the two runs at
+// once: 1070 cycles.  A prompt of 2048 with 32 heads of 128 takes 48 us, 714
+// TFLOP/s, one of 8192 556 us, 989.  Two tiles share what a wave converts (one
+// tile: 75 us for the former), and fill the registers.  Workgroups of two waves
+// start and join less often for what they compute.  Blocks that pass through
+// LDS to eight waves with 64 or 128 rows, converted there or not, took 57 to 65
+// us: their waves wait for each other.
+constexpr int kWaves = 4;   // but for many rows, see plan_of
 
-template <int D, int NR>
-__global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs a, Plan plan) {
+template <int D, int NR, int W>
+__global__ __launch_bounds__(64 * W, 2) void attention_kernel(AttentionArgs a, Plan plan) {
     constexpr int kRows = 16 * NR;
     constexpr int KQ = D / 32;   // k slices of the first product
     constexpr int DT = D / 16;   // 16-dimension tiles of the output
@@ -363,8 +366,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
     // them (with 20 spilled values otherwise; one tile, which reads more than it
     // computes, takes 61.6 instead of 59.5 us so for 32 sequences up to 8191)
     constexpr int BUFS = NR == 1 ? 2 : 1;
-    __shared__ float part_m[kWaves][16], part_l[kWaves][16];
-    __shared__ floatx4 part_o[kWaves][DT][64];
+    __shared__ float part_m[W][16], part_l[W][16];
+    __shared__ floatx4 part_o[W][DT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g4 = lane >> 4;
     const int b = blockIdx.z, head = blockIdx.x;
@@ -372,7 +375,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
     // the ids of the blocks that the wave has where there is no window, read
     // before the length is known
     const int guessed = split * plan.chunk + wave;
-    const int guess = kv_block_id(a.kv, b, guessed + lane * kWaves);
+    const int guess = kv_block_id(a.kv, b, guessed + lane * W);
     const KvSequence s = kv_sequence(a.kv, b);
     const int grid_groups = plan.splits == 1 ? gridDim.y : gridDim.y / plan.splits;
     const int all_rows = s.rows * a.group;
@@ -402,10 +405,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
             tile[n].clear();
         }
         // a block's ids and exponents are read 64 blocks at a time, one a lane
-        for (int first = blk0 + wave; first < blk1; first += 64 * kWaves) {
-            const int count = (blk1 - first + kWaves - 1) / kWaves, blocks = count < 64 ? count : 64;
+        for (int first = blk0 + wave; first < blk1; first += 64 * W) {
+            const int count = (blk1 - first + W - 1) / W, blocks = count < 64 ? count : 64;
             int my_id = guess;
-            if (first != guessed) my_id = kv_block_id(a.kv, b, first + lane * kWaves);
+            if (first != guessed) my_id = kv_block_id(a.kv, b, first + lane * W);
             const int my_exps =
                 reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(my_id < 0 ? 0 : my_id) * a.kv.kv_heads + head];
             u32x4 codes[BUFS][2 * KQ];
@@ -455,7 +458,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
                             for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){kNan, kNan, kNan, kNan};
                     }
                     if constexpr (BUFS == 1) fetch(i + 1, 0, KQ, kc);
-                    const int start = (first + i * kWaves) * kKvBlock;
+                    const int start = (first + i * W) * kKvBlock;
                     if (start < all_lo || start + kKvBlock - 1 > p_first) {   // some row does not see some token
                         const int tok = start + 4 * g4;
 #pragma unroll
@@ -515,10 +518,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
             __syncthreads();
             float top = part_m[0][re];
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) top = fmaxf(top, part_m[w][re]);
-            float f[kWaves], total = 0.0f;
+            for (int w = 1; w < W; ++w) top = fmaxf(top, part_m[w][re]);
+            float f[W], total = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
+            for (int w = 0; w < W; ++w) {
                 f[w] = __builtin_amdgcn_exp2f(part_m[w][re] - top);
                 total += f[w] * part_l[w][re];
             }
@@ -528,272 +531,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attention_kernel(AttentionArgs
             const int64_t at = (partial_row(a.kv, plan, b, head, group) + 16 * n + re) * plan.splits + split;
             const float inv = inverse(a.kv, row[n].pos, total);
 #pragma unroll
-            for (int i = 0; i < DT / kWaves; ++i) {
-                const int tile_i = wave * (DT / kWaves) + i, d = 16 * tile_i + 4 * ge;
+            for (int i = 0; i < DT / W; ++i) {
+                const int tile_i = wave * (DT / W) + i, d = 16 * tile_i + 4 * ge;
                 floatx4 acc = part_o[0][tile_i][16 * ge + re] * f[0];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) acc = acc + part_o[w][tile_i][16 * ge + re] * f[w];
+                for (int w = 1; w < W; ++w) acc = acc + part_o[w][tile_i][16 * ge + re] * f[w];
                 if (!whole) *reinterpret_cast<floatx4 *>(ws.o + at * D + d) = acc;
                 else if (a.out_bf16)
                     *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row[n].at + d) = __builtin_convertvector(acc * inv, bf16x4);
                 else *reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + row[n].at + d) = acc * inv;
             }
             if (!whole && wave == 0 && ge == 0) ws.ml[at] = (floatx2){top, total};
-        }
-    }
-}
-
-// ------------------------------------------ rows with their blocks shared
-// A workgroup has kShared waves' rows, two tiles to a wave, and two sets of
-// such waves, which have the same rows and take the blocks in turn.  All waves
-// walk the blocks together, two at a time: each loads its part of a pair one
-// pair early into registers, and the pair passes to all waves through LDS in
-// the cache's own order (a lane's 16 bytes are its operand slices, so the reads
-// have no bank conflicts).  Groups with the most tokens start first.
-//
-// Against attention_kernel with two tiles a workgroup has twice the rows for one
-// start and one join of waves, but its waves wait for each other at every pair:
-// it is for many rows that see little.  What bounds it is the issue of
-// instructions and that start: 8 times 512 rows of 32 heads of 128 take 55 us,
-// 315 TFLOP/s, 8 times 1024 146, 471.  Measured when it ran prompts of 2048 (57
-// us): three tiles a wave 79 (48 values spill); codes that are converted once on
-// their way to LDS, where they take twice the room, 65 against 61; four waves a
-// set 57 against 60.
-constexpr int kShared = 2;
-
-template <int D>
-__global__ __launch_bounds__(2 * 64 * kShared, 2) void attention_tiles_kernel(AttentionArgs a) {
-    constexpr int NR = 2, W = kShared;
-    constexpr int kTileThreads = 2 * 64 * W;
-    constexpr int kSegment = kTileThreads;   // blocks whose ids and exponents are held in LDS
-    constexpr int KQ = D / 32, DT = D / 16;
-    constexpr int kRows = W * 16 * NR;
-    constexpr int kBlock16 = 2 * KQ * 64;                  // 16-byte pieces of a block
-    constexpr int kLoads = 2 * kBlock16 / kTileThreads;    // a thread's of a pair
-    __shared__ u32x4 stage[2][2][kBlock16];
-    __shared__ u32x4 nans[2][2][kBlock16 / 2];   // nan_bytes of the V codes, where there are some (nan_block)
-    __shared__ int32_t nan_block[2][2];
-    __shared__ int32_t ids[kSegment];
-    __shared__ uint16_t exps[kSegment];
-    __shared__ floatx2 other[W][64];    // the second set's m and l
-    const int lane = threadIdx.x & 63;
-    const int wave8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wave = wave8 % W, set = wave8 / W;
-    const int r = lane & 15, g4 = lane >> 4;
-    const int b = blockIdx.z, head = blockIdx.x;
-    // the ids of the first segment where there is no window, read before the
-    // length is known
-    const int guess = kv_block_id(a.kv, b, threadIdx.x);
-    const KvSequence s = kv_sequence(a.kv, b);
-    const int all_rows = s.rows * a.group;
-    const int groups = (all_rows + kRows - 1) / kRows;
-    for (int back = blockIdx.y; back < groups; back += gridDim.y) {
-        const int group = groups - 1 - back;
-        const int rr0 = group * kRows, rr1 = rr0 + kRows < all_rows ? rr0 + kRows : all_rows;
-        const int p_first = s.pos0 + row_of(a, rr0), p_last = s.pos0 + row_of(a, rr1 - 1);
-        const Span sp = span_of(a.kv, p_first, p_last, a.window, 0, 1);
-        const int blk0 = sp.first, blk1 = sp.last;
-        // the wave's own rows
-        const int wr0 = rr0 + wave * (16 * NR), wr1 = wr0 + 16 * NR < rr1 ? wr0 + 16 * NR : rr1;
-        const int w_first = s.pos0 + row_of(a, wr0);
-        const int w_last = wr0 < rr1 ? s.pos0 + row_of(a, wr1 - 1) : -1;
-        const int wave_lo = a.window ? w_first - a.window + 1 : 0;
-        // the first tokens that all rows and that any row of the group see
-        const int group_lo = a.window ? p_last - a.window + 1 : 0, any_lo = a.window ? p_first - a.window + 1 : 0;
-
-        const int first_id = blk0 == 0 ? guess : kv_block_id(a.kv, b, blk0 + threadIdx.x);
-        LaneRow row[NR];
-        bf16x8 q[NR][KQ];
-        Tile<D> tile[NR];
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            row[n] = lane_row(a, s, head, wr0 + 16 * n + r, all_rows, D);
-            load_q<D>(a, row[n].at, g4, q[n]);
-            tile[n].clear();
-        }
-        for (int seg = blk0; seg < blk1; seg += kSegment) {
-            const int blocks = blk1 - seg < kSegment ? blk1 - seg : kSegment;
-            __syncthreads();   // the last segment's ids and stages have been read
-            if (threadIdx.x < 4) (&nan_block[0][0])[threadIdx.x] = -1;
-            // (past the segment's end the blocks of what follows, or none, are read)
-            const int id = seg == blk0 ? first_id : kv_block_id(a.kv, b, seg + threadIdx.x);
-            ids[threadIdx.x] = id;
-            __syncthreads();
-            u32x4 ahead[kLoads];
-            auto held = [&](int i) { return i < kSegment ? i : kSegment - 1; };
-            // the thread's part of a pair is of its first or second block
-            auto in_pair = [&](int j) { return (static_cast<int>(threadIdx.x) + kTileThreads * j) / kBlock16; };
-            // a fetch uses ids that were taken from LDS one pair before
-            int next_id[kLoads];
-            auto take_ids = [&](int pair) {
-#pragma unroll
-                for (int j = 0; j < kLoads; ++j) next_id[j] = ids[held(2 * pair + in_pair(j))];
-            };
-            auto fetch = [&](int pair) {
-#pragma unroll
-                for (int j = 0; j < kLoads; ++j) {
-                    const int id = __builtin_amdgcn_readfirstlane(next_id[j]);
-                    const int64_t plane = (static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head) * 2;
-                    const uint8_t *src = a.kv.data + plane * (kKvBlock * D);
-                    uint32_t at = (threadIdx.x + kTileThreads * j) % kBlock16 * 16;
-                    asm volatile("" : "+v"(at));   // as in attention_kernel
-                    ahead[j] = *reinterpret_cast<const u32x4 *>(src + at);
-                }
-                take_ids(pair + 1);
-            };
-            // some row of the group does not see some token of the pair
-            auto partly_seen = [&](int pair) {
-                const int first = (seg + 2 * pair) * kKvBlock;
-                return first < group_lo || first + 2 * kKvBlock - 1 > p_first;
-            };
-            // Puts the pair that was fetched into its stage for all waves.
-            auto put = [&](int pair, int buf) {
-                if (partly_seen(pair)) {
-                    // what no row sees may hold anything, and what is not a
-                    // number must not meet a weight of 0
-#pragma unroll
-                    for (int j = 0; j < kLoads; ++j) {
-                        const int which = in_pair(j), at = (threadIdx.x + kTileThreads * j) % kBlock16 - KQ * 64;
-                        if (at < 0) continue;
-                        const int tok = (seg + 2 * pair + which) * kKvBlock + 4 * g4;
-                        const uint32_t in0 = bytes_in(tok, any_lo, p_last + 1), in1 = bytes_in(tok + 16, any_lo, p_last + 1);
-                        u32x4 v = ahead[j], n;
-                        v.x &= in0;
-                        v.y &= in1;
-                        v.z &= in0;
-                        v.w &= in1;
-                        uint32_t bad = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            n[k] = nan_bytes(v[k]);
-                            bad |= n[k];
-                            v[k] &= ~((n[k] >> 7) * 0xFFu);
-                        }
-                        nans[buf][which][at] = n;
-                        if (bad) nan_block[buf][which] = pair;
-                        ahead[j] = v;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < kLoads; ++j) (&stage[buf][0][0])[threadIdx.x + kTileThreads * j] = ahead[j];
-            };
-            // One barrier a pair, between the softmax and the second product:
-            // before it the waves put the next pair into the other stage and
-            // take the last of this one's codes, after it they take the next
-            // one's first, which the product hides.
-            u32x4 kw[KQ], vw[KQ];
-            take_ids(0);
-            fetch(0);
-            exps[threadIdx.x] =
-                reinterpret_cast<const uint16_t *>(a.kv.exps)[static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head];
-            put(0, 0);
-            fetch(1);
-            __syncthreads();
-            int id_here = ids[set], e2_here = exps[set];
-#pragma unroll
-            for (int k = 0; k < KQ; ++k) kw[k] = stage[0][set][64 * k + lane];
-            const int pairs = (blocks + 1) / 2;
-            for (int p0 = 0; p0 < pairs; p0 += 2) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int pair = p0 + u, i = 2 * pair + set;
-                    put(pair + 1, u ^ 1);
-                    fetch(pair + 2);
-                    const int id = __builtin_amdgcn_readfirstlane(id_here), e2 = __builtin_amdgcn_readfirstlane(e2_here);
-                    id_here = ids[held(i + 2)];
-                    e2_here = exps[held(i + 2)];
-                    const int start = (seg + i) * kKvBlock;
-                    // not past the end, and something that the wave's rows see
-                    const bool work = i < blocks && start <= w_last && start + kKvBlock > wave_lo;
-                    halfx8 wf[NR];
-                    if (work) {
-                        const BlockScales scales = block_scales(a, e2);
-#pragma unroll
-                        for (int k = 0; k < KQ; ++k) vw[k] = stage[u][set][64 * (KQ + k) + lane];
-                        floatx4 st[NR][2];
-#pragma unroll
-                        for (int tt = 0; tt < 2; ++tt) {
-#pragma unroll
-                            for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){0, 0, 0, 0};
-#pragma unroll
-                            for (int k = 0; k < KQ; ++k) {
-                                const u32x4 w = kw[tt * (KQ / 2) + k / 2];
-                                const bf16x8 kf = k % 2 ? codes_bf16(w.z, w.w) : codes_bf16(w.x, w.y);
-#pragma unroll
-                                for (int n = 0; n < NR; ++n)
-                                    st[n][tt] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[n][k], st[n][tt], 0, 0, 0);
-                            }
-                            if (id < 0)
-#pragma unroll
-                                for (int n = 0; n < NR; ++n) st[n][tt] = (floatx4){kNan, kNan, kNan, kNan};
-                        }
-                        if (partly_seen(pair)) {   // as put() decided
-                            const int tok = start + 4 * g4;
-#pragma unroll
-                            for (int n = 0; n < NR; ++n) hide_unseen(st[n], tok, row[n].lo, row[n].seen);
-                            if (__builtin_amdgcn_readfirstlane(nan_block[u][set]) == pair) {
-#pragma unroll
-                                for (int n = 0; n < NR; ++n) {
-                                    const halfx8 seen = seen_tokens(tok, row[n].lo, row[n].seen);
-#pragma unroll
-                                    for (int d = 0; d < DT; ++d) {
-                                        const u32x4 x = nans[u][set][64 * (d / 2) + lane];
-                                        tile[n].mark_nans(d, (d % 2 ? x.z : x.x) >> 7, (d % 2 ? x.w : x.y) >> 7, seen);
-                                    }
-                                }
-                            }
-                        }
-                        block_weights<D, NR>(tile, st, scales, wf);
-                    }
-                    __syncthreads();
-#pragma unroll
-                    for (int k = 0; k < KQ; ++k) kw[k] = stage[u ^ 1][set][64 * k + lane];
-                    if (work) {
-#pragma unroll
-                        for (int d = 0; d < DT; ++d) {
-                            const u32x4 v = vw[d / 2];
-                            const halfx8 vf = d % 2 ? codes_f16(v.z, v.w) : codes_f16(v.x, v.y);
-#pragma unroll
-                            for (int n = 0; n < NR; ++n)
-                                tile[n].o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, wf[n], tile[n].o[d], 0, 0, 0);
-                        }
-                    }
-                }
-            }
-        }
-        int re = r, ge = g4;   // as in attention_kernel
-        asm volatile("" : "+v"(re), "+v"(ge));
-        floatx4 *pass = reinterpret_cast<floatx4 *>(&stage[0][0][0]) + wave * (DT * 64) + ge * 16 + re;
-        static_assert(sizeof(stage) >= W * DT * 64 * sizeof(floatx4), "a tile of every wave passes through the stages");
-#pragma unroll
-        for (int n = 0; n < NR; ++n) {
-            const float sum = row_sum(tile[n].l);
-            __syncthreads();   // the stages, and the tile before, have been read
-            if (set == 1) {
-#pragma unroll
-                for (int d = 0; d < DT; ++d) pass[64 * d] = tile[n].o[d];
-                other[wave][lane] = (floatx2){tile[n].m, sum};
-            }
-            __syncthreads();
-            if (set == 1 || wr0 + 16 * n + re >= all_rows) continue;
-            const floatx2 ml = other[wave][lane];
-            const float top = fmaxf(tile[n].m, ml.x);
-            const float f0 = __builtin_amdgcn_exp2f(tile[n].m - top), f1 = __builtin_amdgcn_exp2f(ml.x - top);
-            const float total = f0 * sum + f1 * ml.y;
-            const float inv = inverse(a.kv, row[n].pos, total);
-            floatx4 acc[DT];
-#pragma unroll
-            for (int i = 0; i < DT; ++i) acc[i] = pass[64 * i];
-#pragma unroll
-            for (int i = 0; i < DT; ++i) acc[i] = (tile[n].o[i] * f0 + acc[i] * f1) * inv;
-            if (a.out_bf16) {
-                bf16x4 *to = reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + row[n].at + 4 * ge);
-#pragma unroll
-                for (int i = 0; i < DT; ++i) to[4 * i] = __builtin_convertvector(acc[i], bf16x4);
-                continue;
-            }
-            float *to = static_cast<float *>(a.out) + row[n].at;
-#pragma unroll
-            for (int i = 0; i < DT; ++i) *reinterpret_cast<floatx4 *>(to + 16 * i + 4 * ge) = acc[i];
         }
     }
 }
@@ -858,20 +606,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 }
 
 // ------------------------------------------------------------------ launch
-// Which kernel.  Rows see `each` blocks.  attention_tiles_kernel where there
-// are enough groups of 64 rows to fill the chip, as it does not split their
-// blocks, and where these are few, the fewer the fewer groups there are
-// (heads of 128, us against attention_kernel with two tiles):
-//   groups  256: 3 blocks 8.7 / 8.9, 5 blocks 10.5 / 9.7
-//   groups  512: 5 blocks 15.2 / 17.6, 17 blocks 24.3 / 22.7
-//   groups 1024: 9 blocks 32.5 / 34.9, 33 blocks 57 / 55
-//   groups 2048: 9 blocks 55 / 66, 17 blocks 75 / 77;  4096: 17 blocks 146 / 157
-// and heads of 64:
-//   groups 440: 12 blocks 16 / 13;  880: 12 blocks 20.4 / 20.9
-//   groups 1280: 9 blocks 24.5 / 25.7, 64 blocks 72 / 66
-bool share_blocks(int64_t groups64, int64_t each) { return groups64 >= 384 && each < 24 && each < 8 + groups64 / 128; }
-
-// attention_kernel has two tiles a wave where there are more tiles than fit on
+// Two tiles a wave where there are more tiles than fit on
 // the chip at once with one (two workgroups a compute unit for heads of 128,
 // four for heads of 64; us with one / two):
 //   D = 128: 512 tiles, 5 blocks 6.6 / 7.3, 28 blocks 11.3 each; 1024 tiles, 3
@@ -885,6 +620,20 @@ bool share_blocks(int64_t groups64, int64_t each) { return groups64 >= 384 && ea
 constexpr int64_t tiles_at_once(int D) { return D == 64 ? 1024 : 512; }
 constexpr int64_t many_blocks(int D) { return D == 64 ? 200000 : 40000; }
 constexpr int64_t kManyTiles = 64;
+
+// Two waves a workgroup instead of four where there are many workgroups for
+// the blocks that each reads, so that they still even out (workgroups, blocks:
+// us with four / two):
+//   D = 128: 512, 9: 10.4 / 11.8; 1024, 17: 22.7 / 22.3; 1200, 19: 29 / 25; 1313,
+//     95: 77 / 90; 2048, 9: 35 / 27; 2048, 33: 54 / 48; 2048, 121: 142 / 160;
+//     4096, 65: 162 / 152; 8192, 129: 581 / 556
+//   D = 64: 1280, 33: 24 / 29; 2048, 33: 36 / 40; 2560, 65: 67 / 70; 2560, 9: 25 /
+//     22; 6144, 17: 65 / 57
+// and sooner where a window makes them equal:
+//   D = 128: 1400, 24: 39 / 40; 2048, 32: 58 / 53; D = 64: 960, 24: 19.7 / 18.1
+bool two_waves(int64_t groups, int64_t each, bool equal, int D) {
+    return groups >= 768 && each * (D == 64 ? 100 : 25) < groups * (equal ? 4 : 1);
+}
 
 // Blocks of a workgroup of attention_kernel at most, for a sequence much longer
 // than the others of its batch: 8192 tokens, which a workgroup reads in 30 to 85
@@ -919,18 +668,12 @@ Plan plan_of(const AttentionArgs &a, int D) {
     if (a.window && a.window < seen) seen = a.window;
     const int64_t each = seen / kKvBlock + 1;
     Plan p;
-    p.chunk = p.splits = 1;
-    if (rows > 32 && share_blocks((rows + 63) / 64 * sets, each)) {
-        p.group_rows = 64;
-        p.rows_held = 0;
-        p.groups = static_cast<int>((rows + 63) / 64);
-        return p;
-    }
     const int64_t tiles = (rows + 15) / 16 * sets;
     const bool two = tiles > tiles_at_once(D) || (tiles >= kManyTiles && tiles * each >= many_blocks(D));
     p.group_rows = rows > 16 && two ? 32 : 16;
     p.rows_held = rows < p.group_rows ? static_cast<int>(rows) : p.group_rows;
     p.groups = static_cast<int>((rows + p.group_rows - 1) / p.group_rows);
+    p.waves = p.group_rows == 32 && two_waves(p.groups * sets, each, a.window && seen == a.window, D) ? 2 : kWaves;
     int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
     if (a.window) {   // no group reads more than its rows and their window
         const int64_t reach = (static_cast<int64_t>(a.window) + p.group_rows / a.group + kKvBlock) / kKvBlock + 1;
@@ -952,11 +695,11 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
     if (static_cast<int64_t>(grid_groups) * p.splits > 65535) grid_groups = 65535 / p.splits;
     const dim3 grid(a.kv.kv_heads, grid_groups * p.splits, a.kv.batch);
     if (p.group_rows == 16)
-        hipLaunchKernelGGL((attention_kernel<D, 1>), grid, dim3(64 * kWaves), 0, s, a, p);
-    else if (p.group_rows == 32)
-        hipLaunchKernelGGL((attention_kernel<D, 2>), grid, dim3(64 * kWaves), 0, s, a, p);
+        hipLaunchKernelGGL((attention_kernel<D, 1, kWaves>), grid, dim3(64 * kWaves), 0, s, a, p);
+    else if (p.waves == kWaves)
+        hipLaunchKernelGGL((attention_kernel<D, 2, kWaves>), grid, dim3(64 * kWaves), 0, s, a, p);
     else
-        hipLaunchKernelGGL((attention_tiles_kernel<D>), grid, dim3(2 * 64 * kShared), 0, s, a);
+        hipLaunchKernelGGL((attention_kernel<D, 2, 2>), grid, dim3(64 * 2), 0, s, a, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1) return e;
     hipLaunchKernelGGL((attention_join_kernel<D>), dim3(p.rows_held, p.groups * a.kv.kv_heads, a.kv.batch), dim3(256), 0, s, a, p);
@@ -965,12 +708,11 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
 
 }  // namespace
 
-// Which kernel runs and in how many parts depends on the window, which may be
-// any: the most that some window takes.  With less to see a launch may have one
-// tile a group instead of two, or none of attention_tiles_kernel's instead of
-// it; fewer blocks may be split into more parts, but never into more than there
-// are for all of them with the smallest chunk, nor than fill the chip or keep
-// the chunks at kMaxChunk.
+// How many tiles a group has and in how many parts its blocks are depends on the
+// window, which may be any: the most that some window takes.  Fewer blocks may
+// be split into more parts, but never into more than there are for all of them
+// with the smallest chunk, nor than fill the chip or keep the chunks at
+// kMaxChunk.
 size_t attention_workspace(const AttentionArgs &a, int head_dim) {
     const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group, sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
     const int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;

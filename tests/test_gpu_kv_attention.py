@@ -17,7 +17,7 @@ from gpu_helpers import say
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(autouse=True, params=["chosen", "32 rows", "32 rows, split", "64 rows"])
+@pytest.fixture(autouse=True, params=["chosen", "32 rows", "32 rows, split", "32 rows, two waves"])
 def kernel(request, monkeypatch):
     """Every test runs with the kernel that its sizes choose, and with those for
     more rows: max_rows and max_length, which shape a launch, change no result."""
@@ -30,8 +30,8 @@ KERNEL = "chosen"
 def _hint(sets, group):
     """max_rows and max_length that bring a launch of `sets` sequences x kv heads
     to the kernel (without a window)."""
-    return {"32 rows": (1 << 19, 1 << 20), "32 rows, split": (1100 // (sets * group) + 17, 1 << 20),
-            "64 rows": (1 << 19, 64)}[KERNEL]
+    return {"32 rows": (1 << 19, 1 << 25), "32 rows, split": (1100 // (sets * group) + 17, 1 << 20),
+            "32 rows, two waves": (1 << 19, 64)}[KERNEL]
 
 
 def _setup(lengths, rows, heads, group, D, seed, garbage=True, blocks=None):
@@ -119,8 +119,8 @@ def test_windows_of_a_prompt_with_many_heads():
 
 
 def test_sizes_that_choose_the_kernels_for_many_rows():
-    """By their own number: 1368, 384 and 400 groups of 64 rows, 272 of 32, and 32
-    of 32 whose blocks are many."""
+    """By their own number: 2565, 576, 800 and 289 groups of 32 rows, and 32 whose
+    blocks are many."""
     if KERNEL != "chosen":
         return
     _check([150] * 9, [150] * 9, heads=19, group=3, seed=21)
