@@ -300,8 +300,11 @@ __device__ __forceinline__ bool is_split(const Plan &p, int group, int rows) {
 
 // Where a split's partial results of a row are in the workspace: first
 // {m, l} [row][split], then O [row][split][D], rows counted over batch, kv
-// head, group and row of the group.  A split without blocks has {kLowest, 0}
-// and no O.
+// head, group and row of the group.  A split without blocks has {kLowest,
+// kNoBlocks} and no O.  (The O of one that has blocks counts also where its l
+// or its factor is 0: what is not a number stays it.)
+constexpr float kNoBlocks = -1.0f;   // no sum of weights
+
 struct Partials {
     floatx2 *ml;
     float *o;
@@ -323,7 +326,7 @@ __device__ __forceinline__ Partials partials(const AttentionArgs &a, const Plan 
 __device__ __forceinline__ void write_empty(const AttentionArgs &a, const Plan &p, int b, int head, int group, int rows, int split) {
     const Partials ws = partials(a, p);
     const int64_t row = partial_row(a.kv, p, b, head, group);
-    for (int i = threadIdx.x; i < rows; i += blockDim.x) ws.ml[(row + i) * p.splits + split] = (floatx2){kLowest, 0.0f};
+    for (int i = threadIdx.x; i < rows; i += blockDim.x) ws.ml[(row + i) * p.splits + split] = (floatx2){kLowest, kNoBlocks};
 }
 
 __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total) {
@@ -560,7 +563,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
     const int in_group = blockIdx.x;
     const Partials ws = partials(a, plan);
     const int64_t at0 = (partial_row(a.kv, plan, b, head, group) + in_group) * plan.splits;
-    const floatx2 none = {kLowest, 0.0f};
+    const floatx2 none = {kLowest, kNoBlocks};
     floatx2 ml = lane < plan.splits ? ws.ml[at0 + lane] : none;
     const floatx4 *src = reinterpret_cast<const floatx4 *>(ws.o + at0 * D) + x;
     floatx4 ahead[kAhead];
@@ -580,14 +583,14 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
         const int n = plan.splits - i0 < 64 ? plan.splits - i0 : 64;
         if (i0 > 0) ml = lane < n ? ws.ml[at0 + i0 + lane] : none;
         // (a split without blocks has no O: what was read for it is not used)
-        const float f = ml.x == kLowest && ml.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(ml.x - top);
-        total += f * ml.y;
+        const float f = ml.y == kNoBlocks ? kNoBlocks : __builtin_amdgcn_exp2f(ml.x - top);
+        if (f != kNoBlocks) total += f * ml.y;
 #pragma unroll
         for (int k = 0; k < 64 / PARTS; ++k) {
             const int i = y + PARTS * k;
             if (PARTS * k >= n) break;   // the same for the workgroup
             const float fi = __shfl(f, i);
-            if (i < n && fi != 0.0f) acc = acc + (k < kAhead && i0 == 0 ? ahead[k % kAhead] : src[static_cast<int64_t>(i0 + i) * LANES]) * fi;
+            if (i < n && fi != kNoBlocks) acc = acc + (k < kAhead && i0 == 0 ? ahead[k % kAhead] : src[static_cast<int64_t>(i0 + i) * LANES]) * fi;
         }
     }
 #pragma unroll

@@ -1,0 +1,66 @@
+"""q4_kv_attention at the edges of its arithmetic: weights that are small beside
+another token's, factors that underflow in a join, scores that are infinite,
+huge or all equal.  Each with the launch that its sizes choose, split and not,
+and with two tiles of rows a wave."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import decoder_oracle as O
+import q4_weight_only_amd as q4
+
+from decoder_helpers import assert_close, bf16, dev, device_cache, random_table
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+
+def _setup(length, rows, heads, group, D, seed):
+    rng = np.random.default_rng(seed)
+    c = O.Cache.empty(-(-length // 32) + 1, heads, D)
+    O.fill_random(c, rng)
+    table = random_table(rng, [length], c.blocks)
+    return c, table, bf16(rng.standard_normal((rows, heads * group, D)))
+
+
+def _call(c, table, q, length, **kw):
+    say("attention values", q.shape, length, kw)
+    out = q4.kv_attention(dev(q.reshape(q.shape[0], -1), torch.bfloat16), device_cache(c), dev(table),
+                          dev(np.array([length], dtype=np.int32)), dtype=torch.float32, **kw)
+    return out.double().cpu().numpy().reshape(q.shape)
+
+
+def _put(c, table, token, which, codes, exponent=None):
+    """Codes [heads, D] of a token, and its block's exponent."""
+    i = table[0, token // 32]
+    for h in range(c.heads):
+        all_codes = c.block_codes(i, h, which).copy()
+        all_codes[token % 32] = codes[h]
+        c.put(i, h, which, all_codes, c.exps[i, h, which] if exponent is None else exponent)
+
+
+def _check(c, table, q, length, **kw):
+    got = _call(c, table, q, length, **kw)
+    want, bound = O.attention(c, q.astype(np.float64), table, [length], None, kw.get("window", 0), kw.get("scale"))
+    assert_close(got, want, bound * (1 + 2.0 ** -22) + 2.0 ** -22 * np.abs(want), "attention")
+    return got
+
+
+# the launch that the sizes choose (split for the long lengths here), an unsplit one, and two tiles of rows a wave
+HINTS = [{}, dict(max_length=32), dict(max_rows=1 << 15, max_length=32)]
+
+
+@pytest.mark.parametrize("hints", HINTS)
+@pytest.mark.parametrize("rows", [1, 9])
+def test_nan_value_in_a_part_whose_weights_underflow(rows, hints):
+    """Later keys score some hundred higher, so that 2^(m - top) of the blocks
+    before is 0 in fp32; 0 times what is not a number is not a number all the same."""
+    c, table, q = _setup(3000, rows, 2, 2, 64, 30)
+    i = table[0, 2000 // 32]
+    c.exps[i, :, 0] += 10
+    codes = np.stack([c.block_codes(table[0, 3], h, 1)[4] for h in range(2)])
+    codes[:, 7] = 0x7F
+    _put(c, table, 100, 1, codes)
+    got = _check(c, table, q, 3000, **hints)
+    assert np.isnan(got[:, :, 7]).all() and np.isfinite(got[:, :, 8]).all()
