@@ -132,9 +132,10 @@ q4_status q4_kv_append(const q4_kv_cache *cache, const q4_kv_batch *batch, const
  * q: bf16 [rows, q_heads * D], out: [rows, q_heads * D] fp32 or bf16 by
  * out_dtype (device, 16-byte aligned, contiguous).  q_heads is a multiple of
  * kv_heads, at most 64 times.  Products of q with the codes of k are exact and
- * summed in fp32, the softmax's maximum and sum are fp32; the weights are
- * rounded to fp16 for their products with the codes of v, which are summed in
- * fp32.  An output is not finite where the formula's is: a token that a row
+ * summed in fp32, the softmax's maximum and sum are fp32; the weights, times
+ * the scale of their token's v, are rounded to fp16 for their products with the
+ * codes of v, which are summed in fp32: within 2^-11 of each, or 2^-32 of the
+ * row's largest where that is more.  An output is not finite where the formula's is: a token that a row
  * does not see has no effect on it, whatever its codes are.  A token in a
  * block whose id is outside [0, num_blocks), or past table_width, counts as
  * not a number.

@@ -193,8 +193,9 @@ def attention(cache: Cache, q, table, lengths, cu=None, window=0, scale=None):
         them in fp32, D E sum|q k| scale, and of a few roundings of numbers the
         size of the score and of its distance to the maximum; 2^x itself is
         within 2 E.  It changes a weight by that factor, the weights' sum too.
-      weights: fp16, 2^-11 of each, or 2^-25 of the largest u where they are
-        below fp16's normal range;
+      weights: fp16, 2^-11 of each, or, where they are below fp16's normal
+        range, 2^-25; the largest is held at 2^7 or more, so 2^-32 of the
+        largest u;
       sums over n tokens in fp32: n E each, and a rounding per rescaling
         (at most one a block) and per join."""
     rows, hq, D = q.shape
@@ -236,7 +237,7 @@ def attention(cache: Cache, q, table, lengths, cu=None, window=0, scale=None):
                     u = p * 2.0 ** ee
                     seen = pos + 1 - lo
                     rel = 2 * dz + 2.0 ** -11 + (2 * seen + 64) * E
-                    low = 2.0 ** -25 * u.max() * (np.abs(vv) * 2.0 ** -ee[:, None]).sum(0)
+                    low = 2.0 ** -32 * u.max() * (np.abs(vv) * 2.0 ** -ee[:, None]).sum(0)
                     out[row0 + t, h] = o
                     bound[row0 + t, h] = rel * (p @ np.abs(vv)) * 1.01 + low + 1e-30
     return out, bound

@@ -5,12 +5,17 @@
 // with c = scale * log2(e), k_j and v_j the codes and eK, eV the exponents of
 // token j's block.  The kernels work with t_j = s_j + eV, the exponent of
 // token j's weight on its codes: with m at least about max_j t_j,
-//     w_j = 2^(t_j - m),   o = sum_j w_j v_j / sum_j w_j 2^-eV,
-// so the codes go into the matrix products as they are, and w, held to fp16,
-// is exact to 2^-11 wherever it matters for the result, also where the blocks'
-// scales differ widely.  m and the sums are fp32 and are carried over the
-// tokens in one pass.  m is only raised when some t_j passes it by 8: w stays
-// at most 2^8, within fp16, and most blocks need no rescaling.
+//     w_j = 2^(t_j - m + 7),   o = sum_j w_j v_j / sum_j w_j 2^-eV,
+// so the codes go into the matrix products as they are.  m and the sums are
+// fp32 and are carried over the tokens in one pass.  m is only raised when some
+// t_j passes it by 8, so that most blocks need no rescaling (by 4: a prompt of
+// 2048 49.9 us instead of 49.3, by 2: 51.8).  w is rounded to fp16 for the
+// products with V alone (bf16, as fast, would keep 8 bits of it, fp32 products
+// take many times as long): the largest is at least 2^7 and at most 2^15, so
+// w is within 2^-11 of itself down to 2^-21 of the largest, within 2^-32 of
+// the largest below, and lost below that.  Such weights matter where one token
+// leads a great many others and has values close to 0; 2^7 keeps them to a
+// 128th of what 1 would, and cancels between the two sums.
 //
 // Rows.  The rows of a sequence and the heads that share a kv head are one
 // axis: row t, head g of the group is t * group + g, so a group of heads
@@ -40,6 +45,7 @@ typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
 constexpr float kNan = __builtin_nanf("");
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kSlack = 8.0f;   // how far a score may pass m before m is raised
+constexpr float kUp = 7.0f;      // the weight of a score of m is 2^kUp; 2^(kSlack + kUp) is within fp16
 
 // Eight codes as bf16 / fp16 (exact).
 __device__ __forceinline__ bf16x8 codes_bf16(uint32_t lo, uint32_t hi) {
@@ -147,7 +153,7 @@ struct Tile {
     }
 
     __device__ __forceinline__ halfx8 weights(const floatx4 (&st)[2], float c, float ev, float inv_ev) {
-        const float shift = ev - m;
+        const float shift = ev - m + kUp;
         float w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __builtin_amdgcn_exp2f(fmaf(st[i / 4][i % 4], c, shift));

@@ -64,3 +64,23 @@ def test_nan_value_in_a_part_whose_weights_underflow(rows, hints):
     _put(c, table, 100, 1, codes)
     got = _check(c, table, q, 3000, **hints)
     assert np.isnan(got[:, :, 7]).all() and np.isfinite(got[:, :, 8]).all()
+
+
+@pytest.mark.parametrize("hints", HINTS)
+@pytest.mark.parametrize("D,rows,lead", [(64, 1, 17.5), (128, 2, 17.5), (64, 40, 17.5), (128, 40, 14.0), (64, 1, 20.0)])
+def test_one_leading_token_over_a_long_tail(D, rows, lead, hints):
+    """Token 5 leads the others by `lead` nats and has values of zero: what is
+    left is the sum of 20000 weights of about 2^-25 of its own."""
+    length = 20000
+    c, table, q = _setup(length, rows, 1, 2, D, 31)
+    rng = np.random.default_rng(32)
+    q = np.broadcast_to(q[:1, :1], q.shape).copy()     # one query, so that one key leads all of them
+    q[...] = bf16(np.sign(q) * 0.5)
+    for b in range(table.shape[1] - 1):     # values with a common mean, so that the tail does not cancel
+        c.put(table[0, b], 0, 1, O.encode(1.0 + 0.25 * rng.standard_normal((32, D))), 0)
+        c.put(table[0, b], 0, 0, O.encode(0.5 * rng.standard_normal((32, D))), 0)
+    key = O.encode(np.sign(q[0, 0]) * lead / (0.5 * D ** 0.5))
+    _put(c, table, 5, 0, key[None])
+    _put(c, table, 5, 1, np.zeros((1, D), dtype=np.uint8))
+    got = _check(c, table, q, length, **hints)
+    assert (got > 0).all()
