@@ -335,8 +335,11 @@ __device__ __forceinline__ void write_empty(const AttentionArgs &a, const Plan &
     for (int i = threadIdx.x; i < rows; i += blockDim.x) ws.ml[(row + i) * p.splits + split] = (floatx2){kLowest, kNoBlocks};
 }
 
+// What a row's sums are multiplied by: a row without a position sees nothing
+// and gives 0.  Every other one sees its own token, so a total of 0 means
+// scores of -inf alone, whose softmax is not a number (0 times infinity).
 __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total) {
-    return past(kv, pos) ? __builtin_nanf("") : total == 0.0f ? 0.0f : 1.0f / total;
+    return pos < 0 ? 0.0f : past(kv, pos) ? kNan : 1.0f / total;
 }
 
 // A workgroup has NR tiles of 16 rows (of rows x heads of the group) of one

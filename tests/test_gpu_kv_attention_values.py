@@ -84,3 +84,23 @@ def test_one_leading_token_over_a_long_tail(D, rows, lead, hints):
     _put(c, table, 5, 1, np.zeros((1, D), dtype=np.uint8))
     got = _check(c, table, q, length, **hints)
     assert (got > 0).all()
+
+
+@pytest.mark.parametrize("hints", HINTS)
+@pytest.mark.parametrize("length,rows", [(1, 1), (40, 3), (40, 40), (3000, 2)])
+def test_scores_that_are_all_minus_infinity(length, rows, hints):
+    """exp(-inf - -inf) is not a number; only a row that sees nothing gives 0."""
+    c, table, q = _setup(length, rows, 1, 2, 64, 33)
+    for b in range(-(-length // 32)):
+        codes = c.block_codes(table[0, b], 0, 0).copy()
+        codes[:, 3] = 0x30 + rng_bits(b)
+        c.put(table[0, b], 0, 0, codes, c.exps[table[0, b], 0, 0])
+    q[0, 0, 3] = -np.inf
+    got = _check(c, table, q, length, **hints)
+    assert np.isnan(got[0, 0]).all() and np.isfinite(got[0, 1]).all()
+    empty = _call(c, table, q, 0, **hints)
+    assert not empty.any()
+
+
+def rng_bits(b):
+    return np.random.default_rng(b).integers(0, 16, 32).astype(np.uint8)
