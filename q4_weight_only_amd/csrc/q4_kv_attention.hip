@@ -46,6 +46,8 @@ constexpr float kNan = __builtin_nanf("");
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kSlack = 8.0f;   // how far a score may pass m before m is raised
 constexpr float kUp = 7.0f;      // the weight of a score of m is 2^kUp; 2^(kSlack + kUp) is within fp16
+// The rounding of an m below this moves a weight by 2^(2^-4) at most, which fp16 has room for.
+constexpr float kHuge = 1048576.0f;
 
 // Eight codes as bf16 / fp16 (exact).
 __device__ __forceinline__ bf16x8 codes_bf16(uint32_t lo, uint32_t hi) {
@@ -119,14 +121,15 @@ __device__ __forceinline__ BlockScales block_scales(const AttentionArgs &a, int 
 }
 
 // One 16-row tile's running state in a wave: lane (r, g4) holds, for row r, the
-// reference m, its share of the sum l, and dimensions 16 i + 4 g4 + j of O.
+// reference m, the largest score that leaves it (none where m is huge: see
+// block_weights), its share of the sum l, and dimensions 16 i + 4 g4 + j of O.
 template <int D>
 struct Tile {
-    float m, l;
+    float m, limit, l;
     floatx4 o[D / 16];
 
     __device__ __forceinline__ void clear() {
-        m = kLowest;
+        m = limit = kLowest;
         l = 0.0f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i] = (floatx4){0, 0, 0, 0};
@@ -147,13 +150,13 @@ struct Tile {
         const float raised = fmaxf(m, row_max(top));
         const float f = __builtin_amdgcn_exp2f(m - raised);
         m = raised;
+        limit = fabsf(m) > kHuge && m != kLowest ? -__builtin_inff() : m + kSlack;
         l *= f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i] = o[i] * f;
     }
 
-    __device__ __forceinline__ halfx8 weights(const floatx4 (&st)[2], float c, float ev, float inv_ev) {
-        const float shift = ev - m + kUp;
+    __device__ __forceinline__ halfx8 weights(const floatx4 (&st)[2], float c, float shift, float inv_ev) {
         float w[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __builtin_amdgcn_exp2f(fmaf(st[i / 4][i % 4], c, shift));
@@ -190,22 +193,33 @@ __device__ __forceinline__ halfx8 seen_tokens(int first, int lo, uint32_t seen) 
 }
 
 // A block's weights for all of a wave's tiles; m is raised where some score
-// passes it by kSlack.
+// passes it by kSlack.  As a rule a weight's exponent is one fma of the score
+// with eV - m + kUp, whose rounding is that of m.  Where m is raised, or so large
+// that this would matter, the scores are rounded as m was before m is taken from
+// them: the largest is m itself then.
 template <int D, int NR>
-__device__ __forceinline__ void block_weights(Tile<D> (&tile)[NR], const floatx4 (&st)[NR][2], const BlockScales &e,
+__device__ __forceinline__ void block_weights(Tile<D> (&tile)[NR], floatx4 (&st)[NR][2], const BlockScales &e,
                                               halfx8 (&wf)[NR]) {
-    float top[NR];
+    float top[NR], shift[NR], c = e.c;
     bool over = false;
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
         top[n] = tile[n].top(st[n], e.c, e.ev);
-        over |= top[n] > tile[n].m + kSlack;
+        over |= top[n] > tile[n].limit;
+        shift[n] = e.ev - tile[n].m + kUp;
     }
-    if (__any(over))
+    if (__any(over)) {
 #pragma unroll
-        for (int n = 0; n < NR; ++n) tile[n].raise(top[n]);
+        for (int n = 0; n < NR; ++n) {
+            tile[n].raise(top[n]);
 #pragma unroll
-    for (int n = 0; n < NR; ++n) wf[n] = tile[n].weights(st[n], e.c, e.ev, e.inv_ev);
+            for (int i = 0; i < 8; ++i) st[n][i / 4][i % 4] = fmaf(st[n][i / 4][i % 4], c, e.ev) - tile[n].m;
+            shift[n] = kUp;
+        }
+        c = 1.0f;
+    }
+#pragma unroll
+    for (int n = 0; n < NR; ++n) wf[n] = tile[n].weights(st[n], c, shift[n], e.inv_ev);
 }
 
 // Which row of q a lane has, and what it sees.

@@ -104,3 +104,34 @@ def test_scores_that_are_all_minus_infinity(length, rows, hints):
 
 def rng_bits(b):
     return np.random.default_rng(b).integers(0, 16, 32).astype(np.uint8)
+
+
+@pytest.mark.parametrize("hints", HINTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("power", [12, 20, 26, 30, 60])
+def test_huge_scores(power, sign, D, hints):
+    """Scores of about 2^power.  A row that sees one token gives its value, and
+    one whose tokens' scores lie far apart the value of the largest: here they
+    are 1, 2, .. 80 times one score (or, negative, the first token's is the
+    largest)."""
+    rows = 80
+    c, table, q = _setup(rows, rows, 1, 1, D, 34)
+    q[...] = bf16(np.full(q.shape, 2.0 ** (power / 2)))
+    for b in range(3):
+        n = np.arange(32 * b + 1, 32 * b + 33)
+        for j in range(32):      # sum over d of codes with the value n: exact in e4m3 as a sum of two
+            codes = np.zeros(D)
+            codes[0], codes[1] = n[j] // 8 * 8, n[j] % 8
+            c_codes = c.block_codes(table[0, b], 0, 0).copy()
+            c_codes[j] = O.encode(sign * codes)
+            c.put(table[0, b], 0, 0, c_codes, power // 2)
+    got = _call(c, table, q, rows, **hints)
+    k = np.array([O.VALUES[c.block_codes(table[0, t // 32], 0, 0)[t % 32]].sum() for t in range(rows)])
+    assert np.array_equal(k, sign * np.arange(1, rows + 1))
+    v = np.array([O.VALUES[c.block_codes(table[0, t // 32], 0, 1)[t % 32]] * 2.0 ** int(c.exps[table[0, t // 32], 0, 1])
+                  for t in range(rows)])
+    want = v if sign > 0 else np.broadcast_to(v[:1], v.shape)
+    # the next weight is 2^-(2^power / sqrt(D)) of the largest, none that fp32 holds; what is left is the
+    # weight's rounding to fp16, which the sum does not have, and two roundings
+    assert_close(got[:, 0], want, (2.0 ** -11 + 2.0 ** -22) * np.abs(want), "huge scores")
