@@ -132,8 +132,11 @@ q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, co
     a.group = static_cast<int32_t>(q_heads / cache->kv_heads);
     a.group_inverse = a.group > 1 ? static_cast<uint32_t>(((uint64_t(1) << 32) + a.group - 1) / a.group) : 0;
     a.scale_log2 = scale * 1.44269504088896340736f;
-    // the kernels give a token that is not seen a score of -inf * |scale|
-    if (fabsf(a.scale_log2) < 1e-20f) a.scale_log2 = 1e-20f;
+    // The kernels give a token that is not seen a score of -inf * |scale| * 2^eK,
+    // so that product is held to fp32's normal numbers: 2^-94, with the smallest
+    // eK of -32, which is 0 to any q . k below 2^70.
+    constexpr float least = 0x1p-94f;
+    if (fabsf(a.scale_log2) < least) a.scale_log2 = least;
     a.window = static_cast<int32_t>(window);
     a.out_bf16 = out_dtype == Q4_BF16;
     a.max_rows = static_cast<int32_t>(batch->max_rows);

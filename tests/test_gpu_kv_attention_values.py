@@ -135,3 +135,11 @@ def test_huge_scores(power, sign, D, hints):
     # the next weight is 2^-(2^power / sqrt(D)) of the largest, none that fp32 holds; what is left is the
     # weight's rounding to fp16, which the sum does not have, and two roundings
     assert_close(got[:, 0], want, (2.0 ** -11 + 2.0 ** -22) * np.abs(want), "huge scores")
+
+
+@pytest.mark.parametrize("hints", HINTS)
+@pytest.mark.parametrize("rows", [1, 50])
+def test_scale_of_zero_weighs_all_alike(rows, hints):
+    """Also where q . k is large."""
+    c, table, q = _setup(70, rows, 2, 2, 64, 35)
+    _check(c, table, bf16(q * 2.0 ** 60), 70, scale=0.0, **hints)
