@@ -141,7 +141,10 @@ q4_status q4_kv_append(const q4_kv_cache *cache, const q4_kv_batch *batch, const
  * not a number.
  *
  * workspace: device, 16-byte aligned, q4_kv_attention_workspace bytes for the
- * same batch (0: may be NULL), its content free before and after.
+ * same batch (0: may be NULL; never more than 2^18 * (head_dim + 2), 34 MB for
+ * heads of 128), its content free before and after.  A max_length or max_rows
+ * larger than the sequences' costs time (the splits that it asks for have
+ * nothing to do, and are joined) and workspace.
  */
 size_t q4_kv_attention_workspace(const q4_kv_cache *cache, const q4_kv_batch *batch, int64_t q_heads);
 q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, const void *q, int64_t q_heads,

@@ -148,7 +148,8 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, len
 
     lengths and cu_rows as for kv_append; max_rows and max_length, the most
     rows and the largest length, shape the launch (None: what the tensors'
-    shapes allow).  scale: of q . k (None: head_dim ** -0.5); window > 0: the
+    shapes allow, which costs time where the table is much wider than the
+    longest sequence).  scale: of q . k (None: head_dim ** -0.5); window > 0: the
     last `window` tokens only.  A row without tokens gives 0.  workspace: a
     uint8 device tensor kept by the caller, of kv_attention_workspace() bytes;
     None takes one from torch's allocator for the call."""

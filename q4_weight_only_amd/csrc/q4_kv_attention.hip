@@ -661,9 +661,9 @@ bool two_waves(int64_t groups, int64_t each, bool equal, int D) {
     return groups >= 768 && each * (D == 64 ? 100 : 25) < groups * (equal ? 4 : 1);
 }
 
-// Blocks of a workgroup of attention_kernel at most, for a sequence much longer
-// than the others of its batch: 8192 tokens, which a workgroup reads in 30 to 85
-// us, as the others leave it room.
+// Blocks of a workgroup of attention_kernel at most, where the workspace has room,
+// for a sequence much longer than the others of its batch: 8192 tokens, which a
+// workgroup reads in 30 to 85 us, as the others leave it room.
 constexpr int64_t kMaxChunk = 256;
 
 // A wave takes 0.43 us a block where it does not wait for memory (the products,
@@ -676,15 +676,28 @@ constexpr int64_t kMaxChunk = 256;
 constexpr int64_t kSaved = 22;
 constexpr int64_t kMinChunk = kWaves;
 
-// Into how many parts attention_kernel's `work` groups have their blocks split:
-// no more than a workgroup for every compute unit (32 sequences up to 8191
-// tokens 60 us in 256, 62 in 512; 20 sequences of 4000 28 us in 160, 36 in 320),
-// and no chunk over kMaxChunk until sixteen groups a compute unit even out
-// their lengths (and would need much workspace).
-int64_t splits_wanted(int64_t work, int64_t blocks) {
+// Rows of partial results that a launch may write, which is what splits cost
+// beside the join: at most 34 MB of workspace for heads of 128.  (32 heads on 8,
+// D = 128, us and MB with 32768 / 65536 / 131072 rows / no limit:
+//   512 rows over 131072 tokens 1280, 17 / 1204, 34 / 1225, 68 / 1355, 136
+//   2048 rows over them 4640, 0 / 4520, 0 / 4640, 68 / 5340, 545
+//   2048 rows of a prompt in a table for 131072 tokens 62, 0 / 61, 0 / 179, 68 / 364, 545
+//   one sequence of 131072 among 255 of 500 211, 17 / 185, 34 / 230, 68 / 231, 68
+//   one among 511 of 300 361, 17 / 244, 34 / 298, 68; unsplit 613
+//   one among 99 of 500, 5 rows each 414, 17 / 235, 33 / 153, 67 / 154, 213
+//   700 rows over 32768 449, 0 / 454, 23 / 419, 47 / 426, 47
+//   600 sequences of 5000 to 20000 2260, 0 / 2360, 30 / 2360, 30; unsplit 2260)
+constexpr int64_t kMaxPartialRows = 65536;
+
+// Into how many parts attention_kernel's `work` groups of `held` rows have their
+// blocks split: no more than a workgroup for every compute unit (32 sequences up
+// to 8191 tokens 60 us in 256, 62 in 512; 20 sequences of 4000 28 us in 160, 36
+// in 320), or else no chunk over kMaxChunk as far as kMaxPartialRows allows it.
+int64_t splits_wanted(int64_t work, int64_t held, int64_t blocks) {
     if (blocks <= kSaved) return 1;
     const int64_t fill = work < 256 ? 256 / work : 1, least = (blocks + kMaxChunk - 1) / kMaxChunk;
-    return work >= 4096 || least < fill ? fill : least;
+    const int64_t room = kMaxPartialRows / (work * held), parts = least < room ? least : room;
+    return parts < fill ? fill : parts;
 }
 
 Plan plan_of(const AttentionArgs &a, int D) {
@@ -705,7 +718,7 @@ Plan plan_of(const AttentionArgs &a, int D) {
         const int64_t reach = (static_cast<int64_t>(a.window) + p.group_rows / a.group + kKvBlock) / kKvBlock + 1;
         if (reach < blocks) blocks = reach;
     }
-    const int64_t splits = splits_wanted(p.groups * sets, blocks);
+    const int64_t splits = splits_wanted(p.groups * sets, p.rows_held, blocks);
     int64_t chunk = (blocks + splits - 1) / splits;
     if (chunk < kMinChunk) chunk = kMinChunk;
     if (blocks - chunk < kSaved + p.rows_held * p.groups * sets / 128) chunk = blocks < 1 ? 1 : blocks;
@@ -737,15 +750,14 @@ hipError_t launch(const AttentionArgs &a, hipStream_t s) {
 // How many tiles a group has and in how many parts its blocks are depends on the
 // window, which may be any: the most that some window takes.  Fewer blocks may
 // be split into more parts, but never into more than there are for all of them
-// with the smallest chunk, nor than fill the chip or keep the chunks at
-// kMaxChunk.
+// with the smallest chunk, nor than splits_wanted gives for all of them.
 size_t attention_workspace(const AttentionArgs &a, int head_dim) {
     const int64_t rows = static_cast<int64_t>(a.max_rows) * a.group, sets = static_cast<int64_t>(a.kv.kv_heads) * a.kv.batch;
     const int64_t blocks = (static_cast<int64_t>(a.max_length) + kKvBlock - 1) / kKvBlock;
     size_t most = 0;
     for (int64_t tile = 16; tile <= 32; tile += 16) {
         const int64_t held = rows < tile ? rows : tile, groups = (rows + tile - 1) / tile;
-        int64_t splits = splits_wanted(groups * sets, blocks);
+        int64_t splits = splits_wanted(groups * sets, held, blocks);
         if (splits > (blocks + kMinChunk - 1) / kMinChunk) splits = (blocks + kMinChunk - 1) / kMinChunk;
         if (splits <= 1) continue;
         const size_t parts = static_cast<size_t>(groups) * held * sets * splits;   // as in partials()

@@ -1,0 +1,50 @@
+"""Sizes of attention's workspace, and the launches that sizes choose: host code."""
+
+import ctypes
+import itertools
+import os
+import subprocess
+import sys
+
+import pytest
+
+import q4_weight_only_amd as q4
+from q4_weight_only_amd import _decoder as D
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(q4.library_path()):
+        subprocess.run([sys.executable, "-m", "q4_weight_only_amd.build"], check=True)
+    return D.decoder_lib()
+
+
+def _structs(heads, head_dim, batch, rows, max_rows, max_length):
+    return (D._Cache(0x10000, 1 << 20, heads, head_dim),
+            D._Batch(0x10000, 0x10000, 0x10000, 1 << 20, batch, rows, max_rows, max_length))
+
+
+def _workspace(L, heads, group, head_dim, batch, max_rows, max_length):
+    c, b = _structs(heads, head_dim, batch, max(max_rows, batch), max_rows, max_length)
+    return L.q4_kv_attention_workspace(ctypes.byref(c), ctypes.byref(b), heads * group)
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_workspace_is_bounded(L, head_dim):
+    """Whatever the sizes: 2^16 rows of head_dim sums and two more, in fp32."""
+    lengths = (1, 700, 704, 705, 2048, 8192, 8193, 131072, 1 << 20, 1 << 25)
+    rows = (1, 2, 5, 16, 17, 33, 400, 512, 1024, 2048, 3900, 4096, 1 << 15, 1 << 20)
+    for heads, group in ((1, 1), (1, 64), (8, 4), (20, 1), (7, 3), (256, 64)):
+        for batch, most, length in itertools.product((1, 2, 31, 64, 500, 65535), rows, lengths):
+            n = _workspace(L, heads, group, head_dim, batch, most, length)
+            assert 0 <= n <= (1 << 18) * (head_dim + 2), (heads, group, batch, most, length, n)
+            assert n % 16 == 0
+
+
+def test_long_contexts_are_split_while_few_rows_share_them(L):
+    for batch, most, splits in ((1, 1, 32), (2, 1, 16), (64, 1, 16), (1, 512, 4)):
+        rows = batch * most * 32
+        assert _workspace(L, 8, 4, 128, batch, most, 131072) == rows * splits * 130 * 4
+    # 2048 rows of 32 heads fill the chip many times over
+    assert _workspace(L, 8, 4, 128, 1, 2048, 131072) == 0
+    assert _workspace(L, 8, 4, 128, 1, 2048, 1 << 20) == 0
