@@ -152,6 +152,15 @@ q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, co
                           size_t workspace_bytes, void *stream);
 
 /*
+ * The launch that q4_kv_attention takes for these sizes: how many rows (times
+ * the heads of a kv head) a workgroup has, its waves, and into how many parts
+ * the tokens of its rows are divided.  No pointer of the cache or the batch is
+ * read but for whether cu_rows is NULL.
+ */
+q4_status q4_kv_attention_plan(const q4_kv_cache *cache, const q4_kv_batch *batch, int64_t q_heads, int64_t window,
+                               int32_t *rows, int32_t *waves, int32_t *parts);
+
+/*
  * One residual step:
  *     u = y;  u = u / rms(u) * post_weight  (post_weight given);
  *     u = gate * u                          (gate given);

@@ -44,6 +44,7 @@ from ._decoder import (  # noqa: F401
     add_rmsnorm,
     kv_append,
     kv_attention,
+    kv_attention_plan,
     kv_attention_workspace,
     kv_cache_bytes,
     logits_adjust,

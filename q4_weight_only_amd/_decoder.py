@@ -17,7 +17,7 @@ from . import _binding as B
 
 KV_BLOCK = 32
 DECODER_EXPORTS = ("q4_kv_cache_bytes", "q4_kv_append", "q4_kv_attention_workspace", "q4_kv_attention",
-                   "q4_add_rmsnorm", "q4_logits_adjust")
+                   "q4_kv_attention_plan", "q4_add_rmsnorm", "q4_logits_adjust")
 
 _lib = None
 _native = None
@@ -51,6 +51,8 @@ def decoder_lib() -> ctypes.CDLL:
                 L.q4_kv_attention_workspace.restype = ctypes.c_size_t
                 L.q4_kv_attention.argtypes = [vp, vp, vp, i64, f32, i64, vp, i32, vp, ctypes.c_size_t, vp]
                 L.q4_kv_attention.restype = i32
+                L.q4_kv_attention_plan.argtypes = [vp, vp, i64, i64, vp, vp, vp]
+                L.q4_kv_attention_plan.restype = i32
                 L.q4_add_rmsnorm.argtypes = [vp, i32, vp, i32, i64, i64, vp, vp, vp, i64, f32, vp, i64, f32, vp, vp,
                                              i32, vp]
                 L.q4_add_rmsnorm.restype = i32
@@ -160,10 +162,28 @@ def kv_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, len
 def kv_attention_workspace(cache: KVCache, block_table: torch.Tensor, rows: int, q_heads: int, *, max_rows: int,
                            max_length: int) -> int:
     """Bytes of workspace of kv_attention for these sizes."""
-    n, width = block_table.shape
-    c = _Cache(None, cache.num_blocks, cache.kv_heads, cache.head_dim)
-    bt = _Batch(None, None, 4, width, n, int(rows), max(1, int(max_rows)), max(1, int(max_length)))
+    c, bt = _shapes(cache, block_table, rows, max_rows, max_length)
     return int(decoder_lib().q4_kv_attention_workspace(ctypes.byref(c), ctypes.byref(bt), int(q_heads)))
+
+
+def kv_attention_plan(cache: KVCache, block_table: torch.Tensor, rows: int, q_heads: int, *, max_rows: int,
+                      max_length: int, window: int = 0) -> tuple[int, int, int]:
+    """(rows, waves, parts): the launch that kv_attention takes for these sizes:
+    rows (times heads of a kv head) and waves of a workgroup, and into how many
+    parts the tokens of its rows are divided."""
+    c, bt = _shapes(cache, block_table, rows, max_rows, max_length)
+    out = (ctypes.c_int32 * 3)()
+    at = [ctypes.addressof(out) + 4 * i for i in range(3)]
+    B._check(decoder_lib().q4_kv_attention_plan(ctypes.byref(c), ctypes.byref(bt), int(q_heads), int(window), *at),
+             "q4_kv_attention_plan")
+    return tuple(out)
+
+
+def _shapes(cache: KVCache, block_table: torch.Tensor, rows: int, max_rows: int, max_length: int):
+    """The sizes of a call, without its memory."""
+    n, width = block_table.shape
+    return (_Cache(None, cache.num_blocks, cache.kv_heads, cache.head_dim),
+            _Batch(None, None, 4, width, n, int(rows), max(1, int(max_rows)), max(1, int(max_length))))
 
 
 def add_rmsnorm(residual: torch.Tensor, weight: torch.Tensor, y: torch.Tensor | None = None, *,

@@ -115,6 +115,22 @@ size_t q4_kv_attention_workspace(const q4_kv_cache *cache, const q4_kv_batch *ba
     return q4::attention_workspace(a, cache->head_dim);
 }
 
+q4_status q4_kv_attention_plan(const q4_kv_cache *cache, const q4_kv_batch *batch, int64_t q_heads, int64_t window,
+                               int32_t *rows, int32_t *waves, int32_t *parts) {
+    if (const q4_status st = check_shape(cache, batch, q_heads)) return st;
+    if (window < 0 || window > (int64_t(1) << 30)) return Q4_ERR_RANGE;
+    if (!rows || !waves || !parts) return Q4_ERR_NULL;
+    q4::AttentionArgs a = {};
+    a.kv = view(cache, batch);
+    a.q_heads = static_cast<int32_t>(q_heads);
+    a.group = static_cast<int32_t>(q_heads / cache->kv_heads);
+    a.window = static_cast<int32_t>(window);
+    a.max_rows = static_cast<int32_t>(batch->max_rows);
+    a.max_length = static_cast<int32_t>(batch->max_length);
+    q4::attention_plan(a, cache->head_dim, rows, waves, parts);
+    return Q4_OK;
+}
+
 q4_status q4_kv_attention(const q4_kv_cache *cache, const q4_kv_batch *batch, const void *q, int64_t q_heads,
                           float scale, int64_t window, void *out, int out_dtype, void *workspace,
                           size_t workspace_bytes, void *stream) {

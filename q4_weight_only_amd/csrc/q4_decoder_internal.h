@@ -86,6 +86,7 @@ struct AttentionArgs {
     float *workspace;
 };
 size_t attention_workspace(const AttentionArgs &a, int head_dim);
+void attention_plan(const AttentionArgs &a, int head_dim, int32_t *rows, int32_t *waves, int32_t *parts);
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s);
 
 struct NormArgs {

@@ -767,6 +767,13 @@ size_t attention_workspace(const AttentionArgs &a, int head_dim) {
     return most;
 }
 
+void attention_plan(const AttentionArgs &a, int head_dim, int32_t *rows, int32_t *waves, int32_t *parts) {
+    const Plan p = plan_of(a, head_dim);
+    *rows = p.group_rows;
+    *waves = p.waves;
+    *parts = p.splits;
+}
+
 hipError_t launch_kv_attention(const AttentionArgs &a, int head_dim, hipStream_t s) {
     return head_dim == 128 ? launch<128>(a, s) : launch<64>(a, s);
 }

@@ -48,3 +48,41 @@ def test_long_contexts_are_split_while_few_rows_share_them(L):
     # 2048 rows of 32 heads fill the chip many times over
     assert _workspace(L, 8, 4, 128, 1, 2048, 131072) == 0
     assert _workspace(L, 8, 4, 128, 1, 2048, 1 << 20) == 0
+
+
+class _Sizes:
+    """What kv_attention_plan reads of a cache and a block table."""
+
+    def __init__(self, heads, head_dim, batch, width=1 << 20):
+        self.num_blocks, self.kv_heads, self.head_dim = 1 << 20, heads, head_dim
+        self.shape = (batch, width)
+
+
+def _plan(heads, group, head_dim, batch, rows, length, window=0):
+    s = _Sizes(heads, head_dim, batch)
+    return q4.kv_attention_plan(s, s, batch * rows, heads * group, max_rows=rows, max_length=length, window=window)
+
+
+def test_plans_of_ordinary_sizes(L):
+    assert _plan(8, 4, 128, 1, 1, 1505) == (16, 4, 12)
+    assert _plan(8, 4, 128, 32, 1, 8191) == (16, 4, 1)
+    assert _plan(8, 4, 128, 2, 1, 131072) == (16, 4, 16)
+    assert _plan(8, 4, 128, 1, 2048, 2048) == (32, 2, 1)
+    assert _plan(20, 1, 64, 1, 1505, 6020, 750) == (32, 2, 1)
+    assert _plan(20, 1, 64, 1, 700, 3600, 750) == (16, 4, 1)
+    assert _plan(20, 1, 64, 1, 900, 3600, 750) == (32, 4, 1)
+    assert _plan(8, 4, 128, 1, 512, 16384) == (32, 4, 2)
+
+
+def test_plan_refuses_what_a_call_refuses(L):
+    c, b = _structs(2, 64, 2, 2, 1, 64)
+    out = (ctypes.c_int32 * 3)()
+    at = [ctypes.addressof(out) + 4 * i for i in range(3)]
+
+    def call(c=c, b=b, heads=4, window=0, at=at):
+        return L.q4_kv_attention_plan(ctypes.byref(c) if c else None, ctypes.byref(b) if b else None, heads, window, *at)
+
+    assert call() == 0 and out[0] == 16 and out[1] == 4 and out[2] == 1
+    assert call(c=None) == 1 and call(b=None) == 1 and call(at=[None, at[1], at[2]]) == 1 and call(at=[at[0], at[1], None]) == 1
+    assert call(heads=5) == 6 and call(heads=0) == 6 and call(window=-1) == 6 and call(window=2**30 + 1) == 6
+    assert call(c=_structs(2, 80, 2, 2, 1, 64)[0]) == 6 and call(b=_structs(2, 64, 2, 2, 0, 64)[1]) == 6
