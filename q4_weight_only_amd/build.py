@@ -1,10 +1,12 @@
 """Build libq4amd.so in-tree for gfx950 with hipcc.
 
-    python -m q4_weight_only_amd.build
+    python -m q4_weight_only_amd.build [--library] [-v]
 
 Each .hip source is compiled to an object in parallel, then linked into
 q4_weight_only_amd/libq4amd.so (written to a temporary name and renamed, so a
-concurrent reader never sees a half-written library).
+concurrent reader never sees a half-written library).  That takes hipcc alone;
+the decoder operators' Python binding, _q4decoder.so, is linked after it and
+takes a C++ compiler and torch's and Python's headers (--library leaves it out).
 """
 
 from __future__ import annotations
@@ -107,9 +109,12 @@ def _binding_command(out: str):
             [shutil.which("g++") or "c++", "-shared", "-o", out, os.path.join(BUILD_DIR, "decoder_binding.o"), *libs])
 
 
-def build(verbose: bool = False) -> str:
-    """Compile every HIP source for gfx950 and link libq4amd.so, and the Python
-    binding of the decoder operators on top of it; return the library's path."""
+def build(verbose: bool = False, binding: bool = True) -> str:
+    """Compile every HIP source for gfx950 and link libq4amd.so, which takes
+    hipcc alone, then (unless `binding` is false) the Python binding of the
+    decoder operators on top of it, which takes the C++ compiler and torch's and
+    Python's headers; return the library's path.  Where the binding cannot be
+    built, the library is in place before that is raised."""
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     objs = []
@@ -118,25 +123,41 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         objs.append(obj)
         cmds.append([hipcc, *COMMON_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
-    binding_tmp = BINDING + f".tmp{os.getpid()}"
-    compile_binding, link_binding = _binding_command(binding_tmp)
-    cmds.append(compile_binding)
-    with ThreadPoolExecutor(max_workers=len(cmds)) as ex:
-        outs = list(ex.map(_run, cmds))
-    for o in outs:
+
+    def show(out):
         # compiler warnings are always shown; other output only when asked
-        shown = o if verbose else "\n".join(l for l in o.splitlines() if "warning:" in l)
+        shown = out if verbose else "\n".join(l for l in out.splitlines() if "warning:" in l)
         if shown.strip():
             print(shown)
+
+    def compile_binding():
+        compile_cmd, link_cmd = _binding_command(binding_tmp)
+        return _run(compile_cmd), link_cmd
+
+    binding_tmp = BINDING + f".tmp{os.getpid()}"
+    with ThreadPoolExecutor(max_workers=len(cmds) + 1) as ex:
+        # beside the HIP sources; its failure is looked at when the library is there
+        pending = ex.submit(compile_binding) if binding else None
+        for out in ex.map(_run, cmds):
+            show(out)
     _write_build_info()
     tmp = LIB + f".tmp{os.getpid()}"
     _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    _run(link_binding)
-    os.replace(binding_tmp, BINDING)
+    if binding:
+        try:
+            out, link_cmd = pending.result()
+            show(out)
+            _run(link_cmd)
+            os.replace(binding_tmp, BINDING)
+        except Exception as e:
+            if os.path.exists(BINDING):      # of another build: not to be used with this library
+                os.remove(BINDING)
+            raise RuntimeError(f"{LIB} is built (the C ABI and the linears); the decoder operators' Python binding is not: "
+                               f"{e}") from e
     return LIB
 
 
 if __name__ == "__main__":
-    path = build(verbose="-v" in sys.argv)
+    path = build(verbose="-v" in sys.argv, binding="--library" not in sys.argv)
     print(path)
