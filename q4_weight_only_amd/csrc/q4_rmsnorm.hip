@@ -8,10 +8,16 @@
 // each sum instead.
 //
 // What bounds it is memory: 2048 rows of 3072 (fp32 in, bf16 x out) take
-// 15.6 us, 5.6 TB/s, with post norm, gate and modulation 17; 6020 rows of 1280
-// 17.7, 6.1 TB/s.  The stores carry the nontemporal hint, without which the
-// same take 17.7, 18.2 and 22.6.  Two rows of 3072 take 2.5 us: a launch, a
-// load and a sum.
+// 15.5 us, 5.7 TB/s, with a post norm 15.8; 6020 rows of 1280 18.0, 6.0 TB/s.
+// Two rows of 3072 take 2.5 us: a launch, a load and a sum.
+//
+// The new residual, which is read only after the block, is stored with the
+// nontemporal hint (without it 15.6, 18.3 and 22.4).  x is not: the linear after
+// it reads it at once, and pays more than the hint saves here (norm, linear up
+// and linear down, us with / without it on x: 128 rows of 3072 81.4 / 77.1, 256
+// 83.5 / 78.2, 512 92.9 / 90.1, 2048 189 / 187, 4096 363.3 / 362.9, 6020 of 1280
+// 206.6 / 206.0; the norm alone 17.5 / 18.0 for these, 24.2 / 29.1 for 2048 of
+// 5120).
 
 #include "q4_decoder_internal.h"
 
@@ -29,12 +35,17 @@ __device__ __forceinline__ floatx4 load4(const void *p, int64_t i) {   // i: gro
         return reinterpret_cast<const floatx4 *>(p)[i];
 }
 
-template <int BF16>
+// STREAM: with the nontemporal hint, for what no kernel reads soon.
+template <int BF16, bool STREAM>
 __device__ __forceinline__ void store4(void *p, int64_t i, floatx4 v) {
-    if constexpr (BF16)
-        __builtin_nontemporal_store(__builtin_convertvector(v, bf16x4), reinterpret_cast<bf16x4 *>(p) + i);
-    else
-        __builtin_nontemporal_store(v, reinterpret_cast<floatx4 *>(p) + i);
+    if constexpr (BF16) {
+        const bf16x4 h = __builtin_convertvector(v, bf16x4);
+        if constexpr (STREAM) __builtin_nontemporal_store(h, reinterpret_cast<bf16x4 *>(p) + i);
+        else reinterpret_cast<bf16x4 *>(p)[i] = h;
+    } else {
+        if constexpr (STREAM) __builtin_nontemporal_store(v, reinterpret_cast<floatx4 *>(p) + i);
+        else reinterpret_cast<floatx4 *>(p)[i] = v;
+    }
 }
 
 __device__ __forceinline__ float sum_sq(floatx4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
@@ -99,7 +110,7 @@ __global__ __launch_bounds__(kBlock<T>) void add_rmsnorm_kernel(NormArgs a) {
             const int i = tid + T * v;
             if (a.y && i < groups) {
                 r[v] = r[v] + update<YB>(a, y[v], inv, gate, i);
-                store4<RB>(a.residual_out, base + i, r[v]);
+                store4<RB, true>(a.residual_out, base + i, r[v]);
             }
             ss += sum_sq(r[v]);
         }
@@ -110,7 +121,7 @@ __global__ __launch_bounds__(kBlock<T>) void add_rmsnorm_kernel(NormArgs a) {
             if (i < groups) {
                 floatx4 x = r[v] * inv * load4<0>(a.weight, i);
                 if (mod) x = x * (1.0f + load4<0>(mod, i));
-                store4<XB>(a.x, base + i, x);
+                store4<XB, false>(a.x, base + i, x);
             }
         }
     } else {
@@ -129,10 +140,10 @@ __global__ __launch_bounds__(kBlock<T>) void add_rmsnorm_kernel(NormArgs a) {
         const float inv_r = 1.0f / sqrtf(row_sum<T>(ss, part[1]) * inv_c + a.eps);
         for (int i = tid; i < groups; i += T) {
             const floatx4 r = value(i);   // before residual_out, which may be the residual itself, gets it
-            if (a.y) store4<RB>(a.residual_out, base + i, r);
+            if (a.y) store4<RB, true>(a.residual_out, base + i, r);
             floatx4 x = r * inv_r * load4<0>(a.weight, i);
             if (mod) x = x * (1.0f + load4<0>(mod, i));
-            store4<XB>(a.x, base + i, x);
+            store4<XB, false>(a.x, base + i, x);
         }
     }
 }
