@@ -637,28 +637,45 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttentionArgs a, Pl
 // four for heads of 64; us with one / two):
 //   D = 128: 512 tiles, 5 blocks 6.6 / 7.3, 28 blocks 11.3 each; 1024 tiles, 3
 //     blocks 10.6 / 8.9, 9 blocks 12.6 / 10.4; 2048 tiles, 17 blocks 29 / 23
-//   D = 64: 640 tiles, 9 blocks 6.0 / 7.3; 1280 tiles, 5 blocks 8.7 / 8.9, 17
-//     blocks 11.4 / 11.8; 1536 tiles, 5 blocks 9.2 / 8.4
+//   D = 64: 640 tiles, 9 blocks 6.0 / 7.3; 1280 tiles, 5 blocks 8.7 / 8.9, 15
+//     blocks 15.1 / 12.9, 17 blocks 11.2 / 11.9, 30 blocks 20.7 / 16.8, 78 blocks
+//     34 / 29; 1536 tiles, 5 blocks 9.2 / 8.4
 // or, of at least kManyTiles, where these have many blocks:
-//   D = 128: 256 tiles, 126 blocks 19 / 25, 254 blocks 35.5 / 35.4, 510 blocks
-//     74 / 56; 512 tiles, 60 blocks 16.6 / 16.4, 250 blocks 56 / 47
-//   D = 64: 320 tiles, 252 blocks 41 / 38; 768 tiles, 248 blocks 48 / 52
+//   D = 128: 128 tiles, 256 blocks 26 / 23, 512 blocks 42 / 32; 256 tiles, 126
+//     blocks 19 / 25, 254 blocks 35.5 / 35.4, 510 blocks 74 / 56; 512 tiles, 60
+//     blocks 16.6 / 16.4, 250 blocks 56 / 47
+//   D = 64: 640 tiles, 375 blocks on average 81 / 70; 960 tiles, 245 blocks 82 / 55
+// For D = 64 with fewer, how the workgroups divide over the compute units decides:
+// 500 tiles, 88 blocks 16.8 / 22.8, 151 blocks 27 / 34; 600, 151 blocks 31 / 33; 768,
+// 62 blocks 17.7 / 19.2; but 160, 249 blocks 31 / 22; 320, 253 blocks 41 / 37; 640, 63
+// blocks (16 sequences) 30 / 19.5; 960, 82 blocks 27 / 23.  They keep one tile.
 constexpr int64_t tiles_at_once(int D) { return D == 64 ? 1024 : 512; }
 constexpr int64_t many_blocks(int D) { return D == 64 ? 200000 : 40000; }
 constexpr int64_t kManyTiles = 64;
 
-// Two waves a workgroup instead of four where there are many workgroups for
-// the blocks that each reads, so that they still even out (workgroups, blocks:
-// us with four / two):
-//   D = 128: 512, 9: 10.4 / 11.8; 1024, 17: 22.7 / 22.3; 1200, 19: 29 / 25; 1313,
-//     95: 77 / 90; 2048, 9: 35 / 27; 2048, 33: 54 / 48; 2048, 121: 142 / 160;
-//     4096, 65: 162 / 152; 8192, 129: 581 / 556
-//   D = 64: 1280, 33: 24 / 29; 2048, 33: 36 / 40; 2560, 65: 67 / 70; 2560, 9: 25 /
-//     22; 6144, 17: 65 / 57
+// Two waves a workgroup instead of four where there are more workgroups than fit
+// on the chip at once with four, and many for the blocks that each reads, so that
+// they still even out (workgroups, blocks: us with four / two):
+//   D = 128: 512, 9: 10.4 / 11.8; 520, 9: 14.4 / 13.0; 600, 10: 16.8 / 14.2; 640,
+//     2: 13.0 / 8.2; 640, 31: 22.8 / 25.1; 744, 12: 18.8 / 16.8; 768, 82: 44 / 53;
+//     1024, 17: 22.9 / 22.6; 1024, 30: 29.9 / 26.4; 1400, 22: 34.5 / 31.1; 1313, 95:
+//     77 / 90; 2048, 9: 35 / 27; 2048, 33: 55 / 49; 2048, 121: 142 / 160; 4096, 65:
+//     162 / 152; 8192, 129: 581 / 556
+//   D = 64: 640, 3: 8.1 / 7.4; 768, 3: 7.7 / 7.0; 800, 5: 11.0 / 9.7; 880, 22: 16.3 /
+//     19.9; 1280, 33: 24 / 29; 1920, 16: 25.3 / 23.9; 2048, 33: 36 / 40; 2560, 65: 68 /
+//     70; 2560, 9: 25 / 22; 6144, 17: 65 / 57
 // and sooner where a window makes them equal:
-//   D = 128: 1400, 24: 39 / 40; 2048, 32: 58 / 53; D = 64: 960, 24: 19.7 / 18.1
+//   D = 128: 520, 24: 22.2 / 20.5; 520, 94: 47.9 / 55.3; 744, 24: 23.7 / 21.9; 744,
+//     94: 50 / 57; 1000, 24: 29.0 / 23.5; 1024, 65: 48 / 45; 1024, 129: 82 / 81;
+//     1104, 24: 35 / 33; 1400, 94: 90 / 107; 1512, 24: 41.0 / 42.5; 2048, 33: 59 / 57;
+//     2504, 24: 63 / 56; 3000, 33: 84 / 75
+//   D = 64: 760, 24: 15.2 / 17.5; 820, 24: 19.5 / 17.7; 820, 79: 38.3 / 38.1; 960, 24:
+//     19.8 / 18.1; 960, 63: 33.0 / 32.6; 1260, 24: 23.1 / 23.2; 1260, 79: 45 / 52;
+//     1880, 79: 67 / 78; 2380, 24: 40 / 35; 2380, 79: 82.2 / 80.5
 bool two_waves(int64_t groups, int64_t each, bool equal, int D) {
-    return groups >= 768 && each * (D == 64 ? 100 : 25) < groups * (equal ? 4 : 1);
+    if (groups <= (D == 64 ? 767 : 512)) return false;
+    if (equal) return each * 25 < groups * (D == 64 ? 1 : 2);
+    return each * (D == 64 ? 100 : 25) < groups;
 }
 
 // Blocks of a workgroup of attention_kernel at most, where the workspace has room,
