@@ -10,18 +10,12 @@
 // heads a thread.
 //
 // What bounds it is memory: 4515 rows of 32 + 2 * 8 heads of 128 in fp32
-// (157 MB) take 32 us, 4.9 TB/s; 8192 rows of 20 + 2 * 20 heads of 64 37 us,
+// (157 MB) take 31 us, 5.1 TB/s; 8192 rows of 20 + 2 * 20 heads of 64 37 us,
 // 4.5 TB/s.  Lanes run along a row's dimensions four at a time, so that a
 // wave's loads are whole lines (16 dimensions a lane: 52 and 66 us), and both
 // halves of the turned pairs are in one thread, which reads each of them once.
 // One token for each of 32 sequences takes 4.8 us: bounds and block ids, rows
 // and old codes, the largest value, the codes, one after the other.
-//
-// The rotated q, which the attention after it reads at once, is stored through to
-// the device's scope (append and attention, us with nontemporal / plain / these
-// stores: 3 prompts of 1505 117.2 / 114.7 / 114.2, 8 of 256 37.6 / 36.8 / 36.8, one
-// token for each of 64 sequences of 1000 32.8 / 33.4 / 33.0; append alone 31.1 /
-// 32.6 / 32.2, 14.0 / 14.1 / 14.1 and 6.3 / 6.4 / 6.3).
 //
 // The rotation's products are rounded before they are added, so that a value
 // on the edge between two exponents does not depend on how the compiler pairs
@@ -265,8 +259,7 @@ __device__ __forceinline__ void rotate_q(const AppendArgs &a, int64_t row, int p
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bf16x4 y = pos >= 0 ? __builtin_convertvector(x[h][i], bf16x4) : (bf16x4){};
-            __hip_atomic_store(reinterpret_cast<uint64_t *>(dst + (i ? piece.hi : piece.lo)), __builtin_bit_cast(uint64_t, y),
-                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);   // see above
+            __builtin_nontemporal_store(y, reinterpret_cast<bf16x4 *>(dst + (i ? piece.hi : piece.lo)));
         }
     }
 }
