@@ -10,12 +10,21 @@
 // heads a thread.
 //
 // What bounds it is memory: 4515 rows of 32 + 2 * 8 heads of 128 in fp32
-// (157 MB) take 31 us, 5.1 TB/s; 8192 rows of 20 + 2 * 20 heads of 64 37 us,
+// (157 MB) take 32 us, 4.9 TB/s; 8192 rows of 20 + 2 * 20 heads of 64 37 us,
 // 4.5 TB/s.  Lanes run along a row's dimensions four at a time, so that a
 // wave's loads are whole lines (16 dimensions a lane: 52 and 66 us), and both
 // halves of the turned pairs are in one thread, which reads each of them once.
 // One token for each of 32 sequences takes 4.8 us: bounds and block ids, rows
 // and old codes, the largest value, the codes, one after the other.
+//
+// The rotated q is stored with the nontemporal hint for few rows of a sequence,
+// and without it for a prompt's, which the attention after it reads many times
+// (append and attention, us with / without: one token for each of 64 sequences of
+// 1000 33.0 / 33.6, for each of 32 of 411 13.6 / 13.7; 512 rows over 2048 36.5 /
+// 35.9; 3 prompts of 1505 117.0 / 114.7, with neighbours as pairs 118.5 / 115.5; 8 of
+// 256 37.8 / 36.9; append alone 30.7 / 32.4 for these 3, 14.0 / 14.1 for the 8, 15.0 /
+// 14.0 for one prompt of 2048 with neighbours as pairs).  Stores through to the
+// device's scope write such pairs twice (18.2 for the last).
 //
 // The rotation's products are rounded before they are added, so that a value
 // on the edge between two exponents does not depend on how the compiler pairs
@@ -235,10 +244,12 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, const KvSequen
     __syncthreads();   // the block has been read
 }
 
+constexpr int kManyRows = 32;   // from here on the rotated q is read many times
+
 // A piece of kHeads heads' rotated q, for which the angles are read once.
 constexpr int kHeads = 2;
 
-template <int D, typename T>
+template <int D, typename T, bool STREAM>
 __device__ __forceinline__ void rotate_q(const AppendArgs &a, int64_t row, int pos, int head0, int c) {
     const int heads = a.q_heads - head0 < kHeads ? a.q_heads - head0 : kHeads;
     const Piece piece = piece_of(a, c);
@@ -259,12 +270,16 @@ __device__ __forceinline__ void rotate_q(const AppendArgs &a, int64_t row, int p
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const bf16x4 y = pos >= 0 ? __builtin_convertvector(x[h][i], bf16x4) : (bf16x4){};
-            __builtin_nontemporal_store(y, reinterpret_cast<bf16x4 *>(dst + (i ? piece.hi : piece.lo)));
+            bf16x4 *to = reinterpret_cast<bf16x4 *>(dst + (i ? piece.hi : piece.lo));
+            if constexpr (STREAM) __builtin_nontemporal_store(y, to);
+            else *to = y;
         }
     }
 }
 
-template <int D, typename T>
+// STREAM: with the nontemporal hint on the rotated q (a branch in the kernel would
+// not do: the compiler joins two stores that differ by the hint alone).
+template <int D, typename T, bool STREAM>
 __global__ __launch_bounds__(2 * D) void kv_append_kernel(AppendArgs a, int block_units, int q_units) {
     __shared__ u32x4 block[2 * D];
     __shared__ float wave_max[D / 32];
@@ -287,7 +302,7 @@ __global__ __launch_bounds__(2 * D) void kv_append_kernel(AppendArgs a, int bloc
     for (int64_t u = static_cast<int64_t>(unit) * (2 * D) + threadIdx.x; u < total;
          u += static_cast<int64_t>(q_units) * (2 * D)) {
         const int t = static_cast<int>(u / per_row), in_row = static_cast<int>(u % per_row);
-        rotate_q<D, T>(a, s.row0 + t, s.pos0 + t, in_row / (D / 8) * kHeads, in_row % (D / 8));
+        rotate_q<D, T, STREAM>(a, s.row0 + t, s.pos0 + t, in_row / (D / 8) * kHeads, in_row % (D / 8));
     }
 }
 
@@ -301,9 +316,13 @@ hipError_t launch(const AppendArgs &a, hipStream_t s) {
     const int64_t per_row = (a.q_heads + kHeads - 1) / kHeads * (D / 8);
     int64_t q_units = (a.max_rows * per_row + 2 * D - 1) / (2 * D);
     if (q_units > (1 << 20)) q_units = 1 << 20;
-    hipLaunchKernelGGL((kv_append_kernel<D, T>),
-                       dim3(static_cast<uint32_t>(block_units + q_units), static_cast<uint32_t>(a.kv.batch)),
-                       dim3(2 * D), 0, s, a, static_cast<int>(block_units), static_cast<int>(q_units));
+    const dim3 grid(static_cast<uint32_t>(block_units + q_units), static_cast<uint32_t>(a.kv.batch));
+    if (a.max_rows < kManyRows)
+        hipLaunchKernelGGL((kv_append_kernel<D, T, true>), grid, dim3(2 * D), 0, s, a, static_cast<int>(block_units),
+                           static_cast<int>(q_units));
+    else
+        hipLaunchKernelGGL((kv_append_kernel<D, T, false>), grid, dim3(2 * D), 0, s, a, static_cast<int>(block_units),
+                           static_cast<int>(q_units));
     return hipGetLastError();
 }
 
