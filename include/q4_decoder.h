@@ -113,8 +113,8 @@ typedef struct {
  * the new scale.  Writing the same rows again gives the same cache.
  *
  * Rows without a position, or past the rope table, and ids outside the cache:
- * q_out is 0 for a row without a position and not a number past the table
- * (so are the codes of k); a block whose id is outside [0, num_blocks) or past
+ * q_out is 0 for a row without a position, and past the table not a number in
+ * the dimensions that are turned (so are the codes of k); a block whose id is outside [0, num_blocks) or past
  * table_width is not written.  Two sequences of one call must not write the
  * same block.
  */
@@ -135,10 +135,11 @@ q4_status q4_kv_append(const q4_kv_cache *cache, const q4_kv_batch *batch, const
  * summed in fp32, the softmax's maximum and sum are fp32; the weights, times
  * the scale of their token's v, are rounded to fp16 for their products with the
  * codes of v, which are summed in fp32: within 2^-11 of each, or 2^-32 of the
- * row's largest where that is more.  An output is not finite where the formula's is: a token that a row
- * does not see has no effect on it, whatever its codes are.  A token in a
- * block whose id is outside [0, num_blocks), or past table_width, counts as
- * not a number.
+ * row's largest where that is more.  Within fp32's range an output is finite
+ * where the formula's is, and not a number where that is not: a token that a
+ * row does not see has no effect on it, whatever its codes are, and one that it
+ * sees has, however small its weight.  A token in a block whose id is outside
+ * [0, num_blocks), or past table_width, counts as not a number.
  *
  * workspace: device, 16-byte aligned, q4_kv_attention_workspace bytes for the
  * same batch (0: may be NULL; never more than 2^18 * (head_dim + 2), 34 MB for

@@ -364,18 +364,18 @@ __device__ __forceinline__ float inverse(const KvView &kv, int pos, float total)
 //
 // What bounds it for single tokens is reading the cache: two sequences of
 // 131072 tokens of 8 heads of 128 (537 MB) take 85 us, 6.3 TB/s; 32 sequences
-// of 2048 to 8191 (332 MB) 59 us, 5.6 TB/s.  The loads are nontemporal, as
+// of 2048 to 8191 (332 MB) 59 us, 5.7 TB/s.  The loads are nontemporal, as
 // nothing is read twice (99 -> 91 us for the former, 80 -> 74 for the latter
 // when measured).  Short caches are bound by what follows from each other:
 // length and block ids together, codes, a block's products, the join of the
-// waves: one token over 64 takes 4.1 us, over 512 5.7 and over 1505, in 12
-// splits, 7.7, of which the join of the splits is 2.5.
+// waves: one token over 64 takes 4.3 us, over 512 5.9 and over 1505, in 12
+// splits, 7.5, of which the join of the splits is 2.5.
 //
 // For many rows it is the issue of instructions: a wave's 32 rows and a block of
 // heads of 128 are 32 MFMAs of 16 cycles and about 170 other instructions of 2
 // to 8 (64 conversions of codes, 16 exponentials), and little of the two runs at
-// once: 1070 cycles.  A prompt of 2048 with 32 heads of 128 takes 48 us, 714
-// TFLOP/s, one of 8192 556 us, 989.  Two tiles share what a wave converts (one
+// once: 1080 cycles.  A prompt of 2048 with 32 heads of 128 takes 49 us, 700
+// TFLOP/s, one of 8192 585 us, 940.  Two tiles share what a wave converts (one
 // tile: 75 us for the former), and fill the registers.  Workgroups of two waves
 // start and join less often for what they compute.  Blocks that pass through
 // LDS to eight waves with 64 or 128 rows, converted there or not, took 57 to 65
@@ -526,7 +526,7 @@ __global__ __launch_bounds__(64 * W, 2) void attention_kernel(AttentionArgs a, P
                 }
             }
         }
-        // join the four waves.  (The lane is hidden from the loop over the
+        // join the waves.  (The lane is hidden from the loop over the
         // groups, out of which the compiler would take the addresses below and
         // hold them all.)
         int re = r, ge = g4;
@@ -688,8 +688,8 @@ constexpr int64_t kMaxChunk = 256;
 // join 2.5 us and 1 more a thousand rows: blocks are split where that leaves a
 // workgroup kSaved fewer of them, and one more for every 128 rows.  (One row:
 // 700 tokens 7.1 us either way, 1200 7.4 against 8.8, 1505 7.7 against 10; 128
-// rows of 20 heads over 1000 tokens 12.0 against 6.7.)  The smallest chunk has a
-// block for each wave (3000 tokens 7.7 us, 9.0 with four).
+// rows of 20 heads over 1000 tokens 12.0 against 6.7.)  The smallest chunk has one
+// block for each wave (3000 tokens 7.5 us; 8.8 with four blocks for each).
 constexpr int64_t kSaved = 22;
 constexpr int64_t kMinChunk = kWaves;
 
