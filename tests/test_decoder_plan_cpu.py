@@ -86,3 +86,31 @@ def test_plan_refuses_what_a_call_refuses(L):
     assert call(c=None) == 1 and call(b=None) == 1 and call(at=[None, at[1], at[2]]) == 1 and call(at=[at[0], at[1], None]) == 1
     assert call(heads=5) == 6 and call(heads=0) == 6 and call(window=-1) == 6 and call(window=2**30 + 1) == 6
     assert call(c=_structs(2, 80, 2, 2, 1, 64)[0]) == 6 and call(b=_structs(2, 64, 2, 2, 0, 64)[1]) == 6
+
+
+def test_workspace_holds_the_parts_of_every_window(L):
+    """What a launch writes of partial results fits the workspace, which is the
+    same for every window."""
+    import random
+
+    rng = random.Random(1)
+    split = 0
+    for _ in range(20000):
+        heads, group = rng.choice(((8, 4), (1, 1), (20, 1), (7, 3), (2, 8), (1, 64), (64, 1)))
+        head_dim, batch = rng.choice((64, 128)), int(2 ** rng.uniform(0, 10))
+        most, length = int(2 ** rng.uniform(0, 15)), int(2 ** rng.uniform(0, 25))
+        window = rng.choice((0, 1, 750, int(2 ** rng.uniform(0, 25))))
+        c, b = _structs(heads, head_dim, batch, most, most, length)
+        out = (ctypes.c_int32 * 3)()
+        at = [ctypes.addressof(out) + 4 * i for i in range(3)]
+        assert L.q4_kv_attention_plan(ctypes.byref(c), ctypes.byref(b), heads * group, window, *at) == 0
+        tile, waves, parts = out
+        assert (tile, waves) in ((16, 4), (32, 4), (32, 2)) and parts >= 1
+        if parts == 1:
+            continue
+        split += 1
+        rows = most * group
+        partial = -(-rows // tile) * min(rows, tile) * heads * batch * parts
+        need = ((partial * 2 + 3) // 4 * 4 + partial * head_dim) * 4
+        assert need <= L.q4_kv_attention_workspace(ctypes.byref(c), ctypes.byref(b), heads * group), (heads, group, batch, most, length, window)
+    assert split > 1000
