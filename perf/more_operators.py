@@ -449,7 +449,7 @@ def _fork(s):
     src, dst = torch.where(copies & (got >= 0), last, -1), torch.where(copies, got, -1)
     at = torch.where(copies, have - 1, have)
     table = torch.where((want > 0)[:, None] & (place == at[:, None]), got[:, None].int(), table)
-    refs = refs.index_add(0, last.clamp(min=0), -(copies & (got >= 0)).long())
+    refs = refs.index_add(0, last.clamp(min=0), -copies.long())
     refs = refs.index_add(0, torch.where(got >= 0, got, blocks), torch.ones_like(got))[:blocks]
     short = torch.where((want > 0) & (got < 0), 1, 0)
     _copy_blocks(s, src, dst)
