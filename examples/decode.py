@@ -1,6 +1,7 @@
-"""A decoder on this library's operators: prompts, then single tokens.
+"""A decoder on this library's operators: prompts, then single tokens, and beam
+search.
 
-    python examples/decode.py [--steps 16]
+    python examples/decode.py [--steps 16] [--beams 4] [--keep 0]
 
 Everything between the token ids and the adjusted logits runs in the library:
 the 4-bit linears (embedding, fused QKV, O, fused gate/up with SwiGLU, down,
@@ -8,6 +9,10 @@ LM head) and, between them, the fused norms, the append to the paged 8-bit
 cache, the attention over it and the penalties on the logits.  Weights are
 random; the sizes are arguments of Decoder.  Sequences of unequal length share
 one batch, blocks are handed out as they are needed.
+
+Beam search shares the blocks of what beams have in common, and copies one when
+two of them go on in it.  With --keep attention reads that many blocks of a
+sequence, the ones that matter most to each token.
 """
 
 from __future__ import annotations
@@ -49,16 +54,24 @@ class Decoder:
     def caches(self, num_blocks):
         return [q4.KVCache.empty(num_blocks, self.kv_heads, self.head_dim, self.device) for _ in self.layers]
 
-    def forward(self, ids, caches, table, lengths, rope, cu_rows=None, *, max_rows, max_length, last=None):
-        """Logits [rows or len(last), vocab] of the rows `ids`; `last`: the rows whose logits are wanted."""
+    def forward(self, ids, caches, table, lengths, rope, cu_rows=None, *, max_rows, max_length, last=None, summaries=None,
+                keep=0):
+        """Logits [rows or len(last), vocab] of the rows `ids`; `last`: the rows whose logits are wanted.
+        summaries: kv_summary's of the caches, which are kept up to date; keep: read that many blocks alone."""
         shape = dict(max_rows=max_rows, max_length=max_length)
         r = q4.embed_gguf(self.blocks, self.vocab, self.dim, ids)
         y = None
-        for layer, cache in zip(self.layers, caches):
+        for i, (layer, cache) in enumerate(zip(self.layers, caches)):
             r, x = q4.add_rmsnorm(r, layer["attn_norm"], y)
             q, k, v = q4.linear_multi(x, layer["qkv"])
             q = q4.kv_append(q, k, v, cache, table, lengths, rope, cu_rows, max_rows=max_rows)
-            a = q4.kv_attention(q, cache, table, lengths, cu_rows, window=self.window, **shape)
+            if summaries is not None:
+                q4.kv_summarize(cache, summaries[i], table, lengths, cu_rows, rows=ids.shape[0], max_rows=max_rows)
+            if keep:
+                chosen = q4.kv_select(q, cache, summaries[i], table, lengths, cu_rows, keep=keep, **shape)
+                a = q4.kv_attention_blocks(q, cache, chosen, table, lengths, cu_rows, max_rows=max_rows)
+            else:
+                a = q4.kv_attention(q, cache, table, lengths, cu_rows, window=self.window, **shape)
             r, x = q4.add_rmsnorm(r, layer["ffn_norm"], q4.linear(a, layer["o"]))
             y = q4.linear(q4.linear_swiglu(x, layer["gate"], layer["up"], dtype=torch.bfloat16), layer["down"])
         _, x = q4.add_rmsnorm(r, self.final_norm, y)
@@ -129,9 +142,53 @@ def generate(model, prompts, steps, *, repetition=1.2, presence=0.1, mask=None, 
     return [h[:e].tolist() for h, e in zip(history.cpu(), ends)], z
 
 
+def beam_search(model, prompts, steps, *, beams=4, eos=-1, pad=0, keep=0, positions=4096, blocks=None, each_step=None):
+    """The `beams` best continuations of each prompt: (tokens [prompts, beams, room], their lengths, scores), on
+    the device.  `keep`: blocks of a sequence that a token reads (0: all).  `each_step` is called with the stack of
+    caches, the block table and the lengths before a step's tokens are appended."""
+    dev, n = model.device, len(prompts)
+    i32 = dict(dtype=torch.int32, device=dev)
+    limit = max(len(p) for p in prompts) + steps
+    width = -(-limit // q4.KV_BLOCK)
+    blocks = blocks or n * (beams + 1) * width
+    stack = q4.KVStack.empty(len(model.layers), blocks, model.kv_heads, model.head_dim, dev)
+    summaries = torch.zeros((len(stack), blocks, model.kv_heads, 2, model.head_dim), dtype=torch.int8, device=dev) if keep else None
+    rope = q4.rope_table(positions, model.head_dim, device=dev)
+    sequences = torch.full((n, limit), pad, **i32)
+    for b, p in enumerate(prompts):
+        sequences[b, :len(p)] = torch.tensor(p, **i32)
+    counts = torch.tensor([len(p) for p in prompts], **i32)
+    # blocks for the prompts, out of an empty table
+    row = torch.arange(n, **i32)
+    f = q4.kv_fork(torch.full((n, width), -1, **i32), torch.zeros(n, **i32), row, blocks, grow=counts)
+    cu = torch.cat((torch.zeros(1, **i32), counts.cumsum(0).int()))
+    logits = model.forward(torch.cat([sequences[b, :len(p)] for b, p in enumerate(prompts)]), stack, f.block_table, f.lengths, rope,
+                           cu, max_rows=int(counts.max()), max_length=int(counts.max()), last=(cu[1:] - 1).long(), summaries=summaries,
+                           keep=keep)
+    scores = torch.zeros((n, 1), dtype=torch.float32, device=dev)
+    finished = torch.zeros((n, 1), **i32)
+    lengths = counts
+    for step in range(steps):
+        parents, tokens, scores = q4.beam_select(logits, scores, beams, finished=finished, pad=pad)
+        sequences, lengths, done = q4.beam_advance(sequences, lengths, parents, tokens, finished=finished, eos=eos, pad=pad)
+        finished = done.view(n, beams)
+        if step == steps - 1:
+            break
+        # the tables of the beams that go on; their last blocks before they are written
+        f = q4.kv_fork(f.block_table, f.lengths, parents, blocks, grow=1)
+        q4.kv_copy_blocks(stack, f.src, f.dst, summaries=summaries)
+        if each_step:
+            each_step(stack, f.block_table, f.lengths)
+        logits = model.forward(tokens.view(-1), stack, f.block_table, f.lengths, rope, max_rows=1, max_length=limit,
+                               summaries=summaries, keep=keep)
+    return sequences.view(n, beams, limit), lengths.view(n, beams), scores
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--steps", type=int, default=16)
+    ap.add_argument("--beams", type=int, default=4)
+    ap.add_argument("--keep", type=int, default=0)
     a = ap.parse_args()
     model = Decoder()
     g = torch.Generator().manual_seed(1)
@@ -144,6 +201,16 @@ def main():
               f"{(time.perf_counter() - t) * 1e3:.1f} ms")
     for p, i in zip(prompts, ids):
         print(len(p), "->", i[len(p):])
+    if a.beams:
+        for _ in range(2):
+            torch.cuda.synchronize()
+            t = time.perf_counter()
+            ids, _, scores = beam_search(model, prompts, a.steps, beams=a.beams, keep=a.keep)
+            torch.cuda.synchronize()
+            took = time.perf_counter() - t
+        print(f"{len(prompts)} x {a.beams} beams, {a.steps} tokens each in {took * 1e3:.1f} ms")
+        for p, i, s in zip(prompts, ids.tolist(), scores.tolist()):
+            print(len(p), "->", i[0][len(p):len(p) + a.steps], "%.2f" % s[0])
 
 
 if __name__ == "__main__":

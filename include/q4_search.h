@@ -1,0 +1,199 @@
+/*
+ * q4_search.h -- C ABI of libq4amd's operators around a decoder's paged cache
+ * for AMD Instinct MI355X (gfx950): several continuations of one prompt, and
+ * contexts that are too long to be read for every token.
+ *
+ *   q4_beam_select          the best continuations of a group's beams;
+ *   q4_beam_advance         the tokens of the beams that were kept;
+ *   q4_kv_fork              block tables of sequences that go on from others:
+ *                           blocks are shared, and one that is about to be
+ *                           written gets a copy; blocks for new tokens; blocks
+ *                           that nobody holds any more are free;
+ *   q4_kv_compact           block tables of a cache whose blocks move together;
+ *   q4_kv_copy_blocks       the copies that these two ask for, in every layer;
+ *   q4_kv_summarize         bounds of the keys of a cache's blocks;
+ *   q4_kv_select            the blocks that matter most to a row, by the bounds;
+ *   q4_kv_attention_blocks  attention over the selected blocks alone.
+ *
+ * The conventions of q4_decoder.h hold: device pointers, the caller's buffers
+ * and stream, every argument checked before any HIP call, nothing allocated,
+ * results equal bit for bit from call to call; what lies in device memory is
+ * checked by the kernels, which never read or write out of range for it.
+ * Outputs must not overlap inputs, nor a workspace.  A workspace's content is
+ * free before and after a call; calls that may run at the same time need one
+ * each.
+ */
+#ifndef Q4_SEARCH_H
+#define Q4_SEARCH_H
+
+#include "q4_decoder.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * Beam search's selection.  There are `groups` groups of `beams` beams; row
+ * g * beams + b of logits [groups * beams, V] (fp32, device) has the logits of
+ * the next token of beam b of group g, scores [groups, beams] (fp32) the
+ * beams' scores so far.  Token v behind a beam has the score
+ *     s = scores[g, b] + (z_v - log sum_u exp z_u),
+ * in 64 bits; a beam whose `finished` [groups, beams] (int32, may be NULL) is
+ * not 0 has one candidate, the token `pad`, with s = scores[g, b].  What has no
+ * finite s is no candidate: masked tokens (z = -inf), beams with a score of
+ * -inf, and rows whose logits hold +inf or what is not a number.
+ *
+ * Of each group the `keep` candidates of largest s are returned in falling
+ * order, of equal ones the one of the lower beam, then of the lower token:
+ * parents [groups, keep] int32, the row of the beam (g * beams + b), tokens
+ * [groups, keep] int32 and out_scores [groups, keep], s rounded to fp32.  Where
+ * there are fewer candidates the rest have parent -1, token -1 and score -inf.
+ *
+ * 0 <= groups, 1 <= beams <= 64, groups * beams <= 65535, 1 <= V <= 2^24,
+ * 1 <= keep <= 128, 0 <= pad < 2^31.  All pointers 4-byte aligned (workspace:
+ * 16), rows contiguous.
+ */
+size_t q4_beam_select_workspace(int64_t groups, int64_t beams, int64_t V);   /* 0 if invalid, or nothing to do */
+q4_status q4_beam_select(const float *logits, int64_t groups, int64_t beams, int64_t V, const float *scores,
+                         const int32_t *finished, int32_t pad, int64_t keep, int32_t *parents, int32_t *tokens,
+                         float *out_scores, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The tokens of the sequences that go on.  sequences [rows, width] int32 holds
+ * the tokens so far, lengths [rows] int32 how many of them, finished [rows]
+ * int32 (may be NULL: none) whether a sequence has ended.  Sequence i of the
+ * n_out new ones is that of row parents[i], followed by tokens[i] unless it has
+ * ended or there is no room for it; the rest of its row is `pad`.  It has ended
+ * where its parent had, where there was no room, and where tokens[i] == eos
+ * (eos < 0: no token ends).  A parent outside [0, rows) gives an empty
+ * sequence that has ended.  Lengths are held to 0 .. width.
+ * 0 <= rows, n_out <= 2^20, 1 <= width <= 2^24.  All pointers 4-byte aligned.
+ */
+q4_status q4_beam_advance(const int32_t *sequences, int64_t rows, int64_t width, const int32_t *lengths,
+                          const int32_t *finished, const int32_t *parents, const int32_t *tokens, int64_t n_out,
+                          int32_t eos, int32_t pad, int32_t *out_sequences, int32_t *out_lengths,
+                          int32_t *out_finished, void *stream);
+
+/*
+ * Block tables of sequences that go on from others.  The tables say which
+ * blocks are in use: a block is held by the sequences whose first
+ * ceil(length / 32) table entries name it, and by `held` [num_blocks] int32
+ * (may be NULL) others that the tables do not show (a store of prefixes,
+ * sequences of another batch); what nobody holds is free.
+ *
+ * block_table [rows, table_width] and lengths [rows] describe the sequences
+ * before the call, lengths without the tokens to come.  New sequence i of n_out
+ * is a copy of sequence parents[i] (several may have one parent; a parent
+ * outside [0, rows) gives an empty sequence, which is how one ends) that can
+ * take grow[i] more tokens (grow NULL: `grow_each`; for a new sequence in a
+ * free slot the parent is a row of length 0; negative counts as 0):
+ *   - its last block, where that is partly filled, tokens are to come and
+ *     others hold it as well, is replaced by a free one, and the two are
+ *     returned as src[i], dst[i] (-1: no copy).  Of the new sequences that all go
+ *     on in a block that nobody else holds the last one keeps it;
+ *   - free blocks follow for the tokens that its blocks have no room for.
+ * Free blocks are handed out in rising order of their ids, to the sequences in
+ * their order, a copy's before the new ones.  Where none is left, or the table
+ * has no room, the table entry is -1 and short_of[i] counts it (0 otherwise): the
+ * caller has to look before it goes on with that sequence.
+ *
+ * Outputs: out_table [n_out, table_width], -1 past a sequence's blocks,
+ * out_lengths [n_out] with the tokens to come (as q4_kv_append takes them),
+ * refs [num_blocks], how many hold each block now, src, dst, short_of [n_out].
+ * Ids outside [0, num_blocks) are passed on and hold nothing; lengths are held
+ * to 0 .. 32 * table_width.
+ * 0 <= rows, n_out <= 65535, 1 <= table_width <= 2^20, rows * table_width and n_out * table_width < 2^31,
+ * 1 <= num_blocks <= 2^24, grow up to 2^25.  All pointers 4-byte aligned.
+ */
+size_t q4_kv_fork_workspace(int64_t n_out, int64_t num_blocks);   /* 0 if invalid, or nothing to do */
+q4_status q4_kv_fork(const int32_t *block_table, int64_t rows, int64_t table_width, const int32_t *lengths,
+                     const int32_t *parents, int64_t n_out, const int32_t *grow, int64_t grow_each,
+                     const int32_t *held, int64_t num_blocks, int32_t *out_table, int32_t *out_lengths,
+                     int32_t *refs, int32_t *src, int32_t *dst, int32_t *short_of, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Moves a cache's blocks together.  With L blocks in use (held by a sequence or
+ * by `held`), those with ids of L and more move, in rising order, to the free
+ * ids below L, in rising order; ones that `held` names stay where they are, since
+ * their holders cannot be told.  Returned are the copies, src and dst
+ * [max(1, num_blocks / 2)] (-1 past the last), out_table [rows, table_width] (-1
+ * past a sequence's blocks), and live [1], L.  After the copies all blocks from
+ * L on that `held` does not name are free.  Ids outside [0, num_blocks) become -1.
+ * Limits and alignment as for q4_kv_fork.
+ */
+size_t q4_kv_compact_workspace(int64_t num_blocks);   /* 0 if invalid */
+q4_status q4_kv_compact(const int32_t *block_table, int64_t rows, int64_t table_width, const int32_t *lengths,
+                        const int32_t *held, int64_t num_blocks, int32_t *out_table, int32_t *src, int32_t *dst,
+                        int32_t *live, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Copies block src[i] to block dst[i], codes and exponents, in each of `layers`
+ * caches of one shape: cache->data is not used, data[l] (a host array) is the
+ * data of layer l.  summaries (a host array, may be NULL) are those of
+ * q4_kv_summarize, which are copied too.  Pairs with an id outside
+ * [0, num_blocks) are passed over.  No block may be in dst twice, or in both.
+ * 0 <= n, 0 <= layers <= 1024; data 16-byte aligned, summaries 16, src and dst 4.
+ */
+q4_status q4_kv_copy_blocks(const q4_kv_cache *cache, void *const *data, void *const *summaries, int64_t layers,
+                            const int32_t *src, const int32_t *dst, int64_t n, void *stream);
+
+/*
+ * Bounds of the keys of a block, for each kv head and dimension over the tokens
+ * that the block has: int8 [num_blocks][kv_heads][hi | lo][head_dim],
+ *     hi = ceil(max code / 4),  lo = floor(min code / 4),
+ * so that 4 lo 2^e <= k <= 4 hi 2^e with the block's exponent e.  With a code
+ * that is not a number hi is 127 and lo -127.
+ *
+ * Written are the bounds of the blocks that hold the batch's rows, that is
+ * after q4_kv_append with the same batch: as long as every append is followed
+ * by it, the bounds of all blocks hold.  summary: device, 16-byte aligned.
+ * Unlike elsewhere batch->max_length is not used.
+ */
+size_t q4_kv_summary_bytes(int64_t num_blocks, int64_t kv_heads, int64_t head_dim);   /* 0 if invalid */
+q4_status q4_kv_summarize(const q4_kv_cache *cache, const q4_kv_batch *batch, void *summary, void *stream);
+
+/*
+ * The blocks that matter most to each row and kv head, of those that hold
+ * tokens that the row sees.  With q_h the heads of the group,
+ *     Q+ = sum_h max(q_h, 0),  Q- = sum_h min(q_h, 0),
+ * both quantized to whole multiples of 2^(E - 13), E the smallest with
+ * |Q+|, |Q-| < 2^E (ties to even), a block's score is
+ *     2^e (Q+ . hi + Q- . lo):
+ * but for the quantization of Q an upper bound of sum_h q_h . k_j over its tokens, times a
+ * constant.  The sums are whole numbers and exact; the score is rounded to
+ * fp32.  A row of q that is not finite has scores of 0; a block whose id is outside
+ * [0, num_blocks) or past table_width has -inf.
+ *
+ * The first `first` blocks and the last `recent` ones (up to the row's own) are
+ * chosen in any case, the others by their score, of equal ones the one in front.
+ * chosen: int32 [rows, kv_heads, keep], indices of blocks within the sequence in
+ * rising order, -1 past the last; a row without a position has none.  A row at a
+ * position of batch->max_length (rounded up to whole blocks) or more has none
+ * either: max_length has to cover the sequences.
+ * q as in q4_kv_attention.  1 <= keep <= 2^16, first, recent >= 0, first + recent <= keep.
+ * workspace: 16-byte aligned.
+ */
+size_t q4_kv_select_workspace(const q4_kv_cache *cache, const q4_kv_batch *batch);
+q4_status q4_kv_select(const q4_kv_cache *cache, const q4_kv_batch *batch, const void *summary, const void *q,
+                       int64_t q_heads, int64_t keep, int64_t first, int64_t recent, int32_t *chosen,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * q4_kv_attention over the chosen blocks alone: chosen [rows, kv_heads, keep] as
+ * q4_kv_select returns it.  Entries that are negative, or name a block past the
+ * row's own, are passed over, the order does not matter but for rounding, and a block that is
+ * named twice counts twice.  A row that sees nothing gives 0.  In all else as
+ * q4_kv_attention (without a window); max_length is not used.
+ */
+size_t q4_kv_attention_blocks_workspace(const q4_kv_cache *cache, const q4_kv_batch *batch, int64_t q_heads,
+                                        int64_t keep);
+q4_status q4_kv_attention_blocks(const q4_kv_cache *cache, const q4_kv_batch *batch, const void *q, int64_t q_heads,
+                                 const int32_t *chosen, int64_t keep, float scale, void *out, int out_dtype,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* Q4_SEARCH_H */

@@ -2,8 +2,8 @@
 between the linears.
 
 The computation lives in libq4amd.so (HIP kernels for gfx950 behind the C ABI
-of include/q4_0.h and include/q4_decoder.h); this package is its thin Python binding.  The library is
-loaded on first use and a missing build raises instead of falling back.
+of include/q4_0.h, include/q4_decoder.h and include/q4_search.h); this package is its thin Python binding.
+The library is loaded on first use and a missing build raises instead of falling back.
 """
 
 from ._binding import (  # noqa: F401
@@ -49,4 +49,24 @@ from ._decoder import (  # noqa: F401
     kv_cache_bytes,
     logits_adjust,
     rope_table,
+)
+from ._search import (  # noqa: F401
+    SEARCH_EXPORTS,
+    KVCompact,
+    KVFork,
+    KVStack,
+    beam_advance,
+    beam_select,
+    beam_select_workspace,
+    kv_attention_blocks,
+    kv_attention_blocks_workspace,
+    kv_compact,
+    kv_compact_workspace,
+    kv_copy_blocks,
+    kv_fork,
+    kv_fork_workspace,
+    kv_select,
+    kv_select_workspace,
+    kv_summarize,
+    kv_summary,
 )

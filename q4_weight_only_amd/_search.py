@@ -1,0 +1,254 @@
+"""Python interface of libq4amd's operators around the paged cache
+(include/q4_search.h): beam search, the cache's pages, and attention over blocks
+that a score selects.
+
+The computation runs in the HIP library on the current stream of the tensors'
+device; the calls go through the native binding, which checks the tensors and
+makes the outputs.  A missing build raises.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import threading
+from typing import NamedTuple
+
+import torch
+
+from . import _binding as B
+from . import _decoder as D
+
+SEARCH_EXPORTS = ("q4_beam_select_workspace", "q4_beam_select", "q4_beam_advance", "q4_kv_fork_workspace", "q4_kv_fork",
+                  "q4_kv_compact_workspace", "q4_kv_compact", "q4_kv_copy_blocks", "q4_kv_summary_bytes", "q4_kv_summarize",
+                  "q4_kv_select_workspace", "q4_kv_select", "q4_kv_attention_blocks_workspace", "q4_kv_attention_blocks")
+
+_lib = None
+_lock = threading.Lock()
+
+
+def search_lib() -> ctypes.CDLL:
+    """libq4amd with these operators' argument types set."""
+    global _lib
+    if _lib is None:
+        with _lock:
+            if _lib is None:
+                L = B.lib()
+                vp, i64, i32, f32, size = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_size_t
+                for name, args in {"q4_beam_select_workspace": [i64, i64, i64], "q4_kv_fork_workspace": [i64, i64],
+                                   "q4_kv_compact_workspace": [i64], "q4_kv_summary_bytes": [i64, i64, i64],
+                                   "q4_kv_select_workspace": [vp, vp],
+                                   "q4_kv_attention_blocks_workspace": [vp, vp, i64, i64]}.items():
+                    getattr(L, name).argtypes = args
+                    getattr(L, name).restype = size
+                for name, args in {
+                        "q4_beam_select": [vp, i64, i64, i64, vp, vp, i32, i64, vp, vp, vp, vp, size, vp],
+                        "q4_beam_advance": [vp, i64, i64, vp, vp, vp, vp, i64, i32, i32, vp, vp, vp, vp],
+                        "q4_kv_fork": [vp, i64, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp, size, vp],
+                        "q4_kv_compact": [vp, i64, i64, vp, vp, i64, vp, vp, vp, vp, vp, size, vp],
+                        "q4_kv_copy_blocks": [vp, vp, vp, i64, vp, vp, i64, vp],
+                        "q4_kv_summarize": [vp, vp, vp, vp],
+                        "q4_kv_select": [vp, vp, vp, vp, i64, i64, i64, i64, vp, vp, size, vp],
+                        "q4_kv_attention_blocks": [vp, vp, vp, i64, vp, i64, f32, vp, i32, vp, size, vp]}.items():
+                    getattr(L, name).argtypes = args
+                    getattr(L, name).restype = ctypes.c_int
+                _lib = L
+    return _lib
+
+
+# ------------------------------------------------------------ beam search
+def beam_select(logits: torch.Tensor, scores: torch.Tensor, keep: int, *, finished: torch.Tensor | None = None, pad: int = 0,
+                out: tuple | None = None, workspace: torch.Tensor | None = None):
+    """(parents, tokens, scores), each [groups, keep]: of every group of beams
+    the best continuations, in falling order.
+
+    logits fp32 [groups * beams, V] (logits_adjust's result goes in as it is),
+    scores fp32 [groups, beams], the beams' so far; a continuation has the beam's
+    score plus the token's log-probability, in 64 bits.  finished int32 [groups,
+    beams]: a beam where it is not 0 has one continuation, `pad`, with its score.
+    parents int32 are rows of the logits, tokens int32; ties go to the lower
+    beam, then the lower token.  Where there are fewer continuations (of finite
+    score) than `keep`, at most 128, the rest have parent and token -1 and score
+    -inf.  workspace: uint8, beam_select_workspace() bytes; None takes one from
+    torch's allocator for the call."""
+    return (D._native or D._load()).beam_select(logits, scores, keep, finished, pad, out, workspace)
+
+
+def beam_select_workspace(groups: int, beams: int, vocab: int) -> int:
+    """Bytes of workspace of beam_select."""
+    return int(search_lib().q4_beam_select_workspace(int(groups), int(beams), int(vocab)))
+
+
+def beam_advance(sequences: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor, tokens: torch.Tensor, *,
+                 finished: torch.Tensor | None = None, eos: int = -1, pad: int = 0, out: tuple | None = None):
+    """(sequences, lengths, finished) of the beams that go on: the tokens of
+    row parents[i] followed by tokens[i], unless that row has ended (finished) or
+    has no room; the rest of a row is `pad`.  A sequence has ended with the token
+    `eos` (negative: none), where it had before, and where there was no room; one
+    without a parent is empty and has ended.  All int32: sequences [rows, width], lengths and finished
+    of rows values, parents and tokens (beam_select's) of any shape."""
+    return (D._native or D._load()).beam_advance(sequences, lengths, parents, tokens, finished, eos, pad, out)
+
+
+# ------------------------------------------------------------------- pages
+class KVStack:
+    """The caches of all layers in one uint8 tensor [layers, bytes], whose rows
+    are of one shape and start on 16 bytes (KVStack.empty makes one); stack[i] is the
+    KVCache of layer i."""
+
+    __slots__ = ("data", "num_blocks", "kv_heads", "head_dim")
+
+    def __init__(self, data: torch.Tensor, num_blocks: int, kv_heads: int, head_dim: int):
+        if not (1 <= num_blocks <= 1 << 24 and 1 <= kv_heads <= 256 and head_dim in (64, 128)):
+            raise ValueError("need 1..2^24 blocks, 1..256 kv heads and a head_dim of 64 or 128")
+        if not isinstance(data, torch.Tensor) or not data.is_cuda or data.dtype != torch.uint8 or data.dim() != 2:
+            raise ValueError("data must be a uint8 CUDA/HIP tensor [layers, bytes]")
+        if data.size(1) < num_blocks * kv_heads * 2 * (D.KV_BLOCK * head_dim + 1) or data.stride(1) != 1 or \
+                data.stride(0) % 16 or data.data_ptr() % 16:
+            raise ValueError("each layer must have its bytes in one piece, starting on 16 bytes")
+        self.data, self.num_blocks, self.kv_heads, self.head_dim = data, num_blocks, kv_heads, head_dim
+
+    @classmethod
+    def empty(cls, layers: int, num_blocks: int, kv_heads: int, head_dim: int, device="cuda") -> "KVStack":
+        """Caches of zeros."""
+        nbytes = (D.kv_cache_bytes(num_blocks, kv_heads, head_dim) + 15) // 16 * 16
+        return cls(torch.zeros((layers, nbytes), dtype=torch.uint8, device=device), num_blocks, kv_heads, head_dim)
+
+    def __len__(self) -> int:
+        return self.data.size(0)
+
+    def __getitem__(self, layer: int) -> D.KVCache:
+        nbytes = self.num_blocks * self.kv_heads * 2 * (D.KV_BLOCK * self.head_dim + 1)
+        return D.KVCache(self.data[layer, :nbytes], self.num_blocks, self.kv_heads, self.head_dim)
+
+
+class KVFork(NamedTuple):
+    """kv_fork's result: block_table [n, width], lengths [n] with the tokens to
+    come, refs [num_blocks], the copies src -> dst [n] (-1: none), and short [n],
+    how many blocks a sequence could not have."""
+
+    block_table: torch.Tensor
+    lengths: torch.Tensor
+    refs: torch.Tensor
+    src: torch.Tensor
+    dst: torch.Tensor
+    short: torch.Tensor
+
+
+class KVCompact(NamedTuple):
+    """kv_compact's result: block_table [rows, width], the copies src -> dst
+    [num_blocks // 2] (-1 past the last), and live [1], the blocks in use."""
+
+    block_table: torch.Tensor
+    src: torch.Tensor
+    dst: torch.Tensor
+    live: torch.Tensor
+
+
+def kv_fork(block_table: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor, num_blocks: int, *,
+            grow: int | torch.Tensor = 1, held: torch.Tensor | None = None, out: tuple | None = None,
+            workspace: torch.Tensor | None = None) -> KVFork:
+    """Block tables of sequences that go on from others (all int32).
+
+    New sequence i continues row parents[i] of block_table [rows, width] and
+    lengths [rows] (its tokens so far), sharing its blocks, and has room for `grow` more tokens
+    (one number, or one for each); a parent outside the rows ends a sequence.  A
+    partly filled last block that others hold as well is replaced by a copy, src[i] ->
+    dst[i], which kv_copy_blocks makes; other blocks come from those that no
+    sequence and no `held` [num_blocks] count holds any more, lowest first.  The
+    lengths that come back count the new tokens, as kv_append takes them.  Where
+    blocks run out the entry is -1 and `short` counts it."""
+    return KVFork._make((D._native or D._load()).kv_fork(block_table, lengths, parents, num_blocks, grow, held, out, workspace))
+
+
+def kv_fork_workspace(sequences: int, num_blocks: int) -> int:
+    """Bytes of workspace of kv_fork for `sequences` new sequences."""
+    return int(search_lib().q4_kv_fork_workspace(int(sequences), int(num_blocks)))
+
+
+def kv_compact(block_table: torch.Tensor, lengths: torch.Tensor, num_blocks: int, *, held: torch.Tensor | None = None,
+               out: tuple | None = None, workspace: torch.Tensor | None = None) -> KVCompact:
+    """Moves a cache's blocks together: the blocks in use, `live` of them, at ids
+    of `live` and more go to the free ids below it, except those that `held` int32
+    [num_blocks] counts.  kv_copy_blocks makes the copies."""
+    return KVCompact._make((D._native or D._load()).kv_compact(block_table, lengths, num_blocks, held, out, workspace))
+
+
+def kv_compact_workspace(num_blocks: int) -> int:
+    """Bytes of workspace of kv_compact."""
+    return int(search_lib().q4_kv_compact_workspace(int(num_blocks)))
+
+
+def kv_copy_blocks(caches, src: torch.Tensor, dst: torch.Tensor, *, summaries=None) -> None:
+    """Copies blocks src[i] to dst[i] (int32, -1: none) in all caches: a KVStack,
+    a KVCache or a list of KVCache of one shape.  summaries: those of kv_summarize in the same
+    form, an int8 tensor with a row for each layer, or a list of tensors."""
+    first = caches
+    if isinstance(caches, KVStack):
+        data = caches.data
+    else:
+        if isinstance(caches, D.KVCache):
+            caches = [caches]
+        if not caches:
+            return
+        first = caches[0]
+        if any((c.num_blocks, c.kv_heads, c.head_dim) != (first.num_blocks, first.kv_heads, first.head_dim) for c in caches):
+            raise ValueError("the caches must have one shape")
+        data = [c.data for c in caches]
+    if isinstance(summaries, torch.Tensor):
+        summaries = summaries.flatten(1) if isinstance(data, torch.Tensor) else [summaries]
+    (D._native or D._load()).kv_copy_blocks(data, first.num_blocks, first.kv_heads, first.head_dim, src, dst, summaries)
+
+
+# -------------------------------------------------------- selected blocks
+def kv_summary(cache: D.KVCache) -> torch.Tensor:
+    """An empty summary of a cache: int8 [num_blocks, kv_heads, 2, head_dim]."""
+    return torch.zeros((cache.num_blocks, cache.kv_heads, 2, cache.head_dim), dtype=torch.int8, device=cache.device)
+
+
+def kv_summarize(cache: D.KVCache, summary: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor,
+                 cu_rows: torch.Tensor | None = None, *, rows: int, max_rows: int | None = None) -> None:
+    """Bounds of the keys of the blocks that kv_append's `rows` rows are in, into
+    the cache's summary (int8 [num_blocks, kv_heads, hi and lo, head_dim]).  To be called after every kv_append,
+    with its block_table, lengths, cu_rows and max_rows."""
+    (D._native or D._load()).kv_summarize(summary, cache.data, cache.num_blocks, cache.kv_heads, cache.head_dim, block_table,
+                                          lengths, cu_rows, max_rows, None, rows)
+
+
+def kv_select(q: torch.Tensor, cache: D.KVCache, summary: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor,
+              cu_rows: torch.Tensor | None = None, *, keep: int, first: int = 1, recent: int = 2, max_rows: int | None = None,
+              max_length: int | None = None, out: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The blocks of a sequence that matter most to each row of q [rows, q_heads
+    * D] (bf16, kv_append's result) and kv head: int32 [rows, kv_heads, keep],
+    indices within the sequence in rising order, -1 past the last.
+
+    A block's score is an upper bound of the sum of q . k over the heads of the group, for its
+    keys; the `first` first and the `recent` last blocks are chosen in any case.
+    max_length has to cover the sequences (None: what the table allows): a row
+    at a later position has no blocks.  The others as for kv_attention."""
+    return (D._native or D._load()).kv_select(q, summary, cache.data, cache.num_blocks, cache.kv_heads, cache.head_dim, block_table,
+                                              lengths, cu_rows, max_rows, max_length, keep, first, recent, out, workspace)
+
+
+def kv_select_workspace(cache: D.KVCache, block_table: torch.Tensor, rows: int, *, max_length: int) -> int:
+    """Bytes of workspace of kv_select for these sizes."""
+    c, bt = D._shapes(cache, block_table, rows, 1, max_length)
+    return int(search_lib().q4_kv_select_workspace(ctypes.byref(c), ctypes.byref(bt)))
+
+
+def kv_attention_blocks(q: torch.Tensor, cache: D.KVCache, chosen: torch.Tensor, block_table: torch.Tensor, lengths: torch.Tensor,
+                        cu_rows: torch.Tensor | None = None, *, max_rows: int | None = None, scale: float | None = None,
+                        out: torch.Tensor | None = None, dtype: torch.dtype = torch.bfloat16,
+                        workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """kv_attention over the blocks `chosen` int32 [rows, kv_heads, keep] of each
+    row alone (kv_select's result; negative entries and blocks past the row's are
+    passed over, a block named twice counts twice)."""
+    return (D._native or D._load()).kv_attention_blocks(q, chosen, cache.data, cache.num_blocks, cache.kv_heads, cache.head_dim,
+                                                        block_table, lengths, cu_rows, max_rows, None, scale, out, dtype,
+                                                        workspace)
+
+
+def kv_attention_blocks_workspace(cache: D.KVCache, block_table: torch.Tensor, rows: int, q_heads: int, keep: int) -> int:
+    """Bytes of workspace of kv_attention_blocks for these sizes."""
+    c, bt = D._shapes(cache, block_table, rows, 1, 1)
+    return int(search_lib().q4_kv_attention_blocks_workspace(ctypes.byref(c), ctypes.byref(bt), int(q_heads), int(keep)))

@@ -26,7 +26,8 @@ LIB = os.path.join(PKG, "libq4amd.so")
 BINDING = os.path.join(PKG, "_q4decoder.so")     # the decoder operators' Python binding
 
 SOURCES = ("q4_0_format.hip", "q4_1_format.hip", "q4_0_linear.hip", "q4_0_measure.hip", "q4_0_abi.hip",
-           "q4_kv_append.hip", "q4_kv_attention.hip", "q4_rmsnorm.hip", "q4_logits.hip", "q4_decoder_abi.hip")
+           "q4_kv_append.hip", "q4_kv_attention.hip", "q4_rmsnorm.hip", "q4_logits.hip", "q4_decoder_abi.hip",
+           "q4_beam.hip", "q4_kv_pages.hip", "q4_kv_select.hip", "q4_kv_blocks.hip", "q4_search_abi.hip")
 ARCH = "gfx950"
 
 COMMON_FLAGS = [

@@ -1,0 +1,172 @@
+// What the functions of the Python binding share: tensors and numbers out of
+// their arguments, with the checks that these need.
+#pragma once
+
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <ATen/hip/EmptyTensor.h>
+#include <c10/hip/HIPGuard.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include "q4_decoder.h"
+
+namespace {
+
+PyObject *g_error = nullptr;   // called with (status, name): the exception of a status
+
+// A tensor argument, or null for None.
+const at::Tensor *optional(PyObject *o, const char *name) {
+    if (o == Py_None) return nullptr;
+    TORCH_CHECK_VALUE(THPVariable_Check(o), name, " must be a tensor");
+    return &THPVariable_Unpack(o);
+}
+
+const at::Tensor &required(PyObject *o, const char *name) {
+    const at::Tensor *t = optional(o, name);
+    TORCH_CHECK_VALUE(t, name, " must be a tensor");
+    return *t;
+}
+
+c10::Device device_of(const at::Tensor &t, const char *name) {
+    TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA/HIP tensor");
+    return t.device();
+}
+
+int type_code(at::ScalarType t, const char *name) {
+    TORCH_CHECK_VALUE(t == at::kFloat || t == at::kBFloat16, name, " must be float32 or bfloat16, got ", t);
+    return t == at::kBFloat16 ? Q4_BF16 : Q4_F32;
+}
+
+// The address of a contiguous tensor of one type on one device (null for none).
+void *address(const at::Tensor *t, const char *name, at::ScalarType type, c10::Device dev) {
+    if (!t) return nullptr;
+    TORCH_CHECK_VALUE(t->device() == dev, name, " must be a CUDA/HIP tensor on the inputs' device");
+    TORCH_CHECK_VALUE(t->scalar_type() == type, name, " must be ", type, ", got ", t->scalar_type());
+    TORCH_CHECK_VALUE(t->is_contiguous(), name, " must be contiguous");
+    return t->data_ptr();
+}
+
+template <typename T>
+T *address(const at::Tensor *t, const char *name, at::ScalarType type, c10::Device dev) {
+    return static_cast<T *>(address(t, name, type, dev));
+}
+
+void has_shape(const at::Tensor *t, const char *name, at::IntArrayRef shape) {
+    TORCH_CHECK_VALUE(!t || t->sizes() == shape, name, " must be ", shape);
+}
+
+at::Tensor output(PyObject *given, const char *name, at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
+    if (const at::Tensor *t = optional(given, name)) {
+        address(t, name, type, dev);
+        has_shape(t, name, shape);
+        return *t;
+    }
+    return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));   // at::empty without its dispatch
+}
+
+int64_t integer(PyObject *o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw python_error();
+    return v;
+}
+
+// `none` where the argument is None
+int64_t integer_or(PyObject *o, int64_t none) { return o == Py_None ? none : integer(o); }
+
+double number(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw python_error();
+    return v;
+}
+
+at::ScalarType dtype_of(PyObject *o) {
+    TORCH_CHECK_VALUE(THPDtype_Check(o), "dtype must be a torch.dtype");
+    return reinterpret_cast<THPDtype *>(o)->scalar_type;
+}
+
+void check(q4_status st, const char *what) {
+    if (st == Q4_OK) return;
+    PyObject *e = PyObject_CallFunction(g_error, "is", static_cast<int>(st), what);
+    if (e) {
+        PyErr_SetObject(reinterpret_cast<PyObject *>(Py_TYPE(e)), e);
+        Py_DECREF(e);
+    }
+    throw python_error();
+}
+
+void want(Py_ssize_t got, Py_ssize_t n) { TORCH_CHECK_TYPE(got == n, "takes ", n, " arguments, got ", got); }
+
+// (data, num_blocks, kv_heads, head_dim)
+q4_kv_cache cache_of(PyObject *const *a, c10::Device dev) {
+    q4_kv_cache c;
+    const at::Tensor &data = required(a[0], "the cache");
+    TORCH_CHECK_VALUE(data.device() == dev, "the cache is on ", data.device(), ", not ", dev);
+    c.data = address(&data, "the cache", at::kByte, dev);
+    c.num_blocks = integer(a[1]);
+    c.kv_heads = static_cast<int32_t>(integer(a[2]));
+    c.head_dim = static_cast<int32_t>(integer(a[3]));
+    TORCH_CHECK_VALUE(data.numel() == static_cast<int64_t>(q4_kv_cache_bytes(c.num_blocks, c.kv_heads, c.head_dim)),
+                      "the cache's data does not have its size");
+    return c;
+}
+
+// (block_table, lengths, cu_rows or None, max_rows or None, max_length or None)
+q4_kv_batch batch_of(PyObject *const *a, int64_t rows, c10::Device dev) {
+    const at::Tensor &table = required(a[0], "block_table"), &lengths = required(a[1], "lengths");
+    const at::Tensor *cu = optional(a[2], "cu_rows");
+    q4_kv_batch b;
+    b.block_table = address<int32_t>(&table, "block_table", at::kInt, dev);
+    b.lengths = address<int32_t>(&lengths, "lengths", at::kInt, dev);
+    TORCH_CHECK_VALUE(table.dim() == 2 && lengths.dim() == 1 && table.size(0) == lengths.size(0),
+                      "block_table must be [batch, width] and lengths [batch]");
+    b.batch = table.size(0);
+    b.table_width = table.size(1);
+    b.cu_rows = address<int32_t>(cu, "cu_rows", at::kInt, dev);
+    has_shape(cu, "cu_rows", {b.batch + 1});
+    b.rows = rows;
+    const int64_t each = cu || !b.batch ? rows : rows / b.batch;
+    b.max_rows = std::max<int64_t>(1, integer_or(a[3], each));
+    b.max_length = std::max<int64_t>(1, integer_or(a[4], b.table_width * Q4_KV_BLOCK));
+    return b;
+}
+
+// The caller's workspace, or one of torch's allocator for the call, which goes
+// back to it for work on this stream after the call's.
+struct Workspace {
+    c10::DataPtr own;
+    void *data = nullptr;
+    size_t bytes = 0;
+    Workspace(PyObject *given, int64_t need, c10::Device dev) {
+        bytes = static_cast<size_t>(need);
+        if (const at::Tensor *t = optional(given, "workspace")) {
+            data = address(t, "workspace", at::kByte, dev);
+            bytes = static_cast<size_t>(t->numel());
+            TORCH_CHECK_VALUE(t->numel() >= need, "workspace must hold ", need, " bytes");
+        } else if (need) {
+            own = c10::GetAllocator(dev.type())->allocate(need);
+            data = own.get();
+        }
+    }
+};
+
+// Item i of `out`, a tuple or list of n tensors or None.
+PyObject *out_item(PyObject *out, Py_ssize_t n, Py_ssize_t i) {
+    if (out == Py_None) return Py_None;
+    TORCH_CHECK_VALUE(PyTuple_Check(out) || PyList_Check(out), "out must be a tuple of ", n, " tensors");
+    TORCH_CHECK_VALUE(PySequence_Fast_GET_SIZE(out) == n, "out must be a tuple of ", n, " tensors");
+    return PySequence_Fast_GET_ITEM(out, i);
+}
+
+// A new tuple of the tensors.
+PyObject *tuple_of(std::initializer_list<at::Tensor *> tensors) {
+    PyObject *t = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
+    if (!t) throw python_error();
+    Py_ssize_t i = 0;
+    for (at::Tensor *x : tensors) PyTuple_SET_ITEM(t, i++, THPVariable_Wrap(std::move(*x)));
+    return t;
+}
+
+}  // namespace

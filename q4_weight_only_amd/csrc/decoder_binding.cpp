@@ -1,141 +1,16 @@
-// Python binding of the decoder operators (include/q4_decoder.h): checks of
-// the tensors, their outputs and workspace from torch's allocator, the current
-// stream, and the call.
+// Python binding of the decoder operators (include/q4_decoder.h, and
+// include/q4_search.h in search_binding.h): checks of the tensors, their
+// outputs and workspace from torch's allocator, the current stream, and the
+// call.
 //
 // It is native because these operators are short: a decode step's norm runs
 // for 2.5 us, and the same checks written in Python with a ctypes call take 13 us
 // (this: 4.5 us, launch included).  Nothing is computed here.
 
-#include <Python.h>
-
-#include <ATen/ATen.h>
-#include <ATen/hip/EmptyTensor.h>
-#include <c10/hip/HIPGuard.h>
-#include <c10/hip/HIPStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include "q4_decoder.h"
+#include "binding_helpers.h"
+#include "search_binding.h"
 
 namespace {
-
-PyObject *g_error = nullptr;   // called with (status, name): the exception of a status
-
-// A tensor argument, or null for None.
-const at::Tensor *optional(PyObject *o, const char *name) {
-    if (o == Py_None) return nullptr;
-    TORCH_CHECK_VALUE(THPVariable_Check(o), name, " must be a tensor");
-    return &THPVariable_Unpack(o);
-}
-
-const at::Tensor &required(PyObject *o, const char *name) {
-    const at::Tensor *t = optional(o, name);
-    TORCH_CHECK_VALUE(t, name, " must be a tensor");
-    return *t;
-}
-
-c10::Device device_of(const at::Tensor &t, const char *name) {
-    TORCH_CHECK_VALUE(t.is_cuda(), name, " must be a CUDA/HIP tensor");
-    return t.device();
-}
-
-int type_code(at::ScalarType t, const char *name) {
-    TORCH_CHECK_VALUE(t == at::kFloat || t == at::kBFloat16, name, " must be float32 or bfloat16, got ", t);
-    return t == at::kBFloat16 ? Q4_BF16 : Q4_F32;
-}
-
-// The address of a contiguous tensor of one type on one device (null for none).
-void *address(const at::Tensor *t, const char *name, at::ScalarType type, c10::Device dev) {
-    if (!t) return nullptr;
-    TORCH_CHECK_VALUE(t->device() == dev, name, " must be a CUDA/HIP tensor on the inputs' device");
-    TORCH_CHECK_VALUE(t->scalar_type() == type, name, " must be ", type, ", got ", t->scalar_type());
-    TORCH_CHECK_VALUE(t->is_contiguous(), name, " must be contiguous");
-    return t->data_ptr();
-}
-
-template <typename T>
-T *address(const at::Tensor *t, const char *name, at::ScalarType type, c10::Device dev) {
-    return static_cast<T *>(address(t, name, type, dev));
-}
-
-void has_shape(const at::Tensor *t, const char *name, at::IntArrayRef shape) {
-    TORCH_CHECK_VALUE(!t || t->sizes() == shape, name, " must be ", shape);
-}
-
-at::Tensor output(PyObject *given, const char *name, at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
-    if (const at::Tensor *t = optional(given, name)) {
-        address(t, name, type, dev);
-        has_shape(t, name, shape);
-        return *t;
-    }
-    return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));   // at::empty without its dispatch
-}
-
-int64_t integer(PyObject *o) {
-    const long long v = PyLong_AsLongLong(o);
-    if (v == -1 && PyErr_Occurred()) throw python_error();
-    return v;
-}
-
-// `none` where the argument is None
-int64_t integer_or(PyObject *o, int64_t none) { return o == Py_None ? none : integer(o); }
-
-double number(PyObject *o) {
-    const double v = PyFloat_AsDouble(o);
-    if (v == -1.0 && PyErr_Occurred()) throw python_error();
-    return v;
-}
-
-at::ScalarType dtype_of(PyObject *o) {
-    TORCH_CHECK_VALUE(THPDtype_Check(o), "dtype must be a torch.dtype");
-    return reinterpret_cast<THPDtype *>(o)->scalar_type;
-}
-
-void check(q4_status st, const char *what) {
-    if (st == Q4_OK) return;
-    PyObject *e = PyObject_CallFunction(g_error, "is", static_cast<int>(st), what);
-    if (e) {
-        PyErr_SetObject(reinterpret_cast<PyObject *>(Py_TYPE(e)), e);
-        Py_DECREF(e);
-    }
-    throw python_error();
-}
-
-void want(Py_ssize_t got, Py_ssize_t n) { TORCH_CHECK_TYPE(got == n, "takes ", n, " arguments, got ", got); }
-
-// (data, num_blocks, kv_heads, head_dim)
-q4_kv_cache cache_of(PyObject *const *a, c10::Device dev) {
-    q4_kv_cache c;
-    const at::Tensor &data = required(a[0], "the cache");
-    TORCH_CHECK_VALUE(data.device() == dev, "the cache is on ", data.device(), ", not ", dev);
-    c.data = address(&data, "the cache", at::kByte, dev);
-    c.num_blocks = integer(a[1]);
-    c.kv_heads = static_cast<int32_t>(integer(a[2]));
-    c.head_dim = static_cast<int32_t>(integer(a[3]));
-    TORCH_CHECK_VALUE(data.numel() == static_cast<int64_t>(q4_kv_cache_bytes(c.num_blocks, c.kv_heads, c.head_dim)),
-                      "the cache's data does not have its size");
-    return c;
-}
-
-// (block_table, lengths, cu_rows or None, max_rows or None, max_length or None)
-q4_kv_batch batch_of(PyObject *const *a, int64_t rows, c10::Device dev) {
-    const at::Tensor &table = required(a[0], "block_table"), &lengths = required(a[1], "lengths");
-    const at::Tensor *cu = optional(a[2], "cu_rows");
-    q4_kv_batch b;
-    b.block_table = address<int32_t>(&table, "block_table", at::kInt, dev);
-    b.lengths = address<int32_t>(&lengths, "lengths", at::kInt, dev);
-    TORCH_CHECK_VALUE(table.dim() == 2 && lengths.dim() == 1 && table.size(0) == lengths.size(0),
-                      "block_table must be [batch, width] and lengths [batch]");
-    b.batch = table.size(0);
-    b.table_width = table.size(1);
-    b.cu_rows = address<int32_t>(cu, "cu_rows", at::kInt, dev);
-    has_shape(cu, "cu_rows", {b.batch + 1});
-    b.rows = rows;
-    const int64_t each = cu || !b.batch ? rows : rows / b.batch;
-    b.max_rows = std::max<int64_t>(1, integer_or(a[3], each));
-    b.max_length = std::max<int64_t>(1, integer_or(a[4], b.table_width * Q4_KV_BLOCK));
-    return b;
-}
 
 // kv_append(q, k, v, cache x 4, batch x 5, rope, interleaved, out)
 PyObject *kv_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -336,6 +211,14 @@ PyMethodDef methods[] = {{"kv_append", fast(kv_append), METH_FASTCALL, nullptr},
                          {"kv_attention", fast(kv_attention), METH_FASTCALL, nullptr},
                          {"add_rmsnorm", fast(add_rmsnorm), METH_FASTCALL, nullptr},
                          {"logits_adjust", fast(logits_adjust), METH_FASTCALL, nullptr},
+                         {"beam_select", fast(beam_select), METH_FASTCALL, nullptr},
+                         {"beam_advance", fast(beam_advance), METH_FASTCALL, nullptr},
+                         {"kv_fork", fast(kv_fork), METH_FASTCALL, nullptr},
+                         {"kv_compact", fast(kv_compact), METH_FASTCALL, nullptr},
+                         {"kv_copy_blocks", fast(kv_copy_blocks), METH_FASTCALL, nullptr},
+                         {"kv_summarize", fast(kv_summarize), METH_FASTCALL, nullptr},
+                         {"kv_select", fast(kv_select), METH_FASTCALL, nullptr},
+                         {"kv_attention_blocks", fast(kv_attention_blocks), METH_FASTCALL, nullptr},
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 

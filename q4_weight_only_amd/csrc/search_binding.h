@@ -1,0 +1,271 @@
+// Python binding of the operators around the paged cache (include/q4_search.h).
+#pragma once
+
+#include <vector>
+
+#include "binding_helpers.h"
+#include "q4_search.h"
+
+namespace {
+
+void *stream_of(c10::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
+
+// beam_select(logits, scores, keep, finished, pad, out, workspace)
+PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 7);
+    const at::Tensor &z = required(a[0], "logits"), &scores = required(a[1], "scores");
+    const c10::Device dev = device_of(z, "logits");
+    const float *src = address<float>(&z, "logits", at::kFloat, dev);
+    const float *base = address<float>(&scores, "scores", at::kFloat, dev);
+    TORCH_CHECK_VALUE(z.dim() == 2 && scores.dim() == 2 && z.size(0) == scores.numel(),
+                      "scores must be [groups, beams] and logits [groups * beams, V]");
+    const int64_t groups = scores.size(0), beams = scores.size(1), v = z.size(1), keep = integer(a[2]), pad = integer(a[4]);
+    const at::Tensor *done = optional(a[3], "finished");
+    const int32_t *ended = address<int32_t>(done, "finished", at::kInt, dev);
+    has_shape(done, "finished", scores.sizes());
+    TORCH_CHECK_VALUE(keep >= 1 && keep <= 128, "keep must be 1 .. 128");
+    TORCH_CHECK_VALUE(pad >= 0 && pad <= INT32_MAX, "pad must be a token");
+    at::Tensor parents = output(out_item(a[5], 3, 0), "parents", {groups, keep}, at::kInt, dev);
+    at::Tensor tokens = output(out_item(a[5], 3, 1), "tokens", {groups, keep}, at::kInt, dev);
+    at::Tensor best = output(out_item(a[5], 3, 2), "scores", {groups, keep}, at::kFloat, dev);
+    const c10::hip::HIPGuard guard(dev.index());
+    const Workspace ws(a[6], static_cast<int64_t>(q4_beam_select_workspace(groups, beams, v)), dev);
+    check(q4_beam_select(src, groups, beams, v, base, ended, static_cast<int32_t>(pad), keep, parents.data_ptr<int32_t>(),
+                         tokens.data_ptr<int32_t>(), best.data_ptr<float>(), ws.data, ws.bytes, stream_of(dev)),
+          "q4_beam_select");
+    return tuple_of({&parents, &tokens, &best});
+    END_HANDLE_TH_ERRORS
+}
+
+// beam_advance(sequences, lengths, parents, tokens, finished, eos, pad, out)
+PyObject *beam_advance(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 8);
+    const at::Tensor &seq = required(a[0], "sequences"), &lengths = required(a[1], "lengths"), &parents = required(a[2], "parents"),
+                     &tokens = required(a[3], "tokens");
+    const c10::Device dev = device_of(seq, "sequences");
+    const int32_t *src = address<int32_t>(&seq, "sequences", at::kInt, dev);
+    TORCH_CHECK_VALUE(seq.dim() == 2, "sequences must be [rows, width]");
+    const int64_t rows = seq.size(0), width = seq.size(1), n_out = parents.numel();
+    const int32_t *len = address<int32_t>(&lengths, "lengths", at::kInt, dev);
+    TORCH_CHECK_VALUE(lengths.numel() == rows, "lengths must have one value for each row of sequences");
+    const int32_t *from = address<int32_t>(&parents, "parents", at::kInt, dev), *next = address<int32_t>(&tokens, "tokens", at::kInt, dev);
+    TORCH_CHECK_VALUE(tokens.numel() == n_out, "tokens must have as many values as parents");
+    const at::Tensor *done = optional(a[4], "finished");
+    const int32_t *ended = address<int32_t>(done, "finished", at::kInt, dev);
+    TORCH_CHECK_VALUE(!done || done->numel() == rows, "finished must have one value for each row of sequences");
+    const int64_t eos = integer(a[5]), pad = integer(a[6]);
+    TORCH_CHECK_VALUE(eos >= INT32_MIN && eos <= INT32_MAX && pad >= INT32_MIN && pad <= INT32_MAX, "eos and pad must be int32 values");
+    at::Tensor out = output(out_item(a[7], 3, 0), "sequences", {n_out, width}, at::kInt, dev);
+    at::Tensor out_len = output(out_item(a[7], 3, 1), "lengths", {n_out}, at::kInt, dev);
+    at::Tensor out_done = output(out_item(a[7], 3, 2), "finished", {n_out}, at::kInt, dev);
+    const c10::hip::HIPGuard guard(dev.index());
+    check(q4_beam_advance(src, rows, width, len, ended, from, next, n_out, static_cast<int32_t>(eos), static_cast<int32_t>(pad),
+                          out.data_ptr<int32_t>(), out_len.data_ptr<int32_t>(), out_done.data_ptr<int32_t>(), stream_of(dev)),
+          "q4_beam_advance");
+    return tuple_of({&out, &out_len, &out_done});
+    END_HANDLE_TH_ERRORS
+}
+
+// A block table and its lengths.
+struct Tables {
+    const int32_t *table, *lengths;
+    int64_t rows, width;
+    c10::Device dev;
+};
+Tables tables_of(PyObject *table, PyObject *lengths) {
+    const at::Tensor &t = required(table, "block_table"), &l = required(lengths, "lengths");
+    const c10::Device dev = device_of(t, "block_table");
+    TORCH_CHECK_VALUE(t.dim() == 2 && l.dim() == 1 && t.size(0) == l.size(0), "block_table must be [batch, width] and lengths [batch]");
+    return {address<int32_t>(&t, "block_table", at::kInt, dev), address<int32_t>(&l, "lengths", at::kInt, dev), t.size(0), t.size(1), dev};
+}
+
+// `held`, one count for each block.
+const int32_t *held_of(PyObject *o, int64_t num_blocks, c10::Device dev) {
+    const at::Tensor *held = optional(o, "held");
+    has_shape(held, "held", {num_blocks});
+    return address<int32_t>(held, "held", at::kInt, dev);
+}
+
+// kv_fork(block_table, lengths, parents, num_blocks, grow, held, out, workspace)
+PyObject *kv_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 8);
+    const Tables t = tables_of(a[0], a[1]);
+    const at::Tensor &parents = required(a[2], "parents");
+    const int32_t *from = address<int32_t>(&parents, "parents", at::kInt, t.dev);
+    const int64_t n_out = parents.numel(), num_blocks = integer(a[3]);
+    TORCH_CHECK_VALUE(num_blocks >= 1 && num_blocks <= 1 << 24, "num_blocks must be 1 .. 2^24");
+    const int32_t *grow = nullptr;
+    int64_t each = 0;
+    if (THPVariable_Check(a[4])) {
+        const at::Tensor &g = THPVariable_Unpack(a[4]);
+        grow = address<int32_t>(&g, "grow", at::kInt, t.dev);
+        TORCH_CHECK_VALUE(g.numel() == n_out, "grow must have as many values as parents");
+    } else {
+        each = integer(a[4]);
+    }
+    const int32_t *held = held_of(a[5], num_blocks, t.dev);
+    at::Tensor table = output(out_item(a[6], 6, 0), "block_table", {n_out, t.width}, at::kInt, t.dev);
+    at::Tensor lengths = output(out_item(a[6], 6, 1), "lengths", {n_out}, at::kInt, t.dev);
+    at::Tensor refs = output(out_item(a[6], 6, 2), "refs", {num_blocks}, at::kInt, t.dev);
+    at::Tensor src = output(out_item(a[6], 6, 3), "src", {n_out}, at::kInt, t.dev);
+    at::Tensor dst = output(out_item(a[6], 6, 4), "dst", {n_out}, at::kInt, t.dev);
+    at::Tensor short_of = output(out_item(a[6], 6, 5), "short", {n_out}, at::kInt, t.dev);
+    const c10::hip::HIPGuard guard(t.dev.index());
+    const Workspace ws(a[7], static_cast<int64_t>(q4_kv_fork_workspace(n_out, num_blocks)), t.dev);
+    check(q4_kv_fork(t.table, t.rows, t.width, t.lengths, from, n_out, grow, each, held, num_blocks, table.data_ptr<int32_t>(),
+                     lengths.data_ptr<int32_t>(), refs.data_ptr<int32_t>(), src.data_ptr<int32_t>(), dst.data_ptr<int32_t>(),
+                     short_of.data_ptr<int32_t>(), ws.data, ws.bytes, stream_of(t.dev)),
+          "q4_kv_fork");
+    return tuple_of({&table, &lengths, &refs, &src, &dst, &short_of});
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_compact(block_table, lengths, num_blocks, held, out, workspace)
+PyObject *kv_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 6);
+    const Tables t = tables_of(a[0], a[1]);
+    const int64_t num_blocks = integer(a[2]);
+    TORCH_CHECK_VALUE(num_blocks >= 1 && num_blocks <= 1 << 24, "num_blocks must be 1 .. 2^24");
+    const int32_t *held = held_of(a[3], num_blocks, t.dev);
+    const int64_t half = std::max<int64_t>(1, num_blocks / 2);
+    at::Tensor table = output(out_item(a[4], 4, 0), "block_table", {t.rows, t.width}, at::kInt, t.dev);
+    at::Tensor src = output(out_item(a[4], 4, 1), "src", {half}, at::kInt, t.dev);
+    at::Tensor dst = output(out_item(a[4], 4, 2), "dst", {half}, at::kInt, t.dev);
+    at::Tensor live = output(out_item(a[4], 4, 3), "live", {1}, at::kInt, t.dev);
+    const c10::hip::HIPGuard guard(t.dev.index());
+    const Workspace ws(a[5], static_cast<int64_t>(q4_kv_compact_workspace(num_blocks)), t.dev);
+    check(q4_kv_compact(t.table, t.rows, t.width, t.lengths, held, num_blocks, table.data_ptr<int32_t>(), src.data_ptr<int32_t>(),
+                        dst.data_ptr<int32_t>(), live.data_ptr<int32_t>(), ws.data, ws.bytes, stream_of(t.dev)),
+          "q4_kv_compact");
+    return tuple_of({&table, &src, &dst, &live});
+    END_HANDLE_TH_ERRORS
+}
+
+// A tensor of `rows` rows of at least `bytes` contiguous bytes each, or a list of
+// such rows: their addresses.
+std::vector<void *> layers_of(PyObject *o, const char *name, at::ScalarType type, int64_t bytes, c10::Device dev) {
+    std::vector<void *> at;
+    if (THPVariable_Check(o)) {
+        const at::Tensor &t = THPVariable_Unpack(o);
+        TORCH_CHECK_VALUE(t.device() == dev, name, " must be a CUDA/HIP tensor on the inputs' device");
+        TORCH_CHECK_VALUE(t.scalar_type() == type && t.dim() == 2 && t.size(1) >= bytes && (t.size(1) <= 1 || t.stride(1) == 1), name,
+                          " must be ", type, " [layers, bytes] with rows of at least ", bytes, " contiguous bytes");
+        auto *base = static_cast<uint8_t *>(t.data_ptr());
+        for (int64_t l = 0; l < t.size(0); ++l) at.push_back(base + l * t.stride(0));
+        return at;
+    }
+    TORCH_CHECK_VALUE(PyTuple_Check(o) || PyList_Check(o), name, " must be a list of tensors");
+    for (Py_ssize_t l = 0; l < PySequence_Fast_GET_SIZE(o); ++l) {
+        const at::Tensor &t = required(PySequence_Fast_GET_ITEM(o, l), name);
+        at.push_back(address(&t, name, type, dev));
+        TORCH_CHECK_VALUE(t.numel() >= bytes, name, " must hold ", bytes, " bytes");
+    }
+    return at;
+}
+
+// kv_copy_blocks(data, num_blocks, kv_heads, head_dim, src, dst, summaries)
+PyObject *kv_copy_blocks(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 7);
+    const at::Tensor &src = required(a[4], "src"), &dst = required(a[5], "dst");
+    const c10::Device dev = device_of(src, "src");
+    const int32_t *from = address<int32_t>(&src, "src", at::kInt, dev), *to = address<int32_t>(&dst, "dst", at::kInt, dev);
+    TORCH_CHECK_VALUE(src.numel() == dst.numel(), "src and dst must have as many values");
+    q4_kv_cache c;
+    c.data = nullptr;
+    c.num_blocks = integer(a[1]);
+    c.kv_heads = static_cast<int32_t>(integer(a[2]));
+    c.head_dim = static_cast<int32_t>(integer(a[3]));
+    const int64_t bytes = static_cast<int64_t>(q4_kv_cache_bytes(c.num_blocks, c.kv_heads, c.head_dim));
+    TORCH_CHECK_VALUE(bytes > 0, "need 1..2^24 blocks, 1..256 kv heads and a head_dim of 64 or 128");
+    const std::vector<void *> data = layers_of(a[0], "the caches", at::kByte, bytes, dev);
+    std::vector<void *> summaries;
+    if (a[6] != Py_None) {
+        summaries = layers_of(a[6], "summaries", at::kChar, static_cast<int64_t>(q4_kv_summary_bytes(c.num_blocks, c.kv_heads, c.head_dim)), dev);
+        TORCH_CHECK_VALUE(summaries.size() == data.size(), "need a summary for each of the ", data.size(), " layers");
+    }
+    const c10::hip::HIPGuard guard(dev.index());
+    check(q4_kv_copy_blocks(&c, data.data(), summaries.empty() ? nullptr : summaries.data(), static_cast<int64_t>(data.size()), from, to,
+                            src.numel(), stream_of(dev)),
+          "q4_kv_copy_blocks");
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+void *summary_of(PyObject *o, const q4_kv_cache &c, c10::Device dev) {
+    const at::Tensor &t = required(o, "summary");
+    void *p = address(&t, "summary", at::kChar, dev);
+    TORCH_CHECK_VALUE(t.numel() == static_cast<int64_t>(q4_kv_summary_bytes(c.num_blocks, c.kv_heads, c.head_dim)),
+                      "summary does not have the cache's size");
+    return p;
+}
+
+// kv_summarize(summary, cache x 4, batch x 5, rows)
+PyObject *kv_summarize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 11);
+    const c10::Device dev = device_of(required(a[0], "summary"), "summary");
+    const q4_kv_cache c = cache_of(a + 1, dev);
+    void *summary = summary_of(a[0], c, dev);
+    const q4_kv_batch b = batch_of(a + 5, integer(a[10]), dev);
+    const c10::hip::HIPGuard guard(dev.index());
+    check(q4_kv_summarize(&c, &b, summary, stream_of(dev)), "q4_kv_summarize");
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_select(q, summary, cache x 4, batch x 5, keep, first, recent, out, workspace)
+PyObject *kv_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 16);
+    const at::Tensor &q = required(a[0], "q");
+    const c10::Device dev = device_of(q, "q");
+    const void *src = address(&q, "q", at::kBFloat16, dev);
+    const q4_kv_cache c = cache_of(a + 2, dev);
+    void *summary = summary_of(a[1], c, dev);
+    TORCH_CHECK_VALUE(q.dim() == 2 && q.size(1) % c.head_dim == 0, "q must be [rows, heads * ", c.head_dim, "]");
+    const q4_kv_batch b = batch_of(a + 6, q.size(0), dev);
+    const int64_t keep = integer(a[11]), first = integer(a[12]), recent = integer(a[13]);
+    TORCH_CHECK_VALUE(keep >= 1 && keep <= 1 << 16, "keep must be 1 .. 65536");
+    at::Tensor out = output(a[14], "out", {q.size(0), c.kv_heads, keep}, at::kInt, dev);
+    const c10::hip::HIPGuard guard(dev.index());
+    const Workspace ws(a[15], static_cast<int64_t>(q4_kv_select_workspace(&c, &b)), dev);
+    check(q4_kv_select(&c, &b, summary, src, q.size(1) / c.head_dim, keep, first, recent, out.data_ptr<int32_t>(), ws.data, ws.bytes,
+                       stream_of(dev)),
+          "q4_kv_select");
+    return THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_attention_blocks(q, chosen, cache x 4, batch x 5, scale or None, out, dtype, workspace)
+PyObject *kv_attention_blocks(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    want(n, 15);
+    const at::Tensor &q = required(a[0], "q"), &chosen = required(a[1], "chosen");
+    const c10::Device dev = device_of(q, "q");
+    const void *src = address(&q, "q", at::kBFloat16, dev);
+    const int32_t *list = address<int32_t>(&chosen, "chosen", at::kInt, dev);
+    const q4_kv_cache c = cache_of(a + 2, dev);
+    TORCH_CHECK_VALUE(q.dim() == 2 && q.size(1) % c.head_dim == 0, "q must be [rows, heads * ", c.head_dim, "]");
+    TORCH_CHECK_VALUE(chosen.dim() == 3 && chosen.size(0) == q.size(0) && chosen.size(1) == c.kv_heads && chosen.size(2) >= 1 &&
+                          chosen.size(2) <= 1 << 16,
+                      "chosen must be [rows, ", c.kv_heads, ", keep]");
+    const q4_kv_batch b = batch_of(a + 6, q.size(0), dev);
+    const int64_t heads = q.size(1) / c.head_dim, keep = chosen.size(2);
+    const float scale = a[11] == Py_None ? 1.0f / std::sqrt(static_cast<float>(c.head_dim)) : static_cast<float>(number(a[11]));
+    const at::ScalarType type = dtype_of(a[13]);
+    const int out_code = type_code(type, "dtype");
+    at::Tensor out = output(a[12], "out", q.sizes(), type, dev);
+    const c10::hip::HIPGuard guard(dev.index());
+    const Workspace ws(a[14], static_cast<int64_t>(q4_kv_attention_blocks_workspace(&c, &b, heads, keep)), dev);
+    check(q4_kv_attention_blocks(&c, &b, src, heads, list, keep, scale, out.data_ptr(), out_code, ws.data, ws.bytes, stream_of(dev)),
+          "q4_kv_attention_blocks");
+    return THPVariable_Wrap(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
+}  // namespace
