@@ -31,13 +31,20 @@ struct Scan {
     float *top;       // [rows][parts]
     float *segment;   // [rows][segments]
     int32_t parts, segments, loads;
+    uint32_t part_inverse, segment_inverse;   // of chunks of 64 of a row (see beam_pick_kernel)
 };
+
+// 2^32 / d, rounded up (0 for 1): i / d is i * that >> 32 for i < 2^19 and d <= 2^13.
+uint32_t inverse_of(int64_t d) { return d == 1 ? 0 : static_cast<uint32_t>(((int64_t(1) << 32) + d - 1) / d); }
+__device__ __forceinline__ int divide(int i, uint32_t inverse) {
+    return inverse ? static_cast<int>(__umulhi(static_cast<uint32_t>(i), inverse)) : i;
+}
 
 // Loads of four tokens that a lane has: more of them mean fewer parts to join,
 // fewer more waves to read with.
 int loads_of(int64_t rows, int64_t V) {
     const int64_t waves = rows * ((V + 255) / 256);
-    return waves >= 32768 ? 8 : waves >= 8192 ? 4 : waves >= 4096 ? 2 : 1;
+    return waves >= 32768 ? 8 : waves >= 8192 ? 4 : 2;
 }
 
 Scan scan_of(void *workspace, int64_t rows, int64_t V) {
@@ -45,43 +52,98 @@ Scan scan_of(void *workspace, int64_t rows, int64_t V) {
     s.loads = loads_of(rows, V);
     s.parts = static_cast<int32_t>((V + 256 * s.loads - 1) / (256 * s.loads));
     s.segments = static_cast<int32_t>((V + kBeamSegment - 1) / kBeamSegment);
+    s.part_inverse = inverse_of((s.parts + 63) / 64);
+    s.segment_inverse = inverse_of((s.segments + 63) / 64);
     s.sum = static_cast<double *>(workspace);
     s.top = reinterpret_cast<float *>(s.sum + rows * s.parts);
     s.segment = s.top + rows * s.parts;
     return s;
 }
 
-// The larger of the lane's and another lane's.
+// Sums and maxima over lanes without a way through LDS: DPP within 16 lanes, swaps of
+// rows beyond.
 template <int CTRL>
-__device__ __forceinline__ float max_dpp(float v) {
+__device__ __forceinline__ float from_lane(float v) {
     const int w = __float_as_int(v);
-    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(w, w, CTRL, 0xF, 0xF, false)));
+    return __int_as_float(__builtin_amdgcn_update_dpp(w, w, CTRL, 0xF, 0xF, false));
 }
-
-// Largest of each 8 lanes, in all of them.
-__device__ __forceinline__ float max_of_8(float v) {
-    v = max_dpp<0xB1>(v);    // lane ^ 1
-    v = max_dpp<0x4E>(v);    // lane ^ 2
-    return max_dpp<0x141>(v);   // 7 - lane, within 8
+template <int CTRL>
+__device__ __forceinline__ double from_lane(double v) {
+    const uint64_t w = static_cast<uint64_t>(__double_as_longlong(v));
+    const int lo = static_cast<int>(w), hi = static_cast<int>(w >> 32);
+    const uint32_t l = __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, false), h = __builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, false);
+    return __longlong_as_double(static_cast<long long>(uint64_t(h) << 32 | l));
 }
+constexpr int kLane1 = 0xB1, kLane2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;   // lane ^ 1, lane ^ 2, 7 - lane, 15 - lane
 
-// e^x for x <= 0 (a difference of two fp32 values), within 3e-10 of itself:
-// 2^n times a Taylor sum of degree 8 on [-1/2, 1/2] ln 2.  Below -80 it is 0, which no
-// sum of 2^24 terms with a largest one of 1 notices; what is not a number stays it.
+// The two values that the pairs of rows of 16 (HALF: of 32) lanes hold, in both.
+template <bool HALF>
+__device__ __forceinline__ void both_rows(uint32_t v, uint32_t &x, uint32_t &y) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    const u32x2 r = __builtin_bit_cast(u32x2, HALF ? __builtin_amdgcn_permlane32_swap(v, v, false, false)
+                                                   : __builtin_amdgcn_permlane16_swap(v, v, false, false));
+    x = r.x;
+    y = r.y;
+}
+template <bool HALF, typename Join>
+__device__ __forceinline__ float join_rows(float v, Join join) {
+    uint32_t x, y;
+    both_rows<HALF>(__float_as_uint(v), x, y);
+    return join(__uint_as_float(x), __uint_as_float(y));
+}
+template <bool HALF, typename Join>
+__device__ __forceinline__ double join_rows(double v, Join join) {
+    const uint64_t w = static_cast<uint64_t>(__double_as_longlong(v));
+    uint32_t lx, ly, hx, hy;
+    both_rows<HALF>(static_cast<uint32_t>(w), lx, ly);
+    both_rows<HALF>(static_cast<uint32_t>(w >> 32), hx, hy);
+    return join(__longlong_as_double(static_cast<long long>(uint64_t(hx) << 32 | lx)),
+                __longlong_as_double(static_cast<long long>(uint64_t(hy) << 32 | ly)));
+}
+template <typename T, typename Join>
+__device__ __forceinline__ T join_8(T v, Join join) {
+    v = join(v, from_lane<kLane1>(v));
+    v = join(v, from_lane<kLane2>(v));
+    return join(v, from_lane<kMirror8>(v));
+}
+template <typename T, typename Join>
+__device__ __forceinline__ T join_64_of_8(T v, Join join) {   // of 8 lanes that hold the same
+    v = join(v, from_lane<kMirror16>(v));
+    v = join_rows<false>(v, join);
+    return join_rows<true>(v, join);
+}
+__device__ __forceinline__ float larger(float x, float y) { return fmaxf(x, y); }
+__device__ __forceinline__ double added(double x, double y) { return x + y; }
+__device__ __forceinline__ float max_of_8(float v) { return join_8(v, larger); }
+__device__ __forceinline__ float max_of_64(float v) { return join_64_of_8(join_8(v, larger), larger); }
+__device__ __forceinline__ double sum_of_64(double v) { return join_64_of_8(join_8(v, added), added); }
+
+// e^x for -80 <= x <= 0, within 5e-11 of itself: 2^n times a polynomial on
+// [-1/2, 1/2] ln 2 that equalizes the relative error (its coefficients are from an
+// exchange over that interval).  n comes out of the sum's low bits and goes into
+// the exponent: 12 instructions on 64 bits, 4 cycles each, where a conversion or a
+// scaling by a power of two takes 16.
 __device__ __forceinline__ double exp64(double x) {
-    const double y = x * 1.4426950408889634074;
-    const double n = __builtin_rint(y);
-    const double f = (y - n) * 0.69314718055994530942;
-    double p = 1.0 / 40320;
-    p = fma(p, f, 1.0 / 5040);
-    p = fma(p, f, 1.0 / 720);
-    p = fma(p, f, 1.0 / 120);
-    p = fma(p, f, 1.0 / 24);
-    p = fma(p, f, 1.0 / 6);
-    p = fma(p, f, 0.5);
-    p = fma(p, f, 1.0);
-    p = fma(p, f, 1.0);
-    return x < -80.0 ? 0.0 : __builtin_ldexp(p, x >= -80.0 ? static_cast<int>(n) : 0);
+    constexpr double kShift = 6755399441055744.0;   // 1.5 * 2^52
+    const double t = fma(x, 1.4426950408889634074, kShift);
+    const double f = fma(t - kShift, -0.69314718055994530942, x);
+    double p = 0.00019775170819355867;
+    p = fma(p, f, 0.0013948183326349026);
+    p = fma(p, f, 0.008333561091856493);
+    p = fma(p, f, 0.041666225425543775);
+    p = fma(p, f, 0.16666665126127003);
+    p = fma(p, f, 0.5000000104536173);
+    p = fma(p, f, 1.0000000002430987);
+    p = fma(p, f, 0.9999999999616821);
+    const uint64_t n = static_cast<uint64_t>(__double_as_longlong(t)) << 52;
+    return __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(__double_as_longlong(p)) + n));
+}
+
+// The same for fp32 differences from m of any size: below -80 it is 0, which no sum
+// of 2^24 terms with a largest one of 1 notices.  (What is not a number gives 0 too.)
+__device__ __forceinline__ double exp_below(float z, double m, float least) {
+    const double e = exp64(z - m);
+    return z >= least ? e : 0.0;
 }
 
 // A wave has 256 * J consecutive tokens of a row, loads all of them, and waits
@@ -114,18 +176,20 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(BeamArgs a, Scan out) {
         seg[j] = max_of_8(fmaxf(fmaxf(z[j][0], z[j][1]), fmaxf(z[j][2], z[j][3])));
         top = fmaxf(top, seg[j]);
     }
-    top = fmaxf(top, __shfl_xor(top, 8));
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const double m = top == kNone ? 0.0 : top;   // all -inf: the sum is 0
+    top = join_64_of_8(top, larger);
+    const float m = top == kNone ? 0.0f : top, least = m - 80.0f;   // all -inf: the sum is 0
     double sum = 0.0;
+    bool bad = false;   // +inf, or what is not a number
 #pragma unroll
     for (int j = 0; j < J; ++j) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum += exp64(z[j][i] - m);
+        for (int i = 0; i < 4; ++i) {
+            sum += exp_below(z[j][i], m, least);
+            bad |= !(z[j][i] < __builtin_inff());
+        }
     }
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) sum += __shfl_xor(sum, i);
+    if (bad) sum = __builtin_nan("");
+    sum = sum_of_64(sum);
     if (lane == 0) {
         out.sum[row * out.parts + part] = sum;
         out.top[row * out.parts + part] = top;
@@ -150,134 +214,209 @@ __device__ __forceinline__ uint64_t ordered(double s) {
     return b >> 63 ? ~b : b | (uint64_t(1) << 63);
 }
 
-constexpr int kPickThreads = 1024;
-constexpr int kSlots = 256;       // the items of four threads are a slot
-constexpr int kListed = 512;     // segments that may be listed before they are cut down to `keep`
+// fp32 in the order of unsigned numbers, and back.
+__device__ __forceinline__ uint32_t ordered(float s) {
+    const uint32_t b = __float_as_uint(s);
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key); }
 
-// A workgroup has one group.  The n-th of the first items of its 256 slots is a
-// bound that at least n items do not stand behind, and hardly more where they are spread
-// evenly; those are listed and the n first of them found by counting, for each, the
-// ones in front.  Where too many are in front of the bound (they lie together,
-// or are equal), the n-th item itself is found, bit by bit.
+constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
+constexpr int kSlots = 256;       // the items of four threads are a slot
+constexpr int kListed = 512;      // segments that may be listed before they are cut down to `keep`
+constexpr int kAhead = 4;         // parts of a row, or items, of a lane that are loaded together
+
+// A workgroup has one group.  Its items are the waves' parts of its beams' rows, or,
+// where `keep` is a large share of these, the segments; 64 of one beam a chunk, the
+// chunks to the waves in turn.  A bound that n of its 256 slots reach is one that at
+// least n items reach, and hardly more where they are spread evenly.  The segments that
+// reach it are listed, and the n first of them found by counting, for each, the ones
+// in front.  Where too many reach the bound (they lie together, or are equal), the
+// n-th segment itself is found, bit by bit.
+//
+// The bound is found in fp32, on z + (score - lse), which is off by two roundings:
+// with n items at b or more, the n first have a score of b less one error or more, and
+// so a sum of b less two, and are listed; the order among those listed is that of the
+// scores in 64 bits.
+//
+// What bounds it is one step after the other, on one compute unit: what it reads
+// comes from the others' caches at some 20 bytes a cycle, so it reads few segments (all
+// of them: 128 KB and 6 us of 17 for 8 beams of 131072 tokens), and each step's code is fetched
+// as it goes.
 __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Scan in) {
     __shared__ double base[kMaxBeams], lse[kMaxBeams];
+    __shared__ float offset[kMaxBeams];   // score - lse; -inf for beams without tokens as candidates
     __shared__ int32_t ended[kMaxBeams];
-    __shared__ double slot_s[kSlots];
-    __shared__ int32_t slot_id[kSlots];
+    __shared__ __align__(16) uint32_t slot[kSlots];
+    __shared__ float bound_near;
+    __shared__ int32_t part_list[kListed];
     __shared__ double list_s[kListed];
     __shared__ int32_t list_id[kListed];
     __shared__ int32_t segment_id[kMaxKeep];
     __shared__ double bound_s;
-    __shared__ int32_t bound_id, listed, counted[2];
+    __shared__ int32_t listed, parts_listed, counted;
     extern __shared__ __align__(16) uint8_t dynamic[];   // keep * 32 elements: s, then ids
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = a.keep, group = blockIdx.x;
-    const int segments = in.segments, items = a.beams * segments;
+    const int segments = in.segments;
     double *element_s = reinterpret_cast<double *>(dynamic);
     int32_t *element_id = reinterpret_cast<int32_t *>(element_s + n * kBeamSegment);
+    const float *segment = in.segment + static_cast<int64_t>(group) * a.beams * segments;
+    const bool coarse = a.beams * in.parts >= 4 * n;
 
-    for (int b = wave; b < a.beams; b += kPickThreads / 64) {
+    for (int b = wave; b < a.beams; b += kPickWaves) {
         const int64_t row = static_cast<int64_t>(group) * a.beams + b;
+        const float before = a.scores[row];
         const bool done = a.finished && a.finished[row];
-        double l = 0.0;
+        float m = kNone;       // the lane's largest so far, and its sum relative to that
+        double sum = 0.0;
         if (!done) {
             const float *tops = in.top + row * in.parts;
             const double *sums = in.sum + row * in.parts;
-            float top = kNone;
-            for (int i = lane; i < in.parts; i += 64) top = fmaxf(top, tops[i]);
+            for (int i0 = lane; i0 < in.parts; i0 += 64 * kAhead) {
+                float top[kAhead];
+                double part[kAhead];
 #pragma unroll
-            for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
-            double sum = 0.0;
-            for (int i = lane; i < in.parts; i += 64)   // a part without a logit has 0, or what is not a number
-                sum += tops[i] == kNone ? sums[i] : sums[i] * exp64(static_cast<double>(tops[i]) - top);
+                for (int k = 0; k < kAhead; ++k) {
+                    const int i = i0 + 64 * k;
+                    top[k] = i < in.parts ? tops[i] : kNone;
+                    part[k] = i < in.parts ? sums[i] : 0.0;
+                }
+                float most = m;
 #pragma unroll
-            for (int i = 1; i < 64; i *= 2) sum += __shfl_xor(sum, i);
-            l = top + log(sum);
+                for (int k = 0; k < kAhead; ++k) most = fmaxf(most, top[k]);
+                const float least = most - 80.0f;
+                sum *= m > kNone && m >= least ? exp64(static_cast<double>(m) - most) : 0.0;   // (0 so far where m is -inf)
+                m = most;
+                // a part without a logit has a sum of 0, or of what is not a number
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k) sum += top[k] == kNone ? part[k] : part[k] * exp_below(top[k], most, least);
+            }
         }
+        const float top = max_of_64(m);
+        // (what is not a number stays it times 0)
+        sum = sum_of_64(m == kNone ? sum : sum * exp_below(m, top, top - 80.0f));
+        const double l = top + log(sum), off = before - l;
         if (lane == 0) {
-            base[b] = a.scores[row] + 0.0;
+            base[b] = before + 0.0;
             lse[b] = l;
             ended[b] = done;
+            offset[b] = !done && __builtin_isfinite(off) ? static_cast<float>(off) : kNone;
         }
     }
-    if (tid == 0) listed = 0;
+    if (tid == 0) listed = parts_listed = 0;
     __syncthreads();
 
     const auto score = [&](int b, float z) {
         const double s = base[b] + (z - lse[b]) + 0.0;   // no -0, which would be equal to 0 and ordered before it
         return __builtin_isfinite(s) ? s : static_cast<double>(kNone);
     };
-    // every item of the thread: its place.  An ended beam has one candidate, in its first item.
-    const float *segment = in.segment + static_cast<int64_t>(group) * items;
-    const auto each_item = [&](auto f) {
-        int b = 0, at = tid;
-        for (int id = tid; id < items; id += kPickThreads, at += kPickThreads) {
-            while (at >= segments) {
-                at -= segments;
-                ++b;
+    // items of the thread, `per` of a beam: their beam, place among its items, and largest logit
+    const auto each_of = [&](const float *from, int per, uint32_t inverse, auto f) {
+        const int each = (per + 63) / 64, chunks = a.beams * each;
+        for (int c0 = wave; c0 < chunks; c0 += kPickWaves * kAhead) {
+            float z[kAhead];
+            int b[kAhead], at[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int chunk = c0 + kPickWaves * k;
+                b[k] = divide(chunk, inverse);
+                at[k] = (chunk - b[k] * each) * 64 + lane;
+                if (chunk >= chunks || at[k] >= per) b[k] = -1;
+                z[k] = b[k] >= 0 ? from[static_cast<int64_t>(b[k]) * per + at[k]] : kNone;
             }
-            Place p;
-            p.id = id;
-            if (ended[b]) p.s = at == 0 && __builtin_isfinite(base[b]) ? base[b] : static_cast<double>(kNone);
-            else p.s = score(b, segment[id]);
-            f(p);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (b[k] >= 0) f(b[k], at[k], z[k]);
         }
     };
-    Place best = {kNone, 0x7fffffff};
-    each_item([&](const Place &p) {
-        if (precedes(p, best)) best = p;
-    });
-#pragma unroll
-    for (int i = 1; i < 4; i *= 2) {
-        const Place other = {__shfl_xor(best.s, i), __shfl_xor(best.id, i)};
-        if (precedes(other, best)) best = other;
-    }
-    if (tid % 4 == 0) {
-        slot_s[tid / 4] = best.s;
-        slot_id[tid / 4] = best.id;
-    }
-    __syncthreads();
-    {   // the n-th slot (n <= 128): each of its four threads compares with a quarter
-        const int mine = tid / 4;
-        int front = 0;
-#pragma unroll 8
-        for (int i = 0; i < kSlots / 4; ++i) {
-            const int other = i * 4 + tid % 4;
-            const Place p = {slot_s[other], slot_id[other]};
-            front += precedes(p, best) || (p.s == best.s && p.id == best.id && other < mine);   // empty slots are alike
-        }
-        front += __shfl_xor(front, 1);
-        front += __shfl_xor(front, 2);
-        if (tid % 4 == 0 && front == n - 1) {
-            bound_s = best.s;
-            bound_id = best.id;
-        }
-    }
-    __syncthreads();
-    Place bound = {bound_s, bound_id};
-    const auto list_items = [&] {
-        each_item([&](const Place &p) {
-            if (p.s == kNone || precedes(bound, p)) return;
-            const int at = atomicAdd(&listed, 1);   // their order does not matter: they are counted below
-            if (at < kListed) {
-                list_s[at] = p.s;
-                list_id[at] = p.id;
-            }
+    // every candidate segment: its place in 64 bits.  An ended beam has one candidate, in its first segment.
+    const auto each_segment = [&](auto f) {
+        each_of(segment, segments, in.segment_inverse, [&](int b, int at, float z) {
+            Place p;
+            p.id = b * segments + at;
+            p.s = ended[b] ? (at == 0 && __builtin_isfinite(base[b]) ? base[b] : static_cast<double>(kNone)) : score(b, z);
+            f(p);
         });
     };
-    list_items();
+    // the items of beams that have not ended, with their sums in fp32 (what is no candidate: -inf, or not a number)
+    const auto each_sum = [&](auto f) {
+        each_of(coarse ? in.top + static_cast<int64_t>(group) * a.beams * in.parts : segment, coarse ? in.parts : segments,
+                coarse ? in.part_inverse : in.segment_inverse, [&](int b, int at, float z) { f(b, at, z + offset[b]); });
+    };
+    const bool my_ended = tid < a.beams && ended[tid] && __builtin_isfinite(base[tid]);   // a candidate of its own
+    float best = my_ended ? static_cast<float>(base[tid]) : kNone;
+    each_sum([&](int, int, float s) { best = fmaxf(best, s); });
+    best = fmaxf(best, from_lane<kLane1>(best));
+    best = fmaxf(best, from_lane<kLane2>(best));
+    if (tid % 4 == 0) slot[tid / 4] = ordered(best);
+    const float widest = max_of_64(lane < a.beams && offset[lane] > kNone ? fabsf(offset[lane]) : 0.0f);   // of the offsets
     __syncthreads();
+    if (wave == 0) {   // the n-th of the slots (n <= 128), or a little below it
+        uint32_t mine[kSlots / 64], least = 0;
+#pragma unroll
+        for (int k = 0; k < kSlots / 64; ++k) mine[k] = slot[lane * (kSlots / 64) + k];
+#pragma unroll 1
+        for (int bit = 31; bit >= 8; --bit) {
+            const uint32_t probe = least | 1u << bit;
+            int c = 0;
+#pragma unroll
+            for (int k = 0; k < kSlots / 64; ++k) c += __builtin_popcountll(__ballot(mine[k] >= probe));
+            if (c >= n) least = probe;
+            if (c >= n && c <= n + n / 4) break;
+        }
+        if (lane == 0) bound_near = unordered(least);
+    }
+    __syncthreads();
+    // (not a number, or -inf: fewer than n slots have a candidate, and all of them are listed)
+    const float near = bound_near > kNone ? bound_near - 0x1p-21f * (fabsf(bound_near) + widest) : kNone;
+    const bool exact = widest > 1e30f || !(near < __builtin_inff());   // sums might not be finite
+    const auto list = [&](int id, double s) {
+        if (s == kNone) return;
+        const int at = atomicAdd(&listed, 1);   // their order does not matter: they are counted below
+        if (at < kListed) {
+            list_s[at] = s;
+            list_id[at] = id;
+        }
+    };
+    if (exact) {
+        if (tid == 0) listed = kListed + 1;
+    } else {
+        if (my_ended && static_cast<float>(base[tid]) >= near) list(tid * segments, base[tid]);
+        each_sum([&](int b, int at, float s) {
+            if (!(s >= near) || s == kNone) return;
+            if (coarse) {
+                const int i = atomicAdd(&parts_listed, 1);
+                if (i < kListed) part_list[i] = b * in.parts + at;
+            } else {
+                list(b * segments + at, score(b, segment[b * segments + at]));
+            }
+        });
+    }
+    __syncthreads();
+    if (coarse && !exact) {   // the same for the workgroup
+        const int parts = parts_listed < kListed ? parts_listed : kListed, per = 8 * in.loads;   // segments of a part
+        for (int i = tid; i < parts * per; i += kPickThreads) {
+            const int part = part_list[i / per], b = part / in.parts, at = (part - b * in.parts) * per + i % per;
+            if (at >= segments) continue;
+            const float z = segment[b * segments + at], s = z + offset[b];
+            if (s >= near && s > kNone) list(b * segments + at, score(b, z));
+        }
+        __syncthreads();
+        if (tid == 0 && parts_listed > kListed) listed = kListed + 1;
+        __syncthreads();
+    }
     if (listed > kListed) {   // the same for the workgroup
-        const auto count = [&](auto f) {   // of items; the counters take turns
-            if (tid < 2) counted[tid] = 0;
+        const auto count = [&](auto f) {   // of items
+            if (tid == 0) counted = 0;
             __syncthreads();
             int c = 0;
-            each_item([&](const Place &p) { c += p.s != kNone && f(p); });
+            each_segment([&](const Place &p) { c += p.s != kNone && f(p); });
 #pragma unroll
             for (int i = 1; i < 64; i *= 2) c += __shfl_xor(c, i);
-            if (lane == 0) atomicAdd(&counted[0], c);
+            if (lane == 0) atomicAdd(&counted, c);
             __syncthreads();
-            const int total = counted[0];
+            const int total = counted;
             __syncthreads();
             return total;
         };
@@ -293,22 +432,25 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
             const int32_t higher = last | 1 << bit;
             if (count([&](const Place &p) { return ordered(p.s) == key && p.id < higher; }) < want) last = higher;
         }
-        bound.s = __longlong_as_double(static_cast<long long>(key >> 63 ? key & ~(uint64_t(1) << 63) : ~key));
-        bound.id = last;
+        // (0: there are fewer than n)
+        const double bound = key ? __longlong_as_double(static_cast<long long>(key >> 63 ? key & ~(uint64_t(1) << 63) : ~key)) : static_cast<double>(kNone);
         if (tid == 0) listed = 0;
         __syncthreads();
-        list_items();
+        each_segment([&](const Place &p) {
+            if (p.s > bound || (p.s == bound && p.id <= last)) list(p.id, p.s);
+        });
         __syncthreads();
     }
     const int found = listed;   // at most kListed now
     const int taken = found < n ? found : n;
     __syncthreads();
-    if (tid < found) {
-        const Place me = {list_s[tid], list_id[tid]};
+    // a wave has one of them at a time, its lanes those that may be in front
+    for (int i = wave; i < found; i += kPickWaves) {
+        const Place me = {list_s[i], list_id[i]};
         int front = 0;
-        for (int i = 0; i < found; ++i) front += precedes(Place{list_s[i], list_id[i]}, me);
-        if (front < n) segment_id[front] = me.id;
-        if (front == taken - 1) bound_s = me.s;   // with n segments, n elements have at least this
+        for (int j = lane; j - lane < found; j += 64) front += __builtin_popcountll(__ballot(j < found && precedes(Place{list_s[j], list_id[j]}, me)));
+        if (lane == 0 && front < n) segment_id[front] = me.id;
+        if (lane == 0 && front == taken - 1) bound_s = me.s;   // with n segments, n elements have at least this
     }
     if (tid == 0) listed = 0;
     __syncthreads();
@@ -331,11 +473,12 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
     __syncthreads();
     const int elements = listed;
     const int64_t out = static_cast<int64_t>(group) * n;
-    for (int j = tid; j < elements; j += kPickThreads) {
-        const Place me = {element_s[j], element_id[j]};
+    for (int i = wave; i < elements; i += kPickWaves) {
+        const Place me = {element_s[i], element_id[i]};
         int front = 0;
-        for (int i = 0; i < elements; ++i) front += precedes(Place{element_s[i], element_id[i]}, me);
-        if (front >= n) continue;
+        for (int j = lane; j - lane < elements; j += 64)
+            front += __builtin_popcountll(__ballot(j < elements && precedes(Place{element_s[j], element_id[j]}, me)));
+        if (lane != 0 || front >= n) continue;
         const int b = me.id >> 24;
         a.parents[out + front] = group * a.beams + b;
         a.tokens[out + front] = ended[b] ? a.pad : me.id & 0xFFFFFF;
@@ -391,7 +534,6 @@ hipError_t launch_beam_select(const BeamArgs &a, hipStream_t s) {
     const Scan scan = scan_of(a.workspace, rows, a.V);
     const dim3 grid((scan.parts + 3) / 4, static_cast<uint32_t>(rows));
     switch (scan.loads) {
-        case 1: hipLaunchKernelGGL((beam_scan_kernel<1>), grid, dim3(256), 0, s, a, scan); break;
         case 2: hipLaunchKernelGGL((beam_scan_kernel<2>), grid, dim3(256), 0, s, a, scan); break;
         case 4: hipLaunchKernelGGL((beam_scan_kernel<4>), grid, dim3(256), 0, s, a, scan); break;
         default: hipLaunchKernelGGL((beam_scan_kernel<8>), grid, dim3(256), 0, s, a, scan); break;

@@ -22,8 +22,11 @@ def _check(z, scores, keep, finished=None, pad=0):
     wp, wt, ws = S.beam_select(z, scores, keep, finished, pad)
     assert np.array_equal(p.cpu().numpy(), wp)
     assert np.array_equal(t.cpu().numpy(), wt)
-    got, none = s.double().cpu().numpy(), np.isneginf(ws)
-    assert np.array_equal(np.isneginf(got), none)
+    with np.errstate(over="ignore"):
+        none = np.isinf(ws.astype(np.float32))    # there is none, or its score is beyond fp32
+    got = s.double().cpu().numpy()
+    assert np.array_equal(got[none], ws.astype(np.float32)[none])
+    assert np.array_equal(np.isinf(got), none)
     assert (np.abs(got[~none] - ws[~none]) <= 2.0 ** -24 * np.abs(ws[~none]) + 1e-9).all()
     return wp
 
@@ -180,3 +183,14 @@ def test_refusals():
                 lambda: q4.beam_advance(i, i[0, :4], i[0], i[0], eos=2**40)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_scores_as_large_as_numbers_get():
+    """Where sums in fp32 would not be finite, with fewer candidates than are kept, and with more."""
+    z = np.full((4, 700), -np.inf)
+    z[:, [3, 500]] = [[1, 2], [3.4e38, -3.4e38], [-3e38, -3.3e38], [0, 1]]
+    scores = np.array([[3.3e38, -3.4e38], [-3.2e38, 1e31]])
+    _check(z, scores, 7)
+    rng = np.random.default_rng(9)
+    z = rng.standard_normal((4, 700)) * 1e38
+    _check(z, scores, 7, finished=np.array([[0, 1], [0, 0]]))
