@@ -18,8 +18,7 @@ namespace q4 {
 namespace {
 
 typedef float floatx4 __attribute__((ext_vector_type(4)));
-typedef float floatx4_row __attribute__((ext_vector_type(4), aligned(4)));   // rows start on 4 bytes only
-typedef int32_t i32x4_row __attribute__((ext_vector_type(4), aligned(4)));
+typedef int32_t i32x4_row __attribute__((ext_vector_type(4), aligned(4)));   // rows start on 4 bytes only
 
 constexpr float kNone = -__builtin_inff();
 
@@ -60,18 +59,21 @@ Scan scan_of(void *workspace, int64_t rows, int64_t V) {
     return s;
 }
 
+// The larger of two, or not a number where one is not: one instruction, where fmaxf
+// takes a second for each operand that came from memory.
+__device__ __forceinline__ float larger(float x, float y) { return __builtin_elementwise_maximum(x, y); }
+__device__ __forceinline__ double added(double x, double y) { return x + y; }
+
 // Sums and maxima over lanes without a way through LDS: DPP within 16 lanes, swaps of
 // rows beyond.
 template <int CTRL>
 __device__ __forceinline__ float from_lane(float v) {
-    const int w = __float_as_int(v);
-    return __int_as_float(__builtin_amdgcn_update_dpp(w, w, CTRL, 0xF, 0xF, false));
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 template <int CTRL>
 __device__ __forceinline__ double from_lane(double v) {
     const uint64_t w = static_cast<uint64_t>(__double_as_longlong(v));
-    const int lo = static_cast<int>(w), hi = static_cast<int>(w >> 32);
-    const uint32_t l = __builtin_amdgcn_update_dpp(lo, lo, CTRL, 0xF, 0xF, false), h = __builtin_amdgcn_update_dpp(hi, hi, CTRL, 0xF, 0xF, false);
+    const uint32_t l = __builtin_amdgcn_mov_dpp(static_cast<int>(w), CTRL, 0xF, 0xF, true), h = __builtin_amdgcn_mov_dpp(static_cast<int>(w >> 32), CTRL, 0xF, 0xF, true);
     return __longlong_as_double(static_cast<long long>(uint64_t(h) << 32 | l));
 }
 constexpr int kLane1 = 0xB1, kLane2 = 0x4E, kMirror8 = 0x141, kMirror16 = 0x140;   // lane ^ 1, lane ^ 2, 7 - lane, 15 - lane
@@ -112,13 +114,11 @@ __device__ __forceinline__ T join_64_of_8(T v, Join join) {   // of 8 lanes that
     v = join_rows<false>(v, join);
     return join_rows<true>(v, join);
 }
-__device__ __forceinline__ float larger(float x, float y) { return fmaxf(x, y); }
-__device__ __forceinline__ double added(double x, double y) { return x + y; }
 __device__ __forceinline__ float max_of_8(float v) { return join_8(v, larger); }
 __device__ __forceinline__ float max_of_64(float v) { return join_64_of_8(join_8(v, larger), larger); }
 __device__ __forceinline__ double sum_of_64(double v) { return join_64_of_8(join_8(v, added), added); }
 
-// e^x for -80 <= x <= 0, within 5e-11 of itself: 2^n times a polynomial on
+// e^x for |x| <= 700, within 5e-11 of itself: 2^n times a polynomial on
 // [-1/2, 1/2] ln 2 that equalizes the relative error (its coefficients are from an
 // exchange over that interval).  n comes out of the sum's low bits and goes into
 // the exponent: 12 instructions on 64 bits, 4 cycles each, where a conversion or a
@@ -135,19 +135,24 @@ __device__ __forceinline__ double exp64(double x) {
     p = fma(p, f, 0.5000000104536173);
     p = fma(p, f, 1.0000000002430987);
     p = fma(p, f, 0.9999999999616821);
-    const uint64_t n = static_cast<uint64_t>(__double_as_longlong(t)) << 52;
-    return __longlong_as_double(static_cast<long long>(static_cast<uint64_t>(__double_as_longlong(p)) + n));
+    // (what is not a number has 0 in the low bits, also one from fp32, and stays it)
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(p));
+    const uint32_t high = static_cast<uint32_t>(bits >> 32) + (static_cast<uint32_t>(__double_as_longlong(t)) << 20);
+    return __longlong_as_double(static_cast<long long>(uint64_t(high) << 32 | static_cast<uint32_t>(bits)));
 }
 
-// The same for fp32 differences from m of any size: below -80 it is 0, which no sum
-// of 2^24 terms with a largest one of 1 notices.  (What is not a number gives 0 too.)
-__device__ __forceinline__ double exp_below(float z, double m, float least) {
-    const double e = exp64(z - m);
-    return z >= least ? e : 0.0;
-}
+// The same for fp32 differences from m of up to 700: those below -80 (least = m - 80) count as
+// -80, 2e-35, which no sum of 2^24 terms with one of 1 or more notices.
+__device__ __forceinline__ double exp_below(float z, double m, float least) { return exp64(larger(z, least) - m); }
 
 // A wave has 256 * J consecutive tokens of a row, loads all of them, and waits
-// for nobody.
+// for nobody.  Each load's tokens are worked on as it arrives, relative to the largest
+// logit of the first one: in 64 bits a sum may be e^600 times larger than what it is relative
+// to, and where a logit is beyond that, or all were -inf so far, the sum follows it.  +inf and what
+// is not a number make the sum no number, and the part's largest logit either of them.
+constexpr int kBufferWord3 = 0x00020000;
+constexpr float kReach = 600.0f;
+
 template <int J>
 __global__ __launch_bounds__(256) void beam_scan_kernel(BeamArgs a, Scan out) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -156,48 +161,42 @@ __global__ __launch_bounds__(256) void beam_scan_kernel(BeamArgs a, Scan out) {
     if (part >= out.parts) return;
     if (a.finished && a.finished[row]) return;   // nothing of it is read
     const int base = part * 256 * J;
-    const float *src = a.logits + row * a.V;
+    // (what lies past the row's end is not read)
+    const __amdgpu_buffer_rsrc_t src = __builtin_amdgcn_make_buffer_rsrc(const_cast<float *>(a.logits + row * a.V), 0, 4 * a.V, kBufferWord3);
     floatx4 z[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+        z[j] = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(src, 4 * (base + 256 * j + 4 * lane), 0, 2));   // streaming
+    float top = kNone, limit = kNone;      // limit: -inf until there is a logit
+    float from = 0.0f, least = 0.0f;       // what the sum is relative to
+    double sum = 0.0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int t = base + 256 * j + 4 * lane;
-        if (t + 4 <= a.V) {
-            z[j] = *reinterpret_cast<const floatx4_row *>(src + t);
-        } else {
-            z[j] = (floatx4){kNone, kNone, kNone, kNone};
+        if (base + 256 * (j + 1) > a.V) {   // the row's last: the same for the wave
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
-                if (t + i < a.V) z[j][i] = src[t + i];
+            for (int i = 0; i < 4; ++i) z[j][i] = t + i < a.V ? z[j][i] : kNone;
         }
-    }
-    float top = kNone, seg[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        seg[j] = max_of_8(fmaxf(fmaxf(z[j][0], z[j][1]), fmaxf(z[j][2], z[j][3])));
-        top = fmaxf(top, seg[j]);
-    }
-    top = join_64_of_8(top, larger);
-    const float m = top == kNone ? 0.0f : top, least = m - 80.0f;   // all -inf: the sum is 0
-    double sum = 0.0;
-    bool bad = false;   // +inf, or what is not a number
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sum += exp_below(z[j][i], m, least);
-            bad |= !(z[j][i] < __builtin_inff());
-        }
-    }
-    if (bad) sum = __builtin_nan("");
-    sum = sum_of_64(sum);
-    if (lane == 0) {
-        out.sum[row * out.parts + part] = sum;
-        out.top[row * out.parts + part] = top;
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
+        const float segment = max_of_8(larger(larger(larger(z[j][0], z[j][1]), z[j][2]), z[j][3]));
         const int s = (base + 256 * j) / kBeamSegment + lane / 8;
-        if (lane % 8 == 0 && s < out.segments) out.segment[row * out.segments + s] = seg[j];
+        if (lane % 8 == 0 && s < out.segments) out.segment[row * out.segments + s] = segment;
+        top = larger(top, segment);
+        if (__any(!(segment <= limit))) {
+            const float to = join_64_of_8(top, larger);
+            sum = limit > kNone && to - from < 700.0f ? sum * exp64(static_cast<double>(from) - to) : 0.0;
+            from = to;
+            limit = to + kReach;
+            least = to - 80.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum += exp_below(z[j][i], from, least);
+    }
+    sum = sum_of_64(sum);
+    top = join_64_of_8(top, larger);
+    if (lane == 0) {
+        // relative to the largest, where there is one
+        out.sum[row * out.parts + part] = limit == kNone ? 0.0 : sum * exp64(static_cast<double>(from) - top);
+        out.top[row * out.parts + part] = top;
     }
 }
 
@@ -284,7 +283,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
                 }
                 float most = m;
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) most = fmaxf(most, top[k]);
+                for (int k = 0; k < kAhead; ++k) most = larger(most, top[k]);
                 const float least = most - 80.0f;
                 sum *= m > kNone && m >= least ? exp64(static_cast<double>(m) - most) : 0.0;   // (0 so far where m is -inf)
                 m = most;
