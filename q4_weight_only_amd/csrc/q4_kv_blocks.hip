@@ -196,44 +196,58 @@ __global__ __launch_bounds__(64 * kBlocksWaves, 2) void attention_blocks_kernel(
     }
 }
 
-// Joins the splits of a row's head: a wave each, D / 64 dimensions a lane.  (At most
-// 64 splits: plan_blocks.)
+// Joins the splits of a row's head: a wave each, whose lanes have D / 4 sets of four
+// dimensions, and 256 / D of such sets the splits side by side.  All loads, for up to
+// kJoinAhead splits a set, are on their way together.  (At most 64 splits: plan_blocks.)
+constexpr int kJoinAhead = 8;
+
 template <int D>
 __global__ __launch_bounds__(256) void blocks_join_kernel(AttentionArgs a, BlocksPlan plan) {
-    constexpr int EACH = D / 64;
+    constexpr int LANES = D / 4, SETS = 64 / LANES;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int x = lane % LANES, set = lane / LANES;
     const int b = blockIdx.z, q_head = blockIdx.x * 4 + wave;
     if (q_head >= a.q_heads) return;
     const KvSequence s = kv_sequence(a.kv, b);
+    const BlocksPartials ws = blocks_partials(a, plan);
     for (int t = blockIdx.y; t < s.rows; t += gridDim.y) {
         const int64_t at = static_cast<int64_t>(s.row0 + t) * a.q_heads + q_head;
-        const BlocksPartials ws = blocks_partials(a, plan);
         const floatx2 ml = lane < plan.splits ? ws.ml[at * plan.splits + lane] : (floatx2){kLowest, kUnseen};
-        const uint64_t some = __ballot(ml.y != kUnseen);   // (what is not a number is not kUnseen)
-        float top = ml.x;
+        const floatx4 *o = reinterpret_cast<const floatx4 *>(ws.o + at * plan.splits * D) + x;
+        floatx4 acc = {0, 0, 0, 0};
+        float top = ml.x, f = 0.0f;
+        for (int i0 = 0; i0 < plan.splits; i0 += SETS * kJoinAhead) {
+            floatx4 part[kJoinAhead];
 #pragma unroll
-        for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
-        const float f = ml.y != kUnseen ? __builtin_amdgcn_exp2f(ml.x - top) : 0.0f;
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const int i = i0 + SETS * k + set;
+                part[k] = o[(i < plan.splits ? i : 0) * LANES];
+            }
+            if (i0 == 0) {
+#pragma unroll
+                for (int i = 1; i < 64; i *= 2) top = fmaxf(top, __shfl_xor(top, i));
+                f = ml.y != kUnseen ? __builtin_amdgcn_exp2f(ml.x - top) : kUnseen;
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const int i = i0 + SETS * k + set;
+                const float fi = __shfl(f, i & 63);
+                // (a split that saw nothing has no O: what was read for it is not used)
+                if (i < plan.splits && fi != kUnseen) acc = acc + part[k] * fi;
+            }
+        }
         float total = ml.y != kUnseen ? f * ml.y : 0.0f;
+        const bool some = __ballot(ml.y != kUnseen) != 0;   // (what is not a number is not kUnseen)
 #pragma unroll
         for (int i = 1; i < 64; i *= 2) total += __shfl_xor(total, i);
-        float acc[EACH];
 #pragma unroll
-        for (int k = 0; k < EACH; ++k) acc[k] = 0.0f;
-        for (uint64_t left = some; left; left &= left - 1) {
-            const int i = __builtin_ctzll(left);
-            const float fi = __shfl(f, i);
-            const float *o = ws.o + (at * plan.splits + i) * D + lane * EACH;
+        for (int i = LANES; i < 64; i *= 2)
 #pragma unroll
-            for (int k = 0; k < EACH; ++k) acc[k] += o[k] * fi;
-        }
-        const float inv = some ? 1.0f / total : 0.0f;
-#pragma unroll
-        for (int k = 0; k < EACH; ++k) {
-            const int64_t to = at * D + lane * EACH + k;
-            if (a.out_bf16) static_cast<__bf16 *>(a.out)[to] = static_cast<__bf16>(acc[k] * inv);
-            else static_cast<float *>(a.out)[to] = acc[k] * inv;
-        }
+            for (int k = 0; k < 4; ++k) acc[k] += __shfl_xor(acc[k], i);
+        acc = acc * (some ? 1.0f / total : 0.0f);
+        if (set != 0) continue;
+        if (a.out_bf16) reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(a.out) + at * D)[x] = __builtin_convertvector(acc, bf16x4);
+        else reinterpret_cast<floatx4 *>(static_cast<float *>(a.out) + at * D)[x] = acc;
     }
 }
 

@@ -15,36 +15,49 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
 
 // ------------------------------------------------------------------ bounds
-// The smaller or larger over the 16 lanes of a row of lanes.
-template <int CTRL, bool MAX>
-__device__ __forceinline__ int pick_dpp(int v) {
-    const int other = __builtin_amdgcn_update_dpp(v, v, CTRL, 0xF, 0xF, false);
-    return MAX ? (other > v ? other : v) : (other < v ? other : v);
+// Codes two at a time as fp16, which holds every value of theirs, and not a number as
+// such: the larger or smaller of two is not a number where one is not.
+__device__ __forceinline__ uint32_t pair_of(uint32_t word, bool high) {
+    return __builtin_bit_cast(uint32_t, high ? __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true)
+                                             : __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false));
 }
 template <bool MAX>
-__device__ __forceinline__ int pick_of_16(int v) {
-    v = pick_dpp<0xB1, MAX>(v);     // lane ^ 1
-    v = pick_dpp<0x4E, MAX>(v);     // lane ^ 2
-    v = pick_dpp<0x141, MAX>(v);    // 7 - lane, within 8
-    return pick_dpp<0x140, MAX>(v); // 15 - lane, within 16
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y) {
+    const halfx2 a = __builtin_bit_cast(halfx2, x), b = __builtin_bit_cast(halfx2, y);
+    return __builtin_bit_cast(uint32_t, MAX ? __builtin_elementwise_maximum(a, b) : __builtin_elementwise_minimum(a, b));
 }
+constexpr uint32_t kLeast = 0xFC00FC00u, kMost = 0x7C007C00u;   // -inf and inf, two each
 
-// A code's place in the order of the values: a code of sign and magnitude as a whole number.
-__device__ __forceinline__ int place_of(uint32_t code) { return code & 0x80 ? -static_cast<int>(code & 0x7F) : static_cast<int>(code & 0x7F); }
-
-// The value at that place, over 4.
-__device__ __forceinline__ float quarter_of(int place) {
-    const uint32_t code = place < 0 ? 0x80u | static_cast<uint32_t>(-place) : static_cast<uint32_t>(place);
-    return __builtin_amdgcn_cvt_f32_fp8(code, 0) * 0.25f;
+// One step of picking over lanes: a lane and its mate, CTRL, have 2 N words each, and
+// each is left with N of them, the mate's picked in: the upper ones where `upper`.
+template <int CTRL, bool MAX, int N>
+__device__ __forceinline__ void halve(uint32_t (&v)[8], bool upper) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint32_t keep = upper ? v[N + i] : v[i], send = upper ? v[i] : v[N + i];
+        v[i] = pick<MAX>(keep, __builtin_amdgcn_mov_dpp(send, CTRL, 0xF, 0xF, true));
+    }
 }
-
-constexpr int kNanPlace = 127;   // of 0x7F; -127 of 0xFF
+// Over 16 lanes, of 16 values in 8 words: the lane is left with its value in the
+// low half, that of place_of_lane.
+template <bool MAX>
+__device__ __forceinline__ uint32_t pick_of_16(uint32_t (&v)[8], int lane) {
+    halve<0x140, MAX, 4>(v, lane & 8);   // 15 - lane
+    halve<0x141, MAX, 2>(v, lane & 4);   // 7 - lane, within 8
+    halve<0x4E, MAX, 1>(v, lane & 2);    // lane ^ 2
+    const uint32_t mine = lane & 1 ? v[0] >> 16 : v[0] & 0xFFFF, other = lane & 1 ? v[0] & 0xFFFF : v[0] >> 16;
+    return pick<MAX>(mine, __builtin_amdgcn_mov_dpp(other, 0xB1, 0xF, 0xF, true));
+}
+__device__ __forceinline__ int place_of_lane(int lane) { return lane & 15; }   // the steps above take its bits from the top
 
 // A wave has the keys of one block and kv head.  Lane l of a 1 KB piece has 16
-// dimensions, l / 16, of one token, l % 16.
+// dimensions, l / 16, of one token, l % 16; after four steps over 16 lanes, in each of
+// which a lane hands on half of what it has, it has one dimension of all tokens.  (All
+// 16 dimensions in every lane: 7.5 us for one token of each of 8 heads, which is
+// the time that its code takes to arrive.)
 template <int D>
 __global__ __launch_bounds__(256) void summarize_kernel(SelectArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -68,146 +81,169 @@ __global__ __launch_bounds__(256) void summarize_kernel(SelectArgs a) {
         int8_t *out = a.summary + plane * (2 * D);
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) {
-            uint32_t hi[4] = {0, 0, 0, 0}, lo[4] = {0, 0, 0, 0};
+            uint32_t top[8], low[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                int top = -128, low = 128;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int p = place_of(codes[h][j][i / 4] >> (i % 4 * 8) & 0xFF);
-                    if (there[h]) {
-                        top = p > top ? p : top;
-                        low = p < low ? p : low;
-                    }
-                }
-                top = pick_of_16<true>(top);
-                low = pick_of_16<false>(low);
-                const bool bad = top == kNanPlace || low == -kNanPlace;
-                const int up = bad ? 127 : static_cast<int>(ceilf(quarter_of(top)));
-                const int down = bad ? -127 : static_cast<int>(floorf(quarter_of(low)));
-                hi[i / 4] |= static_cast<uint32_t>(up & 0xFF) << (i % 4 * 8);
-                lo[i / 4] |= static_cast<uint32_t>(down & 0xFF) << (i % 4 * 8);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t x = pair_of(codes[0][j][i / 2], i % 2), y = pair_of(codes[1][j][i / 2], i % 2);
+                top[i] = pick<true>(there[0] ? x : kLeast, there[1] ? y : kLeast);
+                low[i] = pick<false>(there[0] ? x : kMost, there[1] ? y : kMost);
             }
-            if (lane % 16 == 0) {
-                const int d = 64 * j + lane;   // 16 * (lane / 16)
-                *reinterpret_cast<u32x4 *>(out + d) = (u32x4){hi[0], hi[1], hi[2], hi[3]};
-                *reinterpret_cast<u32x4 *>(out + D + d) = (u32x4){lo[0], lo[1], lo[2], lo[3]};
-            }
+            const uint32_t most = pick_of_16<true>(top, lane), least = pick_of_16<false>(low, lane);
+            const float up = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(most)));
+            const float down = static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(least)));
+            const int d = 64 * j + (lane & 48) + place_of_lane(lane);
+            const bool bad = !(up - down < __builtin_inff());   // not a number among them
+            out[d] = static_cast<int8_t>(bad ? 127 : static_cast<int>(ceilf(up * 0.25f)));
+            out[D + d] = static_cast<int8_t>(bad ? -127 : static_cast<int>(floorf(down * 0.25f)));
         }
     }
 }
 
 // ------------------------------------------------------------------ scores
-constexpr int kScoreTiles = 2;   // of 16 blocks, of a wave at a time
 constexpr int kScoreWaves = 4;
 
-// A workgroup has 16 rows of one sequence and kv head and some of its blocks; a
-// wave's product is 16 rows x 16 blocks, the bounds straight from memory to operand
-// registers: lane l has 16 bytes at 16 (l / 16) of each 64 of block l % 16.
-template <int D>
-__global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, int blocks_each) {
+// The largest over each LANES lanes (32 or 64), in all of them.
+template <int CTRL>
+__device__ __forceinline__ int larger_of_lane(int v) {
+    const int other = __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
+    return other > v ? other : v;
+}
+template <int LANES>
+__device__ __forceinline__ int max_of(int v) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    v = larger_of_lane<0xB1>(v);    // lane ^ 1
+    v = larger_of_lane<0x4E>(v);    // lane ^ 2
+    v = larger_of_lane<0x141>(v);   // 7 - lane, within 8
+    v = larger_of_lane<0x140>(v);   // 15 - lane, within 16
+    const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+    v = static_cast<int>(x.x) > static_cast<int>(x.y) ? x.x : x.y;
+    if (LANES == 64) {
+        const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+        v = static_cast<int>(y.x) > static_cast<int>(y.y) ? y.x : y.y;
+    }
+    return v;
+}
+
+// How the workgroups divide: units of 16 rows of a sequence and a range of its
+// blocks, each for every kv head.
+struct ScorePlan {
+    int tiles;     // of 16 rows, of the sequence with most of them
+    int ranges;    // of 16 * TILES blocks for each wave
+    int units;     // tiles * ranges * sequences
+};
+
+// A workgroup has 16 rows of one sequence and kv head and a range of its blocks; a
+// wave's product is 16 rows x 16 blocks, TILES of them side by side, the bounds
+// straight from memory to operand registers: lane l has 16 bytes at 16 (l / 16) of
+// each 64 of block l % 16.  They are on their way while the rows' sums are formed.
+//
+// What bounds it is memory.  A block's exponents of all heads are in one line, so
+// a unit's heads are given to one of the 8 dies, one after the other.
+template <int D, int TILES>
+__global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, ScorePlan plan) {
     constexpr int KK = 2 * D / 64, kStride = 2 * D + 16;   // bytes of a row of q in LDS
+    constexpr int kEach = kScoreWaves * 16 * TILES;        // blocks of a workgroup
     __shared__ __align__(16) uint8_t parts[2][16][kStride];   // high and low 7 bits of Q+ and Q-
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
-    const int b = blockIdx.z, head = blockIdx.x % a.kv.kv_heads, begin = blockIdx.x / a.kv.kv_heads * blocks_each;
+    const int head = blockIdx.x / 8, unit = blockIdx.y * 8 + blockIdx.x % 8;   // workgroups are dealt to the dies in turn
+    if (unit >= plan.units) return;
+    const int range = unit % plan.ranges, b = unit / plan.ranges / plan.tiles, tile = unit / plan.ranges % plan.tiles;
     const KvSequence s = kv_sequence(a.kv, b);
-    for (int t0 = blockIdx.y * 16; t0 < s.rows; t0 += gridDim.y * 16) {
+    for (int t0 = tile * 16; t0 < s.rows; t0 += plan.tiles * 16) {
         const int rows = s.rows - t0 < 16 ? s.rows - t0 : 16;
         const int last = s.pos0 + t0 + rows - 1;   // position of the last row
         int end = last < 0 ? 0 : last / kKvBlock + 1;
         end = end < a.max_blocks ? end : a.max_blocks;
-        if (begin >= end) continue;                // the same for the workgroup
-        __syncthreads();                           // the rows before have been read
-        {   // D / 2 lanes have a row, a pair of dimensions each
-            constexpr int kLanes = D / 2, kAtOnce = 64 * kScoreWaves / kLanes;
-            const int pair = threadIdx.x % kLanes;
+        for (int begin = range * kEach; begin < end; begin += plan.ranges * kEach) {   // the same for the workgroup
+            const int first = begin + wave * 16 * TILES;
+            int32_t id[TILES];
+            i32x4 bounds[TILES][KK];
+            int e[TILES];
 #pragma unroll
-            for (int i = 0; i < 16 / kAtOnce; ++i) {
-                const int row = i * kAtOnce + threadIdx.x / kLanes;
-                if (i > 0 && i * kAtOnce >= rows) {   // no row of these
-                    for (int p = 0; p < 2; ++p) {
-                        *reinterpret_cast<uint16_t *>(&parts[p][row][2 * pair]) = 0;
-                        *reinterpret_cast<uint16_t *>(&parts[p][row][D + 2 * pair]) = 0;
-                    }
-                    continue;
-                }
-                double up[2] = {0, 0}, down[2] = {0, 0};
-                if (row < rows) {
-                    const uint32_t *q = reinterpret_cast<const uint32_t *>(
-                        a.q + (static_cast<int64_t>(s.row0 + t0 + row) * a.q_heads + head * a.group) * D) + pair;
-                    for (int h = 0; h < a.group; ++h) {
-                        const uint32_t v = q[h * (D / 2)];
-                        const float x[2] = {__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u)};
+            for (int t = 0; t < TILES; ++t) id[t] = first + 16 * t + r < end ? kv_block_id(a.kv, b, first + 16 * t + r) : -1;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            // what is not a number goes into both
-                            up[k] += x[k] < 0.0f ? 0.0f : x[k];
-                            down[k] += x[k] > 0.0f ? 0.0f : x[k];
-                        }
-                    }
-                }
-                double top = fmax(fmax(up[0], up[1]), -fmin(down[0], down[1]));
-                bool fine = __builtin_isfinite(up[0]) && __builtin_isfinite(up[1]) && __builtin_isfinite(down[0]) && __builtin_isfinite(down[1]);
-#pragma unroll
-                for (int m = 1; m < kLanes; m *= 2) top = fmax(top, __shfl_xor(top, m));
-                const uint64_t all = __ballot(fine);
-                fine = kLanes == 64 ? all == ~uint64_t(0) : static_cast<uint32_t>(lane < 32 ? all : all >> 32) == ~0u;
-                const int e = static_cast<int>(static_cast<uint64_t>(__double_as_longlong(top)) >> 52 & 0x7FF) - 1022;   // top < 2^e
-                uint32_t high[2] = {0, 0}, low[2] = {0, 0};
-                if (fine && top > 0.0) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int v = static_cast<int>(__builtin_rint(__builtin_ldexp(k < 2 ? up[k & 1] : down[k & 1], 13 - e)));
-                        high[k / 2] |= static_cast<uint32_t>((v >> 7) & 0xFF) << (k % 2 * 8);
-                        low[k / 2] |= static_cast<uint32_t>(v & 0x7F) << (k % 2 * 8);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    *reinterpret_cast<uint16_t *>(&parts[0][row][k * D + 2 * pair]) = static_cast<uint16_t>(high[k]);
-                    *reinterpret_cast<uint16_t *>(&parts[1][row][k * D + 2 * pair]) = static_cast<uint16_t>(low[k]);
-                }
-            }
-        }
-        __syncthreads();
-        i32x4 qa[2][KK];
-#pragma unroll
-        for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int k = 0; k < KK; ++k) qa[p][k] = *reinterpret_cast<const i32x4 *>(&parts[p][r][64 * k + 16 * g]);
-        const int stop = begin + blocks_each < end ? begin + blocks_each : end;
-        for (int first = begin + wave * 16 * kScoreTiles; first < stop; first += kScoreWaves * 16 * kScoreTiles) {
-            int32_t id[kScoreTiles];
-            i32x4 bounds[kScoreTiles][KK];
-            int e[kScoreTiles];
-#pragma unroll
-            for (int t = 0; t < kScoreTiles; ++t) id[t] = first + 16 * t + r < stop ? kv_block_id(a.kv, b, first + 16 * t + r) : -1;
-#pragma unroll
-            for (int t = 0; t < kScoreTiles; ++t) {
+            for (int t = 0; t < TILES; ++t) {
                 const int64_t plane = static_cast<int64_t>(id[t] < 0 ? 0 : id[t]) * a.kv.kv_heads + head;
-                e[t] = a.kv.exps[plane * 2];
                 const i32x4 *src = reinterpret_cast<const i32x4 *>(a.summary + plane * (2 * D)) + g;
 #pragma unroll
                 for (int k = 0; k < KK; ++k) bounds[t][k] = __builtin_nontemporal_load(src + 4 * k);
+                e[t] = a.kv.exps[plane * 2];
+            }
+            __syncthreads();                       // what was there before has been read
+            {   // D / 2 lanes have a row, a pair of dimensions each
+                constexpr int kLanes = D / 2, kAtOnce = 64 * kScoreWaves / kLanes;
+                const int pair = threadIdx.x % kLanes;
+                for (int i = 0; i < 16 / kAtOnce; ++i) {
+                    const int row = i * kAtOnce + threadIdx.x / kLanes;
+                    double up[2] = {0, 0}, down[2] = {0, 0};
+                    if (row < rows) {
+                        const uint32_t *q = reinterpret_cast<const uint32_t *>(
+                            a.q + (static_cast<int64_t>(s.row0 + t0 + row) * a.q_heads + head * a.group) * D) + pair;
+                        for (int h0 = 0; h0 < a.group; h0 += 4) {
+                            uint32_t v[4];   // (a head past the group is 0)
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) v[h] = h0 + h < a.group ? q[(h0 + h) * (D / 2)] : 0;
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) {
+                                const float x[2] = {__uint_as_float(v[h] << 16), __uint_as_float(v[h] & 0xFFFF0000u)};
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    // what is not a number goes into both
+                                    up[k] += x[k] < 0.0f ? 0.0f : x[k];
+                                    down[k] += x[k] > 0.0f ? 0.0f : x[k];
+                                }
+                            }
+                        }
+                    }
+                    const double most = fmax(fmax(up[0], up[1]), -fmin(down[0], down[1]));
+                    const bool fine = __builtin_isfinite(up[0] + up[1] - down[0] - down[1]);
+                    int e2 = static_cast<int>(static_cast<uint64_t>(__double_as_longlong(most)) >> 52 & 0x7FF);   // most < 2^(e2 - 1022)
+                    e2 = max_of<kLanes>(e2);
+                    const uint64_t all = __ballot(fine);
+                    const bool every = kLanes == 64 ? all == ~uint64_t(0) : static_cast<uint32_t>(lane < 32 ? all : all >> 32) == ~0u;
+                    uint32_t high[2] = {0, 0}, low[2] = {0, 0};
+                    if (every && e2 > 0) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int v = static_cast<int>(__builtin_rint(__builtin_ldexp(k < 2 ? up[k & 1] : down[k & 1], 13 + 1022 - e2)));
+                            high[k / 2] |= static_cast<uint32_t>((v >> 7) & 0xFF) << (k % 2 * 8);
+                            low[k / 2] |= static_cast<uint32_t>(v & 0x7F) << (k % 2 * 8);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        *reinterpret_cast<uint16_t *>(&parts[0][row][k * D + 2 * pair]) = static_cast<uint16_t>(high[k]);
+                        *reinterpret_cast<uint16_t *>(&parts[1][row][k * D + 2 * pair]) = static_cast<uint16_t>(low[k]);
+                    }
+                    if ((i + 1) * kAtOnce >= rows) break;   // rows past the last hold anything: their sums are not used
+                }
+            }
+            __syncthreads();
+            if (first >= end) continue;
+            i32x4 sum[TILES][2];
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) sum[t][0] = sum[t][1] = (i32x4){0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KK; ++k) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const i32x4 q = *reinterpret_cast<const i32x4 *>(&parts[p][r][64 * k + 16 * g]);
+#pragma unroll
+                    for (int t = 0; t < TILES; ++t) sum[t][p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(q, bounds[t][k], sum[t][p], 0, 0, 0);
+                }
             }
 #pragma unroll
-            for (int t = 0; t < kScoreTiles; ++t) {
-                i32x4 high = {0, 0, 0, 0}, low = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    high = __builtin_amdgcn_mfma_i32_16x16x64_i8(qa[0][k], bounds[t][k], high, 0, 0, 0);
-                    low = __builtin_amdgcn_mfma_i32_16x16x64_i8(qa[1][k], bounds[t][k], low, 0, 0, 0);
-                }
+            for (int t = 0; t < TILES; ++t) {
                 const int block = first + 16 * t + r;
-                if (block >= stop) continue;
+                if (block >= end) continue;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int row = 4 * g + j;
                     if (row >= rows) break;
-                    const float sum = static_cast<float>(high[j] * 128 + low[j]);   // below 2^28, rounded once
+                    const float total = static_cast<float>(sum[t][0][j] * 128 + sum[t][1][j]);   // below 2^28, rounded once
                     a.scores[(static_cast<int64_t>(s.row0 + t0 + row) * a.kv.kv_heads + head) * a.max_blocks + block] =
-                        id[t] < 0 ? -__builtin_inff() : __builtin_ldexpf(sum, e[t]);
+                        id[t] < 0 ? -__builtin_inff() : __builtin_ldexpf(total, e[t]);
                 }
             }
         }
@@ -222,13 +258,13 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 }
 
 // A workgroup has one row and kv head.  The m-th largest of the scores between the
-// first and the last blocks is found bit by bit, each time counting how many
+// first and the last blocks is found two bits at a time, each time counting how many
 // scores are no less, until that is m; then those are written in their order.
 // LOOP: more scores than the workgroup's registers hold, read each time.
 template <int THREADS, int EACH, bool LOOP>
 __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
     constexpr int WAVES = THREADS / 64, kHeld = THREADS * EACH;
-    __shared__ int32_t counter[3];
+    __shared__ int32_t counter[3][3];   // of a step, for each of its values
     __shared__ uint32_t folded[2][WAVES];
     __shared__ int32_t sums[2][WAVES];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -279,7 +315,7 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
             folded[0][wave] = all_and;
             folded[1][wave] = all_or;
         }
-        if (tid < 3) counter[tid] = 0;
+        if (tid < 9) counter[tid / 3][tid % 3] = 0;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
@@ -290,23 +326,32 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
         int bit = differ ? 31 - __builtin_clz(differ) : -1;
         uint32_t least = bit < 31 ? all_and >> (bit + 1) << (bit + 1) : 0;   // (bit 31: no common bits)
         int reach = n;   // how many keys are at least `least`
-        for (int step = 0; bit >= 0 && reach != m; --bit, ++step) {
-            const uint32_t probe = least | 1u << bit;
-            int c = 0;
+        // two bits a step: of the three values that they may add, the largest that m keys reach
+        for (int step = 0; bit >= 0 && reach != m; bit -= 2, ++step) {
+            const uint32_t unit = bit > 0 ? 1u << (bit - 1) : 1;
+            const int most = bit > 0 ? 3 : 1;   // (the last bit may be one)
+            int c[3] = {0, 0, 0};
             for (int turn = 0; turn < turns; ++turn) {
                 if (LOOP) load(turn);
 #pragma unroll
-                for (int k = 0; k < EACH; ++k) c += __builtin_popcountll(__ballot(key[k] >= probe));
+                for (int k = 0; k < EACH; ++k)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) c[i] += __builtin_popcountll(__ballot(key[k] >= least + (i + 1) * unit));
             }
-            // three counters in turn: one barrier a step
-            if (lane == 0) atomicAdd(&counter[step % 3], c);
-            if (tid == 0) counter[(step + 1) % 3] = 0;
+            // three sets of counters in turn: one barrier a step
+            if (lane < 3) atomicAdd(&counter[step % 3][lane], lane == 0 ? c[0] : lane == 1 ? c[1] : c[2]);
+            if (tid < 3) counter[(step + 1) % 3][tid] = 0;
             __syncthreads();
-            c = counter[step % 3];
-            if (c >= m) {
-                least = probe;
-                reach = c;
+            int add = 0;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                const int all = counter[step % 3][i];
+                if (i < most && all >= m) {
+                    add = i + 1;
+                    reach = all;
+                }
             }
+            least += add * unit;
         }
         // all above `least`, and of those equal to it the first; where m are at
         // least that, all of these
@@ -352,23 +397,33 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
     }
 }
 
+// Four tiles of blocks a wave where that leaves two workgroups for every compute
+// unit, one otherwise; the kernels loop where a launch cannot hold all units.
+constexpr int64_t kMostUnits = 8 * 65535;
+
+template <int D, int TILES>
+void launch_score(const SelectArgs &a, hipStream_t s) {
+    ScorePlan p;
+    const int64_t batch = a.kv.batch, each = kScoreWaves * 16 * TILES;
+    int64_t ranges = (a.max_blocks + each - 1) / each, tiles = (static_cast<int64_t>(a.max_rows) + 15) / 16;
+    if (ranges * batch > kMostUnits) ranges = kMostUnits / batch;
+    if (tiles * ranges * batch > kMostUnits) tiles = kMostUnits / (ranges * batch);
+    p.tiles = static_cast<int>(tiles);
+    p.ranges = static_cast<int>(ranges);
+    p.units = static_cast<int>(tiles * ranges * batch);
+    hipLaunchKernelGGL((score_kernel<D, TILES>), dim3(8 * a.kv.kv_heads, (p.units + 7) / 8), dim3(64 * kScoreWaves), 0, s, a, p);
+}
+
 template <int D>
 hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
-    const int64_t tiles = (static_cast<int64_t>(a.max_rows) + 15) / 16, sets = a.kv.kv_heads * static_cast<int64_t>(a.kv.batch) * tiles;
-    // blocks of a workgroup: as many as leave four workgroups for every compute unit
-    constexpr int kLeast = kScoreWaves * 16 * kScoreTiles;
-    int64_t ranges = 1024 / sets;
-    const int64_t most = (a.max_blocks + kLeast - 1) / kLeast;
-    ranges = ranges < 1 ? 1 : ranges > most ? most : ranges;
-    const int64_t each = ((a.max_blocks + ranges - 1) / ranges + kLeast - 1) / kLeast * kLeast;
-    ranges = (a.max_blocks + each - 1) / each;
-    const dim3 grid(static_cast<uint32_t>(a.kv.kv_heads * ranges), static_cast<uint32_t>(tiles < 65535 ? tiles : 65535), a.kv.batch);
-    hipLaunchKernelGGL((score_kernel<D>), grid, dim3(64 * kScoreWaves), 0, s, a, static_cast<int>(each));
+    const int64_t sets = a.kv.kv_heads * static_cast<int64_t>(a.kv.batch) * ((static_cast<int64_t>(a.max_rows) + 15) / 16);
+    if (sets * ((a.max_blocks + 255) / 256) >= 512) launch_score<D, 4>(a, s);
+    else launch_score<D, 1>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 rows(a.kv.kv_heads, a.max_rows < 65535 ? a.max_rows : 65535, a.kv.batch);
     if (a.max_blocks <= 1024) hipLaunchKernelGGL((choose_kernel<256, 4, false>), rows, dim3(256), 0, s, a);
-    else if (a.max_blocks <= 4096) hipLaunchKernelGGL((choose_kernel<1024, 4, false>), rows, dim3(1024), 0, s, a);
+    else if (a.max_blocks <= 4096) hipLaunchKernelGGL((choose_kernel<256, 16, false>), rows, dim3(256), 0, s, a);
     else if (a.max_blocks <= 16384) hipLaunchKernelGGL((choose_kernel<1024, 16, false>), rows, dim3(1024), 0, s, a);
     else hipLaunchKernelGGL((choose_kernel<1024, 16, true>), rows, dim3(1024), 0, s, a);
     return hipGetLastError();
