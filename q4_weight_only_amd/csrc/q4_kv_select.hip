@@ -100,26 +100,25 @@ __global__ __launch_bounds__(256) void summarize_kernel(SelectArgs a) {
 }
 
 // ------------------------------------------------------------------ scores
-constexpr int kScoreWaves = 4;
+constexpr int kScoreWaves = 4, kScoreBlocks = 16 * kScoreWaves;   // of a workgroup
 
-// The largest over each LANES lanes (32 or 64), in all of them.
+// What `join` makes of the values of each LANES lanes (32 or 64), in all of them.
 template <int CTRL>
-__device__ __forceinline__ int larger_of_lane(int v) {
-    const int other = __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, true);
-    return other > v ? other : v;
+__device__ __forceinline__ uint32_t from_lane(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(v), CTRL, 0xF, 0xF, true));
 }
-template <int LANES>
-__device__ __forceinline__ int max_of(int v) {
+template <int LANES, typename Join>
+__device__ __forceinline__ uint32_t fold(uint32_t v, Join join) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    v = larger_of_lane<0xB1>(v);    // lane ^ 1
-    v = larger_of_lane<0x4E>(v);    // lane ^ 2
-    v = larger_of_lane<0x141>(v);   // 7 - lane, within 8
-    v = larger_of_lane<0x140>(v);   // 15 - lane, within 16
+    v = join(v, from_lane<0xB1>(v));    // lane ^ 1
+    v = join(v, from_lane<0x4E>(v));    // lane ^ 2
+    v = join(v, from_lane<0x141>(v));   // 7 - lane, within 8
+    v = join(v, from_lane<0x140>(v));   // 15 - lane, within 16
     const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
-    v = static_cast<int>(x.x) > static_cast<int>(x.y) ? x.x : x.y;
+    v = join(x.x, x.y);
     if (LANES == 64) {
         const u32x2 y = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
-        v = static_cast<int>(y.x) > static_cast<int>(y.y) ? y.x : y.y;
+        v = join(y.x, y.y);
     }
     return v;
 }
@@ -128,21 +127,20 @@ __device__ __forceinline__ int max_of(int v) {
 // blocks, each for every kv head.
 struct ScorePlan {
     int tiles;     // of 16 rows, of the sequence with most of them
-    int ranges;    // of 16 * TILES blocks for each wave
+    int ranges;    // of 16 blocks for each wave
     int units;     // tiles * ranges * sequences
 };
 
 // A workgroup has 16 rows of one sequence and kv head and a range of its blocks; a
-// wave's product is 16 rows x 16 blocks, TILES of them side by side, the bounds
-// straight from memory to operand registers: lane l has 16 bytes at 16 (l / 16) of
-// each 64 of block l % 16.  They are on their way while the rows' sums are formed.
+// wave's product is 16 rows x 16 blocks, the bounds straight from memory to operand
+// registers: lane l has 16 bytes at 16 (l / 16) of each 64 of block l % 16.  They are on
+// their way while the rows' sums are formed.
 //
 // What bounds it is memory.  A block's exponents of all heads are in one line, so
 // a unit's heads are given to one of the 8 dies, one after the other.
-template <int D, int TILES>
+template <int D>
 __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, ScorePlan plan) {
     constexpr int KK = 2 * D / 64, kStride = 2 * D + 16;   // bytes of a row of q in LDS
-    constexpr int kEach = kScoreWaves * 16 * TILES;        // blocks of a workgroup
     __shared__ __align__(16) uint8_t parts[2][16][kStride];   // high and low 7 bits of Q+ and Q-
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -155,21 +153,15 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, S
         const int last = s.pos0 + t0 + rows - 1;   // position of the last row
         int end = last < 0 ? 0 : last / kKvBlock + 1;
         end = end < a.max_blocks ? end : a.max_blocks;
-        for (int begin = range * kEach; begin < end; begin += plan.ranges * kEach) {   // the same for the workgroup
-            const int first = begin + wave * 16 * TILES;
-            int32_t id[TILES];
-            i32x4 bounds[TILES][KK];
-            int e[TILES];
+        for (int begin = range * kScoreBlocks; begin < end; begin += plan.ranges * kScoreBlocks) {   // the same for the workgroup
+            const int block = begin + 16 * wave + r;
+            const int32_t id = block < end ? kv_block_id(a.kv, b, block) : -1;
+            const int64_t plane = static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head;
+            const i32x4 *src = reinterpret_cast<const i32x4 *>(a.summary + plane * (2 * D)) + g;
+            i32x4 bounds[KK];
 #pragma unroll
-            for (int t = 0; t < TILES; ++t) id[t] = first + 16 * t + r < end ? kv_block_id(a.kv, b, first + 16 * t + r) : -1;
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-                const int64_t plane = static_cast<int64_t>(id[t] < 0 ? 0 : id[t]) * a.kv.kv_heads + head;
-                const i32x4 *src = reinterpret_cast<const i32x4 *>(a.summary + plane * (2 * D)) + g;
-#pragma unroll
-                for (int k = 0; k < KK; ++k) bounds[t][k] = __builtin_nontemporal_load(src + 4 * k);
-                e[t] = a.kv.exps[plane * 2];
-            }
+            for (int k = 0; k < KK; ++k) bounds[k] = src[4 * k];   // a line is two of them: not nontemporal
+            const int e = a.kv.exps[plane * 2];
             __syncthreads();                       // what was there before has been read
             {   // D / 2 lanes have a row, a pair of dimensions each
                 constexpr int kLanes = D / 2, kAtOnce = 64 * kScoreWaves / kLanes;
@@ -198,8 +190,9 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, S
                     }
                     const double most = fmax(fmax(up[0], up[1]), -fmin(down[0], down[1]));
                     const bool fine = __builtin_isfinite(up[0] + up[1] - down[0] - down[1]);
-                    int e2 = static_cast<int>(static_cast<uint64_t>(__double_as_longlong(most)) >> 52 & 0x7FF);   // most < 2^(e2 - 1022)
-                    e2 = max_of<kLanes>(e2);
+                    // most < 2^(e2 - 1022)
+                    const int e2 = static_cast<int>(fold<kLanes>(static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(most)) >> 52 & 0x7FF),
+                                                                 [](uint32_t x, uint32_t y) { return x > y ? x : y; }));
                     const uint64_t all = __ballot(fine);
                     const bool every = kLanes == 64 ? all == ~uint64_t(0) : static_cast<uint32_t>(lane < 32 ? all : all >> 32) == ~0u;
                     uint32_t high[2] = {0, 0}, low[2] = {0, 0};
@@ -220,31 +213,20 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, S
                 }
             }
             __syncthreads();
-            if (first >= end) continue;
-            i32x4 sum[TILES][2];
+            i32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-            for (int t = 0; t < TILES; ++t) sum[t][0] = sum[t][1] = (i32x4){0, 0, 0, 0};
+            for (int k = 0; k < KK; ++k)
 #pragma unroll
-            for (int k = 0; k < KK; ++k) {
+                for (int p = 0; p < 2; ++p)
+                    sum[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4 *>(&parts[p][r][64 * k + 16 * g]), bounds[k], sum[p], 0, 0, 0);
+            if (block >= end) continue;
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const i32x4 q = *reinterpret_cast<const i32x4 *>(&parts[p][r][64 * k + 16 * g]);
-#pragma unroll
-                    for (int t = 0; t < TILES; ++t) sum[t][p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(q, bounds[t][k], sum[t][p], 0, 0, 0);
-                }
-            }
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-                const int block = first + 16 * t + r;
-                if (block >= end) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int row = 4 * g + j;
-                    if (row >= rows) break;
-                    const float total = static_cast<float>(sum[t][0][j] * 128 + sum[t][1][j]);   // below 2^28, rounded once
-                    a.scores[(static_cast<int64_t>(s.row0 + t0 + row) * a.kv.kv_heads + head) * a.max_blocks + block] =
-                        id[t] < 0 ? -__builtin_inff() : __builtin_ldexpf(total, e[t]);
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int row = 4 * g + j;
+                if (row >= rows) break;
+                const float total = static_cast<float>(sum[0][j] * 128 + sum[1][j]);   // below 2^28, rounded once
+                a.scores[(static_cast<int64_t>(s.row0 + t0 + row) * a.kv.kv_heads + head) * a.max_blocks + block] =
+                    id < 0 ? -__builtin_inff() : __builtin_ldexpf(total, e);
             }
         }
     }
@@ -259,15 +241,20 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 
 // A workgroup has one row and kv head.  The m-th largest of the scores between the
 // first and the last blocks is found two bits at a time, each time counting how many
-// scores are no less, until that is m; then those are written in their order.
+// scores are no less, until that is m; then those are written in their order.  A
+// thread has EACH / 4 times four scores next to each other, THREADS * 4 apart.
 // LOOP: more scores than the workgroup's registers hold, read each time.
+//
+// What bounds it is one step after the other: lengths, scores, some ten counts with a
+// barrier each.
 template <int THREADS, int EACH, bool LOOP>
 __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
-    constexpr int WAVES = THREADS / 64, kHeld = THREADS * EACH;
+    constexpr int WAVES = THREADS / 64, kHeld = THREADS * EACH, SETS = EACH / 4;
+    typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
     __shared__ int32_t counter[3][3];   // of a step, for each of its values
     __shared__ uint32_t folded[2][WAVES];
-    __shared__ int32_t sums[2][WAVES];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ int32_t sums[2][2][SETS][WAVES];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int b = blockIdx.z, head = blockIdx.x;
     const KvSequence s = kv_sequence(a.kv, b);
     for (int t = blockIdx.y; t < s.rows; t += gridDim.y) {
@@ -280,36 +267,44 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
             continue;
         }
         const int lo = a.first, n = count - a.recent - lo, m = a.keep - a.first - a.recent;   // m of n
-        for (int i = tid; i < a.first; i += THREADS) out[i] = i;
-        for (int i = tid; i < a.recent; i += THREADS) out[a.keep - a.recent + i] = count - a.recent + i;
-        if (m == 0) continue;
         const float *scores = a.scores + set * a.max_blocks + lo;
         const int turns = LOOP ? (n + kHeld - 1) / kHeld : 1;
-        uint32_t key[EACH];
+        const auto index = [&](int turn, int k) { return turn * kHeld + (k / 4 * THREADS + tid) * 4 + k % 4; };
+        uint32_t key[EACH];   // 0 past the last
         const auto load = [&](int turn) {
 #pragma unroll
-            for (int k = 0; k < EACH; ++k) {
-                const int i = turn * kHeld + tid * EACH + k;
-                key[k] = i < n ? ordered(scores[i]) : 0;
+            for (int k = 0; k < EACH; k += 4) {
+                const int i = index(turn, k);
+                float v[4] = {0, 0, 0, 0};
+                if (i + 4 <= n) {
+                    const floatx4_any x = *reinterpret_cast<const floatx4_any *>(scores + i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = x[j];
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 3; ++j)
+                        if (i + j < n) v[j] = scores[i + j];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) key[k + j] = i + j < n ? ordered(v[j]) : 0;
             }
         };
         if (!LOOP) load(0);
+        for (int i = tid; i < a.first; i += THREADS) out[i] = i;
+        for (int i = tid; i < a.recent; i += THREADS) out[a.keep - a.recent + i] = count - a.recent + i;
+        if (m == 0) continue;
         // the bits that all keys share
         uint32_t all_and = ~0u, all_or = 0;
         for (int turn = 0; turn < turns; ++turn) {
             if (LOOP) load(turn);
 #pragma unroll
-            for (int k = 0; k < EACH; ++k)
-                if (turn * kHeld + tid * EACH + k < n) {
-                    all_and &= key[k];
-                    all_or |= key[k];
-                }
+            for (int k = 0; k < EACH; ++k) {
+                all_and &= key[k] ? key[k] : ~0u;
+                all_or |= key[k];
+            }
         }
-#pragma unroll
-        for (int i = 1; i < 64; i *= 2) {
-            all_and &= __shfl_xor(all_and, i);
-            all_or |= __shfl_xor(all_or, i);
-        }
+        all_and = fold<64>(all_and, [](uint32_t x, uint32_t y) { return x & y; });
+        all_or = fold<64>(all_or, [](uint32_t x, uint32_t y) { return x | y; });
         __syncthreads();   // the row before is done
         if (lane == 0) {
             folded[0][wave] = all_and;
@@ -355,70 +350,89 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
         }
         // all above `least`, and of those equal to it the first; where m are at
         // least that, all of these
-        int above = 0, equal = 0;
-        const bool whole = reach == m;
+        const uint32_t above = reach == m ? least - 1 : least;
         int need = 0;   // of the equal ones
-        if (!whole) {
+        if (reach != m) {
             int c = 0;
             for (int turn = 0; turn < turns; ++turn) {
                 if (LOOP) load(turn);
 #pragma unroll
-                for (int k = 0; k < EACH; ++k) c += key[k] > least;
+                for (int k = 0; k < EACH; ++k) c += __builtin_popcountll(__ballot(key[k] > above));
             }
-            int32_t total;
             __syncthreads();
-            scan_group(c, sums[0], total);
-            need = m - total;
+            if (lane == 0) folded[0][wave] = c;
             __syncthreads();
+            need = m;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w) need -= static_cast<int>(folded[0][w]);
         }
+        int up_before = 0, equal_before = 0;   // of the turns before
         for (int turn = 0; turn < turns; ++turn) {
             if (LOOP) load(turn);
-            int mine = 0;   // both counts in one word: 16 bits each hold kHeld
+            // for each set: how many the lanes before have, and the waves
+            int up_at[SETS], equal_at[SETS];
 #pragma unroll
-            for (int k = 0; k < EACH; ++k) {
-                const bool up = whole ? key[k] >= least && key[k] != 0 : key[k] > least;
-                mine += up ? 0x10000 : !whole && key[k] == least && key[k] != 0 ? 1 : 0;
-            }
-            int32_t total;
-            const uint32_t before = static_cast<uint32_t>(scan_group(mine, sums[turn & 1], total));
-            int up_at = above + static_cast<int>(before >> 16), equal_at = equal + static_cast<int>(before & 0xFFFF);
+            for (int k = 0; k < SETS; ++k) {
+                int up = 0, equal = 0;
+                up_at[k] = equal_at[k] = 0;
 #pragma unroll
-            for (int k = 0; k < EACH; ++k) {
-                const bool up = whole ? key[k] >= least && key[k] != 0 : key[k] > least;
-                const bool same = !up && !whole && key[k] == least && key[k] != 0;
-                const int at = up_at + (equal_at < need ? equal_at : need);
-                if (up || (same && equal_at < need)) out[a.first + at] = lo + turn * kHeld + tid * EACH + k;
-                up_at += up;
-                equal_at += same;
+                for (int j = 0; j < 4; ++j) {
+                    const uint64_t u = __ballot(key[4 * k + j] > above);
+                    up += __builtin_popcountll(u);
+                    up_at[k] = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(u >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(u), up_at[k]));
+                    if (need > 0) {
+                        const uint64_t e = __ballot(key[4 * k + j] == above);
+                        equal += __builtin_popcountll(e);
+                        equal_at[k] = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(e >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(e), equal_at[k]));
+                    }
+                }
+                if (lane == 0) {
+                    sums[turn & 1][0][k][wave] = up;
+                    sums[turn & 1][1][k][wave] = equal;
+                }
             }
-            above += static_cast<int>(static_cast<uint32_t>(total) >> 16);
-            equal += total & 0xFFFF;
+            __syncthreads();
+#pragma unroll
+            for (int k = 0; k < SETS; ++k) {
+                int at = up_before, same_at = equal_before;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) {
+                    const int u = sums[turn & 1][0][k][w], e = sums[turn & 1][1][k][w];
+                    if (w < wave) {
+                        at += u;
+                        same_at += e;
+                    }
+                    up_before += u;
+                    equal_before += e;
+                }
+                at += up_at[k];
+                same_at += equal_at[k];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool up = key[4 * k + j] > above, same = need > 0 && key[4 * k + j] == above;
+                    if (up || (same && same_at < need)) out[a.first + at + (same_at < need ? same_at : need)] = lo + index(turn, 4 * k + j);
+                    at += up;
+                    same_at += same;
+                }
+            }
         }
     }
 }
 
-// Four tiles of blocks a wave where that leaves two workgroups for every compute
-// unit, one otherwise; the kernels loop where a launch cannot hold all units.
+// The kernels loop where a launch cannot hold all units.
 constexpr int64_t kMostUnits = 8 * 65535;
 
-template <int D, int TILES>
-void launch_score(const SelectArgs &a, hipStream_t s) {
+template <int D>
+hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     ScorePlan p;
-    const int64_t batch = a.kv.batch, each = kScoreWaves * 16 * TILES;
-    int64_t ranges = (a.max_blocks + each - 1) / each, tiles = (static_cast<int64_t>(a.max_rows) + 15) / 16;
+    const int64_t batch = a.kv.batch;
+    int64_t ranges = (a.max_blocks + kScoreBlocks - 1) / kScoreBlocks, tiles = (static_cast<int64_t>(a.max_rows) + 15) / 16;
     if (ranges * batch > kMostUnits) ranges = kMostUnits / batch;
     if (tiles * ranges * batch > kMostUnits) tiles = kMostUnits / (ranges * batch);
     p.tiles = static_cast<int>(tiles);
     p.ranges = static_cast<int>(ranges);
     p.units = static_cast<int>(tiles * ranges * batch);
-    hipLaunchKernelGGL((score_kernel<D, TILES>), dim3(8 * a.kv.kv_heads, (p.units + 7) / 8), dim3(64 * kScoreWaves), 0, s, a, p);
-}
-
-template <int D>
-hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
-    const int64_t sets = a.kv.kv_heads * static_cast<int64_t>(a.kv.batch) * ((static_cast<int64_t>(a.max_rows) + 15) / 16);
-    if (sets * ((a.max_blocks + 255) / 256) >= 512) launch_score<D, 4>(a, s);
-    else launch_score<D, 1>(a, s);
+    hipLaunchKernelGGL((score_kernel<D>), dim3(8 * a.kv.kv_heads, (p.units + 7) / 8), dim3(64 * kScoreWaves), 0, s, a, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 rows(a.kv.kv_heads, a.max_rows < 65535 ? a.max_rows : 65535, a.kv.batch);
