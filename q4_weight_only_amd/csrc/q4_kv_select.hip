@@ -156,61 +156,63 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, S
         for (int begin = range * kScoreBlocks; begin < end; begin += plan.ranges * kScoreBlocks) {   // the same for the workgroup
             const int block = begin + 16 * wave + r;
             const int32_t id = block < end ? kv_block_id(a.kv, b, block) : -1;
+            // D / 2 lanes have a row of q, a pair of dimensions each; the first rows' first heads are read ahead of the bounds
+            constexpr int kLanes = D / 2, kAtOnce = 64 * kScoreWaves / kLanes;
+            const int pair = threadIdx.x % kLanes;
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(
+                a.q + (static_cast<int64_t>(s.row0 + t0 + threadIdx.x / kLanes) * a.q_heads + head * a.group) * D) + pair;
+            const int64_t q_step = static_cast<int64_t>(kAtOnce) * a.q_heads * (D / 2);
+            const auto heads_of = [&](int i, int h0, uint32_t(&v)[4]) {   // (what is past the rows or the group is 0)
+                const bool there = i * kAtOnce + static_cast<int>(threadIdx.x) / kLanes < rows;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) v[h] = there && h0 + h < a.group ? q[i * q_step + (h0 + h) * (D / 2)] : 0;
+            };
+            uint32_t v[4];
+            heads_of(0, 0, v);
             const int64_t plane = static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head;
             const i32x4 *src = reinterpret_cast<const i32x4 *>(a.summary + plane * (2 * D)) + g;
             i32x4 bounds[KK];
 #pragma unroll
             for (int k = 0; k < KK; ++k) bounds[k] = src[4 * k];   // a line is two of them: not nontemporal
             const int e = a.kv.exps[plane * 2];
-            __syncthreads();                       // what was there before has been read
-            {   // D / 2 lanes have a row, a pair of dimensions each
-                constexpr int kLanes = D / 2, kAtOnce = 64 * kScoreWaves / kLanes;
-                const int pair = threadIdx.x % kLanes;
-                for (int i = 0; i < 16 / kAtOnce; ++i) {
-                    const int row = i * kAtOnce + threadIdx.x / kLanes;
-                    double up[2] = {0, 0}, down[2] = {0, 0};
-                    if (row < rows) {
-                        const uint32_t *q = reinterpret_cast<const uint32_t *>(
-                            a.q + (static_cast<int64_t>(s.row0 + t0 + row) * a.q_heads + head * a.group) * D) + pair;
-                        for (int h0 = 0; h0 < a.group; h0 += 4) {
-                            uint32_t v[4];   // (a head past the group is 0)
+            for (int i = 0; i < 16 / kAtOnce; ++i) {
+                const int row = i * kAtOnce + threadIdx.x / kLanes;
+                double up[2] = {0, 0}, down[2] = {0, 0};
+                for (int h0 = 0; h0 < a.group; h0 += 4) {
+                    if (i + h0 > 0) heads_of(i, h0, v);
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) v[h] = h0 + h < a.group ? q[(h0 + h) * (D / 2)] : 0;
+                    for (int h = 0; h < 4; ++h) {
+                        const float x[2] = {__uint_as_float(v[h] << 16), __uint_as_float(v[h] & 0xFFFF0000u)};
 #pragma unroll
-                            for (int h = 0; h < 4; ++h) {
-                                const float x[2] = {__uint_as_float(v[h] << 16), __uint_as_float(v[h] & 0xFFFF0000u)};
-#pragma unroll
-                                for (int k = 0; k < 2; ++k) {
-                                    // what is not a number goes into both
-                                    up[k] += x[k] < 0.0f ? 0.0f : x[k];
-                                    down[k] += x[k] > 0.0f ? 0.0f : x[k];
-                                }
-                            }
+                        for (int k = 0; k < 2; ++k) {
+                            // what is not a number goes into both
+                            up[k] += x[k] < 0.0f ? 0.0f : x[k];
+                            down[k] += x[k] > 0.0f ? 0.0f : x[k];
                         }
                     }
-                    const double most = fmax(fmax(up[0], up[1]), -fmin(down[0], down[1]));
-                    const bool fine = __builtin_isfinite(up[0] + up[1] - down[0] - down[1]);
-                    // most < 2^(e2 - 1022)
-                    const int e2 = static_cast<int>(fold<kLanes>(static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(most)) >> 52 & 0x7FF),
-                                                                 [](uint32_t x, uint32_t y) { return x > y ? x : y; }));
-                    const uint64_t all = __ballot(fine);
-                    const bool every = kLanes == 64 ? all == ~uint64_t(0) : static_cast<uint32_t>(lane < 32 ? all : all >> 32) == ~0u;
-                    uint32_t high[2] = {0, 0}, low[2] = {0, 0};
-                    if (every && e2 > 0) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int v = static_cast<int>(__builtin_rint(__builtin_ldexp(k < 2 ? up[k & 1] : down[k & 1], 13 + 1022 - e2)));
-                            high[k / 2] |= static_cast<uint32_t>((v >> 7) & 0xFF) << (k % 2 * 8);
-                            low[k / 2] |= static_cast<uint32_t>(v & 0x7F) << (k % 2 * 8);
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        *reinterpret_cast<uint16_t *>(&parts[0][row][k * D + 2 * pair]) = static_cast<uint16_t>(high[k]);
-                        *reinterpret_cast<uint16_t *>(&parts[1][row][k * D + 2 * pair]) = static_cast<uint16_t>(low[k]);
-                    }
-                    if ((i + 1) * kAtOnce >= rows) break;   // rows past the last hold anything: their sums are not used
                 }
+                const double most = fmax(fmax(up[0], up[1]), -fmin(down[0], down[1]));
+                const bool fine = __builtin_isfinite(up[0] + up[1] - down[0] - down[1]);
+                // most < 2^(e2 - 1022)
+                const int e2 = static_cast<int>(fold<kLanes>(static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(most)) >> 52 & 0x7FF),
+                                                             [](uint32_t x, uint32_t y) { return x > y ? x : y; }));
+                const uint64_t all = __ballot(fine);
+                const bool every = kLanes == 64 ? all == ~uint64_t(0) : static_cast<uint32_t>(lane < 32 ? all : all >> 32) == ~0u;
+                uint32_t high[2] = {0, 0}, low[2] = {0, 0};
+                if (every && e2 > 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int x = static_cast<int>(__builtin_rint(__builtin_ldexp(k < 2 ? up[k & 1] : down[k & 1], 13 + 1022 - e2)));
+                        high[k / 2] |= static_cast<uint32_t>((x >> 7) & 0xFF) << (k % 2 * 8);
+                        low[k / 2] |= static_cast<uint32_t>(x & 0x7F) << (k % 2 * 8);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    *reinterpret_cast<uint16_t *>(&parts[0][row][k * D + 2 * pair]) = static_cast<uint16_t>(high[k]);
+                    *reinterpret_cast<uint16_t *>(&parts[1][row][k * D + 2 * pair]) = static_cast<uint16_t>(low[k]);
+                }
+                if ((i + 1) * kAtOnce >= rows) break;   // rows past the last hold anything: their sums are not used
             }
             __syncthreads();
             i32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
@@ -219,15 +221,15 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, S
 #pragma unroll
                 for (int p = 0; p < 2; ++p)
                     sum[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4 *>(&parts[p][r][64 * k + 16 * g]), bounds[k], sum[p], 0, 0, 0);
-            if (block >= end) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int row = 4 * g + j;
-                if (row >= rows) break;
+                if (block >= end || row >= rows) break;
                 const float total = static_cast<float>(sum[0][j] * 128 + sum[1][j]);   // below 2^28, rounded once
                 a.scores[(static_cast<int64_t>(s.row0 + t0 + row) * a.kv.kv_heads + head) * a.max_blocks + block] =
                     id < 0 ? -__builtin_inff() : __builtin_ldexpf(total, e);
             }
+            __syncthreads();   // the rows' sums have been read
         }
     }
 }
@@ -239,14 +241,21 @@ __device__ __forceinline__ uint32_t ordered(float s) {
     return w >> 31 ? ~w : w | 0x80000000u;
 }
 
-// A workgroup has one row and kv head.  The m-th largest of the scores between the
-// first and the last blocks is found two bits at a time, each time counting how many
-// scores are no less, until that is m; then those are written in their order.  A
-// thread has EACH / 4 times four scores next to each other, THREADS * 4 apart.
-// LOOP: more scores than the workgroup's registers hold, read each time.
+__device__ __forceinline__ float unordered(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key); }
+
+constexpr uint32_t kLowestKey = 0x007FFFFF;   // of -inf
+constexpr int kBins = 1024, kBinListed = 256;   // kBinListed: scores of a bin that may be ranked
+
+// A workgroup has one row and kv head.  The scores between the first and the last
+// blocks are counted in bins of equal width; in the bin that the m-th largest falls
+// into, the scores are ranked one by one (where they are too many, because they are equal
+// or nearly so, the m-th is found two bits at a time, each time counting how many
+// are no less).  Then the m largest are written in their order.  A thread has EACH / 4
+// times four scores next to each other, THREADS * 4 apart.  LOOP: more scores than
+// the workgroup's registers hold, read each time.
 //
-// What bounds it is one step after the other: lengths, scores, some ten counts with a
-// barrier each.
+// What bounds it is one step after the other: lengths, scores, six barriers.  (Two bits
+// at a time alone, some ten counts with a barrier each: 9.8 us for 4096 blocks.)
 template <int THREADS, int EACH, bool LOOP>
 __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
     constexpr int WAVES = THREADS / 64, kHeld = THREADS * EACH, SETS = EACH / 4;
@@ -254,6 +263,12 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
     __shared__ int32_t counter[3][3];   // of a step, for each of its values
     __shared__ uint32_t folded[2][WAVES];
     __shared__ int32_t sums[2][2][SETS][WAVES];
+    __shared__ __align__(16) int32_t bins[kBins];
+    __shared__ uint32_t list_key[kBinListed];
+    __shared__ int32_t list_index[kBinListed];
+    __shared__ int32_t found[4];        // the bin, what is still wanted of it, how many it has, and of these listed
+    __shared__ uint32_t found_key;      // all above it are chosen,
+    __shared__ int32_t found_need;      // and so many of those equal to it
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int b = blockIdx.z, head = blockIdx.x;
     const KvSequence s = kv_sequence(a.kv, b);
@@ -293,78 +308,156 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
         for (int i = tid; i < a.first; i += THREADS) out[i] = i;
         for (int i = tid; i < a.recent; i += THREADS) out[a.keep - a.recent + i] = count - a.recent + i;
         if (m == 0) continue;
-        // the bits that all keys share
-        uint32_t all_and = ~0u, all_or = 0;
+        // the smallest and the largest score, but for -inf
+        uint32_t low = ~0u, high = 0;
         for (int turn = 0; turn < turns; ++turn) {
             if (LOOP) load(turn);
 #pragma unroll
             for (int k = 0; k < EACH; ++k) {
-                all_and &= key[k] ? key[k] : ~0u;
-                all_or |= key[k];
+                const uint32_t least = key[k] > kLowestKey ? key[k] : ~0u;
+                low = least < low ? least : low;
+                high = key[k] > high ? key[k] : high;
             }
         }
-        all_and = fold<64>(all_and, [](uint32_t x, uint32_t y) { return x & y; });
-        all_or = fold<64>(all_or, [](uint32_t x, uint32_t y) { return x | y; });
+        low = fold<64>(low, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+        high = fold<64>(high, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
         __syncthreads();   // the row before is done
         if (lane == 0) {
-            folded[0][wave] = all_and;
-            folded[1][wave] = all_or;
+            folded[0][wave] = low;
+            folded[1][wave] = high;
         }
+        for (int i = tid; i < kBins / 4; i += THREADS) reinterpret_cast<i32x4 *>(bins)[i] = (i32x4){0, 0, 0, 0};
         if (tid < 9) counter[tid / 3][tid % 3] = 0;
+        if (tid == 0) found[0] = -1, found[3] = 0;
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            all_and &= folded[0][w];
-            all_or |= folded[1][w];
+            low = folded[0][w] < low ? folded[0][w] : low;
+            high = folded[1][w] > high ? folded[1][w] : high;
         }
-        const uint32_t differ = all_and ^ all_or;
-        int bit = differ ? 31 - __builtin_clz(differ) : -1;
-        uint32_t least = bit < 31 ? all_and >> (bit + 1) << (bit + 1) : 0;   // (bit 31: no common bits)
-        int reach = n;   // how many keys are at least `least`
-        // two bits a step: of the three values that they may add, the largest that m keys reach
-        for (int step = 0; bit >= 0 && reach != m; bit -= 2, ++step) {
-            const uint32_t unit = bit > 0 ? 1u << (bit - 1) : 1;
-            const int most = bit > 0 ? 3 : 1;   // (the last bit may be one)
-            int c[3] = {0, 0, 0};
+        // bins 1 .. kBins - 1 from the smallest to the largest, -inf in 0; rounding does not change the order
+        const float from = unordered(low), scale = (kBins - 2) / (unordered(high) - from);
+        const bool spread = low < high && scale > 0.0f && scale < __builtin_inff();   // the same for the workgroup
+        const auto bin_of = [&](uint32_t x) {
+            const int bin = static_cast<int>(fmaxf((unordered(x) - from) * scale, 0.0f)) + 1;
+            return x <= kLowestKey ? 0 : bin < kBins ? bin : kBins - 1;
+        };
+        uint32_t above = 0;   // all scores above it are chosen,
+        int need = 0;         // and so many of those equal to it, the first ones
+        if (spread) {
             for (int turn = 0; turn < turns; ++turn) {
                 if (LOOP) load(turn);
 #pragma unroll
                 for (int k = 0; k < EACH; ++k)
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) c[i] += __builtin_popcountll(__ballot(key[k] >= least + (i + 1) * unit));
+                    if (key[k]) atomicAdd(&bins[bin_of(key[k])], 1);
             }
-            // three sets of counters in turn: one barrier a step
-            if (lane < 3) atomicAdd(&counter[step % 3][lane], lane == 0 ? c[0] : lane == 1 ? c[1] : c[2]);
-            if (tid < 3) counter[(step + 1) % 3][tid] = 0;
             __syncthreads();
-            int add = 0;
+            if (wave == 0) {   // from the last bin down, 16 a lane
+                constexpr int kOf = kBins / 64;
+                const int first = kBins - kOf * (lane + 1);
+                int mine[kOf], all = 0;
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const int all = counter[step % 3][i];
-                if (i < most && all >= m) {
-                    add = i + 1;
-                    reach = all;
+                for (int i = 0; i < kOf; i += 4) {
+                    const i32x4 x = *reinterpret_cast<const i32x4 *>(&bins[first + i]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        mine[i + j] = x[j];
+                        all += x[j];
+                    }
+                }
+                int32_t total;
+                int before = scan_wave(all, total);
+#pragma unroll
+                for (int i = kOf - 1; i >= 0; --i) {
+                    if (before < m && before + mine[i] >= m) {
+                        found[0] = first + i;
+                        found[1] = m - before;
+                        found[2] = mine[i];
+                    }
+                    before += mine[i];
                 }
             }
-            least += add * unit;
+            __syncthreads();
         }
-        // all above `least`, and of those equal to it the first; where m are at
-        // least that, all of these
-        const uint32_t above = reach == m ? least - 1 : least;
-        int need = 0;   // of the equal ones
-        if (reach != m) {
-            int c = 0;
+        const int border = found[0], wanted = found[1], size = found[2];
+        if (spread && size <= kBinListed) {   // the same for the workgroup
             for (int turn = 0; turn < turns; ++turn) {
                 if (LOOP) load(turn);
 #pragma unroll
-                for (int k = 0; k < EACH; ++k) c += __builtin_popcountll(__ballot(key[k] > above));
+                for (int k = 0; k < EACH; ++k)
+                    if (key[k] && bin_of(key[k]) == border) {
+                        const int i = atomicAdd(&found[3], 1);
+                        list_key[i] = key[k];
+                        list_index[i] = index(turn, k);
+                    }
             }
             __syncthreads();
-            if (lane == 0) folded[0][wave] = c;
+            // a wave has one of them at a time, its lanes those that may be in front
+            for (int i = wave; i < size; i += WAVES) {
+                const uint32_t mine = list_key[i];
+                const int at = list_index[i];
+                int higher = 0, front = 0, equal = 0;
+                for (int j = lane; j - lane < size; j += 64) {
+                    const uint32_t other = j < size ? list_key[j] : 0;
+                    const bool same = other == mine;
+                    higher += __builtin_popcountll(__ballot(other > mine));
+                    equal += __builtin_popcountll(__ballot(same));
+                    front += __builtin_popcountll(__ballot(same && list_index[j < size ? j : 0] < at));
+                }
+                if (lane == 0 && higher + front == wanted - 1) {   // the last one that is chosen
+                    const bool whole = wanted - higher == equal;   // all that are equal to it are
+                    found_key = whole ? mine - 1 : mine;
+                    found_need = whole ? 0 : wanted - higher;
+                }
+            }
             __syncthreads();
-            need = m;
+            above = found_key;
+            need = found_need;
+        } else {
+            uint32_t least = 0;
+            int reach = n;   // how many keys are at least `least`
+            // two bits a step: of the three values that they may add, the largest that m keys reach
+            for (int bit = 31, step = 0; bit >= 0 && reach != m; bit -= 2, ++step) {
+                const uint32_t unit = 1u << (bit - 1);
+                int c[3] = {0, 0, 0};
+                for (int turn = 0; turn < turns; ++turn) {
+                    if (LOOP) load(turn);
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) need -= static_cast<int>(folded[0][w]);
+                    for (int k = 0; k < EACH; ++k)
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) c[i] += __builtin_popcountll(__ballot(key[k] >= least + (i + 1) * unit));
+                }
+                // three sets of counters in turn: one barrier a step
+                if (lane < 3) atomicAdd(&counter[step % 3][lane], lane == 0 ? c[0] : lane == 1 ? c[1] : c[2]);
+                if (tid < 3) counter[(step + 1) % 3][tid] = 0;
+                __syncthreads();
+                int add = 0;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const int all = counter[step % 3][i];
+                    if (all >= m) {
+                        add = i + 1;
+                        reach = all;
+                    }
+                }
+                least += add * unit;
+            }
+            // where m are at least that, all of these; otherwise the first of those equal to it
+            above = reach == m ? least - 1 : least;
+            if (reach != m) {
+                int c = 0;
+                for (int turn = 0; turn < turns; ++turn) {
+                    if (LOOP) load(turn);
+#pragma unroll
+                    for (int k = 0; k < EACH; ++k) c += __builtin_popcountll(__ballot(key[k] > above));
+                }
+                __syncthreads();
+                if (lane == 0) folded[0][wave] = c;
+                __syncthreads();
+                need = m;
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) need -= static_cast<int>(folded[0][w]);
+            }
         }
         int up_before = 0, equal_before = 0;   // of the turns before
         for (int turn = 0; turn < turns; ++turn) {
