@@ -18,21 +18,157 @@ __device__ __forceinline__ int32_t held_to(int32_t v, int32_t lo, int32_t hi) { 
 
 // ------------------------------------------------------------------- fork
 // The workspace: for each block how many new sequences go on in it and the last of
-// these; for each new sequence how many free blocks it and those before it
-// want; the free blocks in their order, as far as they are wanted.
+// these; the free blocks in their order, as far as they are wanted; for each new sequence
+// how many free blocks it and those before it want.
 struct ForkSpace {
     int32_t *writers, *keeper;   // [num_blocks]
-    int32_t *wanted;             // [n_out]
     int32_t *free;               // [num_blocks]
+    int32_t *wanted;             // [n_out]
 };
-ForkSpace fork_space(int32_t *w, int64_t n_out, int64_t num_blocks) {
+ForkSpace fork_space(int32_t *w, int64_t num_blocks) {
     ForkSpace s;
     s.writers = w;
     s.keeper = w + num_blocks;
     s.free = w + 2 * num_blocks;
     s.wanted = w + 3 * num_blocks;
-    (void)n_out;
     return s;
+}
+
+// A new sequence before its blocks are handed out.
+struct NewSequence {
+    int32_t parent, was, grow, have, need;   // have: blocks so far, need: with the tokens to come
+    bool goes_on;                            // in a partly filled block, its last
+};
+__device__ __forceinline__ NewSequence new_sequence(const ForkArgs &a, int i) {
+    NewSequence s;
+    const int32_t g = a.grow ? a.grow[i] : a.grow_each;
+    s.parent = a.parents[i];
+    if (s.parent < 0 || s.parent >= a.rows) s.parent = -1;
+    s.was = s.parent < 0 ? 0 : held_to(a.lengths[s.parent], 0, a.width * kKvBlock);
+    s.grow = s.parent < 0 ? 0 : held_to(g, 0, 1 << 25);
+    s.have = (s.was + kKvBlock - 1) / kKvBlock;
+    s.need = (s.was + s.grow + kKvBlock - 1) / kKvBlock;
+    s.goes_on = s.was % kKvBlock != 0 && s.grow > 0;
+    return s;
+}
+// Its last block, or -1 where that is none of the cache's.
+__device__ __forceinline__ int32_t last_block(const ForkArgs &a, const NewSequence &s) {
+    const int32_t id = s.have ? a.table[static_cast<int64_t>(s.parent) * a.width + s.have - 1] : -1;
+    return id < a.num_blocks ? id : -1;
+}
+
+// What a new sequence wants: a copy of its last block, if others hold it that do not go
+// on in it, or it is not the last of those that do; and new blocks (none for which the
+// table has no room).
+struct Wants {
+    NewSequence s;
+    int32_t last;
+    bool copy;
+    __device__ __forceinline__ int fresh(const ForkArgs &a) const { return (s.need < a.width ? s.need : a.width) - s.have; }
+};
+
+// One workgroup hands out the blocks: how many each new sequence wants, the free
+// ones, who gets which.  refs counts the holders before that; wants_of: what a
+// sequence wants (asked of thread i % kHandThreads alone), place_of: its blocks so far and
+// whether it gets a copy, writers_of: how many go on in a block, and the last of them.
+// With up to kHandThreads sequences, of few new blocks each, nothing is read twice.
+constexpr int kHandThreads = 1024, kFreeHeld = 2048;
+
+struct HandSpace {
+    int32_t sums[2][kHandThreads / 64];
+    int32_t free[kFreeHeld];     // the first of the free blocks
+    int32_t most;                // new blocks of a sequence
+};
+
+template <typename WantsOf, typename PlaceOf, typename WritersOf>
+__device__ __forceinline__ void hand_out(const ForkArgs &a, const ForkSpace &w, HandSpace &lds, int32_t *refs, WantsOf wants_of, PlaceOf place_of,
+                                         WritersOf writers_of) {
+    const int tid = threadIdx.x;
+    Wants mine;                  // of sequence tid
+    int32_t mine_at = 0;         // the free blocks before its own
+    int32_t want_all = 0;
+    if (tid == 0) lds.most = 0;
+    __syncthreads();
+    for (int i0 = 0, turn = 0; i0 < a.n_out; i0 += kHandThreads, turn ^= 1) {
+        const int i = i0 + tid;
+        int32_t want = 0;
+        if (i < a.n_out) {
+            const Wants x = wants_of(i);
+            want = x.copy + x.fresh(a);
+            if (x.fresh(a) > 4) atomicMax(&lds.most, x.fresh(a));
+            if (i0 == 0) mine = x;
+        }
+        int32_t total;
+        const int32_t before = want_all + scan_group(want, lds.sums[turn], total);
+        if (i < a.n_out) w.wanted[i] = before + want;
+        if (i0 == 0) mine_at = before;
+        want_all += total;
+    }
+    __syncthreads();
+    // the first want_all free blocks, four a thread at a time
+    int32_t found = 0;
+    for (int b0 = 0, turn = 0; b0 < a.num_blocks && found < want_all; b0 += kHandThreads * 4, turn ^= 1) {
+        const int b = b0 + tid * 4;
+        int32_t count[4], n = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) count[k] = b + k < a.num_blocks ? refs[b + k] : 1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) n += count[k] == 0;
+        int32_t total;
+        int32_t at = found + scan_group(n, lds.sums[turn], total);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (count[k] == 0 && at < want_all) {
+                if (at < kFreeHeld) lds.free[at] = b + k;
+                else w.free[at] = b + k;
+                ++at;
+            }
+        found += total;
+    }
+    if (found > want_all) found = want_all;
+    __syncthreads();
+    const auto free_block = [&](int k) { return k >= found ? -1 : k < kFreeHeld ? lds.free[k] : w.free[k]; };
+    const bool shared = lds.most > 0;   // some want many new blocks: they are handed out block by block
+    for (int i = tid; i < a.n_out; i += kHandThreads) {
+        const Wants x = i == tid ? mine : wants_of(i);
+        const int32_t at = i == tid ? mine_at : w.wanted[i - 1], fresh = x.fresh(a), upto = at + x.copy + fresh;
+        int32_t *row = a.out_table + static_cast<int64_t>(i) * a.width;
+        int32_t dst = -1;
+        if (x.copy) {
+            dst = free_block(at);
+            row[x.s.have - 1] = dst;
+        }
+        if (!shared)
+            for (int k = 0; k < fresh; ++k) row[x.s.have + k] = free_block(at + x.copy + k);
+        a.src[i] = dst >= 0 ? x.last : -1;
+        a.dst[i] = dst;
+        a.short_of[i] = (upto > found ? upto - (at > found ? at : found) : 0) + (x.s.need > a.width ? x.s.need - a.width : 0);
+    }
+    if (shared) {
+        for (int k = tid; k < want_all; k += kHandThreads) {
+            int lo = 0, hi = a.n_out - 1;   // the first with wanted > k
+            while (lo < hi) {
+                const int mid = (lo + hi) / 2;
+                if (w.wanted[mid] > k) hi = mid;
+                else lo = mid + 1;
+            }
+            int32_t have;
+            bool copy;
+            place_of(lo, have, copy);
+            const int32_t place = k - (lo ? w.wanted[lo - 1] : 0) - copy;
+            if (place >= 0) a.out_table[static_cast<int64_t>(lo) * a.width + have + place] = free_block(k);
+        }
+    }
+    __syncthreads();   // refs has been read
+    // those that go on in a block, but for one that keeps it, leave it; the last of them writes that
+    for (int i = tid; i < a.n_out; i += kHandThreads) {
+        const Wants x = i == tid ? mine : wants_of(i);
+        int32_t writers, keeper;
+        if (!x.s.goes_on || x.last < 0) continue;
+        writers_of(x.last, i, writers, keeper);
+        if (keeper == i) refs[x.last] -= writers - !x.copy;
+    }
+    for (int k = tid; k < found; k += kHandThreads) refs[free_block(k)] = 1;
 }
 
 __global__ __launch_bounds__(256) void fork_clear_kernel(ForkArgs a, ForkSpace w) {
@@ -44,160 +180,147 @@ __global__ __launch_bounds__(256) void fork_clear_kernel(ForkArgs a, ForkSpace w
     }
 }
 
-// A new sequence before its blocks are handed out.
-struct NewSequence {
-    int32_t parent, was, grow, have, need;   // need: blocks with the tokens to come
-    bool goes_on;                            // in a partly filled block, its last
-};
-__device__ __forceinline__ NewSequence new_sequence(const ForkArgs &a, int i) {
-    NewSequence s;
-    s.parent = a.parents[i];
-    if (s.parent < 0 || s.parent >= a.rows) s.parent = -1;
-    s.was = s.parent < 0 ? 0 : held_to(a.lengths[s.parent], 0, a.width * kKvBlock);
-    s.grow = s.parent < 0 ? 0 : held_to(a.grow ? a.grow[i] : a.grow_each, 0, 1 << 25);
-    s.have = (s.was + kKvBlock - 1) / kKvBlock;
-    s.need = (s.was + s.grow + kKvBlock - 1) / kKvBlock;
-    s.goes_on = s.was % kKvBlock != 0 && s.grow > 0;
-    return s;
-}
-
-// A workgroup has 1024 entries of one new table row: they are copied and counted.
-constexpr int kForkEntries = 1024;
+// A thread has a column of kForkRows new table rows: the entries are copied and
+// counted, those of neighbours that name one block at once.  (262144 entries of 64
+// rows, four and more of which share most blocks: 13.4 us with an atomic for each.)
+constexpr int kForkRows = 8;
 
 __global__ __launch_bounds__(256) void fork_gather_kernel(ForkArgs a, ForkSpace w) {
-    const int i = blockIdx.y;
-    const NewSequence s = new_sequence(a, i);
-    const int32_t *from = a.table + static_cast<int64_t>(s.parent < 0 ? 0 : s.parent) * a.width;
-    int32_t *to = a.out_table + static_cast<int64_t>(i) * a.width;
+    const int first = blockIdx.y * kForkRows, t = blockIdx.x * 256 + threadIdx.x;
+    NewSequence s[kForkRows];
+    int32_t id[kForkRows];
 #pragma unroll
-    for (int k = 0; k < kForkEntries / 256; ++k) {
-        const int t = blockIdx.x * kForkEntries + k * 256 + threadIdx.x;
-        if (t >= a.width) break;
-        int32_t id = -1;
-        if (t < s.have) {
-            id = from[t];
-            if (id >= 0 && id < a.num_blocks) {
-                atomicAdd(&a.refs[id], 1);
-                if (t == s.have - 1 && s.goes_on) {
-                    atomicAdd(&w.writers[id], 1);
-                    atomicMax(&w.keeper[id], i);
-                }
-            }
-        }
-        to[t] = id;
+    for (int k = 0; k < kForkRows; ++k) {
+        s[k].have = 0;
+        s[k].goes_on = false;
+        if (first + k < a.n_out) s[k] = new_sequence(a, first + k);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) a.out_lengths[i] = s.was + s.grow;
+#pragma unroll
+    for (int k = 0; k < kForkRows; ++k)
+        id[k] = t < s[k].have ? a.table[static_cast<int64_t>(s[k].parent) * a.width + t] : -1;
+    int32_t run = 0;
+#pragma unroll
+    for (int k = 0; k < kForkRows; ++k) {
+        const bool known = id[k] >= 0 && id[k] < a.num_blocks;
+        if (first + k < a.n_out && t < a.width) a.out_table[static_cast<int64_t>(first + k) * a.width + t] = id[k];
+        run += known;
+        if (known && (k + 1 == kForkRows || id[k + 1 < kForkRows ? k + 1 : k] != id[k])) {
+            atomicAdd(&a.refs[id[k]], run);
+            run = 0;
+        }
+        if (known && t == s[k].have - 1 && s[k].goes_on) {
+            atomicAdd(&w.writers[id[k]], 1);
+            atomicMax(&w.keeper[id[k]], first + k);
+        }
+        if (t == 0 && first + k < a.n_out) a.out_lengths[first + k] = s[k].was + s[k].grow;
+    }
 }
-
-// Whether new sequence i gets a copy of its last block: others hold it that do not
-// go on in it, or it is not the last of those that do.
-__device__ __forceinline__ bool gets_copy(const ForkArgs &a, const ForkSpace &w, const NewSequence &s, int i, int32_t &last) {
-    last = -1;
-    if (!s.goes_on) return false;
-    last = a.table[static_cast<int64_t>(s.parent) * a.width + s.have - 1];
-    if (last < 0 || last >= a.num_blocks) return false;
-    return w.keeper[last] != i || a.refs[last] > w.writers[last];
-}
-
-// One workgroup: how many blocks each new sequence wants, the free ones, and
-// their handing out.
-constexpr int kHandThreads = 1024;
 
 __global__ __launch_bounds__(kHandThreads) void fork_hand_kernel(ForkArgs a, ForkSpace w) {
-    __shared__ int32_t sums[2][kHandThreads / 64];
+    __shared__ HandSpace lds;
+    const auto wants_of = [&](int i) {
+        Wants x;
+        x.s = new_sequence(a, i);
+        x.last = last_block(a, x.s);
+        x.copy = x.s.goes_on && x.last >= 0 && (w.keeper[x.last] != i || a.refs[x.last] > w.writers[x.last]);
+        return x;
+    };
+    hand_out(a, w, lds, a.refs, wants_of,
+             [&](int i, int32_t &have, bool &copy) {
+                 const Wants x = wants_of(i);
+                 have = x.s.have;
+                 copy = x.copy;
+             },
+             [&](int32_t block, int, int32_t &writers, int32_t &keeper) {
+                 writers = w.writers[block];
+                 keeper = w.keeper[block];
+             });
+}
+
+// All of it in one workgroup, where the tables and the pool are small: the counts are
+// in LDS, and who goes on in the same block is found by looking at all.
+constexpr int kOneRows = 256, kOneBlocks = 8192, kOneAhead = 8;
+constexpr int64_t kOneEntries = 16384;
+
+__global__ __launch_bounds__(kHandThreads) void fork_one_kernel(ForkArgs a, ForkSpace w) {
+    __shared__ HandSpace lds;
+    __shared__ int32_t refs[kOneBlocks];
+    __shared__ __align__(16) int32_t last[kOneRows];    // of those that go on: their last block, or -1
+    __shared__ int32_t parent[kOneRows], have[kOneRows], copied[kOneRows];
     const int tid = threadIdx.x;
-    int32_t want_all = 0;
-    for (int i0 = 0, turn = 0; i0 < a.n_out; i0 += kHandThreads, turn ^= 1) {
-        const int i = i0 + tid;
-        int32_t want = 0;
-        if (i < a.n_out) {
-            const NewSequence s = new_sequence(a, i);
-            int32_t last;
-            const bool copy = gets_copy(a, w, s, i, last);
-            // blocks for which the table has no room take none
-            want = copy + (s.need < a.width ? s.need : a.width) - s.have;
-        }
-        int32_t total;
-        const int32_t before = scan_group(want, sums[turn], total);
-        if (i < a.n_out) w.wanted[i] = want_all + before + want;
-        want_all += total;
+    Wants mine;
+    mine.copy = false;
+    if (tid < kOneRows) last[tid] = -1;
+    if (tid < a.n_out) {
+        mine.s = new_sequence(a, tid);
+        parent[tid] = mine.s.parent;
+        have[tid] = mine.s.have;
+        mine.last = last_block(a, mine.s);
+        last[tid] = mine.s.goes_on ? mine.last : -1;
+        a.out_lengths[tid] = mine.s.was + mine.s.grow;
     }
-    // the first want_all free blocks
-    constexpr int kEach = 4;
-    int32_t found = 0;
-    __syncthreads();
-    for (int b0 = 0, turn = 0; b0 < a.num_blocks && found < want_all; b0 += kHandThreads * kEach, turn ^= 1) {
-        const int b = b0 + tid * kEach;
-        bool free[kEach];
-        int32_t n = 0;
-#pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            free[k] = b + k < a.num_blocks && a.refs[b + k] == 0;
-            n += free[k];
-        }
-        int32_t total;
-        int32_t at = found + scan_group(n, sums[turn], total);
-#pragma unroll
-        for (int k = 0; k < kEach; ++k)
-            if (free[k] && at < want_all) w.free[at++] = b + k;
-        found += total;
+    for (int i = tid; i < a.num_blocks; i += kHandThreads) {
+        const int32_t h = a.held ? a.held[i] : 0;
+        refs[i] = h > 0 ? h : 0;
     }
     __syncthreads();
-    if (found > want_all) found = want_all;
-    for (int i = tid; i < a.n_out; i += kHandThreads) {
-        const NewSequence s = new_sequence(a, i);
-        int32_t last;
-        const bool copy = gets_copy(a, w, s, i, last);
-        const int32_t at = i ? w.wanted[i - 1] : 0, upto = w.wanted[i];
-        int32_t dst = -1;
-        if (copy) {
-            if (at < found) dst = w.free[at];
-            a.out_table[static_cast<int64_t>(i) * a.width + s.have - 1] = dst;
+    const int entries = a.n_out * a.width;
+    const float per = 1.0f / a.width;   // fewer than 2^15 entries: (e + 1/2) / width is off by far less than 1/2 of one
+    for (int e0 = tid; e0 < entries; e0 += kHandThreads * kOneAhead) {
+        int32_t id[kOneAhead];
+#pragma unroll
+        for (int k = 0; k < kOneAhead; ++k) {
+            const int e = e0 + kHandThreads * k, i = static_cast<int>((e + 0.5f) * per), t = e - i * a.width;
+            id[k] = e < entries && t < have[e < entries ? i : 0] ? a.table[static_cast<int64_t>(parent[i]) * a.width + t] : -1;
         }
-        a.src[i] = dst >= 0 ? last : -1;
-        a.dst[i] = dst;
-        a.short_of[i] = (upto > found ? upto - (at > found ? at : found) : 0) + (s.need > a.width ? s.need - a.width : 0);
-    }
-    // new blocks, one a thread: the sequence by bisection
-    for (int k = tid; k < want_all; k += kHandThreads) {
-        int lo = 0, hi = a.n_out - 1;   // the first with wanted > k
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (w.wanted[mid] > k) hi = mid;
-            else lo = mid + 1;
+#pragma unroll
+        for (int k = 0; k < kOneAhead; ++k) {
+            if (id[k] >= 0 && id[k] < a.num_blocks) atomicAdd(&refs[id[k]], 1);
+            if (e0 + kHandThreads * k < entries) a.out_table[e0 + kHandThreads * k] = id[k];
         }
-        const NewSequence s = new_sequence(a, lo);
-        int32_t last;
-        const bool copy = gets_copy(a, w, s, lo, last);
-        const int32_t place = k - (lo ? w.wanted[lo - 1] : 0) - copy;
-        if (place >= 0) a.out_table[static_cast<int64_t>(lo) * a.width + s.have + place] = k < found ? w.free[k] : -1;
     }
-    __syncthreads();   // refs has been read
-    for (int i = tid; i < a.n_out; i += kHandThreads) {
-        const NewSequence s = new_sequence(a, i);
-        int32_t last;
-        if (!s.goes_on) continue;
-        last = a.table[static_cast<int64_t>(s.parent) * a.width + s.have - 1];
-        if (last < 0 || last >= a.num_blocks || w.keeper[last] != i) continue;
-        // the last of those that go on in a block takes all copies from its count
-        const int32_t kept = a.refs[last] > w.writers[last] ? 0 : 1;
-        a.refs[last] -= w.writers[last] - kept;
+    __syncthreads();
+    int32_t writers = 0, keeper = -1;   // of the block that the sequence goes on in
+    if (tid < a.n_out) {
+        const int32_t block = last[tid];
+        if (block >= 0) {
+            for (int j = 0; j < a.n_out; j += 4) {
+                const i32x4 x = *reinterpret_cast<const i32x4 *>(&last[j]);   // (-1 past the last)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    writers += x[k] == block;
+                    keeper = x[k] == block ? j + k : keeper;
+                }
+            }
+            mine.copy = keeper != tid || refs[block] > writers;
+        }
+        copied[tid] = mine.copy;
     }
-    for (int k = tid; k < found; k += kHandThreads) a.refs[w.free[k]] = 1;
+    hand_out(a, w, lds, refs, [&](int) { return mine; },
+             [&](int i, int32_t &so_far, bool &copy) {
+                 so_far = have[i];
+                 copy = copied[i];
+             },
+             [&](int32_t, int, int32_t &n, int32_t &k) {
+                 n = writers;
+                 k = keeper;
+             });
+    __syncthreads();
+    for (int i = tid; i < a.num_blocks; i += kHandThreads) a.refs[i] = refs[i];
 }
 
 // ---------------------------------------------------------------- compact
-// The workspace: a byte for each block that a table names; for each tile of
-// blocks how many are live and how many of these may move; where blocks went.
-constexpr int kTileBlocksHeld = 4096, kTileThreads = 256, kTileEach = kTileBlocksHeld / kTileThreads;
+// The workspace: whether a table names a block; for a block that moves its place among
+// those; for each tile of blocks how many are live and how many of these may move.
+constexpr int kPageTile = 1024, kTileThreads = 256;
 
 struct CompactSpace {
     int32_t *named;     // [num_blocks]: not 0 where a sequence holds the block
-    int32_t *moved;     // [num_blocks]: where it goes
+    int32_t *moved;     // [num_blocks]
     int32_t *live, *movable;   // [tiles]
     int32_t tiles;
 };
-int64_t tiles_of(int64_t num_blocks) { return (num_blocks + kTileBlocksHeld - 1) / kTileBlocksHeld; }
+int64_t tiles_of(int64_t num_blocks) { return (num_blocks + kPageTile - 1) / kPageTile; }
 CompactSpace compact_space(int32_t *w, int64_t num_blocks) {
     CompactSpace s;
     s.tiles = static_cast<int32_t>(tiles_of(num_blocks));
@@ -209,14 +332,7 @@ CompactSpace compact_space(int32_t *w, int64_t num_blocks) {
 }
 
 __global__ __launch_bounds__(256) void compact_clear_kernel(CompactArgs a, CompactSpace w) {
-    const int64_t half = a.num_blocks / 2 > 1 ? a.num_blocks / 2 : 1;
-    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < a.num_blocks; i += gridDim.x * int64_t(256)) {
-        w.named[i] = 0;
-        if (i < half) {
-            a.src[i] = -1;
-            a.dst[i] = -1;
-        }
-    }
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < a.num_blocks; i += gridDim.x * int64_t(256)) w.named[i] = 0;
 }
 
 __global__ __launch_bounds__(256) void compact_mark_kernel(CompactArgs a, CompactSpace w) {
@@ -229,99 +345,88 @@ __global__ __launch_bounds__(256) void compact_mark_kernel(CompactArgs a, Compac
     }
 }
 
-__device__ __forceinline__ void block_state(const CompactArgs &a, const CompactSpace &w, int b, bool &live, bool &movable) {
-    live = movable = false;
-    if (b >= a.num_blocks) return;
-    const bool pinned = a.held && a.held[b] > 0;
-    live = pinned || w.named[b] != 0;
-    movable = live && !pinned;
+// Bit k: block 4 i + k of a tile is live, or may move.
+struct BlockState {
+    uint32_t live, movable;
+};
+__device__ __forceinline__ BlockState block_state(const CompactArgs &a, const CompactSpace &w, int tile) {
+    const int first = tile * kPageTile + 4 * threadIdx.x;
+    int32_t named[4], held[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        named[k] = first + k < a.num_blocks ? w.named[first + k] : 0;
+        held[k] = a.held && first + k < a.num_blocks ? a.held[first + k] : 0;
+    }
+    BlockState s = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        s.live |= static_cast<uint32_t>(named[k] != 0 || held[k] > 0) << k;
+        s.movable |= static_cast<uint32_t>(named[k] != 0 && held[k] <= 0) << k;
+    }
+    return s;
 }
 
 __global__ __launch_bounds__(kTileThreads) void compact_count_kernel(CompactArgs a, CompactSpace w) {
-    __shared__ int32_t sums[2][kTileThreads / 64];
-    int32_t live = 0, movable = 0;
-    for (int k = 0; k < kTileEach; ++k) {
-        bool l, m;
-        block_state(a, w, blockIdx.x * kTileBlocksHeld + k * kTileThreads + threadIdx.x, l, m);
-        live += l;
-        movable += m;
-    }
-    int32_t all_live, all_movable;
-    scan_group(live, sums[0], all_live);
-    scan_group(movable, sums[1], all_movable);
+    __shared__ int32_t sums[kTileThreads / 64];
+    const BlockState s = block_state(a, w, blockIdx.x);
+    int32_t all;   // both counts in one word, at most kPageTile each
+    scan_group(__builtin_popcount(s.live) << 16 | __builtin_popcount(s.movable), sums, all);
     if (threadIdx.x == 0) {
-        w.live[blockIdx.x] = all_live;
-        w.movable[blockIdx.x] = all_movable;
+        w.live[blockIdx.x] = all >> 16;
+        w.movable[blockIdx.x] = all & 0xFFFF;
     }
 }
 
-// Every workgroup works out L and what lies before its tile from all tiles'
-// counts; of the tile that L falls into it counts the blocks itself.
+// Every workgroup works out L, how many blocks move and what lies before its tile, from
+// all tiles' counts; of the tile that L falls into it counts the blocks itself.
 __global__ __launch_bounds__(kTileThreads) void compact_list_kernel(CompactArgs a, CompactSpace w) {
     __shared__ int32_t sums[6][kTileThreads / 64];
     const int tid = threadIdx.x, tile = blockIdx.x;
+    const BlockState mine = block_state(a, w, tile);
     int32_t all = 0;
     for (int i = tid; i < w.tiles; i += kTileThreads) all += w.live[i];
     int32_t limit;
     scan_group(all, sums[0], limit);
-    const int border = limit / kTileBlocksHeld;   // L's tile (past the last where all blocks are live)
-    // free blocks below L in the tiles before, and blocks that move in them
-    int32_t slots_before = 0, moves_before = 0;
-    for (int i = tid; i < tile && i < w.tiles; i += kTileThreads) {
-        if (i < border) slots_before += kTileBlocksHeld - w.live[i];
-        if (i > border) moves_before += w.movable[i];
-    }
-    if (tile > border) {
-        for (int k = 0; k < kTileEach; ++k) {
-            const int b = border * kTileBlocksHeld + k * kTileThreads + tid;
-            bool l, m;
-            block_state(a, w, b, l, m);
-            moves_before += m && b >= limit;
-            slots_before += !l && b < limit;
+    const int border = limit / kPageTile;   // L's tile (past the last where all blocks are live)
+    // bits of a tile's blocks below L
+    const auto below = [&](int i) {
+        const int n = limit - (i * kPageTile + 4 * tid);
+        return n <= 0 ? 0u : n >= 4 ? 15u : (1u << n) - 1;
+    };
+    const BlockState at_border = border < w.tiles ? block_state(a, w, border) : BlockState{0, 0};
+    const int32_t border_moves = __builtin_popcount(at_border.movable & ~below(border));
+    // free blocks below L in the tiles before, blocks that move in them, and all that move
+    int32_t slots_before = 0, moves_before = tile > border ? border_moves : 0, moves_all = border_moves;
+    for (int i = tid; i < w.tiles; i += kTileThreads) {
+        if (i < border && i < tile) slots_before += kPageTile - w.live[i];
+        if (i > border) {
+            moves_all += w.movable[i];
+            if (i < tile) moves_before += w.movable[i];
         }
     }
-    int32_t slots, moves;
+    int32_t slots, moves, total;
     scan_group(slots_before, sums[1], slots);
     scan_group(moves_before, sums[2], moves);
-    const int half = a.num_blocks / 2 > 1 ? a.num_blocks / 2 : 1;
-    const int first = tile * kTileBlocksHeld + tid * kTileEach;
-    int32_t my_slots = 0, my_moves = 0;
-    uint32_t slot_bits = 0, move_bits = 0;
+    scan_group(moves_all, sums[3], total);
+    const int first = tile * kPageTile + 4 * tid;
+    const uint32_t slot = ~mine.live & below(tile), move = mine.movable & ~below(tile);
+    int32_t ignored;
+    int32_t slot_at = slots + scan_group(static_cast<int32_t>(__builtin_popcount(slot)), sums[4], ignored);
+    int32_t move_at = moves + scan_group(static_cast<int32_t>(__builtin_popcount(move)), sums[5], ignored);
 #pragma unroll
-    for (int k = 0; k < kTileEach; ++k) {
-        bool l, m;
-        block_state(a, w, first + k, l, m);
-        const bool slot = first + k < limit && !l, move = first + k >= limit && m;
-        my_slots += slot;
-        my_moves += move;
-        slot_bits |= static_cast<uint32_t>(slot) << k;
-        move_bits |= static_cast<uint32_t>(move) << k;
-    }
-    int32_t total;
-    int32_t slot_at = slots + scan_group(my_slots, sums[3], total), move_at = moves + scan_group(my_moves, sums[4], total);
-#pragma unroll
-    for (int k = 0; k < kTileEach; ++k) {
-        if (slot_bits >> k & 1) {
-            if (slot_at < half) a.dst[slot_at] = first + k;
+    for (int k = 0; k < 4; ++k) {
+        if (slot >> k & 1) {   // there may be more of them than blocks that move
+            if (slot_at < total) a.dst[slot_at] = first + k;
             ++slot_at;
         }
-        if (move_bits >> k & 1) {
-            if (move_at < half) a.src[move_at] = first + k;
-            ++move_at;
+        if (move >> k & 1) {
+            a.src[move_at] = first + k;
+            w.moved[first + k] = move_at++;
         }
     }
-    if (tile == 0 && tid == 0) *a.live = limit;
-}
-
-// There may be more free blocks below L than blocks that move: the rest of dst
-// is cleared.  And where each block went.
-__global__ __launch_bounds__(256) void compact_map_kernel(CompactArgs a, CompactSpace w) {
     const int half = a.num_blocks / 2 > 1 ? a.num_blocks / 2 : 1;
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < half; i += gridDim.x * 256) {
-        const int32_t src = a.src[i];
-        if (src < 0) a.dst[i] = -1;
-        else w.moved[src] = a.dst[i];
-    }
+    for (int i = total + tile * kTileThreads + tid; i < half; i += w.tiles * kTileThreads) a.src[i] = a.dst[i] = -1;
+    if (tile == 0 && tid == 0) *a.live = limit;
 }
 
 __global__ __launch_bounds__(256) void compact_table_kernel(CompactArgs a, CompactSpace w) {
@@ -331,7 +436,7 @@ __global__ __launch_bounds__(256) void compact_table_kernel(CompactArgs a, Compa
     for (int t = blockIdx.x * 256 + threadIdx.x; t < a.width; t += gridDim.x * 256) {
         int32_t id = t < have ? a.table[at + t] : -1;
         if (id < 0 || id >= a.num_blocks) id = -1;
-        else if (id >= limit && !(a.held && a.held[id] > 0)) id = w.moved[id];
+        else if (id >= limit && !(a.held && a.held[id] > 0)) id = a.dst[w.moved[id]];
         a.out_table[at + t] = id;
     }
 }
@@ -391,18 +496,17 @@ size_t fork_workspace(int64_t n_out, int64_t num_blocks) {
 }
 
 hipError_t launch_kv_fork(const ForkArgs &a, hipStream_t s) {
-    const ForkSpace w = fork_space(a.workspace, a.n_out, a.num_blocks);
-    hipLaunchKernelGGL(fork_clear_kernel, dim3(blocks_of(a.num_blocks, 256, 2048)), dim3(256), 0, s, a, w);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.n_out) {
-        hipLaunchKernelGGL(fork_gather_kernel, dim3((a.width + kForkEntries - 1) / kForkEntries, a.n_out), dim3(256), 0, s, a, w);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(fork_hand_kernel, dim3(1), dim3(kHandThreads), 0, s, a, w);
-        e = hipGetLastError();
+    const ForkSpace w = fork_space(a.workspace, a.num_blocks);
+    if (a.n_out <= kOneRows && a.num_blocks <= kOneBlocks && static_cast<int64_t>(a.n_out) * a.width <= kOneEntries) {
+        hipLaunchKernelGGL(fork_one_kernel, dim3(1), dim3(kHandThreads), 0, s, a, w);
+        return hipGetLastError();
     }
-    return e;
+    hipLaunchKernelGGL(fork_clear_kernel, dim3(blocks_of(a.num_blocks, 256, 2048)), dim3(256), 0, s, a, w);
+    if (a.n_out) {
+        hipLaunchKernelGGL(fork_gather_kernel, dim3((a.width + 255) / 256, (a.n_out + kForkRows - 1) / kForkRows), dim3(256), 0, s, a, w);
+        hipLaunchKernelGGL(fork_hand_kernel, dim3(1), dim3(kHandThreads), 0, s, a, w);
+    }
+    return hipGetLastError();
 }
 
 size_t compact_workspace(int64_t num_blocks) {
@@ -416,7 +520,6 @@ hipError_t launch_kv_compact(const CompactArgs &a, hipStream_t s) {
     if (a.rows) hipLaunchKernelGGL(compact_mark_kernel, tables, dim3(256), 0, s, a, w);
     hipLaunchKernelGGL(compact_count_kernel, dim3(w.tiles), dim3(kTileThreads), 0, s, a, w);
     hipLaunchKernelGGL(compact_list_kernel, dim3(w.tiles), dim3(kTileThreads), 0, s, a, w);
-    hipLaunchKernelGGL(compact_map_kernel, blocks, dim3(256), 0, s, a, w);
     if (a.rows) hipLaunchKernelGGL(compact_table_kernel, tables, dim3(256), 0, s, a, w);
     return hipGetLastError();
 }
@@ -425,7 +528,7 @@ hipError_t launch_kv_copy(const CopyArgs &a, hipStream_t s) {
     const int pieces = a.kv_heads * 2 * kKvBlock * a.head_dim / kPiece;
     // a wave for each piece while there is room for that many, then up to 64 pairs a wave
     const int64_t all = static_cast<int64_t>(a.n) * pieces * a.layers;
-    int64_t each = all / 8192;
+    int64_t each = all / 32768;
     each = each < 1 ? 1 : each > 64 ? 64 : each;
     const int64_t chunks = (a.n + each - 1) / each;
     const int64_t rows = static_cast<int64_t>(pieces) * a.layers;   // at most 256 * 2 * 128 / 128 * 32
