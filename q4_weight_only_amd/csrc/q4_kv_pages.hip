@@ -238,7 +238,9 @@ __global__ __launch_bounds__(kHandThreads) void fork_hand_kernel(ForkArgs a, For
 }
 
 // All of it in one workgroup, where the tables and the pool are small: the counts are
-// in LDS, and who goes on in the same block is found by looking at all.
+// in LDS, and who goes on in the same block is found by looking at all.  4 tables of 8
+// entries and a pool of 100 blocks: 6.3 us, as three kernels 10.5; 64 of 60 and 8000
+// blocks 8.6 and 13.0; at the border, 256 of 64 and 8000, both take 13.3.
 constexpr int kOneRows = 256, kOneBlocks = 8192, kOneAhead = 8;
 constexpr int64_t kOneEntries = 16384;
 
@@ -370,7 +372,7 @@ __global__ __launch_bounds__(kTileThreads) void compact_count_kernel(CompactArgs
     __shared__ int32_t sums[kTileThreads / 64];
     const BlockState s = block_state(a, w, blockIdx.x);
     int32_t all;   // both counts in one word, at most kPageTile each
-    scan_group(__builtin_popcount(s.live) << 16 | __builtin_popcount(s.movable), sums, all);
+    scan_group<int32_t>(__builtin_popcount(s.live) << 16 | __builtin_popcount(s.movable), sums, all);
     if (threadIdx.x == 0) {
         w.live[blockIdx.x] = all >> 16;
         w.movable[blockIdx.x] = all & 0xFFFF;
@@ -441,9 +443,119 @@ __global__ __launch_bounds__(256) void compact_table_kernel(CompactArgs a, Compa
     }
 }
 
+// All of it in one launch, where a bit for each block fits LDS and the tables and
+// counts are not much to read for one workgroup: each marks the blocks in bits of its own,
+// from all tables, and with the counts before each word of these has the place of every block
+// that moves; the results are shared out.  40 tables of 60 entries and a pool of 4096
+// blocks: 6.1 us, with the five kernels above 14.0; 16000 entries and 16000 held counts
+// 10.6 and 15.2; at the border, 48000 entries, 15.0 and 15.3 (with 60000 held counts
+// besides 27 and 15.8).
+constexpr int kMapThreads = 1024, kMapBlocks = 65536, kMapWords = kMapBlocks / 32, kMapRows = 1024, kMapAhead = 8;
+constexpr int64_t kMapReads = 49152;
+
+__global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a) {
+    __shared__ uint32_t live[kMapWords], movable[kMapWords];   // a bit for each block
+    __shared__ int32_t live_before[kMapWords], moves_before[kMapWords];
+    __shared__ int32_t have[kMapRows];
+    __shared__ uint32_t sums[2][kMapThreads / 64];
+    const int tid = threadIdx.x, first = blockIdx.x * kMapThreads + tid, step = gridDim.x * kMapThreads;
+    const int words = (a.num_blocks + 31) / 32, entries = a.rows * a.width;
+    const float per = 1.0f / a.width;   // up to 2^16 entries: (e + 1/2) / width is off by far less than 1/2 of one
+    const auto row_of = [&](int e) { return static_cast<int>((e + 0.5f) * per); };
+    for (int i = tid; i < words; i += kMapThreads) live[i] = 0;
+    for (int i = tid; i < a.rows; i += kMapThreads) have[i] = (held_to(a.lengths[i], 0, a.width * kKvBlock) + kKvBlock - 1) / kKvBlock;
+    __syncthreads();
+    for (int e0 = tid; e0 < entries; e0 += kMapThreads * kMapAhead) {
+        int32_t id[kMapAhead];
+#pragma unroll
+        for (int k = 0; k < kMapAhead; ++k) id[k] = e0 + kMapThreads * k < entries ? a.table[e0 + kMapThreads * k] : -1;
+#pragma unroll
+        for (int k = 0; k < kMapAhead; ++k) {
+            const int e = e0 + kMapThreads * k < entries ? e0 + kMapThreads * k : 0, i = row_of(e);
+            if (id[k] >= 0 && id[k] < a.num_blocks && e - i * a.width < have[i]) atomicOr(&live[id[k] >> 5], 1u << (id[k] & 31));
+        }
+    }
+    __syncthreads();
+    if (a.held) {   // a wave has 64 blocks: its ballot is their two words
+        for (int b0 = tid; b0 < words * 32; b0 += kMapThreads * kMapAhead) {
+            int32_t held[kMapAhead];
+#pragma unroll
+            for (int k = 0; k < kMapAhead; ++k) held[k] = b0 + kMapThreads * k < a.num_blocks ? a.held[b0 + kMapThreads * k] : 0;
+#pragma unroll
+            for (int k = 0; k < kMapAhead; ++k) {
+                const int b = b0 + kMapThreads * k;
+                const uint32_t mine = static_cast<uint32_t>(__ballot(held[k] > 0) >> (tid & 32));
+                if ((tid & 31) == 0 && b < words * 32) {
+                    movable[b >> 5] = live[b >> 5] & ~mine;
+                    live[b >> 5] |= mine;
+                }
+            }
+        }
+    } else {
+        for (int i = tid; i < words; i += kMapThreads) movable[i] = live[i];
+    }
+    __syncthreads();
+    int32_t limit = 0, moves = 0;   // L, and how many blocks may move (of those below L too, so far)
+    for (int i0 = 0, turn = 0; i0 < words; i0 += kMapThreads, turn ^= 1) {
+        const int i = i0 + tid;
+        // both counts in one word: a turn's are at most 2^15 each
+        const uint32_t n = i < words ? static_cast<uint32_t>(__builtin_popcount(live[i])) << 16 | __builtin_popcount(movable[i]) : 0;
+        uint32_t total;
+        const uint32_t before = scan_group(n, sums[turn], total);
+        if (i < words) {
+            live_before[i] = limit + (before >> 16);
+            moves_before[i] = moves + (before & 0xFFFF);
+        }
+        limit += total >> 16;
+        moves += total & 0xFFFF;
+    }
+    __syncthreads();
+    const auto bits_below = [](uint32_t word, int b) { return __builtin_popcount(word & ((1u << (b & 31)) - 1)); };
+    const int below = limit >= a.num_blocks ? moves : moves_before[limit >> 5] + bits_below(movable[limit >> 5], limit);
+    const int total = moves - below;   // blocks that move
+    // the free block of rank k
+    const auto slot = [&](int k) {
+        int lo = 0, hi = limit >> 5;   // the last word with at most k free blocks before it
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (32 * mid - live_before[mid] <= k) lo = mid;
+            else hi = mid - 1;
+        }
+        uint32_t free = ~live[lo];
+        int left = k - (32 * lo - live_before[lo]), at = 0;
+#pragma unroll
+        for (int half = 16; half; half /= 2) {
+            const int n = __builtin_popcount(free >> at & ((1u << half) - 1));
+            if (left >= n) {
+                left -= n;
+                at += half;
+            }
+        }
+        return 32 * lo + at;
+    };
+    for (int b = first; b < a.num_blocks; b += step)
+        if (b >= limit && movable[b >> 5] >> (b & 31) & 1) a.src[moves_before[b >> 5] + bits_below(movable[b >> 5], b) - below] = b;
+    const int half = a.num_blocks / 2 > 1 ? a.num_blocks / 2 : 1;
+    for (int k = first; k < half; k += step) {
+        a.dst[k] = k < total ? slot(k) : -1;
+        if (k >= total) a.src[k] = -1;
+    }
+    for (int e = first; e < entries; e += step) {
+        const int i = row_of(e);
+        int32_t id = e - i * a.width < have[i] ? a.table[e] : -1;
+        if (id < 0 || id >= a.num_blocks) id = -1;
+        else if (id >= limit && movable[id >> 5] >> (id & 31) & 1) id = slot(moves_before[id >> 5] + bits_below(movable[id >> 5], id) - below);
+        a.out_table[e] = id;
+    }
+    if (first == 0) *a.live = limit;
+}
+
 // ------------------------------------------------------------------- copy
 // A wave has a piece of 4 KB of the blocks of one layer, for some of the pairs: it
-// reads their ids at once and copies the piece of those that there are.
+// reads their ids at once and copies the piece of those that there are.  The stores
+// are not to stay in the L2: copies of 70 MB took 23.3 us with that hint and 32.1
+// without, and 85 blocks of 4 layers with the attention that reads them right behind
+// 174.8 and 188.6.
 constexpr int kPiece = 4096;
 
 __global__ __launch_bounds__(256) void copy_kernel(CopyArgs a, int pieces, int pairs_each) {
@@ -470,7 +582,7 @@ __global__ __launch_bounds__(256) void copy_kernel(CopyArgs a, int pieces, int p
 #pragma unroll
         for (int k = 0; k < kPiece / 1024; ++k) v[k] = p[64 * k];
 #pragma unroll
-        for (int k = 0; k < kPiece / 1024; ++k) q[64 * k] = v[k];
+        for (int k = 0; k < kPiece / 1024; ++k) __builtin_nontemporal_store(v[k], q + 64 * k);
         if (piece == 0) {
             const int n = a.kv_heads * 2;
             for (int k = lane; k < n; k += 64) exps[to * n + k] = exps[from * n + k];
@@ -514,6 +626,12 @@ size_t compact_workspace(int64_t num_blocks) {
 }
 
 hipError_t launch_kv_compact(const CompactArgs &a, hipStream_t s) {
+    const int64_t entries = static_cast<int64_t>(a.rows) * a.width;
+    if (a.num_blocks <= kMapBlocks && a.rows <= kMapRows && entries + (a.held ? a.num_blocks : 0) <= kMapReads) {
+        const dim3 groups(blocks_of(entries > a.num_blocks ? entries : a.num_blocks, kMapThreads, 64));
+        hipLaunchKernelGGL(compact_map_kernel, groups, dim3(kMapThreads), 0, s, a);
+        return hipGetLastError();
+    }
     const CompactSpace w = compact_space(a.workspace, a.num_blocks);
     const dim3 tables(blocks_of(a.width, 256, 64), a.rows), blocks(blocks_of(a.num_blocks, 256, 2048));
     hipLaunchKernelGGL(compact_clear_kernel, blocks, dim3(256), 0, s, a, w);

@@ -76,12 +76,13 @@ hipError_t launch_kv_attention_blocks(const AttentionArgs &a, const int32_t *cho
 
 #ifdef __HIPCC__
 // Sum over the lanes before this one, and over all.
-__device__ __forceinline__ int32_t scan_wave(int32_t v, int32_t &total) {
+template <typename T>
+__device__ __forceinline__ T scan_wave(T v, T &total) {
     const int lane = threadIdx.x & 63;
-    int32_t sum = v;
+    T sum = v;
 #pragma unroll
     for (int i = 1; i < 64; i *= 2) {
-        const int32_t below = __shfl_up(sum, i);
+        const T below = __shfl_up(sum, i);
         if (lane >= i) sum += below;
     }
     total = __shfl(sum, 63);
@@ -90,14 +91,14 @@ __device__ __forceinline__ int32_t scan_wave(int32_t v, int32_t &total) {
 
 // The same over a workgroup of WAVES waves.  `sums` may be used again after the
 // caller's next barrier.
-template <int WAVES>
-__device__ __forceinline__ int32_t scan_group(int32_t v, int32_t (&sums)[WAVES], int32_t &total) {
+template <typename T, int WAVES>
+__device__ __forceinline__ T scan_group(T v, T (&sums)[WAVES], T &total) {
     const int wave = threadIdx.x >> 6;
-    int32_t mine;
-    const int32_t before = scan_wave(v, mine);
+    T mine;
+    const T before = scan_wave(v, mine);
     if ((threadIdx.x & 63) == 0) sums[wave] = mine;
     __syncthreads();
-    int32_t front = 0;
+    T front = 0;
     total = 0;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {

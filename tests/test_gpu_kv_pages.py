@@ -154,6 +154,31 @@ def test_compact_at_the_borders_of_tiles(blocks):
     _compact(np.array([[5, blocks - 3500, blocks - 3100]]), [96], blocks, held)
 
 
+@pytest.mark.parametrize("blocks", [65535, 65536, 65537, 70001, 131072])
+@pytest.mark.parametrize("rows,width", [(3, 900), (1024, 64), (1025, 3), (40, 1700), (1, 65536)])
+def test_compact_of_large_pools_and_tables(blocks, rows, width):
+    """Around the sizes up to which one launch does it all."""
+    rng = np.random.default_rng(blocks + rows)
+    table, lengths = _tables(rng, rows, width, blocks, spoil=True)
+    _compact(table, lengths, blocks, (rng.random(blocks) < 0.3).astype(int) * 3 - 1)
+    _compact(table, lengths, blocks)
+
+
+@pytest.mark.parametrize("blocks", [66560, 67583, 69632])
+def test_compact_at_the_borders_of_large_tiles(blocks):
+    """As many blocks in use as tiles of 1024 hold, one fewer, one more, all and none."""
+    rng = np.random.default_rng(1)
+    for live in (0, 1, 1023, 1024, 1025, 65536, blocks - 1, blocks):
+        ids = rng.permutation(blocks)[:live]
+        if 0 < live < blocks:
+            ids[0] = blocks - 1
+            ids = np.unique(ids)
+            rng.shuffle(ids)
+        table = np.full((1, blocks), -1)
+        table[0, :len(ids)] = ids
+        _compact(table, [32 * len(ids)], blocks)
+
+
 def test_compact_then_everything_reads_the_same():
     rng = np.random.default_rng(4)
     blocks, heads, D = 90, 2, 64
