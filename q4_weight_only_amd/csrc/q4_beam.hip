@@ -221,17 +221,19 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 __device__ __forceinline__ float unordered(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key); }
 
 constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
-constexpr int kSlots = 256;       // the items of four threads are a slot
+constexpr int kSlots = 256, kFewSlots = 64;   // the items of four waves' lanes are a slot, or of all 16
+constexpr int kFewKeep = 16;      // up to so many the few do: 4 beams of 131072 tokens 9.2 us, with 256 slots 10.6
 constexpr int kListed = 512;      // segments that may be listed before they are cut down to `keep`
 constexpr int kAhead = 4;         // parts of a row, or items, of a lane that are loaded together
+constexpr int kSegmentBits = 19;  // a segment's id: its beam, then its place in the row, of up to 2^24 / 32
 
 // A workgroup has one group.  Its items are the waves' parts of its beams' rows, or,
 // where `keep` is a large share of these, the segments; 64 of one beam a chunk, the
-// chunks to the waves in turn.  A bound that n of its 256 slots reach is one that at
+// chunks to the waves in turn.  A bound that n of its slots reach is one that at
 // least n items reach, and hardly more where they are spread evenly.  The segments that
 // reach it are listed, and the n first of them found by counting, for each, the ones
-// in front.  Where too many reach the bound (they lie together, or are equal), the
-// n-th segment itself is found, bit by bit.
+// in front (so is the bound among the slots).  Where too many reach the bound of parts, it is
+// found for segments; where it is still too many (they are equal), the n-th segment itself is found, bit by bit.
 //
 // The bound is found in fp32, on z + (score - lse), which is off by two roundings:
 // with n items at b or more, the n first have a score of b less one error or more, and
@@ -240,14 +242,14 @@ constexpr int kAhead = 4;         // parts of a row, or items, of a lane that ar
 //
 // What bounds it is one step after the other, on one compute unit: what it reads
 // comes from the others' caches at some 20 bytes a cycle, so it reads few segments (all
-// of them: 128 KB and 6 us of 17 for 8 beams of 131072 tokens), and each step's code is fetched
-// as it goes.
+// of them: 128 KB and 6 us of 17 for 8 beams of 131072 tokens), the items once, on their
+// way while the sums are joined; and each step's code is fetched as it goes.
 __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Scan in) {
     __shared__ double base[kMaxBeams], lse[kMaxBeams];
     __shared__ float offset[kMaxBeams];   // score - lse; -inf for beams without tokens as candidates
     __shared__ int32_t ended[kMaxBeams];
     __shared__ __align__(16) uint32_t slot[kSlots];
-    __shared__ float bound_near;
+    __shared__ uint32_t bound_near;
     __shared__ int32_t part_list[kListed];
     __shared__ double list_s[kListed];
     __shared__ int32_t list_id[kListed];
@@ -263,39 +265,60 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
     const float *segment = in.segment + static_cast<int64_t>(group) * a.beams * segments;
     const bool coarse = a.beams * in.parts >= 4 * n;
 
+    // items of the thread, `per` of a beam: their beam (or -1), place among its items, and largest logit
+    const auto load_items = [&](const float *from, int per, uint32_t inverse, int c0, int (&b)[kAhead], int (&at)[kAhead], float (&z)[kAhead]) {
+        const int each = (per + 63) / 64, chunks = a.beams * each;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int chunk = c0 + kPickWaves * k;
+            b[k] = divide(chunk, inverse);
+            at[k] = (chunk - b[k] * each) * 64 + lane;
+            if (chunk >= chunks || at[k] >= per) b[k] = -1;
+            z[k] = b[k] >= 0 ? from[static_cast<int64_t>(b[k]) * per + at[k]] : kNone;
+        }
+        return c0 + kPickWaves * kAhead < chunks;   // more of them
+    };
+    const auto load_sums = [&](int c0, int (&b)[kAhead], int (&at)[kAhead], float (&z)[kAhead]) {
+        return load_items(coarse ? in.top + static_cast<int64_t>(group) * a.beams * in.parts : segment, coarse ? in.parts : segments,
+                          coarse ? in.part_inverse : in.segment_inverse, c0, b, at, z);
+    };
+    int first_b[kAhead], first_at[kAhead];
+    float first_z[kAhead];
+    const bool more_items = load_sums(wave, first_b, first_at, first_z);
+
     for (int b = wave; b < a.beams; b += kPickWaves) {
         const int64_t row = static_cast<int64_t>(group) * a.beams + b;
         const float before = a.scores[row];
-        const bool done = a.finished && a.finished[row];
+        const bool done = a.finished && a.finished[row];   // its parts hold anything, and nothing comes of them
         float m = kNone;       // the lane's largest so far, and its sum relative to that
         double sum = 0.0;
-        if (!done) {
-            const float *tops = in.top + row * in.parts;
-            const double *sums = in.sum + row * in.parts;
-            for (int i0 = lane; i0 < in.parts; i0 += 64 * kAhead) {
-                float top[kAhead];
-                double part[kAhead];
+        const float *tops = in.top + row * in.parts;
+        const double *sums = in.sum + row * in.parts;
+        for (int i0 = lane; i0 < in.parts; i0 += 64 * kAhead) {
+            float top[kAhead];
+            double part[kAhead];
 #pragma unroll
-                for (int k = 0; k < kAhead; ++k) {
-                    const int i = i0 + 64 * k;
-                    top[k] = i < in.parts ? tops[i] : kNone;
-                    part[k] = i < in.parts ? sums[i] : 0.0;
-                }
-                float most = m;
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) most = larger(most, top[k]);
-                const float least = most - 80.0f;
-                sum *= m > kNone && m >= least ? exp64(static_cast<double>(m) - most) : 0.0;   // (0 so far where m is -inf)
-                m = most;
-                // a part without a logit has a sum of 0, or of what is not a number
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k) sum += top[k] == kNone ? part[k] : part[k] * exp_below(top[k], most, least);
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + 64 * k;
+                top[k] = i < in.parts ? tops[i] : kNone;
+                part[k] = i < in.parts ? sums[i] : 0.0;
             }
+            float most = m;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) most = larger(most, top[k]);
+            const float least = most - 80.0f;
+            sum *= m > kNone && m >= least ? exp64(static_cast<double>(m) - most) : 0.0;   // (0 so far where m is -inf)
+            m = most;
+            // a part without a logit has a sum of 0, or of what is not a number
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) sum += top[k] == kNone ? part[k] : part[k] * exp_below(top[k], most, least);
         }
         const float top = max_of_64(m);
         // (what is not a number stays it times 0)
         sum = sum_of_64(m == kNone ? sum : sum * exp_below(m, top, top - 80.0f));
-        const double l = top + log(sum), off = before - l;
+        // the logarithm, 5e-11 off: in fp32, and what that leaves, 2e-6 or less of e^rough, to the second power
+        const float rough = logf(static_cast<float>(sum));
+        const double e = fma(sum, exp64(-static_cast<double>(rough)), -1.0), l = top + (rough + fma(-0.5 * e, e, e)), off = before - l;
         if (lane == 0) {
             base[b] = before + 0.0;
             lse[b] = l;
@@ -303,73 +326,58 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
             offset[b] = !done && __builtin_isfinite(off) ? static_cast<float>(off) : kNone;
         }
     }
-    if (tid == 0) listed = parts_listed = 0;
-    __syncthreads();
+    const auto start = [&]() {
+        if (tid < kSlots) slot[tid] = 0;
+        if (tid == 0) listed = parts_listed = bound_near = 0;
+        __syncthreads();
+    };
+    start();
 
     const auto score = [&](int b, float z) {
         const double s = base[b] + (z - lse[b]) + 0.0;   // no -0, which would be equal to 0 and ordered before it
         return __builtin_isfinite(s) ? s : static_cast<double>(kNone);
     };
-    // items of the thread, `per` of a beam: their beam, place among its items, and largest logit
-    const auto each_of = [&](const float *from, int per, uint32_t inverse, auto f) {
-        const int each = (per + 63) / 64, chunks = a.beams * each;
-        for (int c0 = wave; c0 < chunks; c0 += kPickWaves * kAhead) {
-            float z[kAhead];
+    const auto each_segment = [&](auto f) {
+        bool more = true;
+        for (int c0 = wave; more; c0 += kPickWaves * kAhead) {
             int b[kAhead], at[kAhead];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int chunk = c0 + kPickWaves * k;
-                b[k] = divide(chunk, inverse);
-                at[k] = (chunk - b[k] * each) * 64 + lane;
-                if (chunk >= chunks || at[k] >= per) b[k] = -1;
-                z[k] = b[k] >= 0 ? from[static_cast<int64_t>(b[k]) * per + at[k]] : kNone;
-            }
+            float z[kAhead];
+            more = load_items(segment, segments, in.segment_inverse, c0, b, at, z);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (b[k] >= 0) f(b[k], at[k], z[k]);
         }
     };
     // every candidate segment: its place in 64 bits.  An ended beam has one candidate, in its first segment.
-    const auto each_segment = [&](auto f) {
-        each_of(segment, segments, in.segment_inverse, [&](int b, int at, float z) {
+    const auto each_place = [&](auto f) {
+        each_segment([&](int b, int at, float z) {
             Place p;
-            p.id = b * segments + at;
+            p.id = b << kSegmentBits | at;
             p.s = ended[b] ? (at == 0 && __builtin_isfinite(base[b]) ? base[b] : static_cast<double>(kNone)) : score(b, z);
             f(p);
         });
     };
     // the items of beams that have not ended, with their sums in fp32 (what is no candidate: -inf, or not a number)
-    const auto each_sum = [&](auto f) {
-        each_of(coarse ? in.top + static_cast<int64_t>(group) * a.beams * in.parts : segment, coarse ? in.parts : segments,
-                coarse ? in.part_inverse : in.segment_inverse, [&](int b, int at, float z) { f(b, at, z + offset[b]); });
+    const auto each_item = [&](auto f) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (first_b[k] >= 0) f(first_b[k], first_at[k], first_z[k] + offset[first_b[k]]);
+        bool more = more_items;
+        for (int c0 = wave + kPickWaves * kAhead; more; c0 += kPickWaves * kAhead) {
+            int b[kAhead], at[kAhead];
+            float z[kAhead];
+            more = load_sums(c0, b, at, z);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (b[k] >= 0) f(b[k], at[k], z[k] + offset[b[k]]);
+        }
+    };
+    const auto each_segment_sum = [&](auto f) {
+        each_segment([&](int b, int at, float z) { f(b, at, z + offset[b]); });
     };
     const bool my_ended = tid < a.beams && ended[tid] && __builtin_isfinite(base[tid]);   // a candidate of its own
-    float best = my_ended ? static_cast<float>(base[tid]) : kNone;
-    each_sum([&](int, int, float s) { best = fmaxf(best, s); });
-    best = fmaxf(best, from_lane<kLane1>(best));
-    best = fmaxf(best, from_lane<kLane2>(best));
-    if (tid % 4 == 0) slot[tid / 4] = ordered(best);
+    const bool few = n <= kFewKeep;
     const float widest = max_of_64(lane < a.beams && offset[lane] > kNone ? fabsf(offset[lane]) : 0.0f);   // of the offsets
-    __syncthreads();
-    if (wave == 0) {   // the n-th of the slots (n <= 128), or a little below it
-        uint32_t mine[kSlots / 64], least = 0;
-#pragma unroll
-        for (int k = 0; k < kSlots / 64; ++k) mine[k] = slot[lane * (kSlots / 64) + k];
-#pragma unroll 1
-        for (int bit = 31; bit >= 8; --bit) {
-            const uint32_t probe = least | 1u << bit;
-            int c = 0;
-#pragma unroll
-            for (int k = 0; k < kSlots / 64; ++k) c += __builtin_popcountll(__ballot(mine[k] >= probe));
-            if (c >= n) least = probe;
-            if (c >= n && c <= n + n / 4) break;
-        }
-        if (lane == 0) bound_near = unordered(least);
-    }
-    __syncthreads();
-    // (not a number, or -inf: fewer than n slots have a candidate, and all of them are listed)
-    const float near = bound_near > kNone ? bound_near - 0x1p-21f * (fabsf(bound_near) + widest) : kNone;
-    const bool exact = widest > 1e30f || !(near < __builtin_inff());   // sums might not be finite
     const auto list = [&](int id, double s) {
         if (s == kNone) return;
         const int at = atomicAdd(&listed, 1);   // their order does not matter: they are counted below
@@ -378,39 +386,88 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
             list_id[at] = id;
         }
     };
-    if (exact) {
-        if (tid == 0) listed = kListed + 1;
-    } else {
-        if (my_ended && static_cast<float>(base[tid]) >= near) list(tid * segments, base[tid]);
-        each_sum([&](int b, int at, float s) {
-            if (!(s >= near) || s == kNone) return;
-            if (coarse) {
-                const int i = atomicAdd(&parts_listed, 1);
-                if (i < kListed) part_list[i] = b * in.parts + at;
-            } else {
-                list(b * segments + at, score(b, segment[b * segments + at]));
+    // lists the segments that reach the bound, of more than kListed some; false: sums might not be finite
+    const auto list_best = [&](const bool parts, auto each_sum) {
+        float best = my_ended ? static_cast<float>(base[tid]) : kNone;
+        each_sum([&](int, int, float s) { best = fmaxf(best, s); });
+        atomicMax(&slot[few ? lane : tid % kSlots], ordered(best));
+        __syncthreads();
+        // the n-th of the slots, by how many reach each of the wave's
+        uint32_t reached = 0;
+        if (few) {
+            const uint32_t all = slot[lane];
+#pragma unroll
+            for (int i = 0; i < kFewSlots / kPickWaves; ++i) {
+                const uint32_t probe = __builtin_amdgcn_readlane(all, wave * (kFewSlots / kPickWaves) + i);
+                reached = __builtin_popcountll(__ballot(all >= probe)) >= n && probe > reached ? probe : reached;
             }
-        });
-    }
-    __syncthreads();
-    if (coarse && !exact) {   // the same for the workgroup
-        const int parts = parts_listed < kListed ? parts_listed : kListed, per = 8 * in.loads;   // segments of a part
-        for (int i = tid; i < parts * per; i += kPickThreads) {
-            const int part = part_list[i / per], b = part / in.parts, at = (part - b * in.parts) * per + i % per;
-            if (at >= segments) continue;
-            const float z = segment[b * segments + at], s = z + offset[b];
-            if (s >= near && s > kNone) list(b * segments + at, score(b, z));
+        } else {
+            constexpr int kEach = kSlots / 64;
+            uint32_t all[kEach];
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) all[k] = slot[lane * kEach + k];
+#pragma unroll 1
+            for (int i = 0; i < kSlots / kPickWaves / kEach; ++i) {   // (unrolled it is slower: code that comes from far)
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const uint32_t probe = __builtin_amdgcn_readlane(all[j], wave * (kSlots / kPickWaves / kEach) + i);
+                    int c = 0;
+#pragma unroll
+                    for (int k = 0; k < kEach; ++k) c += __builtin_popcountll(__ballot(all[k] >= probe));
+                    reached = c >= n && probe > reached ? probe : reached;
+                }
+            }
+        }
+        if (lane == 0) atomicMax(&bound_near, reached);
+        __syncthreads();
+        const float nth = unordered(bound_near);
+        // (not a number, or -inf: fewer than n slots have a candidate, and all of them are listed)
+        const float near = nth > kNone ? nth - 0x1p-21f * (fabsf(nth) + widest) : kNone;
+        const bool exact = widest > 1e30f || !(near < __builtin_inff());   // sums might not be finite
+        if (exact) {
+            if (tid == 0) listed = kListed + 1;
+        } else {
+            if (my_ended && static_cast<float>(base[tid]) >= near) list(tid << kSegmentBits, base[tid]);
+            each_sum([&](int b, int at, float s) {
+                if (!(s >= near) || s == kNone) return;
+                if (parts) {
+                    const int i = atomicAdd(&parts_listed, 1);
+                    if (i < kListed) part_list[i] = b << kSegmentBits | at;
+                } else {
+                    list(b << kSegmentBits | at, score(b, segment[b * segments + at]));
+                }
+            });
         }
         __syncthreads();
-        if (tid == 0 && parts_listed > kListed) listed = kListed + 1;
+        if (parts && !exact) {   // the same for the workgroup
+            const int some = parts_listed < kListed ? parts_listed : kListed;
+            const int shift = in.loads == 2 ? 4 : in.loads == 4 ? 5 : 6;   // a part has 8 * loads segments
+            for (int i = tid; i < some << shift; i += kPickThreads) {
+                const int part = part_list[i >> shift], b = part >> kSegmentBits;
+                const int at = ((part & ((1 << kSegmentBits) - 1)) << shift) + (i & ((1 << shift) - 1));
+                if (at >= segments) continue;
+                const float z = segment[b * segments + at], s = z + offset[b];
+                if (s >= near && s > kNone) list(b << kSegmentBits | at, score(b, z));
+            }
+            __syncthreads();
+            if (tid == 0 && parts_listed > kListed) listed = kListed + 1;
+            __syncthreads();
+        }
+        return !exact;
+    };
+    const bool finite = list_best(coarse, each_item);
+    if (listed > kListed && coarse && finite) {   // the same for the workgroup
+        // too many segments in few parts, for instance those of the one beam that a search begins with
         __syncthreads();
+        start();
+        list_best(false, each_segment_sum);
     }
     if (listed > kListed) {   // the same for the workgroup
         const auto count = [&](auto f) {   // of items
             if (tid == 0) counted = 0;
             __syncthreads();
             int c = 0;
-            each_segment([&](const Place &p) { c += p.s != kNone && f(p); });
+            each_place([&](const Place &p) { c += p.s != kNone && f(p); });
 #pragma unroll
             for (int i = 1; i < 64; i *= 2) c += __shfl_xor(c, i);
             if (lane == 0) atomicAdd(&counted, c);
@@ -435,7 +492,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
         const double bound = key ? __longlong_as_double(static_cast<long long>(key >> 63 ? key & ~(uint64_t(1) << 63) : ~key)) : static_cast<double>(kNone);
         if (tid == 0) listed = 0;
         __syncthreads();
-        each_segment([&](const Place &p) {
+        each_place([&](const Place &p) {
             if (p.s > bound || (p.s == bound && p.id <= last)) list(p.id, p.s);
         });
         __syncthreads();
@@ -455,7 +512,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
     __syncthreads();
     const double least = taken == n ? bound_s : static_cast<double>(kNone);
     for (int i = tid; i < taken * kBeamSegment; i += kPickThreads) {
-        const int id = segment_id[i / kBeamSegment], b = id / segments, token = (id - b * segments) * kBeamSegment + i % kBeamSegment;
+        const int id = segment_id[i / kBeamSegment], b = id >> kSegmentBits, token = (id & ((1 << kSegmentBits) - 1)) * kBeamSegment + i % kBeamSegment;
         double s = kNone;
         int32_t at = token;
         if (ended[b]) {

@@ -91,6 +91,18 @@ def test_what_counts_lies_together(at):
     _check(z, scores, 100)
 
 
+@pytest.mark.parametrize("V", [1000, 32003, 70000])
+@pytest.mark.parametrize("keep", [1, 5, 16, 17, 64, 100, 128])
+def test_one_beam_with_a_score(V, keep):
+    """A search's first step: the other beams are at -inf."""
+    rng, z, scores = _random(3, 8, V, keep)
+    scores[:, 1:] = -np.inf
+    scores[1] = np.roll(scores[1], 5)
+    _check(z, scores, keep)
+    z[:, V // 2:] = -np.inf      # and half of the tokens are not allowed
+    _check(z, scores, keep)
+
+
 def test_few_values_many_ties():
     rng, _, _ = _random(1, 1, 1, 6)
     z, scores = rng.integers(0, 3, (8, 50000)), -np.array([[0.0, 0.3, 0.7, 1.1], [0.9, 0.2, 0.0, 0.1]])
