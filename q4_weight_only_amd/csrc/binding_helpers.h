@@ -160,13 +160,50 @@ PyObject *out_item(PyObject *out, Py_ssize_t n, Py_ssize_t i) {
     return PySequence_Fast_GET_ITEM(out, i);
 }
 
-// A new tuple of the tensors.
-PyObject *tuple_of(std::initializer_list<at::Tensor *> tensors) {
-    PyObject *t = PyTuple_New(static_cast<Py_ssize_t>(tensors.size()));
-    if (!t) throw python_error();
-    Py_ssize_t i = 0;
-    for (at::Tensor *x : tensors) PyTuple_SET_ITEM(t, i++, THPVariable_Wrap(std::move(*x)));
-    return t;
-}
+struct OutputOf {
+    const char *name;
+    at::DimVector shape;
+    at::ScalarType type;
+};
+
+// The results of a call: those that `out` (None, or N tensors or None) names, and the
+// others in one allocation, each from 256 bytes on.  (Six allocations are 2 us more of a
+// call of 5.)
+template <size_t N>
+struct Outputs {
+    at::Tensor t[N];
+    Outputs(PyObject *out, const OutputOf (&of)[N], c10::Device dev) {
+        size_t at[N], bytes = 0;
+        for (size_t i = 0; i < N; ++i) {
+            PyObject *given = out_item(out, N, static_cast<Py_ssize_t>(i));
+            if (given != Py_None) {
+                t[i] = output(given, of[i].name, of[i].shape, of[i].type, dev);
+                continue;
+            }
+            size_t n = c10::elementSize(of[i].type);
+            for (const int64_t d : of[i].shape) n *= static_cast<size_t>(d);
+            at[i] = bytes;
+            bytes += (n + 255) / 256 * 256;
+        }
+        if (!bytes) bytes = 256;   // all of the others are empty, or there are none
+        c10::Storage storage;
+        for (size_t i = 0; i < N; ++i) {
+            if (t[i].defined()) continue;
+            if (!storage) storage = at::detail::empty_cuda({static_cast<int64_t>(bytes)}, at::kByte, dev, std::nullopt).storage();
+            t[i] = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                            c10::scalarTypeToTypeMeta(of[i].type));
+            c10::TensorImpl *impl = t[i].unsafeGetTensorImpl();
+            impl->set_storage_offset(static_cast<int64_t>(at[i] / c10::elementSize(of[i].type)));
+            impl->set_sizes_contiguous(of[i].shape);
+        }
+    }
+    int32_t *ints(size_t i) const { return static_cast<int32_t *>(t[i].data_ptr()); }
+    PyObject *tuple() {
+        PyObject *all = PyTuple_New(N);
+        if (!all) throw python_error();
+        for (size_t i = 0; i < N; ++i) PyTuple_SET_ITEM(all, static_cast<Py_ssize_t>(i), THPVariable_Wrap(std::move(t[i])));
+        return all;
+    }
+};
 
 }  // namespace

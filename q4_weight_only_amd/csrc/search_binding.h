@@ -26,15 +26,13 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
     has_shape(done, "finished", scores.sizes());
     TORCH_CHECK_VALUE(keep >= 1 && keep <= 128, "keep must be 1 .. 128");
     TORCH_CHECK_VALUE(pad >= 0 && pad <= INT32_MAX, "pad must be a token");
-    at::Tensor parents = output(out_item(a[5], 3, 0), "parents", {groups, keep}, at::kInt, dev);
-    at::Tensor tokens = output(out_item(a[5], 3, 1), "tokens", {groups, keep}, at::kInt, dev);
-    at::Tensor best = output(out_item(a[5], 3, 2), "scores", {groups, keep}, at::kFloat, dev);
+    Outputs<3> out(a[5], {{"parents", {groups, keep}, at::kInt}, {"tokens", {groups, keep}, at::kInt}, {"scores", {groups, keep}, at::kFloat}}, dev);
     const c10::hip::HIPGuard guard(dev.index());
     const Workspace ws(a[6], static_cast<int64_t>(q4_beam_select_workspace(groups, beams, v)), dev);
-    check(q4_beam_select(src, groups, beams, v, base, ended, static_cast<int32_t>(pad), keep, parents.data_ptr<int32_t>(),
-                         tokens.data_ptr<int32_t>(), best.data_ptr<float>(), ws.data, ws.bytes, stream_of(dev)),
+    check(q4_beam_select(src, groups, beams, v, base, ended, static_cast<int32_t>(pad), keep, out.ints(0), out.ints(1),
+                         static_cast<float *>(out.t[2].data_ptr()), ws.data, ws.bytes, stream_of(dev)),
           "q4_beam_select");
-    return tuple_of({&parents, &tokens, &best});
+    return out.tuple();
     END_HANDLE_TH_ERRORS
 }
 
@@ -57,14 +55,12 @@ PyObject *beam_advance(PyObject *, PyObject *const *a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(!done || done->numel() == rows, "finished must have one value for each row of sequences");
     const int64_t eos = integer(a[5]), pad = integer(a[6]);
     TORCH_CHECK_VALUE(eos >= INT32_MIN && eos <= INT32_MAX && pad >= INT32_MIN && pad <= INT32_MAX, "eos and pad must be int32 values");
-    at::Tensor out = output(out_item(a[7], 3, 0), "sequences", {n_out, width}, at::kInt, dev);
-    at::Tensor out_len = output(out_item(a[7], 3, 1), "lengths", {n_out}, at::kInt, dev);
-    at::Tensor out_done = output(out_item(a[7], 3, 2), "finished", {n_out}, at::kInt, dev);
+    Outputs<3> out(a[7], {{"sequences", {n_out, width}, at::kInt}, {"lengths", {n_out}, at::kInt}, {"finished", {n_out}, at::kInt}}, dev);
     const c10::hip::HIPGuard guard(dev.index());
     check(q4_beam_advance(src, rows, width, len, ended, from, next, n_out, static_cast<int32_t>(eos), static_cast<int32_t>(pad),
-                          out.data_ptr<int32_t>(), out_len.data_ptr<int32_t>(), out_done.data_ptr<int32_t>(), stream_of(dev)),
+                          out.ints(0), out.ints(1), out.ints(2), stream_of(dev)),
           "q4_beam_advance");
-    return tuple_of({&out, &out_len, &out_done});
+    return out.tuple();
     END_HANDLE_TH_ERRORS
 }
 
@@ -107,19 +103,14 @@ PyObject *kv_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
         each = integer(a[4]);
     }
     const int32_t *held = held_of(a[5], num_blocks, t.dev);
-    at::Tensor table = output(out_item(a[6], 6, 0), "block_table", {n_out, t.width}, at::kInt, t.dev);
-    at::Tensor lengths = output(out_item(a[6], 6, 1), "lengths", {n_out}, at::kInt, t.dev);
-    at::Tensor refs = output(out_item(a[6], 6, 2), "refs", {num_blocks}, at::kInt, t.dev);
-    at::Tensor src = output(out_item(a[6], 6, 3), "src", {n_out}, at::kInt, t.dev);
-    at::Tensor dst = output(out_item(a[6], 6, 4), "dst", {n_out}, at::kInt, t.dev);
-    at::Tensor short_of = output(out_item(a[6], 6, 5), "short", {n_out}, at::kInt, t.dev);
+    Outputs<6> out(a[6], {{"block_table", {n_out, t.width}, at::kInt}, {"lengths", {n_out}, at::kInt}, {"refs", {num_blocks}, at::kInt},
+                          {"src", {n_out}, at::kInt}, {"dst", {n_out}, at::kInt}, {"short", {n_out}, at::kInt}}, t.dev);
     const c10::hip::HIPGuard guard(t.dev.index());
     const Workspace ws(a[7], static_cast<int64_t>(q4_kv_fork_workspace(n_out, num_blocks)), t.dev);
-    check(q4_kv_fork(t.table, t.rows, t.width, t.lengths, from, n_out, grow, each, held, num_blocks, table.data_ptr<int32_t>(),
-                     lengths.data_ptr<int32_t>(), refs.data_ptr<int32_t>(), src.data_ptr<int32_t>(), dst.data_ptr<int32_t>(),
-                     short_of.data_ptr<int32_t>(), ws.data, ws.bytes, stream_of(t.dev)),
+    check(q4_kv_fork(t.table, t.rows, t.width, t.lengths, from, n_out, grow, each, held, num_blocks, out.ints(0), out.ints(1),
+                     out.ints(2), out.ints(3), out.ints(4), out.ints(5), ws.data, ws.bytes, stream_of(t.dev)),
           "q4_kv_fork");
-    return tuple_of({&table, &lengths, &refs, &src, &dst, &short_of});
+    return out.tuple();
     END_HANDLE_TH_ERRORS
 }
 
@@ -132,16 +123,14 @@ PyObject *kv_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(num_blocks >= 1 && num_blocks <= 1 << 24, "num_blocks must be 1 .. 2^24");
     const int32_t *held = held_of(a[3], num_blocks, t.dev);
     const int64_t half = std::max<int64_t>(1, num_blocks / 2);
-    at::Tensor table = output(out_item(a[4], 4, 0), "block_table", {t.rows, t.width}, at::kInt, t.dev);
-    at::Tensor src = output(out_item(a[4], 4, 1), "src", {half}, at::kInt, t.dev);
-    at::Tensor dst = output(out_item(a[4], 4, 2), "dst", {half}, at::kInt, t.dev);
-    at::Tensor live = output(out_item(a[4], 4, 3), "live", {1}, at::kInt, t.dev);
+    Outputs<4> out(a[4], {{"block_table", {t.rows, t.width}, at::kInt}, {"src", {half}, at::kInt}, {"dst", {half}, at::kInt}, {"live", {1}, at::kInt}},
+                   t.dev);
     const c10::hip::HIPGuard guard(t.dev.index());
     const Workspace ws(a[5], static_cast<int64_t>(q4_kv_compact_workspace(num_blocks)), t.dev);
-    check(q4_kv_compact(t.table, t.rows, t.width, t.lengths, held, num_blocks, table.data_ptr<int32_t>(), src.data_ptr<int32_t>(),
-                        dst.data_ptr<int32_t>(), live.data_ptr<int32_t>(), ws.data, ws.bytes, stream_of(t.dev)),
+    check(q4_kv_compact(t.table, t.rows, t.width, t.lengths, held, num_blocks, out.ints(0), out.ints(1), out.ints(2), out.ints(3),
+                        ws.data, ws.bytes, stream_of(t.dev)),
           "q4_kv_compact");
-    return tuple_of({&table, &src, &dst, &live});
+    return out.tuple();
     END_HANDLE_TH_ERRORS
 }
 
