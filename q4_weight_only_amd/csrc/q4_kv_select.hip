@@ -354,27 +354,24 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
             __syncthreads();
             if (wave == 0) {   // from the last bin down, 16 a lane
                 constexpr int kOf = kBins / 64;
-                const int first = kBins - kOf * (lane + 1);
-                int mine[kOf], all = 0;
+                static_assert(kOf == 16, "a lane's bins are those of 16 lanes");
+                int all = 0;
 #pragma unroll
                 for (int i = 0; i < kOf; i += 4) {
-                    const i32x4 x = *reinterpret_cast<const i32x4 *>(&bins[first + i]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        mine[i + j] = x[j];
-                        all += x[j];
-                    }
+                    const i32x4 x = *reinterpret_cast<const i32x4 *>(&bins[kBins - kOf * (lane + 1) + i]);
+                    all += (x[0] + x[1]) + (x[2] + x[3]);
                 }
                 int32_t total;
-                int before = scan_wave(all, total);
-#pragma unroll
-                for (int i = kOf - 1; i >= 0; --i) {
-                    if (before < m && before + mine[i] >= m) {
-                        found[0] = first + i;
-                        found[1] = m - before;
-                        found[2] = mine[i];
-                    }
-                    before += mine[i];
+                const int before = scan_wave(all, total);
+                // the lane whose bins reach m, and of these, a lane each, the one that does
+                const int at = __builtin_ctzll(__ballot(before + all >= m)), last = kBins - 1 - kOf * at;
+                const int mine = lane < kOf ? bins[last - (lane & (kOf - 1))] : 0;
+                const int above = __builtin_amdgcn_readlane(before, at) + scan_wave(mine, total);
+                const int bin = __builtin_ctzll(__ballot(above + mine >= m));
+                if (lane == bin) {
+                    found[0] = last - lane;
+                    found[1] = m - above;
+                    found[2] = mine;
                 }
             }
             __syncthreads();
@@ -530,7 +527,7 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     if (e != hipSuccess) return e;
     const dim3 rows(a.kv.kv_heads, a.max_rows < 65535 ? a.max_rows : 65535, a.kv.batch);
     if (a.max_blocks <= 1024) hipLaunchKernelGGL((choose_kernel<256, 4, false>), rows, dim3(256), 0, s, a);
-    else if (a.max_blocks <= 4096) hipLaunchKernelGGL((choose_kernel<256, 16, false>), rows, dim3(256), 0, s, a);
+    else if (a.max_blocks <= 4096) hipLaunchKernelGGL((choose_kernel<512, 8, false>), rows, dim3(512), 0, s, a);
     else if (a.max_blocks <= 16384) hipLaunchKernelGGL((choose_kernel<1024, 16, false>), rows, dim3(1024), 0, s, a);
     else hipLaunchKernelGGL((choose_kernel<1024, 16, true>), rows, dim3(1024), 0, s, a);
     return hipGetLastError();

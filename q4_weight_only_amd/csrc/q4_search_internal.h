@@ -75,18 +75,19 @@ size_t attention_blocks_workspace(const AttentionArgs &a, int keep, int head_dim
 hipError_t launch_kv_attention_blocks(const AttentionArgs &a, const int32_t *chosen, int keep, int head_dim, hipStream_t s);
 
 #ifdef __HIPCC__
-// Sum over the lanes before this one, and over all.
+// Sum over the lanes before this one, and over all: within 16 lanes by shifts, then the last lane
+// of 16 to the next 16, and of 32 to the next 32.
 template <typename T>
 __device__ __forceinline__ T scan_wave(T v, T &total) {
-    const int lane = threadIdx.x & 63;
-    T sum = v;
-#pragma unroll
-    for (int i = 1; i < 64; i *= 2) {
-        const T below = __shfl_up(sum, i);
-        if (lane >= i) sum += below;
-    }
-    total = __shfl(sum, 63);
-    return sum - v;
+    int sum = static_cast<int>(v);
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x111, 0xF, 0xF, true);    // row_shr:1
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x112, 0xF, 0xF, true);
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x114, 0xF, 0xF, true);
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x118, 0xF, 0xF, true);
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+    sum += __builtin_amdgcn_update_dpp(0, sum, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
+    total = static_cast<T>(__builtin_amdgcn_readlane(sum, 63));
+    return static_cast<T>(sum) - v;
 }
 
 // The same over a workgroup of WAVES waves.  `sums` may be used again after the
