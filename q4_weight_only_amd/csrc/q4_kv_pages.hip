@@ -182,7 +182,8 @@ __global__ __launch_bounds__(256) void fork_clear_kernel(ForkArgs a, ForkSpace w
 
 // A thread has a column of kForkRows new table rows: the entries are copied and
 // counted, those of neighbours that name one block at once.  (262144 entries of 64
-// rows, four and more of which share most blocks: 13.4 us with an atomic for each.)
+// rows, four and more of which share most blocks: 6.7 us, with an atomic for each 13.4.
+// The atomics bound it.)
 constexpr int kForkRows = 8;
 
 __global__ __launch_bounds__(256) void fork_gather_kernel(ForkArgs a, ForkSpace w) {
@@ -239,8 +240,8 @@ __global__ __launch_bounds__(kHandThreads) void fork_hand_kernel(ForkArgs a, For
 
 // All of it in one workgroup, where the tables and the pool are small: the counts are
 // in LDS, and who goes on in the same block is found by looking at all.  4 tables of 8
-// entries and a pool of 100 blocks: 6.3 us, as three kernels 10.5; 64 of 60 and 8000
-// blocks 8.6 and 13.0; at the border, 256 of 64 and 8000, both take 13.3.
+// entries and a pool of 100 blocks: 5.4 us, as three kernels 9.5; 64 of 60 and 8000
+// blocks 7.8 and 12.5; at the border, 256 of 64 and 8000, both take 12.7.
 constexpr int kOneRows = 256, kOneBlocks = 8192, kOneAhead = 8;
 constexpr int64_t kOneEntries = 16384;
 
@@ -447,9 +448,10 @@ __global__ __launch_bounds__(256) void compact_table_kernel(CompactArgs a, Compa
 // counts are not much to read for one workgroup: each marks the blocks in bits of its own,
 // from all tables, and with the counts before each word of these has the place of every block
 // that moves; the results are shared out.  40 tables of 60 entries and a pool of 4096
-// blocks: 6.1 us, with the five kernels above 14.0; 16000 entries and 16000 held counts
-// 10.6 and 15.2; at the border, 48000 entries, 15.0 and 15.3 (with 60000 held counts
-// besides 27 and 15.8).
+// blocks: 5.6 us, with the five kernels above 12.7; 8000 entries and 16000 held counts
+// 10.2 and 13.9; at the border, 48000 entries, 14.2 and 13.8 (with 60000 held counts
+// besides 26 and 14.4).  What bounds it then is what one compute unit reads, some 20
+// bytes a cycle.
 constexpr int kMapThreads = 1024, kMapBlocks = 65536, kMapWords = kMapBlocks / 32, kMapRows = 1024, kMapAhead = 8;
 constexpr int64_t kMapReads = 49152;
 
@@ -555,7 +557,7 @@ __global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a)
 // reads their ids at once and copies the piece of those that there are.  The stores
 // are not to stay in the L2: copies of 70 MB took 23.3 us with that hint and 32.1
 // without, and 85 blocks of 4 layers with the attention that reads them right behind
-// 174.8 and 188.6.
+// 174.8 and 188.6.  What bounds it is memory: 70 MB read and 70 MB written, 6 TB/s.
 constexpr int kPiece = 4096;
 
 __global__ __launch_bounds__(256) void copy_kernel(CopyArgs a, int pieces, int pairs_each) {
@@ -645,6 +647,7 @@ hipError_t launch_kv_compact(const CompactArgs &a, hipStream_t s) {
 hipError_t launch_kv_copy(const CopyArgs &a, hipStream_t s) {
     const int pieces = a.kv_heads * 2 * kKvBlock * a.head_dim / kPiece;
     // a wave for each piece while there is room for that many, then up to 64 pairs a wave
+    // (70 MB of copies 23.5 us, with 8192 waves 28.6, with four times as many as here 23.5)
     const int64_t all = static_cast<int64_t>(a.n) * pieces * a.layers;
     int64_t each = all / 32768;
     each = each < 1 ? 1 : each > 64 ? 64 : each;

@@ -57,7 +57,7 @@ __device__ __forceinline__ int place_of_lane(int lane) { return lane & 15; }   /
 // dimensions, l / 16, of one token, l % 16; after four steps over 16 lanes, in each of
 // which a lane hands on half of what it has, it has one dimension of all tokens.  (All
 // 16 dimensions in every lane: 7.5 us for one token of each of 8 heads, which is
-// the time that its code takes to arrive.)
+// the time that its code takes to arrive; so it is 2.6, the launch and three waits.)
 template <int D>
 __global__ __launch_bounds__(256) void summarize_kernel(SelectArgs a) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -136,7 +136,8 @@ struct ScorePlan {
 // registers: lane l has 16 bytes at 16 (l / 16) of each 64 of block l % 16.  They are on
 // their way while the rows' sums are formed.
 //
-// What bounds it is memory.  A block's exponents of all heads are in one line, so
+// What bounds it is memory: 31 sequences of up to 2047 blocks and 8 heads, 84 MB of bounds
+// and exponents, in 19.2 us or 4.4 TB/s.  A block's exponents of all heads are in one line, so
 // a unit's heads are given to one of the 8 dies, one after the other.
 template <int D>
 __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, ScorePlan plan) {
@@ -254,8 +255,9 @@ constexpr int kBins = 1024, kBinListed = 256;   // kBinListed: scores of a bin t
 // times four scores next to each other, THREADS * 4 apart.  LOOP: more scores than
 // the workgroup's registers hold, read each time.
 //
-// What bounds it is one step after the other: lengths, scores, six barriers.  (Two bits
-// at a time alone, some ten counts with a barrier each: 9.8 us for 4096 blocks.)
+// What bounds it is one step after the other: lengths, scores, six barriers.  1024 blocks
+// 4.7 us, 4096 6.2.  (Two bits at a time alone, some ten counts with a barrier each: 9.8 us
+// for 4096 blocks.)
 template <int THREADS, int EACH, bool LOOP>
 __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
     constexpr int WAVES = THREADS / 64, kHeld = THREADS * EACH, SETS = EACH / 4;
@@ -526,6 +528,8 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 rows(a.kv.kv_heads, a.max_rows < 65535 ? a.max_rows : 65535, a.kv.batch);
+    // the fewest waves whose registers hold the scores, 8 a thread while there are threads (both kernels: 61 rows of
+    // 938 blocks 10.3 us, with 512 threads 12.0; 2 of 4096 13.3, with 256 threads 15.2, with 1024 of 16 scores 19.2)
     if (a.max_blocks <= 1024) hipLaunchKernelGGL((choose_kernel<256, 4, false>), rows, dim3(256), 0, s, a);
     else if (a.max_blocks <= 4096) hipLaunchKernelGGL((choose_kernel<512, 8, false>), rows, dim3(512), 0, s, a);
     else if (a.max_blocks <= 16384) hipLaunchKernelGGL((choose_kernel<1024, 16, false>), rows, dim3(1024), 0, s, a);
