@@ -58,6 +58,8 @@ class Decoder:
                 keep=0):
         """Logits [rows or len(last), vocab] of the rows `ids`; `last`: the rows whose logits are wanted.
         summaries: kv_summary's of the caches, which are kept up to date; keep: read that many blocks alone."""
+        if keep and (self.window or summaries is None):
+            raise ValueError("attention over selected blocks needs summaries, and has no window")
         shape = dict(max_rows=max_rows, max_length=max_length)
         r = q4.embed_gguf(self.blocks, self.vocab, self.dim, ids)
         y = None

@@ -5,6 +5,10 @@ that a score selects.
 The computation runs in the HIP library on the current stream of the tensors'
 device; the calls go through the native binding, which checks the tensors and
 makes the outputs.  A missing build raises.
+
+`out` gives tensors for the results, which must not overlap what the call reads;
+None, or None in a place of the tuple, makes new ones.  New results of one call are
+in one allocation, which lives as long as any of them.
 """
 
 from __future__ import annotations
@@ -195,7 +199,13 @@ def kv_copy_blocks(caches, src: torch.Tensor, dst: torch.Tensor, *, summaries=No
             raise ValueError("the caches must have one shape")
         data = [c.data for c in caches]
     if isinstance(summaries, torch.Tensor):
-        summaries = summaries.flatten(1) if isinstance(data, torch.Tensor) else [summaries]
+        if not isinstance(data, torch.Tensor):
+            summaries = [summaries]
+        else:
+            try:
+                summaries = summaries.view(summaries.shape[0], -1)   # a copy would be written in its place
+            except RuntimeError:
+                raise ValueError("a layer's summary must be in one piece") from None
     (D._native or D._load()).kv_copy_blocks(data, first.num_blocks, first.kv_heads, first.head_dim, src, dst, summaries)
 
 

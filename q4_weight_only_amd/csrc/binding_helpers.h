@@ -160,6 +160,13 @@ PyObject *out_item(PyObject *out, Py_ssize_t n, Py_ssize_t i) {
     return PySequence_Fast_GET_ITEM(out, i);
 }
 
+// An output of the caller must not share memory with what the call reads, nor with another output.
+void apart(const at::Tensor &out, const char *name, const at::Tensor *other) {
+    if (!other || !other->defined()) return;
+    const char *a = static_cast<const char *>(out.data_ptr()), *b = static_cast<const char *>(other->data_ptr());
+    TORCH_CHECK_VALUE(a + out.nbytes() <= b || b + other->nbytes() <= a, name, " must not overlap the call's inputs or other outputs");
+}
+
 struct OutputOf {
     const char *name;
     at::DimVector shape;
@@ -172,12 +179,15 @@ struct OutputOf {
 template <size_t N>
 struct Outputs {
     at::Tensor t[N];
-    Outputs(PyObject *out, const OutputOf (&of)[N], c10::Device dev) {
+    Outputs(PyObject *out, const OutputOf (&of)[N], std::initializer_list<const at::Tensor *> inputs, c10::Device dev) {
         size_t at[N], bytes = 0;
         for (size_t i = 0; i < N; ++i) {
             PyObject *given = out_item(out, N, static_cast<Py_ssize_t>(i));
             if (given != Py_None) {
-                t[i] = output(given, of[i].name, of[i].shape, of[i].type, dev);
+                const at::Tensor x = output(given, of[i].name, of[i].shape, of[i].type, dev);
+                for (const at::Tensor *y : inputs) apart(x, of[i].name, y);
+                for (size_t k = 0; k < i; ++k) apart(x, of[i].name, &t[k]);
+                t[i] = x;
                 continue;
             }
             size_t n = c10::elementSize(of[i].type);

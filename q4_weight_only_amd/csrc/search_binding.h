@@ -26,7 +26,8 @@ PyObject *beam_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
     has_shape(done, "finished", scores.sizes());
     TORCH_CHECK_VALUE(keep >= 1 && keep <= 128, "keep must be 1 .. 128");
     TORCH_CHECK_VALUE(pad >= 0 && pad <= INT32_MAX, "pad must be a token");
-    Outputs<3> out(a[5], {{"parents", {groups, keep}, at::kInt}, {"tokens", {groups, keep}, at::kInt}, {"scores", {groups, keep}, at::kFloat}}, dev);
+    Outputs<3> out(a[5], {{"parents", {groups, keep}, at::kInt}, {"tokens", {groups, keep}, at::kInt}, {"scores", {groups, keep}, at::kFloat}},
+                   {&z, &scores, done}, dev);
     const c10::hip::HIPGuard guard(dev.index());
     const Workspace ws(a[6], static_cast<int64_t>(q4_beam_select_workspace(groups, beams, v)), dev);
     check(q4_beam_select(src, groups, beams, v, base, ended, static_cast<int32_t>(pad), keep, out.ints(0), out.ints(1),
@@ -55,7 +56,8 @@ PyObject *beam_advance(PyObject *, PyObject *const *a, Py_ssize_t n) {
     TORCH_CHECK_VALUE(!done || done->numel() == rows, "finished must have one value for each row of sequences");
     const int64_t eos = integer(a[5]), pad = integer(a[6]);
     TORCH_CHECK_VALUE(eos >= INT32_MIN && eos <= INT32_MAX && pad >= INT32_MIN && pad <= INT32_MAX, "eos and pad must be int32 values");
-    Outputs<3> out(a[7], {{"sequences", {n_out, width}, at::kInt}, {"lengths", {n_out}, at::kInt}, {"finished", {n_out}, at::kInt}}, dev);
+    Outputs<3> out(a[7], {{"sequences", {n_out, width}, at::kInt}, {"lengths", {n_out}, at::kInt}, {"finished", {n_out}, at::kInt}},
+                   {&seq, &lengths, &parents, &tokens, done}, dev);
     const c10::hip::HIPGuard guard(dev.index());
     check(q4_beam_advance(src, rows, width, len, ended, from, next, n_out, static_cast<int32_t>(eos), static_cast<int32_t>(pad),
                           out.ints(0), out.ints(1), out.ints(2), stream_of(dev)),
@@ -66,6 +68,7 @@ PyObject *beam_advance(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // A block table and its lengths.
 struct Tables {
+    const at::Tensor *t, *l;
     const int32_t *table, *lengths;
     int64_t rows, width;
     c10::Device dev;
@@ -74,12 +77,11 @@ Tables tables_of(PyObject *table, PyObject *lengths) {
     const at::Tensor &t = required(table, "block_table"), &l = required(lengths, "lengths");
     const c10::Device dev = device_of(t, "block_table");
     TORCH_CHECK_VALUE(t.dim() == 2 && l.dim() == 1 && t.size(0) == l.size(0), "block_table must be [batch, width] and lengths [batch]");
-    return {address<int32_t>(&t, "block_table", at::kInt, dev), address<int32_t>(&l, "lengths", at::kInt, dev), t.size(0), t.size(1), dev};
+    return {&t, &l, address<int32_t>(&t, "block_table", at::kInt, dev), address<int32_t>(&l, "lengths", at::kInt, dev), t.size(0), t.size(1), dev};
 }
 
 // `held`, one count for each block.
-const int32_t *held_of(PyObject *o, int64_t num_blocks, c10::Device dev) {
-    const at::Tensor *held = optional(o, "held");
+const int32_t *held_of(const at::Tensor *held, int64_t num_blocks, c10::Device dev) {
     has_shape(held, "held", {num_blocks});
     return address<int32_t>(held, "held", at::kInt, dev);
 }
@@ -94,17 +96,20 @@ PyObject *kv_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t n_out = parents.numel(), num_blocks = integer(a[3]);
     TORCH_CHECK_VALUE(num_blocks >= 1 && num_blocks <= 1 << 24, "num_blocks must be 1 .. 2^24");
     const int32_t *grow = nullptr;
+    const at::Tensor *more = nullptr;
     int64_t each = 0;
     if (THPVariable_Check(a[4])) {
-        const at::Tensor &g = THPVariable_Unpack(a[4]);
-        grow = address<int32_t>(&g, "grow", at::kInt, t.dev);
-        TORCH_CHECK_VALUE(g.numel() == n_out, "grow must have as many values as parents");
+        more = &THPVariable_Unpack(a[4]);
+        grow = address<int32_t>(more, "grow", at::kInt, t.dev);
+        TORCH_CHECK_VALUE(more->numel() == n_out, "grow must have as many values as parents");
     } else {
         each = integer(a[4]);
     }
-    const int32_t *held = held_of(a[5], num_blocks, t.dev);
+    const at::Tensor *others = optional(a[5], "held");
+    const int32_t *held = held_of(others, num_blocks, t.dev);
     Outputs<6> out(a[6], {{"block_table", {n_out, t.width}, at::kInt}, {"lengths", {n_out}, at::kInt}, {"refs", {num_blocks}, at::kInt},
-                          {"src", {n_out}, at::kInt}, {"dst", {n_out}, at::kInt}, {"short", {n_out}, at::kInt}}, t.dev);
+                          {"src", {n_out}, at::kInt}, {"dst", {n_out}, at::kInt}, {"short", {n_out}, at::kInt}},
+                   {t.t, t.l, &parents, more, others}, t.dev);
     const c10::hip::HIPGuard guard(t.dev.index());
     const Workspace ws(a[7], static_cast<int64_t>(q4_kv_fork_workspace(n_out, num_blocks)), t.dev);
     check(q4_kv_fork(t.table, t.rows, t.width, t.lengths, from, n_out, grow, each, held, num_blocks, out.ints(0), out.ints(1),
@@ -121,10 +126,11 @@ PyObject *kv_compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const Tables t = tables_of(a[0], a[1]);
     const int64_t num_blocks = integer(a[2]);
     TORCH_CHECK_VALUE(num_blocks >= 1 && num_blocks <= 1 << 24, "num_blocks must be 1 .. 2^24");
-    const int32_t *held = held_of(a[3], num_blocks, t.dev);
+    const at::Tensor *others = optional(a[3], "held");
+    const int32_t *held = held_of(others, num_blocks, t.dev);
     const int64_t half = std::max<int64_t>(1, num_blocks / 2);
     Outputs<4> out(a[4], {{"block_table", {t.rows, t.width}, at::kInt}, {"src", {half}, at::kInt}, {"dst", {half}, at::kInt}, {"live", {1}, at::kInt}},
-                   t.dev);
+                   {t.t, t.l, others}, t.dev);
     const c10::hip::HIPGuard guard(t.dev.index());
     const Workspace ws(a[5], static_cast<int64_t>(q4_kv_compact_workspace(num_blocks)), t.dev);
     check(q4_kv_compact(t.table, t.rows, t.width, t.lengths, held, num_blocks, out.ints(0), out.ints(1), out.ints(2), out.ints(3),
@@ -221,6 +227,7 @@ PyObject *kv_select(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t keep = integer(a[11]), first = integer(a[12]), recent = integer(a[13]);
     TORCH_CHECK_VALUE(keep >= 1 && keep <= 1 << 16, "keep must be 1 .. 65536");
     at::Tensor out = output(a[14], "out", {q.size(0), c.kv_heads, keep}, at::kInt, dev);
+    if (a[14] != Py_None) apart(out, "out", &q);
     const c10::hip::HIPGuard guard(dev.index());
     const Workspace ws(a[15], static_cast<int64_t>(q4_kv_select_workspace(&c, &b)), dev);
     check(q4_kv_select(&c, &b, summary, src, q.size(1) / c.head_dim, keep, first, recent, out.data_ptr<int32_t>(), ws.data, ws.bytes,
@@ -249,6 +256,10 @@ PyObject *kv_attention_blocks(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const at::ScalarType type = dtype_of(a[13]);
     const int out_code = type_code(type, "dtype");
     at::Tensor out = output(a[12], "out", q.sizes(), type, dev);
+    if (a[12] != Py_None) {
+        apart(out, "out", &q);
+        apart(out, "out", &chosen);
+    }
     const c10::hip::HIPGuard guard(dev.index());
     const Workspace ws(a[14], static_cast<int64_t>(q4_kv_attention_blocks_workspace(&c, &b, heads, keep)), dev);
     check(q4_kv_attention_blocks(&c, &b, src, heads, list, keep, scale, out.data_ptr(), out_code, ws.data, ws.bytes, stream_of(dev)),

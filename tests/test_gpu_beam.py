@@ -206,3 +206,17 @@ def test_scores_as_large_as_numbers_get():
     rng = np.random.default_rng(9)
     z = rng.standard_normal((4, 700)) * 1e38
     _check(z, scores, 7, finished=np.array([[0, 1], [0, 0]]))
+
+
+def test_outputs_that_overlap_are_refused():
+    z, s, i = torch.zeros((6, 10), device=DEV), torch.zeros((2, 3), device=DEV), torch.zeros((2, 3), dtype=torch.int32, device=DEV)
+    j, seq = torch.zeros((2, 3), dtype=torch.int32, device=DEV), torch.zeros((4, 8), dtype=torch.int32, device=DEV)
+    n, p = torch.zeros(4, dtype=torch.int32, device=DEV), torch.zeros(4, dtype=torch.int32, device=DEV)
+    for bad in (lambda: q4.beam_select(z, s, 3, out=(None, None, s)), lambda: q4.beam_select(z, s, 3, out=(i, i, None)),
+                lambda: q4.beam_select(z, s, 3, finished=i, out=(None, i, None)),
+                lambda: q4.beam_advance(seq, n, p, p, out=(seq, None, None)), lambda: q4.beam_advance(seq, n, p, p, out=(None, n, None)),
+                lambda: q4.beam_advance(seq, n, p, p, out=(None, None, p))):
+        with pytest.raises(ValueError, match="overlap"):
+            bad()
+    got = q4.beam_select(z, s, 3, out=(i, j, None))
+    assert got[0].data_ptr() == i.data_ptr() and got[1].data_ptr() == j.data_ptr()

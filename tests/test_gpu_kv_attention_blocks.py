@@ -210,3 +210,22 @@ def test_refusals():
                 lambda: q4.kv_attention_blocks(q, c, l, t, n, out=torch.empty((1, 128), dtype=torch.bfloat16, device=DEV))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_outputs_that_overlap_are_refused():
+    c = q4.KVCache.empty(5, 2, 64)
+    t, n = torch.zeros((1, 4), dtype=torch.int32, device=DEV), torch.ones(1, dtype=torch.int32, device=DEV)
+    q, l = torch.zeros((1, 256), dtype=torch.bfloat16, device=DEV), torch.zeros((1, 2, 3), dtype=torch.int32, device=DEV)
+    for bad in (lambda: q4.kv_attention_blocks(q, c, l, t, n, out=q),
+                lambda: q4.kv_select(q, c, q4.kv_summary(c), t, n, keep=3, out=q.view(torch.int32)[:, :6].view(1, 2, 3))):
+        with pytest.raises(ValueError, match="overlap"):
+            bad()
+
+
+def test_the_example_has_no_window_over_selected_blocks():
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import decode
+    with pytest.raises(ValueError, match="window"):
+        decode.beam_search(decode.Decoder(vocab=64, window=40), [[1, 2, 3]], 4, beams=2, keep=4)

@@ -259,3 +259,64 @@ def test_refusals():
     with pytest.raises(IndexError):
         stack[2]
     assert len(stack) == 2 and len(list(stack)) == 2 and torch.equal(stack[1].data, stack.data[1, :stack[1].data.numel()])
+
+
+def test_outputs_that_overlap_are_refused():
+    t, n, p = _i32(np.zeros((3, 4))), _i32([0, 0, 0]), _i32([0, 1, 2])
+    f = q4.kv_fork(t, n, p, 5)
+    c = q4.kv_compact(t, n, 5)
+    flat = _i32(np.zeros(20))
+    for bad in (lambda: q4.kv_fork(t, n, p, 5, out=f._replace(block_table=t)), lambda: q4.kv_fork(t, n, p, 5, out=f._replace(lengths=n)),
+                lambda: q4.kv_fork(t, n, p, 5, out=f._replace(src=p)), lambda: q4.kv_fork(t, n, p, 5, out=f._replace(src=f.dst)),
+                lambda: q4.kv_fork(t, n, flat[:3], 5, out=f._replace(dst=flat[2:5])),
+                lambda: q4.kv_fork(t, n, p, 5, grow=f.dst, out=f), lambda: q4.kv_fork(t, n, p, 5, held=f.refs, out=f),
+                lambda: q4.kv_compact(t, n, 5, out=c._replace(block_table=t)), lambda: q4.kv_compact(t, n, 5, out=c._replace(src=c.dst)),
+                lambda: q4.kv_compact(t, n, 5, held=flat[:5], out=c._replace(live=flat[4:5]))):
+        with pytest.raises(ValueError, match="overlap"):
+            bad()
+    # next to each other, and parts of what an earlier call returned
+    g = q4.kv_fork(t, n, flat[:3], 5, out=(None, None, None, flat[3:6], flat[6:9], None))
+    h = q4.kv_fork(f.block_table, f.lengths, p, 5, out=q4.kv_fork(t, n, p, 5))
+    assert g.src.data_ptr() == flat[3:6].data_ptr() and h.block_table.shape == (3, 4)
+
+
+def test_a_summary_that_is_not_in_one_piece_is_refused():
+    """(A copy of it would be written instead.)"""
+    stack = q4.KVStack.empty(2, 6, 2, 64)
+    wide = torch.zeros((2, 6, 2, 2, 128), dtype=torch.int8, device=DEV)
+    p = _i32([0])
+    for bad in (wide[..., :64], wide[..., ::2], torch.zeros(2, dtype=torch.int8, device=DEV)):
+        with pytest.raises(ValueError):
+            q4.kv_copy_blocks(stack, p, p + 1, summaries=bad)
+    padded = torch.arange(2 * 3200, device=DEV).to(torch.int8).view(2, 3200)[:, :6 * 256]
+    before = padded.clone().view(2, 6, 256)
+    q4.kv_copy_blocks(stack, p, p + 1, summaries=padded)
+    after = padded.reshape(2, 6, 256)
+    assert torch.equal(after[:, 1], before[:, 0]) and torch.equal(after[:, 2:], before[:, 2:]) and torch.equal(after[:, 0], before[:, 0])
+
+
+@pytest.mark.parametrize("rows,width,blocks", [(4, 6, 64), (40, 20, 9000), (300, 8, 900), (60, 900, 70000)])
+def test_graph_replays_follow_their_inputs(rows, width, blocks):
+    """The forms for small and for large tables, replayed over other tables, with eager calls in between."""
+    rng = np.random.default_rng(rows)
+    say("graph", rows, width, blocks)
+    sets = []
+    for _ in range(3):
+        table, lengths = _tables(rng, rows, width, blocks)
+        sets.append((_i32(table), _i32(lengths), _i32(rng.integers(-1, rows, rows))))
+    held = _i32((rng.random(blocks) < 0.2).astype(int))
+    t, n, p = (x.clone() for x in sets[0])
+    q4.kv_fork(t, n, p, blocks, held=held), q4.kv_compact(t, n, blocks, held=held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        f = q4.kv_fork(t, n, p, blocks, held=held)
+        c = q4.kv_compact(f.block_table, f.lengths, blocks, held=held)
+    for i in (1, 2, 0, 1):
+        for x, y in zip((t, n, p), sets[i]):
+            x.copy_(y)
+        graph.replay()
+        wf = q4.kv_fork(*sets[i], blocks, held=held)
+        wc = q4.kv_compact(wf.block_table, wf.lengths, blocks, held=held)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(f, wf)) and all(torch.equal(x, y) for x, y in zip(c, wc))
