@@ -444,57 +444,115 @@ __global__ __launch_bounds__(256) void compact_table_kernel(CompactArgs a, Compa
     }
 }
 
-// All of it in one launch, where a bit for each block fits LDS and the tables and
-// counts are not much to read for one workgroup: each marks the blocks in bits of its own,
-// from all tables, and with the counts before each word of these has the place of every block
-// that moves; the results are shared out.  40 tables of 60 entries and a pool of 4096
-// blocks: 5.6 us, with the five kernels above 12.7; 8000 entries and 16000 held counts
-// 10.2 and 13.9; at the border, 48000 entries, 14.2 and 13.8 (with 60000 held counts
-// besides 26 and 14.4).  What bounds it then is what one compute unit reads, some 20
-// bytes a cycle.
+// Where a bit for each block fits LDS: each workgroup has all of them, and with the
+// counts before each word the place of every block that moves; the results are shared
+// out.  Where tables and counts are not much to read for one workgroup, each makes the
+// bits of its own, from all of them, in one launch (MARKED = false); otherwise
+// compact_bits_kernel makes them, a workgroup from a slice of the entries, and what is left is
+// to join the slices' bits.  With one launch, two, and the five kernels above: 40 tables of 60
+// entries and 4096 blocks 5.1, 7.9 and 12.7 us; 19200 entries of 20000 blocks 8.2, 9.1 and 13.3; 8000 entries
+// and 16000 held counts 9.3, 8.5 and 14.0; 48000 and 60000 25.3, 11.3 and 14.6; 256000 and 65536
+// 57, 12.8 and 13.2; 512000 and 65536 96, 16.4 and 14.5.  What bounds them is one step after the other, and
+// what a compute unit reads, some 20 bytes a cycle.
 constexpr int kMapThreads = 1024, kMapBlocks = 65536, kMapWords = kMapBlocks / 32, kMapRows = 1024, kMapAhead = 8;
-constexpr int64_t kMapReads = 49152;
+constexpr int64_t kMapReads = 24576, kMapEntries = 1 << 18;
+constexpr int kMostSlices = 16, kSliceReads = 4096;
 
-__global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a) {
+struct CompactBits {
+    uint32_t *named;   // [slices][words]
+    uint32_t *held;    // [words]
+    int32_t slices;
+};
+
+__device__ __forceinline__ int entry_row(int e, float per) {   // per: 1 / width; up to 2^18 entries: off by far less than 1/2 of one
+    return static_cast<int>((e + 0.5f) * per);
+}
+__device__ __forceinline__ void map_rows(const CompactArgs &a, int32_t *have) {
+    for (int i = threadIdx.x; i < a.rows; i += kMapThreads) have[i] = (held_to(a.lengths[i], 0, a.width * kKvBlock) + kKvBlock - 1) / kKvBlock;
+}
+// Bits of the blocks that the entries [begin, end) of the tables name, by one workgroup.
+__device__ __forceinline__ void map_entries(const CompactArgs &a, const int32_t *have, uint32_t *named, int begin, int end) {
+    const float per = 1.0f / a.width;
+    for (int e0 = begin + threadIdx.x; e0 < end; e0 += kMapThreads * kMapAhead) {
+        int32_t id[kMapAhead];
+#pragma unroll
+        for (int k = 0; k < kMapAhead; ++k) id[k] = e0 + kMapThreads * k < end ? a.table[e0 + kMapThreads * k] : -1;
+#pragma unroll
+        for (int k = 0; k < kMapAhead; ++k) {
+            const int e = e0 + kMapThreads * k < end ? e0 + kMapThreads * k : begin, i = entry_row(e, per);
+            if (id[k] >= 0 && id[k] < a.num_blocks && e - i * a.width < have[i]) atomicOr(&named[id[k] >> 5], 1u << (id[k] & 31));
+        }
+    }
+}
+// For the words [begin, end), what `held` says of their 32 blocks.  (A wave has 64 blocks: its ballot is their two words.)
+template <typename F>
+__device__ __forceinline__ void map_held(const CompactArgs &a, int begin, int end, F f) {
+    const int tid = threadIdx.x;
+    for (int b0 = begin * 32 + tid; b0 < end * 32; b0 += kMapThreads * kMapAhead) {
+        int32_t held[kMapAhead];
+#pragma unroll
+        for (int k = 0; k < kMapAhead; ++k) {
+            const int b = b0 + kMapThreads * k;
+            held[k] = a.held && b < a.num_blocks && b < end * 32 ? a.held[b] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kMapAhead; ++k) {
+            const int b = b0 + kMapThreads * k;
+            const uint32_t word = static_cast<uint32_t>(__ballot(held[k] > 0) >> (tid & 32));
+            if ((tid & 31) == 0 && b < end * 32) f(b >> 5, word);
+        }
+    }
+}
+
+__global__ __launch_bounds__(kMapThreads) void compact_bits_kernel(CompactArgs a, CompactBits w) {
+    __shared__ uint32_t named[kMapWords];
+    __shared__ int32_t have[kMapRows];
+    const int tid = threadIdx.x, slice = blockIdx.x;
+    const int words = (a.num_blocks + 31) / 32, entries = a.rows * a.width;
+    for (int i = tid; i < words; i += kMapThreads) named[i] = 0;
+    map_rows(a, have);
+    __syncthreads();
+    const int each = (entries + w.slices - 1) / w.slices, begin = slice * each;
+    map_entries(a, have, named, begin, begin + each < entries ? begin + each : entries);
+    const int words_each = (words + w.slices - 1) / w.slices, first = slice * words_each;
+    map_held(a, first, first + words_each < words ? first + words_each : words, [&](int i, uint32_t word) { w.held[i] = word; });
+    __syncthreads();
+    for (int i = tid; i < words; i += kMapThreads) w.named[slice * words + i] = named[i];
+}
+
+template <bool MARKED>
+__global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a, CompactBits w) {
     __shared__ uint32_t live[kMapWords], movable[kMapWords];   // a bit for each block
     __shared__ int32_t live_before[kMapWords], moves_before[kMapWords];
+    __shared__ int32_t free_from[kMapWords + 1];   // the words with the free blocks of rank 0, 32, 64 ..
     __shared__ int32_t have[kMapRows];
     __shared__ uint32_t sums[2][kMapThreads / 64];
     const int tid = threadIdx.x, first = blockIdx.x * kMapThreads + tid, step = gridDim.x * kMapThreads;
     const int words = (a.num_blocks + 31) / 32, entries = a.rows * a.width;
-    const float per = 1.0f / a.width;   // up to 2^16 entries: (e + 1/2) / width is off by far less than 1/2 of one
-    const auto row_of = [&](int e) { return static_cast<int>((e + 0.5f) * per); };
-    for (int i = tid; i < words; i += kMapThreads) live[i] = 0;
-    for (int i = tid; i < a.rows; i += kMapThreads) have[i] = (held_to(a.lengths[i], 0, a.width * kKvBlock) + kKvBlock - 1) / kKvBlock;
-    __syncthreads();
-    for (int e0 = tid; e0 < entries; e0 += kMapThreads * kMapAhead) {
-        int32_t id[kMapAhead];
+    const float per = 1.0f / a.width;
+    map_rows(a, have);
+    if constexpr (MARKED) {
+        for (int i = tid; i < words; i += kMapThreads) {
+            uint32_t named = 0;
+            const uint32_t held = w.held[i];
 #pragma unroll
-        for (int k = 0; k < kMapAhead; ++k) id[k] = e0 + kMapThreads * k < entries ? a.table[e0 + kMapThreads * k] : -1;
-#pragma unroll
-        for (int k = 0; k < kMapAhead; ++k) {
-            const int e = e0 + kMapThreads * k < entries ? e0 + kMapThreads * k : 0, i = row_of(e);
-            if (id[k] >= 0 && id[k] < a.num_blocks && e - i * a.width < have[i]) atomicOr(&live[id[k] >> 5], 1u << (id[k] & 31));
-        }
-    }
-    __syncthreads();
-    if (a.held) {   // a wave has 64 blocks: its ballot is their two words
-        for (int b0 = tid; b0 < words * 32; b0 += kMapThreads * kMapAhead) {
-            int32_t held[kMapAhead];
-#pragma unroll
-            for (int k = 0; k < kMapAhead; ++k) held[k] = b0 + kMapThreads * k < a.num_blocks ? a.held[b0 + kMapThreads * k] : 0;
-#pragma unroll
-            for (int k = 0; k < kMapAhead; ++k) {
-                const int b = b0 + kMapThreads * k;
-                const uint32_t mine = static_cast<uint32_t>(__ballot(held[k] > 0) >> (tid & 32));
-                if ((tid & 31) == 0 && b < words * 32) {
-                    movable[b >> 5] = live[b >> 5] & ~mine;
-                    live[b >> 5] |= mine;
-                }
-            }
+            for (int k = 0; k < kMostSlices; ++k) named |= k < w.slices ? w.named[k * words + i] : 0;
+            live[i] = named | held;
+            movable[i] = named & ~held;
         }
     } else {
-        for (int i = tid; i < words; i += kMapThreads) movable[i] = live[i];
+        for (int i = tid; i < words; i += kMapThreads) live[i] = 0;
+        __syncthreads();
+        map_entries(a, have, live, 0, entries);
+        __syncthreads();
+        if (a.held) {
+            map_held(a, 0, words, [&](int i, uint32_t word) {
+                movable[i] = live[i] & ~word;
+                live[i] |= word;
+            });
+        } else {
+            for (int i = tid; i < words; i += kMapThreads) movable[i] = live[i];
+        }
     }
     __syncthreads();
     int32_t limit = 0, moves = 0;   // L, and how many blocks may move (of those below L too, so far)
@@ -507,6 +565,8 @@ __global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a)
         if (i < words) {
             live_before[i] = limit + (before >> 16);
             moves_before[i] = moves + (before & 0xFFFF);
+            const int rank = 32 * i - live_before[i], upto = rank + 32 - __builtin_popcount(live[i]);
+            if ((rank + 31) / 32 * 32 < upto) free_from[(rank + 31) / 32] = i;   // of 32 ranks at most one is a multiple
         }
         limit += total >> 16;
         moves += total & 0xFFFF;
@@ -515,9 +575,11 @@ __global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a)
     const auto bits_below = [](uint32_t word, int b) { return __builtin_popcount(word & ((1u << (b & 31)) - 1)); };
     const int below = limit >= a.num_blocks ? moves : moves_before[limit >> 5] + bits_below(movable[limit >> 5], limit);
     const int total = moves - below;   // blocks that move
+    const int free_all = 32 * words - limit;   // with those that the last word has past the last block
     // the free block of rank k
     const auto slot = [&](int k) {
-        int lo = 0, hi = limit >> 5;   // the last word with at most k free blocks before it
+        // the last word with at most k free blocks before it
+        int lo = free_from[k >> 5], hi = k + 32 - (k & 31) < free_all ? free_from[(k >> 5) + 1] : words - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
             if (32 * mid - live_before[mid] <= k) lo = mid;
@@ -543,7 +605,7 @@ __global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a)
         if (k >= total) a.src[k] = -1;
     }
     for (int e = first; e < entries; e += step) {
-        const int i = row_of(e);
+        const int i = entry_row(e, per);
         int32_t id = e - i * a.width < have[i] ? a.table[e] : -1;
         if (id < 0 || id >= a.num_blocks) id = -1;
         else if (id >= limit && movable[id >> 5] >> (id & 31) & 1) id = slot(moves_before[id >> 5] + bits_below(movable[id >> 5], id) - below);
@@ -624,14 +686,25 @@ hipError_t launch_kv_fork(const ForkArgs &a, hipStream_t s) {
 }
 
 size_t compact_workspace(int64_t num_blocks) {
-    return (static_cast<size_t>(2 * num_blocks + 2 * tiles_of(num_blocks)) * 4 + 15) / 16 * 16;
+    const int64_t tiles = 2 * num_blocks + 2 * tiles_of(num_blocks), bits = (kMostSlices + 1) * ((num_blocks + 31) / 32);
+    return (static_cast<size_t>(tiles > bits ? tiles : bits) * 4 + 15) / 16 * 16;
 }
 
 hipError_t launch_kv_compact(const CompactArgs &a, hipStream_t s) {
     const int64_t entries = static_cast<int64_t>(a.rows) * a.width;
-    if (a.num_blocks <= kMapBlocks && a.rows <= kMapRows && entries + (a.held ? a.num_blocks : 0) <= kMapReads) {
+    if (a.num_blocks <= kMapBlocks && a.rows <= kMapRows && entries <= kMapEntries) {
         const dim3 groups(blocks_of(entries > a.num_blocks ? entries : a.num_blocks, kMapThreads, 64));
-        hipLaunchKernelGGL(compact_map_kernel, groups, dim3(kMapThreads), 0, s, a);
+        const int64_t reads = entries + (a.held ? a.num_blocks : 0), words = (a.num_blocks + 31) / 32;
+        CompactBits w;
+        w.held = reinterpret_cast<uint32_t *>(a.workspace);
+        w.named = w.held + words;
+        w.slices = static_cast<int32_t>(blocks_of(reads, kSliceReads, kMostSlices));
+        if (reads <= kMapReads) {
+            hipLaunchKernelGGL(compact_map_kernel<false>, groups, dim3(kMapThreads), 0, s, a, w);
+        } else {
+            hipLaunchKernelGGL(compact_bits_kernel, dim3(w.slices), dim3(kMapThreads), 0, s, a, w);
+            hipLaunchKernelGGL(compact_map_kernel<true>, groups, dim3(kMapThreads), 0, s, a, w);
+        }
         return hipGetLastError();
     }
     const CompactSpace w = compact_space(a.workspace, a.num_blocks);

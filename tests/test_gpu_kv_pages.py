@@ -155,7 +155,7 @@ def test_compact_at_the_borders_of_tiles(blocks):
 
 
 @pytest.mark.parametrize("blocks", [65535, 65536, 65537, 70001, 131072])
-@pytest.mark.parametrize("rows,width", [(3, 900), (1024, 64), (1025, 3), (40, 1700), (1, 65536)])
+@pytest.mark.parametrize("rows,width", [(3, 900), (1024, 64), (1025, 3), (40, 1700), (1, 65536), (64, 4096), (64, 4097)])
 def test_compact_of_large_pools_and_tables(blocks, rows, width):
     """Around the sizes up to which one launch does it all."""
     rng = np.random.default_rng(blocks + rows)
