@@ -313,7 +313,7 @@ __global__ __launch_bounds__(kHandThreads) void fork_one_kernel(ForkArgs a, Fork
 }
 
 // ---------------------------------------------------------------- compact
-// The workspace: whether a table names a block; for a block that moves its place among
+// The workspace, for tables of any size: whether a table names a block; for a block that moves its place among
 // those; for each tile of blocks how many are live and how many of these may move.
 constexpr int kPageTile = 1024, kTileThreads = 256;
 
@@ -617,9 +617,9 @@ __global__ __launch_bounds__(kMapThreads) void compact_map_kernel(CompactArgs a,
 // ------------------------------------------------------------------- copy
 // A wave has a piece of 4 KB of the blocks of one layer, for some of the pairs: it
 // reads their ids at once and copies the piece of those that there are.  The stores
-// are not to stay in the L2: copies of 70 MB took 23.3 us with that hint and 32.1
+// are not to stay in the L2: copies of 66 MB took 23.3 us with that hint and 32.1
 // without, and 85 blocks of 4 layers with the attention that reads them right behind
-// 174.8 and 188.6.  What bounds it is memory: 70 MB read and 70 MB written, 6 TB/s.
+// 174.8 and 188.6.  What bounds it is memory: 66 MB read and 66 MB written, 5.8 TB/s.
 constexpr int kPiece = 4096;
 
 __global__ __launch_bounds__(256) void copy_kernel(CopyArgs a, int pieces, int pairs_each) {
@@ -720,7 +720,7 @@ hipError_t launch_kv_compact(const CompactArgs &a, hipStream_t s) {
 hipError_t launch_kv_copy(const CopyArgs &a, hipStream_t s) {
     const int pieces = a.kv_heads * 2 * kKvBlock * a.head_dim / kPiece;
     // a wave for each piece while there is room for that many, then up to 64 pairs a wave
-    // (70 MB of copies 23.5 us, with 8192 waves 28.6, with four times as many as here 23.5)
+    // (66 MB of copies 23.5 us, with 8192 waves 28.6, with four times as many as here 23.5)
     const int64_t all = static_cast<int64_t>(a.n) * pieces * a.layers;
     int64_t each = all / 32768;
     each = each < 1 ? 1 : each > 64 ? 64 : each;
