@@ -136,10 +136,12 @@ __device__ __forceinline__ double exp64(double x) {
     p = fma(p, f, 0.5000000104536173);
     p = fma(p, f, 1.0000000002430987);
     p = fma(p, f, 0.9999999999616821);
-    // (what is not a number has 0 in the low bits, also one from fp32, and stays it)
-    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(p));
-    const uint32_t high = static_cast<uint32_t>(bits >> 32) + (static_cast<uint32_t>(__double_as_longlong(t)) << 20);
-    return __longlong_as_double(static_cast<long long>(uint64_t(high) << 32 | static_cast<uint32_t>(bits)));
+    // (what is not a number has 0 in the low bits, also one from fp32, and stays it; written as a sum of 32 bits,
+    // which is one instruction: as part of one of 64 it is five)
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    u32x2 bits = __builtin_bit_cast(u32x2, p);
+    bits.y += __builtin_bit_cast(u32x2, t).x << 20;
+    return __builtin_bit_cast(double, bits);
 }
 
 // The same for fp32 differences from m of up to 700: those below -80 (least = m - 80) count as
@@ -152,9 +154,9 @@ __device__ __forceinline__ double exp_below(float z, double m, float least) { re
 // to, and where a logit is beyond that, or all were -inf so far, the sum follows it.  +inf and what
 // is not a number make the sum no number, and the part's largest logit either of them.
 //
-// 128 rows of 131072 tokens, 67 MB: 18.5 us, 3.6 TB/s.  What bounds it is the issue of
-// instructions, 26 a token, of which 17 are the exponential in 64 bits and its sum: 23 thousand
-// cycles a SIMD, beside 12 us of reading; 4 rows, 2 MB, 3.3 us, a launch and two waits for memory.
+// 128 rows of 131072 tokens, 67 MB: 18.0 us, 3.7 TB/s.  What bounds it is memory, in one burst
+// that all waves begin with, and then the last ones' exponentials: 17 instructions a token, 18 thousand
+// cycles a SIMD in all, most of them while others read.  4 rows, 2 MB, 3.4 us, a launch and two waits for memory.
 constexpr int kBufferWord3 = 0x00020000;
 constexpr float kReach = 600.0f;
 
