@@ -245,7 +245,7 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 __device__ __forceinline__ float unordered(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7FFFFFFFu : ~key); }
 
 constexpr uint32_t kLowestKey = 0x007FFFFF;   // of -inf
-constexpr int kBins = 1024, kBinListed = 256;   // kBinListed: scores of a bin that may be ranked
+constexpr int kBins = 1024, kBinListed = 64;   // kBinListed: scores of a bin that may be ranked, one a lane
 
 // A workgroup has one row and kv head.  The scores between the first and the last
 // blocks are counted in bins of equal width; in the bin that the m-th largest falls
@@ -257,7 +257,8 @@ constexpr int kBins = 1024, kBinListed = 256;   // kBinListed: scores of a bin t
 //
 // What bounds it is one step after the other: lengths, scores, six barriers.  1024 blocks
 // 4.7 us, 4096 6.2.  (Two bits at a time alone, some ten counts with a barrier each: 9.8 us
-// for 4096 blocks.)
+// for 4096 blocks; but of 250 scores that all fall into one bin, next to one that is far above
+// them, both kernels take 9.5 us that way, and 34.7 ranked one by one.)
 template <int THREADS, int EACH, bool LOOP>
 __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
     constexpr int WAVES = THREADS / 64, kHeld = THREADS * EACH, SETS = EACH / 4;
@@ -392,17 +393,15 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
             }
             __syncthreads();
             // a wave has one of them at a time, its lanes those that may be in front
+            const uint32_t other = lane < size ? list_key[lane] : 0;
+            const int other_at = list_index[lane < size ? lane : 0];
             for (int i = wave; i < size; i += WAVES) {
-                const uint32_t mine = list_key[i];
-                const int at = list_index[i];
-                int higher = 0, front = 0, equal = 0;
-                for (int j = lane; j - lane < size; j += 64) {
-                    const uint32_t other = j < size ? list_key[j] : 0;
-                    const bool same = other == mine;
-                    higher += __builtin_popcountll(__ballot(other > mine));
-                    equal += __builtin_popcountll(__ballot(same));
-                    front += __builtin_popcountll(__ballot(same && list_index[j < size ? j : 0] < at));
-                }
+                const uint32_t mine = __builtin_amdgcn_readlane(other, i);
+                const int at = __builtin_amdgcn_readlane(other_at, i);
+                const bool same = other == mine;
+                const int higher = __builtin_popcountll(__ballot(other > mine));
+                const int equal = __builtin_popcountll(__ballot(same));
+                const int front = __builtin_popcountll(__ballot(same && other_at < at));
                 if (lane == 0 && higher + front == wanted - 1) {   // the last one that is chosen
                     const bool whole = wanted - higher == equal;   // all that are equal to it are
                     found_key = whole ? mine - 1 : mine;
@@ -524,9 +523,11 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     p.tiles = static_cast<int>(tiles);
     p.ranges = static_cast<int>(ranges);
     p.units = static_cast<int>(tiles * ranges * batch);
-    hipLaunchKernelGGL((score_kernel<D>), dim3(8 * a.kv.kv_heads, (p.units + 7) / 8), dim3(64 * kScoreWaves), 0, s, a, p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (a.max_blocks > a.keep) {   // otherwise rows have all of their blocks, and no score is looked at
+        hipLaunchKernelGGL((score_kernel<D>), dim3(8 * a.kv.kv_heads, (p.units + 7) / 8), dim3(64 * kScoreWaves), 0, s, a, p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     const dim3 rows(a.kv.kv_heads, a.max_rows < 65535 ? a.max_rows : 65535, a.kv.batch);
     // the fewest waves whose registers hold the scores, 8 a thread while there are threads (both kernels: 61 rows of
     // 938 blocks 10.3 us, with 512 threads 12.0; 2 of 4096 13.3, with 256 threads 15.2, with 1024 of 16 scores 19.2)

@@ -140,6 +140,30 @@ def test_chunks_of_many_rows():
     _select(c, table, q, [1200, 40], [100, 40], 12, 1, 1, max_rows=1, max_length=1200)
 
 
+@pytest.mark.parametrize("count", [66, 67, 130, 250, 1000, 3000])
+@pytest.mark.parametrize("spread", [3, 30])
+def test_scores_that_are_far_apart(count, spread):
+    """A few blocks whose exponents are far above the others', so that these fall into one bin, or a few."""
+    rng = np.random.default_rng(count)
+    c = O.Cache.empty(count, 1, 64)
+    O.fill_random(c, rng)
+    for b in range(count):
+        c.put(b, 0, 0, c.block_codes(b, 0, 0), 20 if b % 97 == 5 else int(rng.integers(-spread, 1)))
+    table = rng.permutation(count)[None]
+    q = _queries(rng, 3, 4, 64)
+    for keep in (4, 20, 40):
+        _select(c, table, q, [32 * count - 1], [3], keep, 1, 2)
+
+
+@pytest.mark.parametrize("max_length", [639, 640, 641, 672, 5000])
+def test_as_many_as_there_are(max_length):
+    """keep of 20, which is all blocks up to 640 tokens."""
+    rng, c, table = _cache([600, 33, 640], 2, 64, 21)
+    q = _queries(rng, 6, 4, 64)
+    q[0] = np.nan                      # no score is looked at
+    _select(c, table, q, [600, 33, 640], [3, 1, 2], 20, 1, 2, max_length=max_length)
+
+
 def test_positions_past_max_length_have_no_blocks():
     rng, c, table = _cache([300, 90], 1, 64, 4)
     q = _queries(rng, 2, 1, 64)
