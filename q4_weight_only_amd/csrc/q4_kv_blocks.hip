@@ -41,9 +41,9 @@ __device__ __forceinline__ BlocksPartials blocks_partials(const AttentionArgs &a
 // which costs no memory traffic and needs no branch).
 //
 // What bounds it is memory where there are rows enough: 31 rows of 8 kv heads, 96 blocks,
-// 195 MB, 33.6 us or 5.8 TB/s; one row, lengths, list, table and codes one after the other,
+// 195 MB, 33.5 us or 5.8 TB/s; one row, lengths, list, table and codes one after the other,
 // 5.6 us; many rows of few heads, 61 of 8 with 40 blocks that are shared and so in the caches,
-// the instructions for 16 heads of which few are there, 12.2 us.
+// the instructions for 16 heads of which few are there, 12.0 us (256 rows, 96 blocks: 71 us, 11 TB/s).
 template <int D>
 __global__ __launch_bounds__(64 * kBlocksWaves, 2) void attention_blocks_kernel(AttentionArgs a, BlocksPlan plan, const int32_t *chosen, int keep) {
     constexpr int W = kBlocksWaves, KQ = D / 32, DT = D / 16;
