@@ -134,10 +134,10 @@ struct ScorePlan {
 // A workgroup has 16 rows of one sequence and kv head and a range of its blocks; a
 // wave's product is 16 rows x 16 blocks, the bounds straight from memory to operand
 // registers: lane l has 16 bytes at 16 (l / 16) of each 64 of block l % 16.  They are on
-// their way while the rows' sums are formed.
+// their way while the rows' sums are formed, or the blocks before are worked on.
 //
 // What bounds it is memory: 31 sequences of up to 2047 blocks and 8 heads, 84 MB of bounds
-// and exponents, in 19.2 us or 4.4 TB/s.  A block's exponents of all heads are in one line, so
+// and exponents, in 18.2 us or 4.6 TB/s.  A block's exponents of all heads are in one line, so
 // a unit's heads are given to one of the 8 dies, one after the other.
 template <int D>
 __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, ScorePlan plan) {
@@ -154,84 +154,109 @@ __global__ __launch_bounds__(64 * kScoreWaves) void score_kernel(SelectArgs a, S
         const int last = s.pos0 + t0 + rows - 1;   // position of the last row
         int end = last < 0 ? 0 : last / kKvBlock + 1;
         end = end < a.max_blocks ? end : a.max_blocks;
-        for (int begin = range * kScoreBlocks; begin < end; begin += plan.ranges * kScoreBlocks) {   // the same for the workgroup
+        // a wave's blocks of a range: their ids two ranges ahead, their bounds one
+        const int step = plan.ranges * kScoreBlocks;
+        const auto id_of = [&](int begin) {
             const int block = begin + 16 * wave + r;
-            const int32_t id = block < end ? kv_block_id(a.kv, b, block) : -1;
-            // D / 2 lanes have a row of q, a pair of dimensions each; the first rows' first heads are read ahead of the bounds
-            constexpr int kLanes = D / 2, kAtOnce = 64 * kScoreWaves / kLanes;
-            const int pair = threadIdx.x % kLanes;
-            const uint32_t *q = reinterpret_cast<const uint32_t *>(
-                a.q + (static_cast<int64_t>(s.row0 + t0 + threadIdx.x / kLanes) * a.q_heads + head * a.group) * D) + pair;
-            const int64_t q_step = static_cast<int64_t>(kAtOnce) * a.q_heads * (D / 2);
-            const auto heads_of = [&](int i, int h0, uint32_t(&v)[4]) {   // (what is past the rows or the group is 0)
-                const bool there = i * kAtOnce + static_cast<int>(threadIdx.x) / kLanes < rows;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) v[h] = there && h0 + h < a.group ? q[i * q_step + (h0 + h) * (D / 2)] : 0;
-            };
-            uint32_t v[4];
-            heads_of(0, 0, v);
-            const int64_t plane = static_cast<int64_t>(id < 0 ? 0 : id) * a.kv.kv_heads + head;
+            return block < end ? kv_block_id(a.kv, b, block) : -1;
+        };
+        int begin = range * kScoreBlocks;
+        if (begin >= end) continue;   // the same for the workgroup
+        int32_t id[2];
+        i32x4 bounds[2][KK];
+        int exps[2];
+        const auto fetch = [&](int u) {
+            const int64_t plane = static_cast<int64_t>(id[u] < 0 ? 0 : id[u]) * a.kv.kv_heads + head;
             const i32x4 *src = reinterpret_cast<const i32x4 *>(a.summary + plane * (2 * D)) + g;
-            i32x4 bounds[KK];
 #pragma unroll
-            for (int k = 0; k < KK; ++k) bounds[k] = src[4 * k];   // a line is two of them: not nontemporal
-            const int e = a.kv.exps[plane * 2];
-            for (int i = 0; i < 16 / kAtOnce; ++i) {
-                const int row = i * kAtOnce + threadIdx.x / kLanes;
-                double up[2] = {0, 0}, down[2] = {0, 0};
-                for (int h0 = 0; h0 < a.group; h0 += 4) {
-                    if (i + h0 > 0) heads_of(i, h0, v);
+            for (int k = 0; k < KK; ++k) bounds[u][k] = src[4 * k];   // a line is two of them: not nontemporal
+            exps[u] = a.kv.exps[plane * 2];
+        };
+        id[0] = id_of(begin);
+        // D / 2 lanes have a row of q, a pair of dimensions each; the first rows' first heads are read ahead of the bounds
+        constexpr int kLanes = D / 2, kAtOnce = 64 * kScoreWaves / kLanes;
+        const int pair = threadIdx.x % kLanes;
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(
+            a.q + (static_cast<int64_t>(s.row0 + t0 + threadIdx.x / kLanes) * a.q_heads + head * a.group) * D) + pair;
+        const int64_t q_step = static_cast<int64_t>(kAtOnce) * a.q_heads * (D / 2);
+        const auto heads_of = [&](int i, int h0, uint32_t(&v)[4]) {   // (what is past the rows or the group is 0)
+            const bool there = i * kAtOnce + static_cast<int>(threadIdx.x) / kLanes < rows;
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const float x[2] = {__uint_as_float(v[h] << 16), __uint_as_float(v[h] & 0xFFFF0000u)};
+            for (int h = 0; h < 4; ++h) v[h] = there && h0 + h < a.group ? q[i * q_step + (h0 + h) * (D / 2)] : 0;
+        };
+        uint32_t v[4];
+        heads_of(0, 0, v);
+        fetch(0);
+        id[1] = id_of(begin + step);
+        for (int i = 0; i < 16 / kAtOnce; ++i) {
+            const int row = i * kAtOnce + threadIdx.x / kLanes;
+            double up[2] = {0, 0}, down[2] = {0, 0};
+            for (int h0 = 0; h0 < a.group; h0 += 4) {
+                if (i + h0 > 0) heads_of(i, h0, v);
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            // what is not a number goes into both
-                            up[k] += x[k] < 0.0f ? 0.0f : x[k];
-                            down[k] += x[k] > 0.0f ? 0.0f : x[k];
-                        }
+                for (int h = 0; h < 4; ++h) {
+                    const float x[2] = {__uint_as_float(v[h] << 16), __uint_as_float(v[h] & 0xFFFF0000u)};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        // what is not a number goes into both
+                        up[k] += x[k] < 0.0f ? 0.0f : x[k];
+                        down[k] += x[k] > 0.0f ? 0.0f : x[k];
                     }
                 }
-                const double most = fmax(fmax(up[0], up[1]), -fmin(down[0], down[1]));
-                const bool fine = __builtin_isfinite(up[0] + up[1] - down[0] - down[1]);
-                // most < 2^(e2 - 1022)
-                const int e2 = static_cast<int>(fold<kLanes>(static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(most)) >> 52 & 0x7FF),
-                                                             [](uint32_t x, uint32_t y) { return x > y ? x : y; }));
-                const uint64_t all = __ballot(fine);
-                const bool every = kLanes == 64 ? all == ~uint64_t(0) : static_cast<uint32_t>(lane < 32 ? all : all >> 32) == ~0u;
-                uint32_t high[2] = {0, 0}, low[2] = {0, 0};
-                if (every && e2 > 0) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int x = static_cast<int>(__builtin_rint(__builtin_ldexp(k < 2 ? up[k & 1] : down[k & 1], 13 + 1022 - e2)));
-                        high[k / 2] |= static_cast<uint32_t>((x >> 7) & 0xFF) << (k % 2 * 8);
-                        low[k / 2] |= static_cast<uint32_t>(x & 0x7F) << (k % 2 * 8);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    *reinterpret_cast<uint16_t *>(&parts[0][row][k * D + 2 * pair]) = static_cast<uint16_t>(high[k]);
-                    *reinterpret_cast<uint16_t *>(&parts[1][row][k * D + 2 * pair]) = static_cast<uint16_t>(low[k]);
-                }
-                if ((i + 1) * kAtOnce >= rows) break;   // rows past the last hold anything: their sums are not used
             }
-            __syncthreads();
-            i32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+            const double most = fmax(fmax(up[0], up[1]), -fmin(down[0], down[1]));
+            const bool fine = __builtin_isfinite(up[0] + up[1] - down[0] - down[1]);
+            // most < 2^(e2 - 1022)
+            const int e2 = static_cast<int>(fold<kLanes>(static_cast<uint32_t>(static_cast<uint64_t>(__double_as_longlong(most)) >> 52 & 0x7FF),
+                                                         [](uint32_t x, uint32_t y) { return x > y ? x : y; }));
+            const uint64_t all = __ballot(fine);
+            const bool every = kLanes == 64 ? all == ~uint64_t(0) : static_cast<uint32_t>(lane < 32 ? all : all >> 32) == ~0u;
+            uint32_t high[2] = {0, 0}, low[2] = {0, 0};
+            if (every && e2 > 0) {
 #pragma unroll
-            for (int k = 0; k < KK; ++k)
-#pragma unroll
-                for (int p = 0; p < 2; ++p)
-                    sum[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4 *>(&parts[p][r][64 * k + 16 * g]), bounds[k], sum[p], 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int row = 4 * g + j;
-                if (block >= end || row >= rows) break;
-                const float total = static_cast<float>(sum[0][j] * 128 + sum[1][j]);   // below 2^28, rounded once
-                a.scores[(static_cast<int64_t>(s.row0 + t0 + row) * a.kv.kv_heads + head) * a.max_blocks + block] =
-                    id < 0 ? -__builtin_inff() : __builtin_ldexpf(total, e);
+                for (int k = 0; k < 4; ++k) {
+                    const int x = static_cast<int>(__builtin_rint(__builtin_ldexp(k < 2 ? up[k & 1] : down[k & 1], 13 + 1022 - e2)));
+                    high[k / 2] |= static_cast<uint32_t>((x >> 7) & 0xFF) << (k % 2 * 8);
+                    low[k / 2] |= static_cast<uint32_t>(x & 0x7F) << (k % 2 * 8);
+                }
             }
-            __syncthreads();   // the rows' sums have been read
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                *reinterpret_cast<uint16_t *>(&parts[0][row][k * D + 2 * pair]) = static_cast<uint16_t>(high[k]);
+                *reinterpret_cast<uint16_t *>(&parts[1][row][k * D + 2 * pair]) = static_cast<uint16_t>(low[k]);
+            }
+            if ((i + 1) * kAtOnce >= rows) break;   // rows past the last hold anything: their sums are not used
         }
+        __syncthreads();
+        for (bool more = true; more;) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int block = begin + 16 * wave + r;
+                const int32_t now = id[u];
+                more = begin + step < end;
+                if (more) {
+                    fetch(u ^ 1);
+                    id[u] = id_of(begin + 2 * step);
+                }
+                i32x4 sum[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+                for (int k = 0; k < KK; ++k)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        sum[p] = __builtin_amdgcn_mfma_i32_16x16x64_i8(*reinterpret_cast<const i32x4 *>(&parts[p][r][64 * k + 16 * g]), bounds[u][k], sum[p], 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = 4 * g + j;
+                    if (block >= end || row >= rows) break;
+                    const float total = static_cast<float>(sum[0][j] * 128 + sum[1][j]);   // below 2^28, rounded once
+                    a.scores[(static_cast<int64_t>(s.row0 + t0 + row) * a.kv.kv_heads + head) * a.max_blocks + block] =
+                        now < 0 ? -__builtin_inff() : __builtin_ldexpf(total, exps[u]);
+                }
+                begin += step;
+                if (!more) break;
+            }
+        }
+        __syncthreads();   // the rows' sums have been read
     }
 }
 
@@ -510,6 +535,12 @@ __global__ __launch_bounds__(THREADS) void choose_kernel(SelectArgs a) {
     }
 }
 
+// Workgroups that are wanted, four on each compute unit: where there are more ranges, a workgroup
+// takes several, with the rows' sums formed once.  (31 sequences of up to 2047 blocks, both kernels, with
+// 512, 1024, 2048 and any number of them 28.3, 25.9, 26.6 and 31.8 us; 32 of 1875, 20 heads of 64, 39.4, 39.6,
+// 39.4 and, with the sums for each range, 45.6.)
+constexpr int64_t kScoreGroups = 1024;
+
 // The kernels loop where a launch cannot hold all units.
 constexpr int64_t kMostUnits = 8 * 65535;
 
@@ -518,6 +549,8 @@ hipError_t launch_select(const SelectArgs &a, hipStream_t s) {
     ScorePlan p;
     const int64_t batch = a.kv.batch;
     int64_t ranges = (a.max_blocks + kScoreBlocks - 1) / kScoreBlocks, tiles = (static_cast<int64_t>(a.max_rows) + 15) / 16;
+    const int64_t others = batch * tiles * a.kv.kv_heads;
+    if (ranges * others > kScoreGroups) ranges = others < kScoreGroups ? kScoreGroups / others : 1;
     if (ranges * batch > kMostUnits) ranges = kMostUnits / batch;
     if (tiles * ranges * batch > kMostUnits) tiles = kMostUnits / (ranges * batch);
     p.tiles = static_cast<int>(tiles);
