@@ -11,8 +11,8 @@ random; the sizes are arguments of Decoder.  Sequences of unequal length share
 one batch, blocks are handed out as they are needed.
 
 Beam search shares the blocks of what beams have in common, and copies one when
-two of them go on in it.  With --keep attention reads that many blocks of a
-sequence, the ones that matter most to each token.
+two of them go on in it.  With --keep (3 or more) attention reads that many blocks of
+a sequence, the ones that matter most to each token.
 """
 
 from __future__ import annotations

@@ -47,7 +47,7 @@ const char *q4_status_str(int status) {
         case Q4_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
         case Q4_ERR_SEGMENTS: return "bad segment list (need 1<=nseg<=8 and valid entries)";
         case Q4_ERR_HIP: return "HIP runtime error at launch";
-        case Q4_ERR_RANGE: return "a size or flag is outside the range stated in q4_decoder.h";
+        case Q4_ERR_RANGE: return "a size or flag is outside the range stated in q4_decoder.h or q4_search.h";
         default: return "unknown status";
     }
 }
