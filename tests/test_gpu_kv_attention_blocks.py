@@ -106,6 +106,17 @@ def test_entries_in_no_order_negative_and_past_the_row(keep):
     assert (got[0, :2] == 0).all() and (got[1, 2:] == 0).all()
 
 
+@pytest.mark.parametrize("keep", [8, 60, 300])
+@pytest.mark.parametrize("length", [40, 700, 1500])
+def test_lists_longer_than_the_table(length, keep):
+    """Blocks anywhere in a list that is longer than the table is wide, each many times."""
+    def change(rng, c, table, q, chosen):
+        chosen[...] = rng.integers(-1, length // 32 + 1, chosen.shape)
+        chosen[0, 0, : keep // 2] = -1          # only behind the table's width
+
+    _check([length], [1], heads=2, group=4, keep=keep, change=change)
+
+
 def test_a_block_named_twice_counts_twice():
     def change(rng, c, table, q, chosen):
         chosen[:, :, 3:] = chosen[:, :, :3]
