@@ -263,27 +263,31 @@ __global__ __launch_bounds__(256) void blocks_join_kernel(AttentionArgs a, Block
 // 24 blocks 8.8 and 9.2; 96 blocks 21.4 and 14.6.)
 constexpr int kChunkLeast = kBlocksWaves, kSavedEntries = 22, kMostSplits = 64;
 
-// A list that kv_select made has its blocks in front, no more than the table has: so many
-// are divided.  (Another list may have more; the last chunk then takes longer.  Lists of 64 with 10 blocks
-// 6.8 us, divided as if they were full 8.2; 16 rows of them 6.9 and 10.1.)
-BlocksPlan plan_blocks(const AttentionArgs &a, int keep) {
+int64_t splits_wanted(const AttentionArgs &a, int64_t tiles) {
+    const int64_t work = static_cast<int64_t>(a.kv.rows) * a.kv.kv_heads * tiles;
+    const int64_t splits = work < 256 ? 256 / (work < 1 ? 1 : work) : 1;
+    return splits < kMostSplits ? splits : kMostSplits;
+}
+
+// For lists with `entries` to divide.
+BlocksPlan plan_blocks(const AttentionArgs &a, int64_t entries) {
     BlocksPlan p;
-    const int64_t likely = keep < a.kv.table_width ? keep : a.kv.table_width;
     p.tiles = (a.group + kTileHeads - 1) / kTileHeads;
-    const int64_t work = static_cast<int64_t>(a.kv.rows) * a.kv.kv_heads * p.tiles;
-    int64_t splits = work < 256 ? 256 / (work < 1 ? 1 : work) : 1;
-    if (splits > kMostSplits) splits = kMostSplits;
-    int64_t chunk = (likely + splits - 1) / splits;
+    const int64_t splits = splits_wanted(a, p.tiles);
+    int64_t chunk = (entries + splits - 1) / splits;
     if (chunk < kChunkLeast) chunk = kChunkLeast;
-    if (likely - chunk < kSavedEntries + static_cast<int64_t>(a.kv.rows) * a.q_heads / 128) chunk = likely;
+    if (entries - chunk < kSavedEntries + static_cast<int64_t>(a.kv.rows) * a.q_heads / 128) chunk = entries;
     p.chunk = static_cast<int>(chunk);
-    p.splits = static_cast<int>((likely + chunk - 1) / chunk);
+    p.splits = static_cast<int>((entries + chunk - 1) / chunk);
     return p;
 }
 
 template <int D>
 hipError_t launch(const AttentionArgs &a, const int32_t *chosen, int keep, hipStream_t s) {
-    const BlocksPlan p = plan_blocks(a, keep);
+    // A list that kv_select made has its blocks in front, no more than the table has: so many are
+    // divided.  (Another list may have more; the last chunk then takes longer.  Lists of 64 with 10 blocks
+    // 6.8 us, divided as if they were full 8.2; 16 rows of them 6.9 and 10.1.)
+    const BlocksPlan p = plan_blocks(a, keep < a.kv.table_width ? keep : a.kv.table_width);
     int rows = a.max_rows;   // the kernels loop where a launch cannot hold them all
     if (static_cast<int64_t>(rows) * p.splits > 65535) rows = 65535 / p.splits;
     const dim3 grid(a.kv.kv_heads * p.tiles, rows * p.splits, a.kv.batch);
@@ -297,9 +301,11 @@ hipError_t launch(const AttentionArgs &a, const int32_t *chosen, int keep, hipSt
 }  // namespace
 
 size_t attention_blocks_workspace(const AttentionArgs &a, int keep, int head_dim) {
+    // whatever the table's width: what is divided for a list is divided for a longer one
     const BlocksPlan p = plan_blocks(a, keep);
     if (p.splits == 1) return 0;
-    const size_t parts = static_cast<size_t>(a.kv.rows) * a.q_heads * p.splits;   // as in blocks_partials()
+    const int64_t most = (keep + kChunkLeast - 1) / kChunkLeast, wanted = splits_wanted(a, p.tiles);
+    const size_t parts = static_cast<size_t>(a.kv.rows) * a.q_heads * (most < wanted ? most : wanted);   // as in blocks_partials()
     return ((parts * 2 + 3) / 4 * 4 + parts * head_dim) * sizeof(float);
 }
 
