@@ -155,8 +155,8 @@ __device__ __forceinline__ double exp_below(float z, double m, float least) { re
 // is not a number make the sum no number, and the part's largest logit either of them.
 //
 // 128 rows of 131072 tokens, 67 MB: 18.0 us, 3.7 TB/s.  What bounds it is memory, in one burst
-// that all waves begin with, and then the last ones' exponentials: 17 instructions a token, 18 thousand
-// cycles a SIMD in all, most of them while others read.  4 rows, 2 MB, 3.4 us, a launch and two waits for memory.
+// that all waves begin with, and then the last ones' exponentials: 23 thousand cycles a SIMD of
+// issue in all, most of them while others read.  4 rows, 2 MB, 3.4 us, a launch and two waits for memory.
 constexpr int kBufferWord3 = 0x00020000;
 constexpr float kReach = 600.0f;
 

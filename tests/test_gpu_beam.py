@@ -220,3 +220,16 @@ def test_outputs_that_overlap_are_refused():
             bad()
     got = q4.beam_select(z, s, 3, out=(i, j, None))
     assert got[0].data_ptr() == i.data_ptr() and got[1].data_ptr() == j.data_ptr()
+
+
+@pytest.mark.parametrize("byte", [0, 255, 127])
+@pytest.mark.parametrize("V", [100, 32003, 131072])
+def test_what_a_workspace_held_does_not_matter(V, byte):
+    """The rows of beams that have ended are not read, and nothing is written for them."""
+    rng, z, scores = _random(3, 4, V, 11)
+    z, scores = z.astype(np.float32), scores.astype(np.float32)
+    finished = np.array([[0, 1, 0, 0], [1, 1, 1, 1], [1, 0, 1, 1]])
+    want = S.beam_select(z, scores, 6, finished, 5)
+    ws = torch.full((q4.beam_select_workspace(3, 4, V),), byte, dtype=torch.uint8, device=DEV)
+    p, t, s = q4.beam_select(dev(z), dev(scores), 6, finished=dev(finished, torch.int32), pad=5, workspace=ws)
+    assert np.array_equal(p.cpu().numpy(), want[0]) and np.array_equal(t.cpu().numpy(), want[1])
