@@ -13,6 +13,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ int32_t held_to(int32_t v, int32_t lo, int32_t hi) { return v < lo ? lo : v > hi ? hi : v; }
 
@@ -72,6 +73,9 @@ struct Wants {
 // sequence wants (asked of thread i % kHandThreads alone), place_of: its blocks so far and
 // whether it gets a copy, writers_of: how many go on in a block, and the last of them.
 // With up to kHandThreads sequences, of few new blocks each, nothing is read twice.
+// EACH: blocks that a thread looks at together.  Where the free blocks are at the end of a large pool,
+// the search is what one compute unit reads: 170000 blocks, 64 tables of 60 entries 30 us with 8, 43 with 4, 32 with 16;
+// with the free ones in front 11.5, 11.0 and 13.0.  (In LDS 4, whose reads lie side by side.)
 constexpr int kHandThreads = 1024, kFreeHeld = 2048;
 
 struct HandSpace {
@@ -80,7 +84,7 @@ struct HandSpace {
     int32_t most;                // new blocks of a sequence
 };
 
-template <typename WantsOf, typename PlaceOf, typename WritersOf>
+template <int EACH, typename WantsOf, typename PlaceOf, typename WritersOf>
 __device__ __forceinline__ void hand_out(const ForkArgs &a, const ForkSpace &w, HandSpace &lds, int32_t *refs, WantsOf wants_of, PlaceOf place_of,
                                          WritersOf writers_of) {
     const int tid = threadIdx.x;
@@ -105,24 +109,30 @@ __device__ __forceinline__ void hand_out(const ForkArgs &a, const ForkSpace &w, 
         want_all += total;
     }
     __syncthreads();
-    // the first want_all free blocks, four a thread at a time
+    // the first want_all free blocks, EACH a thread at a time
     int32_t found = 0;
-    for (int b0 = 0, turn = 0; b0 < a.num_blocks && found < want_all; b0 += kHandThreads * 4, turn ^= 1) {
-        const int b = b0 + tid * 4;
-        int32_t count[4], n = 0;
+    for (int b0 = 0, turn = 0; b0 < a.num_blocks && found < want_all; b0 += kHandThreads * EACH, turn ^= 1) {
+        const int b = b0 + tid * EACH;
+        i32x4_any count[EACH / 4];
+        uint32_t free = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) count[k] = b + k < a.num_blocks ? refs[b + k] : 1;
+        for (int k = 0; k < EACH; k += 4) {
+            if (b + k + 4 <= a.num_blocks) {
+                count[k / 4] = *reinterpret_cast<const i32x4_any *>(&refs[b + k]);
+            } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) n += count[k] == 0;
-        int32_t total;
-        int32_t at = found + scan_group(n, lds.sums[turn], total);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (count[k] == 0 && at < want_all) {
-                if (at < kFreeHeld) lds.free[at] = b + k;
-                else w.free[at] = b + k;
-                ++at;
+                for (int i = 0; i < 4; ++i) count[k / 4][i] = b + k + i < a.num_blocks ? refs[b + k + i] : 1;
             }
+        }
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) free |= (count[k / 4][k % 4] == 0 ? 1u : 0u) << k;
+        int32_t total;
+        int32_t at = found + scan_group<int32_t>(__builtin_popcount(free), lds.sums[turn], total);
+        for (; free && at < want_all; free &= free - 1, ++at) {
+            const int32_t block = b + __builtin_ctz(free);
+            if (at < kFreeHeld) lds.free[at] = block;
+            else w.free[at] = block;
+        }
         found += total;
     }
     if (found > want_all) found = want_all;
@@ -226,7 +236,7 @@ __global__ __launch_bounds__(kHandThreads) void fork_hand_kernel(ForkArgs a, For
         x.copy = x.s.goes_on && x.last >= 0 && (w.keeper[x.last] != i || a.refs[x.last] > w.writers[x.last]);
         return x;
     };
-    hand_out(a, w, lds, a.refs, wants_of,
+    hand_out<8>(a, w, lds, a.refs, wants_of,
              [&](int i, int32_t &have, bool &copy) {
                  const Wants x = wants_of(i);
                  have = x.s.have;
@@ -299,7 +309,7 @@ __global__ __launch_bounds__(kHandThreads) void fork_one_kernel(ForkArgs a, Fork
         }
         copied[tid] = mine.copy;
     }
-    hand_out(a, w, lds, refs, [&](int) { return mine; },
+    hand_out<4>(a, w, lds, refs, [&](int) { return mine; },
              [&](int i, int32_t &so_far, bool &copy) {
                  so_far = have[i];
                  copy = copied[i];

@@ -320,3 +320,23 @@ def test_graph_replays_follow_their_inputs(rows, width, blocks):
         wc = q4.kv_compact(wf.block_table, wf.lengths, blocks, held=held)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(f, wf)) and all(torch.equal(x, y) for x, y in zip(c, wc))
+
+
+def test_fork_into_tensors_that_start_anywhere():
+    """Counts of a large and nearly full pool, read four at a time, in a tensor that starts on 4 bytes alone."""
+    rng = np.random.default_rng(8)
+    blocks, rows, width = 30011, 20, 30
+    free = np.sort(rng.permutation(blocks)[:rows + 3])
+    held = np.ones(blocks, dtype=int)
+    held[free] = 0
+    table = rng.permutation(np.flatnonzero(held))[:rows * width].reshape(rows, width)
+    table[:, -1] = -1
+    lengths = np.full(rows, 32 * (width - 1))
+    want = S.kv_fork(table, lengths, np.arange(rows), blocks, 1, held)
+    for start in (0, 1, 2, 3):
+        flat = torch.full((blocks + 8,), 77, dtype=torch.int32, device=DEV)
+        got = q4.kv_fork(_i32(table), _i32(lengths), _i32(np.arange(rows)), blocks, held=_i32(held),
+                         out=(None, None, flat[start:start + blocks], None, None, None))
+        for name, a in zip(got._fields, got):
+            assert np.array_equal(a.cpu().numpy(), want[name]), name
+        assert (flat[:start] == 77).all() and (flat[start + blocks:] == 77).all()
