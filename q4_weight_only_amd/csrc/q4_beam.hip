@@ -231,6 +231,9 @@ constexpr int kPickThreads = 1024, kPickWaves = kPickThreads / 64;
 constexpr int kSlots = 256, kFewSlots = 64;   // the items of four waves' lanes are a slot, or of all 16
 constexpr int kFewKeep = 16;      // up to so many the few do: 4 beams of 131072 tokens 9.2 us, with 256 slots 10.6
 constexpr int kListed = 512;      // segments that may be listed before they are cut down to `keep`
+constexpr int kRanked = 256;      // and so many of them, or of tokens, that may be ranked one against all (8 beams of 3000 tokens,
+                                  // keep 100: 20.6 us, with 64 34.8; one beam of 10000 and keep 128 34.2, with 512 42.3)
+constexpr int kListedMore = 64;   // and, of those in listed parts, beyond twice as many as are kept
 constexpr int kAhead = 4;         // parts of a row, or items, of a lane that are loaded together
 constexpr int kSegmentBits = 19;  // a segment's id: its beam, then its place in the row, of up to 2^24 / 32
 
@@ -240,7 +243,8 @@ constexpr int kSegmentBits = 19;  // a segment's id: its beam, then its place in
 // least n items reach, and hardly more where they are spread evenly.  The segments that
 // reach it are listed, and the n first of them found by counting, for each, the ones
 // in front (so is the bound among the slots).  Where too many reach the bound of parts, it is
-// found for segments; where it is still too many (they are equal), the n-th segment itself is found, bit by bit.
+// found for segments; where it is still too many (they are equal), the n-th segment itself is found, bit by bit, and so
+// is the n-th token where there are too many of these.
 //
 // The bound is found in fp32, on z + (score - lse), which is off by two roundings:
 // with n items at b or more, the n first have a score of b less one error or more, and
@@ -265,7 +269,7 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
     __shared__ int32_t list_id[kListed];
     __shared__ int32_t segment_id[kMaxKeep];
     __shared__ double bound_s;
-    __shared__ int32_t listed, parts_listed, counted;
+    __shared__ int32_t listed, parts_listed, counted[3];
     extern __shared__ __align__(16) uint8_t dynamic[];   // keep * 32 elements: s, then ids
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = a.keep, group = blockIdx.x;
@@ -400,7 +404,9 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
     const auto list_best = [&](const bool parts, auto each_sum) {
         float best = my_ended ? static_cast<float>(base[tid]) : kNone;
         each_sum([&](int, int, float s) { best = fmaxf(best, s); });
-        atomicMax(&slot[few ? lane : tid % kSlots], ordered(best));
+        // a wave's lanes follow those of the wave before, of which few have items where a beam has few
+        const int each = parts ? in.parts : segments;
+        atomicMax(&slot[(lane + wave * (each < 64 ? each : 64)) & ((few ? kFewSlots : kSlots) - 1)], ordered(best));
         __syncthreads();
         // the n-th of the slots, by how many reach each of the wave's
         uint32_t reached = 0;
@@ -466,45 +472,74 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
         return !exact;
     };
     const bool finite = list_best(coarse, each_item);
-    if (listed > kListed && coarse && finite) {   // the same for the workgroup
-        // too many segments in few parts, for instance those of the one beam that a search begins with
+    if (listed > 2 * n + kListedMore && coarse && finite) {   // the same for the workgroup
+        // many segments in few parts, for instance those of the one beam that a search begins with: to list
+        // fewer takes less than to rank them
         __syncthreads();
         start();
         list_best(false, each_segment_sum);
     }
-    if (listed > kListed) {   // the same for the workgroup
-        const auto count = [&](auto f) {   // of items
-            if (tid == 0) counted = 0;
+    // Of the places that `each` gives, every thread its own, the n first: those whose score, in order, is above `over`,
+    // and of those equal to it the ones up to the id `last`.
+    const auto cut = [&](auto each, uint64_t &over, int32_t &last) {
+        if (tid < 3) counted[tid] = 0;
+        __syncthreads();
+        int step = 0;   // three counters in turn: one barrier each
+        const auto count = [&](auto f) {   // of places
+            int32_t c = 0, all;
+            each([&](const Place &p) { c += p.s != kNone && f(p); });
+            scan_wave(c, all);
+            if (lane == 0) atomicAdd(&counted[step], all);
+            const int next = step == 2 ? 0 : step + 1;
+            if (tid == 0) counted[next] = 0;
             __syncthreads();
-            int c = 0;
-            each_place([&](const Place &p) { c += p.s != kNone && f(p); });
-#pragma unroll
-            for (int i = 1; i < 64; i *= 2) c += __shfl_xor(c, i);
-            if (lane == 0) atomicAdd(&counted, c);
-            __syncthreads();
-            const int total = counted;
-            __syncthreads();
-            return total;
+            all = counted[step];
+            step = next;
+            return all;
         };
         uint64_t key = 0;
-        for (int bit = 63; bit >= 0; --bit) {
+        int reach = count([&](const Place &) { return true; });   // as many have a score of `key` or more
+        for (int bit = 63; bit >= 0 && reach > n; --bit) {
             const uint64_t higher = key | uint64_t(1) << bit;
-            if (count([&](const Place &p) { return ordered(p.s) >= higher; }) >= n) key = higher;
+            const int c = count([&](const Place &p) { return ordered(p.s) >= higher; });
+            if (c >= n) {
+                key = higher;
+                reach = c;
+            }
         }
-        // of those that are equal to it, the first ones
-        const int want = n - count([&](const Place &p) { return ordered(p.s) > key; });
-        int32_t last = 0;   // the largest id for which fewer than `want` lie below it
-        for (int bit = 25; bit >= 0; --bit) {
-            const int32_t higher = last | 1 << bit;
-            if (count([&](const Place &p) { return ordered(p.s) == key && p.id < higher; }) < want) last = higher;
+        over = key;
+        last = INT32_MAX;
+        if (reach > n) {   // of those that are equal to it, the first ones
+            const int want = n - count([&](const Place &p) { return ordered(p.s) > key; });
+            last = 0;   // the largest id for which fewer than `want` lie below it
+            for (int bit = 29; bit >= 0; --bit) {
+                const int32_t higher = last | 1 << bit;
+                if (count([&](const Place &p) { return ordered(p.s) == key && p.id < higher; }) < want) last = higher;
+            }
         }
-        // (0: there are fewer than n)
-        const double bound = key ? __longlong_as_double(static_cast<long long>(key >> 63 ? key & ~(uint64_t(1) << 63) : ~key)) : static_cast<double>(kNone);
+        __syncthreads();
+    };
+    uint64_t over;
+    int32_t last;
+    const auto first_ones = [&](const Place &p) {
+        const uint64_t key = ordered(p.s);
+        return p.s != kNone && (key > over || (key == over && p.id <= last));
+    };
+    if (listed > kListed) {   // the same for the workgroup: not all of them are in the list
+        cut(each_place, over, last);
         if (tid == 0) listed = 0;
         __syncthreads();
         each_place([&](const Place &p) {
-            if (p.s > bound || (p.s == bound && p.id <= last)) list(p.id, p.s);
+            if (first_ones(p)) list(p.id, p.s);
         });
+        __syncthreads();
+    } else if (listed > kRanked) {
+        const int size = listed;
+        const Place mine = {tid < size ? list_s[tid] : static_cast<double>(kNone), tid < size ? list_id[tid] : 0};
+        cut([&](auto f) { f(mine); }, over, last);
+        if (tid == 0) listed = 0;
+        __syncthreads();
+        if (first_ones(mine)) list(mine.id, mine.s);
         __syncthreads();
     }
     const int found = listed;   // at most kListed now
@@ -537,7 +572,32 @@ __global__ __launch_bounds__(kPickThreads) void beam_pick_kernel(BeamArgs a, Sca
         element_id[place] = b << 24 | at;
     }
     __syncthreads();
-    const int elements = listed;
+    int elements = listed;
+    if (elements > kRanked) {   // the same for the workgroup: equal ones, or a group of few segments
+        constexpr int kEach = kMaxKeep * kBeamSegment / kPickThreads;
+        Place mine[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int i = tid + kPickThreads * k;
+            mine[k].s = i < elements ? element_s[i] : static_cast<double>(kNone);
+            mine[k].id = i < elements ? element_id[i] : 0;
+        }
+        cut([&](auto f) {
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) f(mine[k]);
+        }, over, last);
+        if (tid == 0) listed = 0;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            if (!first_ones(mine[k])) continue;
+            const int place = atomicAdd(&listed, 1);
+            element_s[place] = mine[k].s;
+            element_id[place] = mine[k].id;
+        }
+        __syncthreads();
+        elements = listed;
+    }
     const int64_t out = static_cast<int64_t>(group) * n;
     for (int i = wave; i < elements; i += kPickWaves) {
         const Place me = {element_s[i], element_id[i]};

@@ -103,6 +103,20 @@ def test_one_beam_with_a_score(V, keep):
     _check(z, scores, keep)
 
 
+@pytest.mark.parametrize("groups,beams,V,keep", [(3, 7, 1941, 7), (2, 6, 2497, 6), (4, 5, 4477, 10), (2, 64, 600, 128), (1, 40, 10000, 128),
+                                                 (1, 64, 1000, 17), (2, 8, 3000, 100), (2, 2, 1500, 128), (2, 1, 4096, 128), (1, 1, 4097, 128)])
+def test_few_parts_and_few_segments(groups, beams, V, keep):
+    """A beam has few parts, or a group hardly more segments than are kept; also where one beam has all candidates,
+    and where most tokens are held at the type's lowest value, which is a number."""
+    rng, z, scores = _random(groups, beams, V, V)
+    _check(z, scores, keep)
+    z[:, rng.permutation(V)[: V - 3]] = np.finfo(np.float32).min
+    _check(z, scores, keep)
+    z, scores = _random(groups, beams, V, V + 1)[1:]
+    scores[:, 1:] = -np.inf
+    _check(z, scores, keep)
+
+
 def test_few_values_many_ties():
     rng, _, _ = _random(1, 1, 1, 6)
     z, scores = rng.integers(0, 3, (8, 50000)), -np.array([[0.0, 0.3, 0.7, 1.1], [0.9, 0.2, 0.0, 0.1]])
