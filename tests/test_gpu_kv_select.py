@@ -140,6 +140,20 @@ def test_chunks_of_many_rows():
     _select(c, table, q, [1200, 40], [100, 40], 12, 1, 1, max_rows=1, max_length=1200)
 
 
+@pytest.mark.parametrize("group", [1, 3])
+@pytest.mark.parametrize("top", [0.75, 1.5, 3.0, 6.0, 12.0])
+def test_sums_halfway_between_two_whole_numbers(top, group):
+    """Q in steps of 2^(E - 13), and many halves of them: these go to the even one, whatever the power of two."""
+    rng, c, table = _cache([25000, 20000], 2, 64, 22)
+    q = np.zeros((40, 2 * group, 64))
+    step = 2.0 ** (np.frexp(top)[1] - 13)
+    q[:, ::group] = (2 * rng.integers(-120, 120, (40, 2, 64)) + 1) * step / 2     # odd halves, within 8 bits
+    q[:, :, 0] = 0
+    q[:, ::group, 0] = top
+    assert np.array_equal(bf16(q), q)
+    _select(c, table, q, [25000, 20000], [20, 20], 30, 1, 2)
+
+
 @pytest.mark.parametrize("count", [66, 67, 130, 250, 1000, 3000])
 @pytest.mark.parametrize("spread", [3, 30])
 def test_scores_that_are_far_apart(count, spread):
